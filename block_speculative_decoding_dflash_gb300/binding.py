@@ -586,3 +586,243 @@ class TargetContext(DFlashContext):
         h = _vp()
         self._check(lib.dflash_target_full_ring(self.h, ctypes.byref(h)))
         return RingCache(handle=h.value, owner=self) if h.value else None
+
+
+# ---- paged KV cache ----------------------------------------------------------------
+PAGED_BAD_PAGE, PAGED_BAD_ROWS, PAGED_GAVE_UP = 1, 2, 4
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k", "v", "pos", "table", "length", "status")] + [
+        (n, _i32) for n in ("n_pages", "page_rows", "kv_heads", "head_dim", "n_seq", "max_pages", "dtype")]
+
+
+class PagedAppendArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("q", "k", "v", "row_pos", "start", "rope_pos")] + [
+        ("pair_axis_host", ctypes.c_char_p)] + [(n, _vp) for n in ("q_norm", "k_norm", "q_out", "weight")] + [
+        (n, _i64) for n in ("q_stride", "k_stride", "v_stride")] + [
+        (n, _i32) for n in ("rows", "n_q_heads", "n_axes", "rot_pairs", "rope_neox")] + [
+        (n, ctypes.c_float) for n in ("rope_theta", "rms_eps")]
+
+
+class PagedAttentionArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("q", "q_pos", "start", "slopes", "prefix", "out", "lse", "workspace")] + [
+        (n, _i64) for n in ("workspace_bytes", "q_stride")] + [
+        (n, _i32) for n in ("rows", "n_q_heads", "causal", "window", "max_len")] + [
+        (n, ctypes.c_float) for n in ("scale", "softcap")]
+
+
+class PagedEvictArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("weight", "next_pos", "weight_out", "pos_out", "length_out", "workspace")] + [
+        ("workspace_bytes", _i64), ("budget", _i32), ("recent", _i32)]
+
+
+_sig("dflash_paged_append", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAppendArgs), _vp)
+_sig("dflash_paged_attention_workspace", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs),
+     ctypes.POINTER(_i64))
+_sig("dflash_paged_attention", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs), _vp)
+_sig("dflash_paged_key_weight", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs), _vp,
+     ctypes.c_float, _vp, _vp)
+_sig("dflash_paged_evict_workspace", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedEvictArgs),
+     ctypes.POINTER(_i64))
+_sig("dflash_paged_evict", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedEvictArgs), _vp)
+
+
+class PagedCache:
+    """One layer's paged K and V of many sequences (C: dflash_paged_cache) over
+    the caller's tensors: k, v [n_pages, kv_heads, page_rows, head_dim], pos
+    (int32) and weight (fp32) [n_pages, kv_heads, page_rows], table (int32)
+    [n_seq, max_pages], length (int32) [n_seq], status (int32) [1].
+
+    `length` counts each sequence's rows with the next call's new ones; it and
+    `table` are device tensors that the caller changes in place (so a captured
+    round can be replayed). Every call runs on the current torch stream or on
+    `stream`; the tensors must be ready there. A call's workspace comes from
+    torch's allocator on that stream unless `workspace` (uint8) is given, which
+    a capture that torch does not know of (dflash_capture_begin) needs."""
+
+    def __init__(self, k, v, pos, table, length, weight=None, status=None):
+        if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float32):
+            raise DFlashError(EINVAL, "paged: k must be [n_pages, kv_heads, page_rows, head_dim] in bf16 or fp32")
+        self.device = k.device
+        self.dtype = k.dtype
+        n_pages, kv_heads, page_rows, head_dim = k.shape
+        self._need("k", k, k.dtype, k.shape)
+        self._need("v", v, k.dtype, k.shape)
+        self._need("pos", pos, torch.int32, k.shape[:3])
+        if table.dim() != 2:
+            raise DFlashError(EINVAL, "paged: table must be [n_seq, max_pages]")
+        self._need("table", table, torch.int32, table.shape)
+        self._need("length", length, torch.int32, table.shape[:1])
+        if weight is not None:
+            self._need("weight", weight, torch.float32, k.shape[:3])
+        if status is not None:
+            self._need("status", status, torch.int32, (1,))
+        self.k, self.v, self.pos, self.table, self.length = k, v, pos, table, length
+        self.weight, self.status = weight, status
+        self._paged_shape = k.shape[:3]
+        self.c = PagedCacheC(k.data_ptr(), v.data_ptr(), pos.data_ptr(), table.data_ptr(), length.data_ptr(), _ptr(status),
+                             n_pages, page_rows, kv_heads, head_dim, table.shape[0], table.shape[1],
+                             BF16 if k.dtype == torch.bfloat16 else F32)
+        self._c = ctypes.byref(self.c)
+        # the C side checks sizes and alignment with every call; once here so a
+        # bad cache is refused when it is made
+        probe = PagedEvictArgs(budget=1)
+        self._check(lib.dflash_paged_evict_workspace(self._c, ctypes.byref(probe), ctypes.byref(_i64())))
+
+    @classmethod
+    def allocate(cls, n_pages, page_rows, kv_heads, head_dim, n_seq, max_pages, dtype="bf16", device="cuda"):
+        """A cache over new tensors: pages, positions and weights zero, table -1 (no page), length 0."""
+        dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+        shape = (n_pages, kv_heads, page_rows)
+        return cls(torch.zeros(*shape, head_dim, dtype=dt, device=device), torch.zeros(*shape, head_dim, dtype=dt, device=device),
+                   torch.zeros(shape, dtype=torch.int32, device=device),
+                   torch.full((n_seq, max_pages), -1, dtype=torch.int32, device=device),
+                   torch.zeros(n_seq, dtype=torch.int32, device=device),
+                   weight=torch.zeros(shape, dtype=torch.float32, device=device),
+                   status=torch.zeros(1, dtype=torch.int32, device=device))
+
+    def _check(self, rc):
+        if rc:
+            raise DFlashError(rc, last_error(None))
+
+    def _need(self, name, t, dtype, shape):
+        """A dense tensor of the given type and shape on the cache's device."""
+        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+            raise DFlashError(EINVAL, f"paged: {name} must be a dense {dtype} tensor of shape {tuple(shape)} on {self.device}, "
+                                      f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+    def _rows(self, name, t, heads=None):
+        """[rows, heads, head_dim] whose rows may be apart; its row stride."""
+        hd = self.c.head_dim
+        if (t.dim() != 3 or t.dtype != self.dtype or t.device != self.device or t.shape[2] != hd or (heads is not None and t.shape[1] != heads)
+                or t.shape[0] and (t.stride(2) != 1 or t.shape[1] > 1 and t.stride(1) != hd)):
+            raise DFlashError(EINVAL, f"paged: {name} must be [rows, heads, {hd}] in {self.dtype} on {self.device} with dense rows, "
+                                      f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * hd
+
+    def _launch(self, call, stream):
+        """call(stream handle) with the cache's device current."""
+        if self.device.type != "cuda":
+            raise DFlashError(EINVAL, "paged: the cache is not on a GPU")
+        if self.device.index is not None and self.device.index != torch.cuda.current_device():
+            with torch.cuda.device(self.device):
+                return self._launch(call, stream)
+        self._check(call((stream or torch.cuda.current_stream()).cuda_stream))
+
+    def _workspace(self, nbytes, workspace, stream):
+        if workspace is not None:
+            if workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous():
+                raise DFlashError(EINVAL, f"paged: workspace must be a dense uint8 tensor on {self.device}")
+            return workspace
+        if not nbytes:
+            return None
+        if stream is None:
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+
+    def append(self, q, k, v, row_pos, start, q_out, rope_pos=None, pair_axis=b"", theta=1e6, neox=True, q_norm=None,
+               k_norm=None, eps=1e-6, stream=None):
+        """dflash_paged_append: the new rows q [rows, nq, hd], k, v [rows, kv_heads, hd] (rows may be apart) at positions
+        row_pos [rows]; rope_pos [n_axes, rows] and pair_axis (bytes: the axis of each rotated pair) give the rotation,
+        none without pairs. Their weight becomes 0 when the cache has weights."""
+        hd, n = self.c.head_dim, q.shape[0]
+        a = PagedAppendArgs()
+        a.q_stride = self._rows("q", q)
+        a.k_stride = self._rows("k", k, self.c.kv_heads)
+        a.v_stride = self._rows("v", v, self.c.kv_heads)
+        if k.shape[0] != n or v.shape[0] != n:
+            raise DFlashError(EINVAL, f"paged: q, k and v have {n}, {k.shape[0]} and {v.shape[0]} rows")
+        self._need("row_pos", row_pos, torch.int32, (n,))
+        self._need("start", start, torch.int32, (self.c.n_seq + 1,))
+        self._need("q_out", q_out, self.dtype, q.shape)
+        pair_axis = bytes(pair_axis)
+        if pair_axis:
+            if rope_pos is None or rope_pos.dim() != 2:
+                raise DFlashError(EINVAL, "paged: rope_pos must be [n_axes, rows]")
+            self._need("rope_pos", rope_pos, torch.int32, (rope_pos.shape[0], n))
+            a.rope_pos = rope_pos.data_ptr()
+            a.pair_axis_host = pair_axis
+        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if g is not None:
+                self._need(name, g, self.dtype, (hd,))
+                setattr(a, name, g.data_ptr())
+        a.q, a.k, a.v, a.row_pos, a.start, a.q_out = (q.data_ptr(), k.data_ptr(), v.data_ptr(), row_pos.data_ptr(),
+                                                      start.data_ptr(), q_out.data_ptr())
+        a.weight = _ptr(self.weight)
+        a.rows, a.n_q_heads, a.n_axes, a.rot_pairs = n, q.shape[1], rope_pos.shape[0] if pair_axis else 1, len(pair_axis)
+        a.rope_neox, a.rope_theta, a.rms_eps = 1 if neox else 0, theta, eps
+        self._launch(lambda st: lib.dflash_paged_append(self._c, ctypes.byref(a), st), stream)
+
+    def _attention_args(self, q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len):
+        n, nq = q.shape[0], q.shape[1]
+        a = PagedAttentionArgs()
+        a.q_stride = self._rows("q", q)
+        self._need("q_pos", q_pos, torch.int32, (n,))
+        self._need("start", start, torch.int32, (self.c.n_seq + 1,))
+        if lse is not None:
+            self._need("lse", lse, torch.float32, (n, nq))
+            a.lse = lse.data_ptr()
+        if slopes is not None:
+            self._need("slopes", slopes, torch.float32, (nq,))
+            a.slopes = slopes.data_ptr()
+        if prefix is not None:
+            self._need("prefix", prefix, torch.int32, (self.c.n_seq,))
+            a.prefix = prefix.data_ptr()
+        a.q, a.q_pos, a.start = q.data_ptr(), q_pos.data_ptr(), start.data_ptr()
+        a.rows, a.n_q_heads, a.causal, a.window, a.max_len = n, nq, 1 if causal else 0, window, max_len
+        a.scale, a.softcap = (self.c.head_dim ** -0.5 if scale is None else scale), softcap
+        return a
+
+    def attention(self, q, q_pos, start, out, lse=None, scale=None, causal=True, window=0, softcap=0.0, slopes=None,
+                  prefix=None, max_len=0, workspace=None, stream=None):
+        """dflash_paged_attention: out [rows, nq, hd] and lse [rows, nq] of q [rows, nq, hd] (rows may be apart) at
+        positions q_pos [rows]; rows start[s] .. start[s + 1] - 1 belong to sequence s. scale None: head_dim ** -0.5."""
+        a = self._attention_args(q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len)
+        self._need("out", out, self.dtype, q.shape)
+        a.out = out.data_ptr()
+        need = _i64()
+        self._check(lib.dflash_paged_attention_workspace(self._c, ctypes.byref(a), ctypes.byref(need)))
+        ws = self._workspace(need.value, workspace, stream)
+        if ws is not None:
+            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        self._launch(lambda st: lib.dflash_paged_attention(self._c, ctypes.byref(a), st), stream)
+
+    def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
+                   softcap=0.0, slopes=None, prefix=None, max_len=0, stream=None):
+        """dflash_paged_key_weight: weight_out = decay * weight + the attention each cached row gets from q, whose lse and
+        mask are attention's. weight and weight_out default to the cache's weight."""
+        weight = self.weight if weight is None else weight
+        weight_out = self.weight if weight_out is None else weight_out
+        if weight_out is None or lse is None:
+            raise DFlashError(EINVAL, "paged: key_weight needs lse, and a weight_out where the cache has no weight")
+        a = self._attention_args(q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len)
+        if weight is not None:
+            self._need("weight", weight, torch.float32, self._paged_shape)
+        self._need("weight_out", weight_out, torch.float32, self._paged_shape)
+        self._launch(lambda st: lib.dflash_paged_key_weight(self._c, ctypes.byref(a), _ptr(weight), decay,
+                                                            weight_out.data_ptr(), st), stream)
+
+    def evict(self, budget, recent, next_pos, weight=None, weight_out=None, pos_out=None, length_out=None, workspace=None,
+              stream=None):
+        """dflash_paged_evict: every sequence and kv head keeps its `budget` heaviest rows, those at positions >=
+        next_pos[s] - recent before all others. The outputs default to the cache's own weight, pos and length."""
+        weight = self.weight if weight is None else weight
+        weight_out = self.weight if weight_out is None else weight_out
+        pos_out = self.pos if pos_out is None else pos_out
+        length_out = self.length if length_out is None else length_out
+        if weight is None or weight_out is None:
+            raise DFlashError(EINVAL, "paged: evict needs weights")
+        self._need("weight", weight, torch.float32, self._paged_shape)
+        self._need("weight_out", weight_out, torch.float32, self._paged_shape)
+        self._need("pos_out", pos_out, torch.int32, self._paged_shape)
+        self._need("length_out", length_out, torch.int32, (self.c.n_seq,))
+        self._need("next_pos", next_pos, torch.int32, (self.c.n_seq,))
+        a = PagedEvictArgs(weight.data_ptr(), next_pos.data_ptr(), weight_out.data_ptr(), pos_out.data_ptr(),
+                           length_out.data_ptr(), None, 0, budget, recent)
+        need = _i64()
+        self._check(lib.dflash_paged_evict_workspace(self._c, ctypes.byref(a), ctypes.byref(need)))
+        ws = self._workspace(need.value, workspace, stream)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
+        self._launch(lambda st: lib.dflash_paged_evict(self._c, ctypes.byref(a), st), stream)

@@ -367,4 +367,63 @@ struct SynthArgs {
 };
 cudaError_t launch_synth_target(int dtype, const SynthArgs& a, cudaStream_t st);
 
+// ---- paged KV cache -------------------------------------------------------------
+// Device view of dflash_paged_cache (checked by the C ABI).
+struct PagedView {
+  void* k; void* v;
+  int* pos;
+  const int* table;
+  const int* length;
+  int* status;                 // DFLASH_PAGED_* bits, or NULL
+  int n_pages, lg_rows;        // page_rows = 1 << lg_rows
+  int nkv, hd, n_seq, max_pages;
+};
+constexpr int kPagedMaxPairs = 128;
+struct PagedAppendArgs {
+  PagedView c;
+  const void* q; const void* k; const void* v;
+  const int* row_pos; const int* start; const int* rope_pos;
+  const void* q_norm; const void* k_norm;
+  void* q_out;
+  float* weight;
+  long long q_stride, k_stride, v_stride;
+  int rows, nq, pairs, neox;
+  float eps;
+  // frequency of pair i in turns per position, as a fraction of 2^64
+  unsigned long long freq[kPagedMaxPairs];
+  unsigned char axis[kPagedMaxPairs];
+};
+cudaError_t launch_paged_append(int dtype, const PagedAppendArgs& a, cudaStream_t st);
+
+struct PagedAttnArgs {
+  PagedView c;
+  const void* q;
+  const int* q_pos; const int* start;
+  const float* slopes; const int* prefix;
+  void* out;
+  float* lse;
+  float* part_o;               // [splits][rows * nq][hd], unnormalised
+  float2* part_ml;             // [splits][rows * nq] (maximum in log2 units, sum)
+  long long q_stride;
+  int rows, nq, G, causal, window, splits, max_len;
+  float scale, softcap;
+  // key weights
+  const float* weight_in; float* weight_out;
+  float decay;
+};
+// How an attention call is split: chosen from sizes alone.
+struct PagedPlan { int kind, splits; long long bytes; };
+PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
+cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
+cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st);
+
+struct PagedEvictArgs {
+  PagedView c;
+  const float* weight; const int* next_pos;
+  float* weight_out; int* pos_out; int* length_out;
+  int* moves;                  // [n_seq][nkv][1 + 2 * max_moves]: count, holes, late rows
+  int budget, recent, max_moves;
+};
+cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t st);
+
 }  // namespace dfl

@@ -1,0 +1,190 @@
+// Shared by the paged-cache kernels: their arguments, the page lookup, the
+// search for a CTA's sequence and tile, the mask, and the classification of
+// key tiles.
+#pragma once
+
+#include "common.cuh"
+#include "dflash.h"
+#include "kernels.h"
+#include "launch.cuh"
+
+namespace dfl {
+
+constexpr int kPagedNoPos = INT32_MIN;     // position of a row that is not there
+
+// Rows sequence s has: its length, cut to the table.
+__device__ __forceinline__ int paged_length(const PagedView& c, int s) {
+  const int n = c.length[s], cap = c.max_pages << c.lg_rows;
+  return n < 0 ? 0 : (n > cap ? cap : n);
+}
+// New rows [first, last) of sequence s, cut to [0, rows].
+__device__ __forceinline__ int2 paged_new_rows(const int* start, int s, int rows) {
+  int a = start[s], b = start[s + 1];
+  a = a < 0 ? 0 : (a > rows ? rows : a);
+  b = b < a ? a : (b > rows ? rows : b);
+  return make_int2(a, b);
+}
+// Row index (in units of rows of head_dim) of slot `slot` of sequence s and
+// kv head h, or -1 where its page id is outside the pool. slot < capacity.
+__device__ __forceinline__ long long paged_row(const PagedView& c, int s, int h, int slot) {
+  const int page = c.table[(size_t)s * c.max_pages + (slot >> c.lg_rows)];
+  if ((unsigned)page >= (unsigned)c.n_pages) return -1;
+  return (((long long)page * c.nkv + h) << c.lg_rows) + (slot & ((1 << c.lg_rows) - 1));
+}
+
+// The sequence and the tile within it of tile number `t` of the batch, with
+// `per` new rows (times G) to a tile; called by one full warp. seq = -1 past
+// the last tile.
+struct PagedTile { int seq, tile, first, count; };
+__device__ __forceinline__ PagedTile paged_find_tile(const int* start, int n_seq, int rows, int G, int per, int t) {
+  const int lane = threadIdx.x & 31;
+  PagedTile r{-1, 0, 0, 0};
+  for (int s0 = 0; s0 < n_seq; s0 += 32) {
+    const int s = s0 + lane;
+    int2 ab = make_int2(0, 0);
+    if (s < n_seq) ab = paged_new_rows(start, s, rows);
+    const int tiles = (int)(((long long)(ab.y - ab.x) * G + per - 1) / per);
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t < incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      r.seq = s0 + l;
+      r.tile = t - __shfl_sync(0xffffffffu, incl - tiles, l);
+      r.first = __shfl_sync(0xffffffffu, ab.x, l);
+      r.count = __shfl_sync(0xffffffffu, ab.y - ab.x, l);
+      return r;
+    }
+    t -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
+
+// The mask of the header: whether a query at pq sees a row at pk.
+struct PagedMask { int causal, window, prefix; };
+__device__ __forceinline__ bool paged_sees(const PagedMask& m, int pq, int pk) {
+  const int d = pq - pk;
+  const bool in = (!m.causal || d >= 0) && (m.window <= 0 || abs(d) <= m.window);
+  return pk != kPagedNoPos && (in || pk < m.prefix);
+}
+// Queries at [qmin, qmax], rows at [kmin, kmax] (kmin > kmax: none are there):
+// 0 no query sees any row, 2 every query sees every row (of a tile whose rows
+// are all there), 1 otherwise. Never 0 or 2 wrongly; 1 may be more than needed.
+__device__ __forceinline__ int paged_class(const PagedMask& m, int qmin, int qmax, int kmin, int kmax, bool whole) {
+  if (kmin > kmax || qmin > qmax) return 0;
+  const long long W = m.window > 0 ? m.window : (1ll << 40);
+  const long long ahead = m.causal ? 0 : W;
+  const bool some = kmin < m.prefix || (kmin <= qmax + ahead && kmax >= qmin - W);
+  if (!some) return 0;
+  const bool all = kmax < m.prefix || (kmax <= qmin + ahead && kmin >= qmax - W);
+  return all && whole ? 2 : 1;
+}
+
+// Classifies the key tiles [t0, t1) of `keys` rows of (s, h) against queries
+// at [qmin, qmax]: bit t - t0 of `some` / `all` in shared memory (zeroed here)
+// for classes >= 1 / 2. Called by every thread of the CTA; a warp takes kU
+// tiles at a time so that its loads are in flight together. The caller
+// synchronises afterwards.
+template <int KEYS>
+__device__ __forceinline__ void paged_classify(const PagedView& c, int s, int h, int len, const PagedMask& m, int qmin, int qmax,
+                                               int t0, int t1, unsigned* some, unsigned* all) {
+  constexpr int kU = 4, kPer = KEYS / 32;
+  static_assert(kPer == 2 || kPer == 4, "a lane takes 2 or 4 keys");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+  for (int i = threadIdx.x; i <= (t1 - t0) >> 5; i += blockDim.x) some[i] = all[i] = 0u;
+  __syncthreads();
+  for (int b = t0 + warp * kU; b < t1; b += nw * kU) {
+    int p[kU][kPer];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int slot = (b + u) * KEYS + lane * kPer;
+      const long long row = (b + u < t1 && slot < len) ? paged_row(c, s, h, slot) : -1;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) p[u][j] = kPagedNoPos;
+      if (row >= 0) {
+        if (kPer == 4) {
+          const int4 x = *reinterpret_cast<const int4*>(c.pos + row);
+          p[u][0] = x.x; p[u][1] = x.y; p[u][kPer - 2] = x.z; p[u][kPer - 1] = x.w;
+        } else {
+          const int2 x = *reinterpret_cast<const int2*>(c.pos + row);
+          p[u][0] = x.x; p[u][1] = x.y;
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          if (slot + j >= len) p[u][j] = kPagedNoPos;
+      } else if (b + u < t1 && slot < len && c.status) {
+        atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      int lo = INT32_MAX, hi = INT32_MIN;
+      bool whole = true;
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (p[u][j] == kPagedNoPos) whole = false;
+        else { lo = min(lo, p[u][j]); hi = max(hi, p[u][j]); }
+      }
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      whole = __all_sync(0xffffffffu, whole);
+      if (lane == 0 && b + u < t1) {
+        const int k = paged_class(m, qmin, qmax, lo, hi, whole);
+        if (k >= 1) atomicOr(&some[(b + u - t0) >> 5], 1u << ((b + u - t0) & 31));
+        if (k == 2) atomicOr(&all[(b + u - t0) >> 5], 1u << ((b + u - t0) & 31));
+      }
+    }
+  }
+}
+
+// The tiles that split z of n takes of the key tiles of a sequence. Without a
+// window a split classifies and takes an equal range of tiles; with one, where
+// most tiles are seen by nobody, every split classifies all tiles and takes an
+// equal share of those that are seen (skip .. skip + take - 1 in order).
+struct PagedShare { int t0, t1, skip, take; };
+__device__ __forceinline__ PagedShare paged_range(int tiles, int window, int z, int n) {
+  if (window > 0) return PagedShare{0, tiles, 0, tiles};
+  const int per = (tiles + n - 1) / n;
+  const int a = min(tiles, z * per), b = min(tiles, a + per);
+  return PagedShare{a, b, 0, b - a};
+}
+__device__ __forceinline__ void paged_take(PagedShare& r, const unsigned* some, int window, int z, int n) {
+  int seen = 0;
+  for (int i = 0; i <= (r.t1 - r.t0) >> 5; ++i) seen += __popc(some[i]);
+  if (window > 0) {
+    r.skip = (int)((long long)seen * z / n);
+    r.take = (int)((long long)seen * (z + 1) / n) - r.skip;
+  } else {
+    r.skip = 0;
+    r.take = seen;
+  }
+}
+// Walks the seen tiles of a share in ascending order.
+struct PagedCursor {
+  const unsigned* bits;
+  int word, left;
+  unsigned cur;
+  __device__ __forceinline__ PagedCursor(const unsigned* some, const PagedShare& r) : bits(some), word(0), left(r.take) {
+    int skip = r.skip;
+    cur = left > 0 ? bits[0] : 0u;
+    if (left > 0) {
+      while (skip >= __popc(cur)) { skip -= __popc(cur); cur = bits[++word]; }
+      while (skip-- > 0) cur &= cur - 1;
+    }
+  }
+  // The next tile (relative to t0), or -1.
+  __device__ __forceinline__ int next() {
+    if (left <= 0) return -1;
+    while (!cur) cur = bits[++word];
+    const int b = __ffs(cur) - 1;
+    cur &= cur - 1;
+    --left;
+    return word * 32 + b;
+  }
+};
+
+}  // namespace dfl

@@ -1,0 +1,454 @@
+// Attention over the paged cache on CUDA cores, for fp32 and for the shapes
+// the tensor-core kernel does not take, the merge of split partials, and the
+// key weights for the same shapes.
+//
+// Per (query tile, kv head, split): an online softmax over key tiles. The
+// scores are kept in log2 units, u = t * log2(e), so p = exp2(u - m).
+#include <math.h>
+
+#include "paged.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kBN = 64;                    // keys of a tile
+constexpr int kMaxTiles = (1 << 20) / kBN; // of the longest table
+
+// Score of a raw dot product in log2 units.
+struct PagedScore { float scale2, cap2, inv_cap; };
+__device__ __forceinline__ PagedScore paged_score_of(const PagedAttnArgs& a) {
+  PagedScore s;
+  s.scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+  s.cap2 = a.softcap * kLog2e;
+  s.inv_cap = 0.f;
+  return s;
+}
+__device__ __forceinline__ float paged_score(const PagedAttnArgs& a, const PagedScore& s, float dot, float slope2, int pq, int pk) {
+  float u = dot * s.scale2;
+  if (a.softcap > 0.f) u = s.cap2 * tanhf(u);
+  if (slope2 != 0.f) u -= slope2 * fabsf((float)(pq - pk));
+  return u;
+}
+
+// Rows of `n` values at src into shared rows of HDP + 4 floats, zero past hd
+// and where src is NULL; 16-byte loads, `lanes` threads to a row.
+template <typename T, int HDP>
+__device__ __forceinline__ bool load_row(float* dst, const T* src, int hd, int lane, int lanes) {
+  bool bad = false;
+  for (int d = lane * 8; d < HDP; d += lanes * 8) {
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (src && d < hd) load8(src + d, x);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bad |= !(fabsf(x[i]) <= 3.4028234663852886e38f);
+    *reinterpret_cast<float4*>(dst + d) = make_float4(x[0], x[1], x[2], x[3]);
+    *reinterpret_cast<float4*>(dst + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
+  }
+  return bad;
+}
+
+// BM packed query rows (row r = token r / G, head r % G of the group) against
+// kBN keys at a time. Thread (ty, tx) holds TM rows ty * TM .. and keys tx,
+// tx + 16, .. of the scores, then dims tx * 4 + 64 j of the same rows' output:
+// 16 lanes share a row, so row statistics are shuffles within half a warp.
+// K and V tiles are read from HBM once per query tile; for few query rows
+// that read bounds the kernel, for many the fp32 FMA rate.
+template <typename T, int BM, int TM, int HDP>
+__global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttnArgs a) {
+  constexpr int NT = BM / TM * 16, LD = HDP + 4, NJ = HDP / 64;
+  pdl_enter();
+  extern __shared__ float smf[];
+  float* sq = smf;                          // [BM][LD]
+  float* sk = sq + BM * LD;                 // [kBN][LD]
+  float* sv = sk + kBN * LD;                // [kBN][LD]
+  float* sp = sv + kBN * LD;                // [BM][kBN + 4]
+  int* spos = reinterpret_cast<int*>(sp + BM * (kBN + 4));     // [kBN]
+  unsigned* some = reinterpret_cast<unsigned*>(spos + kBN);
+  unsigned* all = some + kMaxTiles / 32 + 1;
+  __shared__ PagedTile st;
+  __shared__ int s_qmin, s_qmax;
+  const PagedView& c = a.c;
+  const int h = blockIdx.y, z = blockIdx.z, G = a.G;
+  if (threadIdx.x < 32) {
+    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, G, BM, blockIdx.x);
+    int lo = INT32_MAX, hi = INT32_MIN;
+    if (t.seq >= 0) {
+      const int r0 = t.tile * BM, r1 = min(t.count * G, r0 + BM);
+      for (int i = r0 / G + (int)threadIdx.x; i <= (r1 - 1) / G; i += 32) {
+        const int p = a.q_pos[t.first + i];
+        lo = min(lo, p);
+        hi = max(hi, p);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (threadIdx.x == 0) { st = t; s_qmin = lo; s_qmax = hi; }
+  }
+  __syncthreads();
+  const PagedTile t = st;
+  if (t.seq < 0) return;
+  const int len = paged_length(c, t.seq);
+  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[t.seq] : INT32_MIN};
+  PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
+  paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
+
+  const int r0 = t.tile * BM, rows = min(BM, t.count * G - r0);
+  for (int e = threadIdx.x; e < BM * 16; e += NT) {
+    const int r = e >> 4;
+    const T* src = r < rows ? static_cast<const T*>(a.q) + (size_t)(t.first + (r0 + r) / G) * a.q_stride +
+                                  (size_t)(h * G + (r0 + r) % G) * c.hd : nullptr;
+    load_row<T, HDP>(sq + r * LD, src, c.hd, e & 15, 16);
+  }
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  int pq[TM];
+  float slope2[TM], mx[TM], sum[TM], o[TM][NJ * 4];
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = r0 + min(ty * TM + i, rows - 1);
+    pq[i] = a.q_pos[t.first + r / G];
+    slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
+    mx[i] = -INFINITY;
+    sum[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < NJ * 4; ++d) o[i][d] = 0.f;
+  }
+  const PagedScore ps = paged_score_of(a);
+  __syncthreads();
+  paged_take(sh, some, a.window, z, a.splits);
+  PagedCursor cur(some, sh);
+  for (int rel = cur.next(); rel >= 0; rel = cur.next()) {
+    const int k0 = (sh.t0 + rel) * kBN;
+    const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
+    bool bad = false;
+    for (int e = threadIdx.x; e < kBN * 8; e += NT) {
+      const int j = e >> 3, l8 = e & 7;
+      const long long row = k0 + j < len ? paged_row(c, t.seq, h, k0 + j) : -1;
+      load_row<T, HDP>(sk + j * LD, row >= 0 ? static_cast<const T*>(c.k) + row * c.hd : nullptr, c.hd, l8, 8);
+      bad |= load_row<T, HDP>(sv + j * LD, row >= 0 ? static_cast<const T*>(c.v) + row * c.hd : nullptr, c.hd, l8, 8);
+      if (l8 == 0) spos[j] = row >= 0 ? c.pos[row] : kPagedNoPos;
+    }
+    // a tile that some query sees only in part and whose V holds infinities or
+    // NaN: the hidden rows must not be multiplied by their zero weight
+    const bool careful = __syncthreads_or(bad && !full);
+    float s[TM][4];
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < HDP; d += 4) {
+      float4 q[TM], k[4];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * TM + i) * LD + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + d);
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
+          s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
+          s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
+          s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      unsigned seen = 0;
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int pk = spos[tx + 16 * j];
+        const bool v = full || paged_sees(m, pq[i], pk);
+        s[i][j] = v ? paged_score(a, ps, s[i][j], slope2[i], pq[i], pk) : -INFINITY;
+        seen |= (unsigned)v << j;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float mn = fmaxf(mx[i], top);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(mx[i] - base);
+      float add = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        add += p;
+        // a hidden row's weight is -0, a seen one's that underflowed +0
+        sp[(ty * TM + i) * (kBN + 4) + tx + 16 * j] = (seen >> j) & 1u ? p : -0.f;
+      }
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
+      sum[i] = sum[i] * f + add;
+      mx[i] = mn;
+#pragma unroll
+      for (int d = 0; d < NJ * 4; ++d) o[i][d] *= f;
+    }
+    __syncwarp();
+#pragma unroll 2
+    for (int j = 0; j < kBN; j += 4) {
+      float4 p[TM];
+#pragma unroll
+      for (int i = 0; i < TM; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * TM + i) * (kBN + 4) + j);
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+#pragma unroll
+        for (int n = 0; n < NJ; ++n) {
+          const float4 v = *reinterpret_cast<const float4*>(sv + (j + jj) * LD + n * 64 + tx * 4);
+#pragma unroll
+          for (int i = 0; i < TM; ++i) {
+            const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
+            if (careful && __float_as_uint(w) == 0x80000000u) continue;
+            o[i][n * 4 + 0] = fmaf(w, v.x, o[i][n * 4 + 0]);
+            o[i][n * 4 + 1] = fmaf(w, v.y, o[i][n * 4 + 1]);
+            o[i][n * 4 + 2] = fmaf(w, v.z, o[i][n * 4 + 2]);
+            o[i][n * 4 + 3] = fmaf(w, v.w, o[i][n * 4 + 3]);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int r = ty * TM + i;
+    if (r >= rows) continue;
+    const size_t at = (size_t)(t.first + (r0 + r) / G) * a.nq + h * G + (r0 + r) % G;
+    if (a.splits > 1) {
+      float* po = a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd;
+#pragma unroll
+      for (int n = 0; n < NJ; ++n)
+        if (n * 64 + tx * 4 < c.hd)
+          *reinterpret_cast<float4*>(po + n * 64 + tx * 4) = make_float4(o[i][n * 4], o[i][n * 4 + 1], o[i][n * 4 + 2], o[i][n * 4 + 3]);
+      if (tx == 0) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], sum[i]);
+      continue;
+    }
+    const bool none = sum[i] == 0.f;           // nothing seen (a NaN score makes the sum NaN)
+    const float inv = none ? 0.f : 1.f / sum[i];
+    T* out = static_cast<T*>(a.out) + at * c.hd;
+#pragma unroll
+    for (int n = 0; n < NJ; ++n)
+#pragma unroll
+      for (int d = 0; d < 4; ++d)
+        if (n * 64 + tx * 4 + d < c.hd) out[n * 64 + tx * 4 + d] = from_f<T>(none ? 0.f : o[i][n * 4 + d] * inv);
+    if (tx == 0 && a.lse) a.lse[at] = none ? -INFINITY : (mx[i] + log2f(sum[i])) * kLn2;
+  }
+}
+
+// Joins the splits of one (row, head), a warp to each: o = sum_z o_z
+// exp2(m_z - M) / sum_z l_z exp2(m_z - M). Rows of no sequence are left alone.
+template <typename T>
+__global__ void __launch_bounds__(128) paged_attn_merge_kernel(PagedAttnArgs a) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, hd = a.c.hd;
+  const long long at = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int first = max(0, a.start[0]), last = min(a.rows, a.start[a.c.n_seq]);
+  const long long n = (long long)a.rows * a.nq;
+  if (at >= n || at / a.nq < first || at / a.nq >= last) return;
+  float M = -INFINITY;
+  for (int z = lane; z < a.splits; z += 32) M = fmaxf(M, a.part_ml[z * n + at].x);
+  M = warp_max(M);
+  const float base = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int z = 0; z < a.splits; ++z) {
+    const float2 ml = a.part_ml[z * n + at];
+    if (ml.y == 0.f) continue;
+    const float f = exp2f(ml.x - base);
+    L += ml.y * f;
+    const float* o = a.part_o + (z * n + at) * hd;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int d = j * 128 + lane * 4;
+      if (d < hd) {
+        const float4 x = *reinterpret_cast<const float4*>(o + d);
+        acc[j * 4] = fmaf(f, x.x, acc[j * 4]);
+        acc[j * 4 + 1] = fmaf(f, x.y, acc[j * 4 + 1]);
+        acc[j * 4 + 2] = fmaf(f, x.z, acc[j * 4 + 2]);
+        acc[j * 4 + 3] = fmaf(f, x.w, acc[j * 4 + 3]);
+      }
+    }
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  T* out = static_cast<T*>(a.out) + at * hd;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+      if (j * 128 + lane * 4 + d < hd) out[j * 128 + lane * 4 + d] = from_f<T>(acc[j * 4 + d] * inv);
+  if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+// Key weights: a CTA holds kBN keys of one (sequence, kv head) and passes over
+// the sequence's query rows, 64 at a time; thread (ty, tx) has keys ty * 4 ..
+// and query rows tx, tx + 16, .., and adds exp2(u - lse) over its rows. One CTA
+// owns a key, so the sum's order is fixed. Bounded by the FMA rate for more
+// than a few query rows.
+template <typename T, int HDP>
+__global__ void __launch_bounds__(256) paged_weight_simt_kernel(PagedAttnArgs a) {
+  constexpr int LD = HDP + 4;
+  pdl_enter();
+  extern __shared__ float smf[];
+  float* sk = smf;                          // [kBN][LD]
+  float* sq = sk + kBN * LD;                // [64][LD]
+  __shared__ int sqp[64], spos[kBN];
+  __shared__ float slse[64], sslope[64];
+  const PagedView& c = a.c;
+  const int h = blockIdx.y, s = blockIdx.z, G = a.G;
+  const int2 ab = paged_new_rows(a.start, s, a.rows);
+  const int len = paged_length(c, s), R = (ab.y - ab.x) * G;
+  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[s] : INT32_MIN};
+  const PagedScore ps = paged_score_of(a);
+  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  for (int k0 = blockIdx.x * kBN; k0 < len; k0 += gridDim.x * kBN) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < kBN * 16; e += 256) {
+      const int j = e >> 4;
+      const long long row = k0 + j < len ? paged_row(c, s, h, k0 + j) : -1;
+      load_row<T, HDP>(sk + j * LD, row >= 0 ? static_cast<const T*>(c.k) + row * c.hd : nullptr, c.hd, e & 15, 16);
+      if ((e & 15) == 0) spos[j] = row >= 0 ? c.pos[row] : kPagedNoPos;
+    }
+    __syncthreads();
+    int pk[4];
+    float w[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) pk[i] = spos[ty * 4 + i];
+    for (int q0 = 0; q0 < R; q0 += 64) {
+      __syncthreads();
+      for (int e = threadIdx.x; e < 64 * 16; e += 256) {
+        const int r = e >> 4, rr = q0 + r;
+        const bool in = rr < R;
+        const size_t tok = in ? ab.x + rr / G : 0;
+        const int head = in ? h * G + rr % G : 0;
+        load_row<T, HDP>(sq + r * LD, in ? static_cast<const T*>(a.q) + tok * a.q_stride + (size_t)head * c.hd : nullptr, c.hd, e & 15, 16);
+        if ((e & 15) == 0) {
+          const float l = in ? a.lse[tok * a.nq + head] : -INFINITY;
+          sqp[r] = in ? a.q_pos[tok] : 0;
+          slse[r] = l * kLog2e;
+          sslope[r] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+        }
+      }
+      __syncthreads();
+      float acc[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HDP; d += 4) {
+        float4 k[4], q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sk + (ty * 4 + i) * LD + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const float4*>(sq + (tx + 16 * j) * LD + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            acc[i][j] = fmaf(k[i].x, q[j].x, acc[i][j]);
+            acc[i][j] = fmaf(k[i].y, q[j].y, acc[i][j]);
+            acc[i][j] = fmaf(k[i].z, q[j].z, acc[i][j]);
+            acc[i][j] = fmaf(k[i].w, q[j].w, acc[i][j]);
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float l = slse[tx + 16 * j], slope2 = sslope[tx + 16 * j];
+        const int pq = sqp[tx + 16 * j];
+        if (l == -INFINITY) continue;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (paged_sees(m, pq, pk[i])) w[i] += exp2f(paged_score(a, ps, acc[i][j], slope2, pq, pk[i]) - l);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], x);
+      const int slot = k0 + ty * 4 + i;
+      if (tx == 0 && slot < len) {
+        const long long row = paged_row(c, s, h, slot);
+        if (row >= 0) a.weight_out[row] = (a.weight_in ? a.decay * a.weight_in[row] : 0.f) + w[i];
+      }
+    }
+  }
+}
+
+template <int BM, int HDP>
+constexpr size_t simt_smem() {
+  return ((size_t)(BM + 2 * kBN) * (HDP + 4) + BM * (kBN + 4) + kBN) * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
+}
+template <int HDP>
+constexpr size_t weight_smem() { return (size_t)2 * kBN * (HDP + 4) * 4; }
+
+template <typename K>
+cudaError_t big_smem(K* kernel, size_t bytes) {
+  return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+template <typename T, int BM, int TM, int HDP>
+cudaError_t run_simt(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
+  cudaError_t e = big_smem(paged_attn_simt_kernel<T, BM, TM, HDP>, simt_smem<BM, HDP>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_attn_simt_kernel<T, BM, TM, HDP>, grid, dim3(BM / TM * 16), simt_smem<BM, HDP>(), st, a);
+}
+template <typename T, int BM, int TM>
+cudaError_t run_simt_hd(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
+  if (a.c.hd <= 64) return run_simt<T, BM, TM, 64>(a, grid, st);
+  if (a.c.hd <= 128) return run_simt<T, BM, TM, 128>(a, grid, st);
+  return run_simt<T, BM, TM, 256>(a, grid, st);
+}
+template <typename T, int HDP>
+cudaError_t run_weight(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
+  cudaError_t e = big_smem(paged_weight_simt_kernel<T, HDP>, weight_smem<HDP>());
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_weight_simt_kernel<T, HDP>, grid, dim3(256), weight_smem<HDP>(), st, a);
+}
+
+int expected_len(const PagedAttnArgs& a) {
+  const int cap = a.c.max_pages << a.c.lg_rows;
+  return a.max_len > 0 && a.max_len < cap ? a.max_len : cap;
+}
+// Tiles of `per` packed query rows a batch can have at most.
+long long tile_bound(const PagedAttnArgs& a, int per) {
+  return (long long)a.rows * a.G / per + (a.c.n_seq < a.rows ? a.c.n_seq : a.rows);
+}
+bool simt_wide(const PagedAttnArgs& a) { return (long long)a.rows * a.G > 24ll * a.c.n_seq; }
+
+}  // namespace
+
+PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
+  (void)dtype;
+  PagedPlan p{0, 1, 0};
+  p.kind = simt_wide(a) ? 1 : 0;
+  // about two waves of CTAs on 152 SMs, at least 256 keys to a split
+  const long long ctas = tile_bound(a, p.kind ? 64 : 16) * a.c.nkv;
+  const long long by_keys = (expected_len(a) + 255) / 256;
+  long long n = ctas > 0 ? 304 / ctas : 1;
+  n = n < by_keys ? n : by_keys;
+  p.splits = n < 1 ? 1 : (int)n;
+  if (p.splits > 1) p.bytes = (long long)p.splits * a.rows * a.nq * (a.c.hd + 2) * 4;
+  return p;
+}
+
+cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
+  const dim3 grid((unsigned)tile_bound(a, p.kind ? 64 : 16), a.c.nkv, p.splits);
+  cudaError_t e;
+  if (p.kind == 0) e = dtype ? run_simt_hd<bf16, 16, 2>(a, grid, st) : run_simt_hd<float, 16, 2>(a, grid, st);
+  else e = dtype ? run_simt_hd<bf16, 64, 4>(a, grid, st) : run_simt_hd<float, 64, 4>(a, grid, st);
+  if (e != cudaSuccess || p.splits <= 1) return e;
+  const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
+  return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)
+               : launch_pdl(paged_attn_merge_kernel<float>, mg, dim3(128), 0, st, a);
+}
+
+cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st) {
+  long long x = (expected_len(a) + kBN - 1) / kBN;
+  const dim3 grid((unsigned)x, a.c.nkv, a.c.n_seq);
+  if (a.c.hd <= 64) return dtype ? run_weight<bf16, 64>(a, grid, st) : run_weight<float, 64>(a, grid, st);
+  if (a.c.hd <= 128) return dtype ? run_weight<bf16, 128>(a, grid, st) : run_weight<float, 128>(a, grid, st);
+  return dtype ? run_weight<bf16, 256>(a, grid, st) : run_weight<float, 256>(a, grid, st);
+}
+
+}  // namespace dfl

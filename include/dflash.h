@@ -619,6 +619,149 @@ int ring_cache_gather(ring_cache* rc, int64_t pos0, int32_t count,
                       void* k_out, void* v_out);
 const char* ring_cache_last_error(const ring_cache* rc);
 
+/* ---- paged KV cache: append, attention, key weights, eviction ----------------- */
+
+/* One layer's K and V of many sequences of different lengths, in pages. Row r
+ * of sequence s is row r % page_rows of page table[s][r / page_rows]. A cached
+ * row has a position for the masks and the distance bias, kept per kv head
+ * because an eviction keeps other rows in each head; the order of a sequence's
+ * rows says nothing. All arrays are the caller's, on the device, 16-byte
+ * aligned; the calls below allocate nothing, keep nothing, never synchronize
+ * and may be captured. `length` counts the rows of each sequence with the
+ * call's new ones included: an engine raises it (and fills the table) before
+ * the append, and lowers it to trim rejected rows. Calls that write rows
+ * (append, key_weight's output, evict) need the sequences' pages to be
+ * disjoint; attention does not. Positions lie in [0, 2^31).
+ *
+ * What only the device can see is bounded there: a length beyond the table is
+ * cut to it, rows on a page id outside [0, n_pages) are neither read nor
+ * written (and seen by no query), row ranges are cut to [0, rows]. */
+typedef struct dflash_paged_cache {
+  void* k;                  /* [n_pages][kv_heads][page_rows][head_dim] */
+  void* v;                  /* the same */
+  int32_t* pos;             /* [n_pages][kv_heads][page_rows] */
+  const int32_t* table;     /* [n_seq][max_pages] page ids */
+  const int32_t* length;    /* [n_seq] */
+  int32_t* status;          /* [1] or NULL: DFLASH_PAGED_* bits are OR-ed in */
+  int32_t n_pages;          /* n_pages * kv_heads * page_rows < 2^31 */
+  int32_t page_rows;        /* a power of two, 8..4096 */
+  int32_t kv_heads;
+  int32_t head_dim;         /* a multiple of 8, at most 256 */
+  int32_t n_seq;            /* 1..65535 */
+  int32_t max_pages;        /* max_pages * page_rows <= 2^20 */
+  int32_t dtype;            /* DFLASH_F32 or DFLASH_BF16: K, V, q, out and gains */
+} dflash_paged_cache;
+
+/* Bits of dflash_paged_cache.status. */
+#define DFLASH_PAGED_BAD_PAGE 1 /* a page id outside [0, n_pages) */
+#define DFLASH_PAGED_BAD_ROWS 2 /* a length beyond the table, or more new rows than length */
+#define DFLASH_PAGED_GAVE_UP 4  /* a bounded wait in a tensor-core kernel gave up */
+
+/* The new rows start[s] .. start[s + 1] - 1 of sequence s become the last rows
+ * of its cache. Per row: q and k heads get an RMSNorm over head_dim (q_norm /
+ * k_norm, NULL: none), then the rotation: pair i < rot_pairs turns by
+ * rope_pos[pair_axis_host[i]][row] * rope_theta^(-i / rot_pairs), so a pair
+ * follows one of n_axes position axes (time, height, width of a video;
+ * n_axes = 1 is plain RoPE). rope_neox 1: pairs (i, i + rot_pairs), 0:
+ * (2i, 2i + 1); dimensions from 2 * rot_pairs on are not rotated. One rounding
+ * to the storage type, when stored: q into q_out, k and v into their pages,
+ * row_pos into pos (every kv head), 0 into weight (if not NULL). Rows outside
+ * [start[0], start[n_seq]) are skipped. */
+typedef struct dflash_paged_append_args {
+  const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */
+  const void* k;            /* [rows][kv_heads][head_dim], rows k_stride elements apart */
+  const void* v;            /* the same with v_stride */
+  const int32_t* row_pos;   /* [rows] position of each new row */
+  const int32_t* start;     /* [n_seq + 1], ascending */
+  const int32_t* rope_pos;  /* [n_axes][rows] */
+  const uint8_t* pair_axis_host; /* HOST [rot_pairs], each < n_axes; read during the call */
+  const void* q_norm;       /* [head_dim] or NULL */
+  const void* k_norm;       /* [head_dim] or NULL */
+  void* q_out;              /* [rows][n_q_heads][head_dim] dense; may be q when q is dense */
+  float* weight;            /* layout of pos, or NULL */
+  int64_t q_stride, k_stride, v_stride; /* multiples of 8, at least the row's elements */
+  int32_t rows;
+  int32_t n_q_heads;        /* a multiple of kv_heads, at most 128 * kv_heads */
+  int32_t n_axes;           /* 1..4 */
+  int32_t rot_pairs;        /* 0..head_dim / 2 */
+  int32_t rope_neox;
+  float rope_theta;         /* >= 1 */
+  float rms_eps;            /* > 0 */
+} dflash_paged_append_args;
+int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_append_args* args, void* stream);
+
+/* Attention of the new rows over their sequence's cached rows. Query head h
+ * reads kv head h / (n_q_heads / kv_heads). With pq the query's position and
+ * pk the cached row's, the row is seen iff
+ *     (not causal or pk <= pq) and (window <= 0 or |pq - pk| <= window)
+ *     or pk < prefix[s],
+ * and its score is t = scale * q.k; t = c * tanh(t / c) (c = softcap, 0 = no
+ * cap); t -= slopes[h] * |pq - pk|. out = sum softmax(t) v, lse = log sum
+ * exp(t) (natural log); a query that sees nothing gives out = 0 and lse =
+ * -inf. What a query does not see has no influence on it, infinities and NaN
+ * included. Softmax statistics and sums are fp32. Rows outside [start[0],
+ * start[n_seq]) of out and lse are left as they are. */
+typedef struct dflash_paged_attention_args {
+  const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */
+  const int32_t* q_pos;     /* [rows] */
+  const int32_t* start;     /* [n_seq + 1], ascending */
+  const float* slopes;      /* [n_q_heads] or NULL */
+  const int32_t* prefix;    /* [n_seq] or NULL */
+  void* out;                /* [rows][n_q_heads][head_dim] dense (not read or written by key_weight) */
+  float* lse;               /* [rows][n_q_heads]; NULL: not wanted (attention) */
+  void* workspace;          /* dflash_paged_attention_workspace bytes; calls that may overlap
+                               need workspaces of their own */
+  int64_t workspace_bytes;
+  int64_t q_stride;         /* a multiple of 8, at least n_q_heads * head_dim */
+  int32_t rows;             /* rows * n_q_heads < 2^31 */
+  int32_t n_q_heads;        /* a multiple of kv_heads, at most 128 * kv_heads */
+  int32_t causal;
+  int32_t window;
+  int32_t max_len;          /* longest length the caller expects, 0: the table's; sets how the
+                               work is split, longer sequences stay right */
+  float scale;              /* > 0 */
+  float softcap;            /* >= 0 */
+} dflash_paged_attention_args;
+/* Bytes of workspace (0 for most large calls) an attention call needs; the
+ * same for every content of the device arrays. */
+int dflash_paged_attention_workspace(const dflash_paged_cache* cache, const dflash_paged_attention_args* args,
+                                     int64_t* bytes_host);
+int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* args, void* stream);
+
+/* What attention each cached row received: weight_out = decay * weight_in +
+ * sum over the sequence's new rows and the heads of the kv head's group of
+ * exp(t - lse), with t and the mask as in dflash_paged_attention and lse its
+ * output for the same rows (a query whose lse is -inf adds nothing). weight_in
+ * and weight_out have pos's layout and may be the same array; weight_in NULL
+ * is zeros. Rows beyond length are left as they are. The sums are taken in a
+ * fixed order. */
+int dflash_paged_key_weight(const dflash_paged_cache* cache, const dflash_paged_attention_args* args,
+                            const float* weight_in, float decay, float* weight_out, void* stream);
+
+/* Keeps the `budget` heaviest rows of each sequence and kv head. Rows at
+ * positions >= next_pos[s] - recent count as infinitely heavy, a NaN as
+ * lighter than everything; of equally heavy rows the first ones stay. The kept
+ * rows beyond row budget - 1 move, in ascending order, into the evicted rows
+ * before it, in ascending order: K, V, position and weight; rows that stay are
+ * not touched. pos_out and weight_out get the position and weight of every
+ * remaining row, length_out min(length, budget); each may be the array it
+ * follows (cache pos, weight, cache length). Sequences of at most budget rows
+ * stay as they are. */
+typedef struct dflash_paged_evict_args {
+  const float* weight;      /* layout of pos */
+  const int32_t* next_pos;  /* [n_seq] */
+  float* weight_out;
+  int32_t* pos_out;
+  int32_t* length_out;      /* [n_seq] */
+  void* workspace;          /* dflash_paged_evict_workspace bytes */
+  int64_t workspace_bytes;
+  int32_t budget;           /* >= 1 */
+  int32_t recent;           /* >= 0 */
+} dflash_paged_evict_args;
+int dflash_paged_evict_workspace(const dflash_paged_cache* cache, const dflash_paged_evict_args* args,
+                                 int64_t* bytes_host);
+int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
