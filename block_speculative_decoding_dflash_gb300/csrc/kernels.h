@@ -105,6 +105,10 @@ cudaError_t launch_tc_wide(const TcWideArgs& a, int grid, cudaStream_t st);
 
 bool tc_encode_map(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows,
                    uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_rows);
+// The same for a rank-3 tensor, dims and box innermost first, strides of the
+// outer two dims.
+bool tc_encode_map_3d(CUtensorMap* m, const void* base, const uint64_t* dims, const uint64_t* strides_bytes,
+                      const uint32_t* box);
 cudaError_t init_tc_attrs();
 cudaError_t launch_tc_gemm(const TcGemmArgs& a, int bn, int grid, bool pdl, cudaStream_t st);
 
@@ -412,9 +416,10 @@ struct PagedAttnArgs {
   float decay;
 };
 // How an attention call is split: chosen from sizes alone.
-struct PagedPlan { int kind, splits; long long bytes; };
+struct PagedPlan { int kind, splits; long long tiles, bytes; };
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st);
 
 struct PagedEvictArgs {

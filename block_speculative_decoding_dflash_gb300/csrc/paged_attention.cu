@@ -410,32 +410,44 @@ int expected_len(const PagedAttnArgs& a) {
   const int cap = a.c.max_pages << a.c.lg_rows;
   return a.max_len > 0 && a.max_len < cap ? a.max_len : cap;
 }
-// Tiles of `per` packed query rows a batch can have at most.
-long long tile_bound(const PagedAttnArgs& a, int per) {
-  return (long long)a.rows * a.G / per + (a.c.n_seq < a.rows ? a.c.n_seq : a.rows);
+// Tiles a batch of `units` query rows can have at most, `per` to a tile.
+long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
+  return units / per + (a.c.n_seq < a.rows ? a.c.n_seq : a.rows);
 }
-bool simt_wide(const PagedAttnArgs& a) { return (long long)a.rows * a.G > 24ll * a.c.n_seq; }
 
 }  // namespace
 
+// kind 0, 1: CUDA cores, tiles of 16 or 64 packed query rows; 2, 3: tensor
+// cores, one or two tiles of 128.
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
-  (void)dtype;
-  PagedPlan p{0, 1, 0};
-  p.kind = simt_wide(a) ? 1 : 0;
-  // about two waves of CTAs on 152 SMs, at least 256 keys to a split
-  const long long ctas = tile_bound(a, p.kind ? 64 : 16) * a.c.nkv;
-  const long long by_keys = (expected_len(a) + 255) / 256;
-  long long n = ctas > 0 ? 304 / ctas : 1;
-  n = n < by_keys ? n : by_keys;
+  PagedPlan p{0, 1, 0, 0};
+  const long long len = expected_len(a);
+  long long fill, least;
+  if (dtype && a.c.hd <= 128) {
+    const int per = 128 / a.G;
+    p.kind = a.rows > (long long)per * a.c.n_seq ? 3 : 2;
+    p.tiles = tile_bound(a.rows, p.kind == 3 ? 2 * per : per, a);
+    fill = 152;
+    least = 512;
+  } else {
+    p.kind = (long long)a.rows * a.G > 24ll * a.c.n_seq ? 1 : 0;
+    p.tiles = tile_bound((long long)a.rows * a.G, p.kind ? 64 : 16, a);
+    fill = 304;
+    least = 256;
+  }
+  // as many splits as fill the SMs, of at least `least` keys each
+  const long long ctas = p.tiles * a.c.nkv, by_keys = (len + least - 1) / least;
+  const long long n = ctas >= fill ? 1 : (fill / ctas < by_keys ? fill / ctas : by_keys);
   p.splits = n < 1 ? 1 : (int)n;
   if (p.splits > 1) p.bytes = (long long)p.splits * a.rows * a.nq * (a.c.hd + 2) * 4;
   return p;
 }
 
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
-  const dim3 grid((unsigned)tile_bound(a, p.kind ? 64 : 16), a.c.nkv, p.splits);
+  const dim3 grid((unsigned)p.tiles, a.c.nkv, p.splits);
   cudaError_t e;
-  if (p.kind == 0) e = dtype ? run_simt_hd<bf16, 16, 2>(a, grid, st) : run_simt_hd<float, 16, 2>(a, grid, st);
+  if (p.kind >= 2) e = launch_paged_attention_tc(a, p.kind - 1, p.tiles, st);
+  else if (p.kind == 0) e = dtype ? run_simt_hd<bf16, 16, 2>(a, grid, st) : run_simt_hd<float, 16, 2>(a, grid, st);
   else e = dtype ? run_simt_hd<bf16, 64, 4>(a, grid, st) : run_simt_hd<float, 64, 4>(a, grid, st);
   if (e != cudaSuccess || p.splits <= 1) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));

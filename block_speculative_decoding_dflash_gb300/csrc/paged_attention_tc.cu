@@ -1,0 +1,505 @@
+// Attention over the paged cache on the tensor cores (bf16, head_dim <= 128).
+//
+// A CTA takes QT tiles of 128 packed query rows (row r of a tile: new row r / G,
+// head r % G of the kv head's group) and walks the key tiles of 128 rows that
+// any of them sees. S = Q K^T and O += P V are tcgen05 products with S, P and O
+// in TMEM: a softmax thread owns one query row (one TMEM lane), so row maxima
+// and sums need no exchange between threads, and P, in bf16, takes the place
+// of the S it came from and is the A operand of P V where it lies.
+//
+// Warps: 4 per query tile for the softmax, then one that issues the TMA loads
+// of K and V (a ring of stages, filled page by page), one that issues the MMAs,
+// two that look after V. With two query tiles the MMAs of one run while the
+// other's softmax does; with one, S has two buffers for the same purpose.
+//
+// The running maximum is raised, and O rescaled, only when a row's maximum
+// grows by more than 8 (in log2 units): p stays below 2^8, which costs neither
+// fp32 sums nor bf16 products any relative accuracy, and after the first tiles
+// nearly no tile needs it.
+//
+// P's rounding to bf16 (half a step, 2^-8 relative at most, independent from
+// key to key) adds about as much error to an output as the output's own
+// rounding to bf16 does; the sum of p is taken before it, in fp32.
+//
+// Rows that a query does not see get p = 0, but 0 times an infinite or NaN V is
+// NaN. So in every tile that is not wholly seen by all its queries two warps
+// look for such rows of V and zero them in shared memory, and the queries that
+// do see them add p v themselves.
+#include <math.h>
+
+#include "paged_tc.cuh"
+
+namespace dfl {
+
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kMaxTiles = (1 << 20) / kPtKeys;
+constexpr int kBitWords = kMaxTiles / 32 + 1;
+constexpr float kLazy = 8.f;
+
+template <int HDP, int QT>
+struct TcShape {
+  static constexpr int kHalves = HDP / 64;
+  static constexpr int kTileB = kPtKeys * HDP * 2;      // a Q, K or V tile
+  static constexpr int kHalfB = kPtKeys * 128;
+  static constexpr int kStages = HDP == 64 ? 8 : (QT == 2 ? 4 : 5);   // at most 8: see v_ok
+  static constexpr int kSoft = QT * 128;                // softmax threads
+  static constexpr int kThreads = kSoft + 128;
+  static constexpr int kQ = 0, kKV = QT * kTileB, kEnd = kKV + kStages * kTileB;
+  static constexpr size_t kSmem = kEnd + 1024;
+};
+
+template <int HDP, int QT>
+__global__ void __launch_bounds__(QT * 128 + 128, 1)
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
+  using C = TcShape<HDP, QT>;
+  constexpr int NS = C::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t q_full, o_final, kv_full[NS], kv_empty[NS], v_ok[4], s_full[2], p_ready[2], o_done;
+  __shared__ uint32_t tmem_holder;
+  __shared__ PagedTile s_tile;
+  __shared__ int s_qmin, s_qmax;
+  __shared__ unsigned some[kBitWords], all[kBitWords];
+  __shared__ unsigned bad[4][4];                        // of V tile i: [i & 3]
+  __shared__ __align__(16) int kpos[QT * 4][kPtKeys];
+
+  const PagedView& c = a.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = blockIdx.y, z = blockIdx.z, G = a.G;
+  const int tpt = kPtKeys / G;                          // new rows of a tile
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
+  constexpr int wLoad = QT * 4, wMma = QT * 4 + 1;
+
+  pdl_launch_dependents();
+  if (warp == wMma) tmem_alloc(&tmem_holder, 512);
+  if (threadIdx.x == wLoad * 32) {
+    mbar_init(&q_full, 1);
+    mbar_init(&o_final, 1);
+    mbar_init(&o_done, 1);
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    // four: at most NS / 2 tiles of V are in the ring
+    for (int i = 0; i < 4; ++i) mbar_init(&v_ok[i], 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_ready[i], 128);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&mq);
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
+  pdl_wait();
+  if (warp == 0) {
+    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, blockIdx.x);
+    int lo = INT32_MAX, hi = INT32_MIN;
+    if (t.seq >= 0) {
+      const int r0 = t.tile * QT * tpt, r1 = min(t.count, r0 + QT * tpt);
+      for (int i = r0 + lane; i < r1; i += 32) {
+        const int p = a.q_pos[t.first + i];
+        lo = min(lo, p);
+        hi = max(hi, p);
+      }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) { s_tile = t; s_qmin = lo; s_qmax = hi; }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const PagedTile t = s_tile;
+  const uint32_t tmem = tmem_holder;
+  if (t.seq < 0) {
+    __syncthreads();
+    if (warp == wMma) tmem_dealloc(tmem, 512);
+    return;
+  }
+  const int len = paged_length(c, t.seq);
+  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[t.seq] : INT32_MIN};
+  PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
+  paged_classify<kPtKeys>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
+  __syncthreads();
+  paged_take(sh, some, a.window, z, a.splits);
+  const int N = sh.take;                                 // tiles this CTA works on
+  const int row0 = t.tile * QT * tpt;                    // its first new row, within the sequence
+  const int nt = (QT == 2 && row0 + tpt < t.count) ? 2 : 1;
+  PagedCursor cur(some, sh);
+  bool ok = true;
+
+  if (warp == wLoad) {
+    // ---- loads: Q, then K and V of every tile, a box per page (or per 128 rows of one)
+    if (N > 0 && lane == 0) {
+      mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
+      for (int i = 0; i < nt; ++i)
+        for (int x = 0; x < C::kHalves; ++x)
+          tma_load_3d(sm + C::kQ + i * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, t.first + row0 + i * tpt, &q_full);
+    }
+    const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
+    const int beyond = (c.n_pages * c.nkv) << c.lg_rows;   // a row past the pool reads as zeros
+    for (int i = 0; i < N; ++i) {
+      const int slot = (sh.t0 + cur.next()) * kPtKeys + lane * box;
+      int y = beyond;
+      if (lane < boxes && slot < len) {
+        const long long row = paged_row(c, t.seq, h, slot);
+        if (row >= 0) y = (int)row;
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int n = 2 * i + kv, s = n % NS;
+        if (n >= NS) paged_wait(&kv_empty[s], (n / NS - 1) & 1, ok);
+        if (lane == 0) mbar_expect_tx(&kv_full[s], C::kTileB);
+        __syncwarp();
+        if (lane < boxes)
+#pragma unroll
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_2d(sm + C::kKV + s * C::kTileB + x * C::kHalfB + lane * box * 128, kv ? &mv : &mk, x * 64, y, &kv_full[s]);
+      }
+    }
+  } else if (warp == wMma) {
+    // ---- MMAs, all from one thread, so that they run in the order issued
+    if (lane == 0 && N > 0) {
+      const uint32_t sb = smem_u32(sm);
+      const int ksteps = (c.hd + 15) >> 4;
+      const uint32_t idesc_s = idesc_bf16(128, 128), idesc_o = idesc_bf16(128, ksteps * 16) | kIdescBMnMajor;
+      auto qk = [&](int q, int buf, int i) {
+        const uint32_t ka = sb + C::kKV + ((2 * i) % NS) * C::kTileB, qa = sb + C::kQ + q * C::kTileB;
+        for (int k = 0; k < ksteps; ++k)
+          tc_mma_bf16(tmem + buf * 128, smem_desc_sw128(qa + (k >> 2) * C::kHalfB + (k & 3) * 32),
+                      smem_desc_sw128(ka + (k >> 2) * C::kHalfB + (k & 3) * 32), idesc_s, k ? 1u : 0u);
+        tc_commit(&s_full[buf]);
+      };
+      auto pv = [&](int q, int buf, int i) {
+        const uint32_t va = sb + C::kKV + ((2 * i + 1) % NS) * C::kTileB;
+        for (int k = 0; k < 8; ++k)
+          tc_mma_bf16_ta(tmem + 256 + q * HDP, tmem + buf * 128 + k * 8, smem_desc_sw128_mn(va + k * 2048, C::kHalfB), idesc_o, 1u);
+      };
+      auto wait_k = [&](int i) { paged_wait(&kv_full[(2 * i) % NS], (2 * i / NS) & 1, ok); };
+      auto wait_v = [&](int i) { paged_wait(&v_ok[i & 3], (i >> 2) & 1, ok); };
+      paged_wait(&q_full, 0, ok);
+      wait_k(0);
+      qk(0, 0, 0);
+      if (QT == 2) {
+        if (nt == 2) qk(1, 1, 0);
+        tc_commit(&kv_empty[0]);
+        for (int i = 0; i < N; ++i) {
+          wait_v(i);
+          for (int q = 0; q < nt; ++q) {
+            paged_wait(&p_ready[q], i & 1, ok);
+            tc_fence_after();
+            pv(q, q, i);
+            if (q == nt - 1) tc_commit(&kv_empty[(2 * i + 1) % NS]);
+            if (i + 1 < N) {
+              if (q == 0) wait_k(i + 1);
+              qk(q, q, i + 1);
+              if (q == nt - 1) tc_commit(&kv_empty[(2 * i + 2) % NS]);
+            }
+          }
+        }
+      } else {
+        tc_commit(&kv_empty[0]);
+        if (N > 1) {
+          wait_k(1);
+          qk(0, 1, 1);
+          tc_commit(&kv_empty[2 % NS]);
+        }
+        for (int i = 0; i < N; ++i) {
+          wait_v(i);
+          paged_wait(&p_ready[i & 1], (i >> 1) & 1, ok);
+          tc_fence_after();
+          pv(0, i & 1, i);
+          tc_commit(&o_done);
+          tc_commit(&kv_empty[(2 * i + 1) % NS]);
+          if (i + 2 < N) {
+            wait_k(i + 2);
+            qk(0, i & 1, i + 2);
+            tc_commit(&kv_empty[(2 * i + 4) % NS]);
+          }
+        }
+      }
+      tc_commit(&o_final);
+    }
+  } else if (warp > wMma) {
+    // ---- V's non-finite rows, in tiles that some query sees only in part
+    const int half = warp - wMma - 1;
+    for (int i = 0; i < N; ++i) {
+      const int rel = cur.next(), n = 2 * i + 1, s = n % NS;
+      paged_wait(&kv_full[s], (n / NS) & 1, ok);
+      if (!((all[rel >> 5] >> (rel & 31)) & 1u)) {
+        uint8_t* v = sm + C::kKV + s * C::kTileB;
+        for (int x = 0; x < 2; ++x) {
+          const int r = half * 64 + x * 32 + lane;
+          unsigned acc = 0;
+#pragma unroll
+          for (int y = 0; y < C::kHalves; ++y)
+#pragma unroll
+            for (int d = 0; d < 8; ++d) {
+              const uint4 u = *reinterpret_cast<const uint4*>(v + y * C::kHalfB + r * 128 + ((d ^ (r & 7)) << 4));
+              // an exponent of all ones carries into the sign's place
+              acc |= ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                     ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
+            }
+          const bool is_bad = (acc & 0x80008000u) != 0;
+          const unsigned who = __ballot_sync(0xffffffffu, is_bad);
+          if (lane == 0) bad[i & 3][half * 2 + x] = who;
+          if (is_bad)
+            for (int y = 0; y < C::kHalves; ++y)
+              for (int d = 0; d < 8; ++d) *reinterpret_cast<uint4*>(v + y * C::kHalfB + r * 128 + (d << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_shared();
+        __syncwarp();
+      }
+      if (lane == 0) mbar_arrive(&v_ok[i & 3]);
+    }
+  } else if (QT == 1 || (warp >> 2) < nt) {
+    // ---- softmax: one query row to a thread
+    const int q = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
+    const int tl = r / G, g = r - tl * G, head = h * G + g;
+    const int at_row = row0 + q * tpt + tl;
+    const bool valid = tl < tpt && at_row < t.count;
+    const int tok = t.first + (valid ? at_row : row0);
+    const bool work = __any_sync(0xffffffffu, valid);
+    const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t o_at = tmem + lanes + 256 + q * HDP;
+    const int pq = a.q_pos[tok];
+    const float slope2 = a.slopes ? a.slopes[valid ? head : h * G] * kLog2e : 0.f;
+    const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
+    const float cap2 = a.softcap * kLog2e;
+    int* kp = kpos[warp];
+    float mx = -INFINITY, sum = 0.f;
+
+    // positions of the tile's keys, four to a lane, loaded a tile ahead where
+    // they will be needed
+    int rel = cur.next();
+    int4 pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
+    auto fetch = [&]() {
+      pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
+      if (rel < 0 || (!a.slopes && ((all[rel >> 5] >> (rel & 31)) & 1u))) return;
+      const int slot = (sh.t0 + rel) * kPtKeys + lane * 4;
+      const long long row = slot < len ? paged_row(c, t.seq, h, slot) : -1;
+      if (row >= 0) {
+        pos4 = *reinterpret_cast<const int4*>(c.pos + row);
+        if (slot + 1 >= len) pos4.y = kPagedNoPos;
+        if (slot + 2 >= len) pos4.z = kPagedNoPos;
+        if (slot + 3 >= len) pos4.w = kPagedNoPos;
+      }
+    };
+    if (work) fetch();
+    if (N > 0 && work) {
+      const uint32_t zero[32] = {};
+#pragma unroll
+      for (int d = 0; d < HDP; d += 32) tmem_st32(o_at + d, zero);
+      tmem_st_wait();
+    }
+    for (int i = 0; i < N; ++i) {
+      const int buf = QT == 2 ? q : (i & 1);
+      const uint32_t s_at = tmem + lanes + buf * 128;
+      paged_wait(&s_full[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1), ok);
+      tc_fence_after();
+      if (!work) {                                       // rows of nobody: their P may be anything
+        cur.next();
+        mbar_arrive(&p_ready[buf]);
+        continue;
+      }
+      const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
+      const int tile = sh.t0 + rel;
+      float s[128];
+#pragma unroll
+      for (int d = 0; d < 128; d += 32) tmem_ld32(s_at + d, &s[d]);
+      tmem_ld_wait();
+      float sc = scale2;
+      if (!full || a.slopes) {
+        __syncwarp();
+        *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
+        __syncwarp();
+      }
+      if (a.softcap > 0.f) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = cap_tanh(s[j] * scale2, cap2);
+        sc = 1.f;
+      }
+      if (a.slopes) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf((float)(pq - kp[j])), s[j] * sc);
+        sc = 1.f;
+      }
+      if (!full) {
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = paged_sees(m, pq, kp[j]) ? s[j] : -INFINITY;
+      }
+      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < 128; ++j) top4[j & 3] = fmaxf(top4[j & 3], s[j]);
+      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * sc;
+      if (__any_sync(0xffffffffu, top > mx + kLazy)) {
+        const float mn = fmaxf(mx, top);
+        const float f = mn == -INFINITY ? 1.f : ex2(mx - mn);
+        sum *= f;
+        mx = mn;
+        if (i > 0) {
+          // O holds the tiles before this one: their P V is done (with two
+          // query tiles because S of this tile was issued after it)
+          if (QT == 1) {
+            paged_wait(&o_done, (i - 1) & 1, ok);
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int d = 0; d < HDP; d += 32) {
+            float o[32];
+            tmem_ld32(o_at + d, o);
+            tmem_ld_wait();
+            uint32_t w[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] * f);
+            tmem_st32(o_at + d, w);
+          }
+          tmem_st_wait();
+        }
+      }
+      const float base = mx == -INFINITY ? 0.f : mx;
+      float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int d = 0; d < 128; d += 64) {
+        uint32_t w[32];
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          const float p0 = ex2(fmaf(s[d + j], sc, -base)), p1 = ex2(fmaf(s[d + j + 1], sc, -base));
+          add[j & 3] += p0;
+          add[(j + 1) & 3] += p1;
+          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
+          w[j >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        tmem_st32(s_at + (d >> 1), w);
+      }
+      sum += (add[0] + add[1]) + (add[2] + add[3]);
+      tmem_st_wait();
+      if (!full) {
+        const unsigned* who = bad[i & 3];
+        paged_wait(&v_ok[i & 3], (i >> 2) & 1, ok);
+        const unsigned any = who[0] | who[1] | who[2] | who[3];
+        if (any && QT == 1 && i > 0) {
+          paged_wait(&o_done, (i - 1) & 1, ok);
+          tc_fence_after();
+        }
+        for (int w = 0; any && w < 4; ++w)
+          for (unsigned b = who[w]; b; b &= b - 1) {
+            const int j = w * 32 + __ffs(b) - 1, slot = tile * kPtKeys + j;
+            if (slot >= len) continue;
+            const uint32_t pp = tmem_ld1(s_at + (j >> 1));
+            tmem_ld_wait();
+            const float p = j & 1 ? bf_hi(pp) : bf_lo(pp);
+            const long long row = paged_row(c, t.seq, h, slot);
+            if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
+            const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
+            for (int d = 0; d < HDP; d += 32) {
+              float o[32];
+              tmem_ld32(o_at + d, o);
+              tmem_ld_wait();
+              uint32_t ow[32];
+#pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                const float v = d + x < c.hd ? to_f(vrow[d + x]) : 0.f;
+                ow[x] = __float_as_uint(p != 0.f ? fmaf(p, v, o[x]) : o[x]);
+              }
+              tmem_st32(o_at + d, ow);
+            }
+            tmem_st_wait();
+          }
+      }
+      tc_fence_before();
+      mbar_arrive(&p_ready[buf]);
+      rel = cur.next();
+      fetch();
+    }
+    // ---- the row's output, or its split's partial
+    if (N > 0) {
+      paged_wait(&o_final, 0, ok);
+      tc_fence_after();
+    }
+    const size_t at = (size_t)tok * a.nq + head;
+    const bool none = sum == 0.f;                        // nothing seen (a NaN score makes the sum NaN)
+    const float inv = none ? 0.f : 1.f / sum;
+    if (work) {
+#pragma unroll
+      for (int d = 0; d < HDP; d += 32) {
+        float o[32];
+        if (N > 0) {
+          tmem_ld32(o_at + d, o);
+          tmem_ld_wait();
+        }
+        if (valid && a.splits > 1) {
+          float* po = a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)
+            if (d + x < c.hd && !none) *reinterpret_cast<float4*>(po + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+        } else if (valid) {
+          bf16* out = static_cast<bf16*>(a.out) + at * c.hd + d;
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (!none) {
+              uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
+                w[y] = *reinterpret_cast<const uint32_t*>(&b);
+              }
+            }
+            if (d + x < c.hd) *reinterpret_cast<uint4*>(out + x) = u;
+          }
+        }
+      }
+      if (valid) {
+        if (a.splits > 1) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx, sum);
+        else if (a.lse) a.lse[at] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
+      }
+    }
+  }
+  if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == wMma) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HDP, int QT>
+cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  CUtensorMap mq, mk, mv;
+  if (!paged_map_rows(&mq, a.q, a, kPtKeys / a.G) || !paged_map_pages(&mk, a.c.k, a.c) || !paged_map_pages(&mv, a.c.v, a.c))
+    return cudaErrorInvalidValue;
+  using C = TcShape<HDP, QT>;
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<HDP, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(paged_attn_tc_kernel<HDP, QT>, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(C::kThreads), C::kSmem, st, mq, mk, mv, a);
+}
+
+}  // namespace
+
+bool paged_map_pages(CUtensorMap* m, const void* base, const PagedView& c) {
+  const int rows = 1 << c.lg_rows;
+  return tc_encode_map(m, base, c.hd, ((uint64_t)c.n_pages * c.nkv) << c.lg_rows, (uint64_t)c.hd * 2, 64,
+                       rows < kPtKeys ? rows : kPtKeys);
+}
+
+bool paged_map_rows(CUtensorMap* m, const void* base, const PagedAttnArgs& a, int per) {
+  const uint64_t dims[3] = {(uint64_t)a.c.hd, (uint64_t)a.nq, (uint64_t)a.rows};
+  const uint64_t strides[2] = {(uint64_t)a.c.hd * 2, (uint64_t)a.q_stride * 2};
+  const uint32_t box[3] = {64, (uint32_t)a.G, (uint32_t)per};
+  return tc_encode_map_3d(m, base, dims, strides, box);
+}
+
+cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st) {
+  if (a.c.hd <= 64) return q_tiles == 2 ? run<64, 2>(a, tiles, st) : run<64, 1>(a, tiles, st);
+  return q_tiles == 2 ? run<128, 2>(a, tiles, st) : run<128, 1>(a, tiles, st);
+}
+
+}  // namespace dfl
