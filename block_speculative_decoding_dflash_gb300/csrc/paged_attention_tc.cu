@@ -44,7 +44,10 @@ struct TcShape {
   static constexpr int kHalves = HDP / 64;
   static constexpr int kTileB = kPtKeys * HDP * 2;      // a Q, K or V tile
   static constexpr int kHalfB = kPtKeys * 128;
-  static constexpr int kStages = HDP == 64 ? 8 : (QT == 2 ? 4 : 5);   // at most 8: see v_ok
+  // K and V tiles take turns; an even number, so that a stage always holds the
+  // same of the two and who waits for one kind only sees every phase of its
+  // barriers. At most 8: see v_ok.
+  static constexpr int kStages = HDP == 64 ? 8 : 4;
   static constexpr int kSoft = QT * 128;                // softmax threads
   static constexpr int kThreads = kSoft + 128;
   static constexpr int kQ = 0, kKV = QT * kTileB, kEnd = kKV + kStages * kTileB;
@@ -143,7 +146,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     }
     const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
     const int beyond = (c.n_pages * c.nkv) << c.lg_rows;   // a row past the pool reads as zeros
-    for (int i = 0; i < N; ++i) {
+    int issued = 0;
+    for (int i = 0; i < N && ok; ++i) {
       const int slot = (sh.t0 + cur.next()) * kPtKeys + lane * box;
       int y = beyond;
       if (lane < boxes && slot < len) {
@@ -154,14 +158,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       for (int kv = 0; kv < 2; ++kv) {
         const int n = 2 * i + kv, s = n % NS;
         if (n >= NS) paged_wait(&kv_empty[s], (n / NS - 1) & 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;                                    // the stage is not free: no further load
+          break;
+        }
         if (lane == 0) mbar_expect_tx(&kv_full[s], C::kTileB);
         __syncwarp();
+        issued = n + 1;
         if (lane < boxes)
 #pragma unroll
           for (int x = 0; x < C::kHalves; ++x)
             tma_load_2d(sm + C::kKV + s * C::kTileB + x * C::kHalfB + lane * box * 128, kv ? &mv : &mk, x * 64, y, &kv_full[s]);
       }
     }
+    // no copy may be in flight when the CTA ends, whatever became of the others
+    bool landed = true;
+    if (N > 0) paged_wait(&q_full, 0, landed);
+    for (int n = issued > NS ? issued - NS : 0; n < issued; ++n) paged_wait(&kv_full[n % NS], (n / NS) & 1, landed);
+    ok = ok && landed;
   } else if (warp == wMma) {
     // ---- MMAs, all from one thread, so that they run in the order issued
     if (lane == 0 && N > 0) {
@@ -188,10 +202,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       if (QT == 2) {
         if (nt == 2) qk(1, 1, 0);
         tc_commit(&kv_empty[0]);
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N && ok; ++i) {
           wait_v(i);
           for (int q = 0; q < nt; ++q) {
             paged_wait(&p_ready[q], i & 1, ok);
+            if (!ok) break;
             tc_fence_after();
             pv(q, q, i);
             if (q == nt - 1) tc_commit(&kv_empty[(2 * i + 1) % NS]);
@@ -209,9 +224,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           qk(0, 1, 1);
           tc_commit(&kv_empty[2 % NS]);
         }
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N && ok; ++i) {
           wait_v(i);
           paged_wait(&p_ready[i & 1], (i >> 1) & 1, ok);
+          if (!ok) break;
           tc_fence_after();
           pv(0, i & 1, i);
           tc_commit(&o_done);
@@ -224,6 +240,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         }
       }
       tc_commit(&o_final);
+      bool done = true;
+      paged_wait(&o_final, 0, done);
+      ok = ok && done;
     }
   } else if (warp > wMma) {
     // ---- V's non-finite rows, in tiles that some query sees only in part
@@ -231,6 +250,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     for (int i = 0; i < N; ++i) {
       const int rel = cur.next(), n = 2 * i + 1, s = n % NS;
       paged_wait(&kv_full[s], (n / NS) & 1, ok);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       if (!((all[rel >> 5] >> (rel & 31)) & 1u)) {
         uint8_t* v = sm + C::kKV + s * C::kTileB;
         for (int x = 0; x < 2; ++x) {
@@ -301,6 +324,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       const int buf = QT == 2 ? q : (i & 1);
       const uint32_t s_at = tmem + lanes + buf * 128;
       paged_wait(&s_full[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1), ok);
+      if (!__all_sync(0xffffffffu, ok)) {
+        ok = false;
+        break;
+      }
       tc_fence_after();
       if (!work) {                                       // rows of nobody: their P may be anything
         cur.next();

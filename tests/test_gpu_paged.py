@@ -592,6 +592,66 @@ def test_calls_on_two_streams_at_once(B):
         assert all(torch.equal(x, first) for x in o)
 
 
+def dense64(s, cache):
+    """out, sum p |v| and lse of causal attention in torch fp64 on the GPU, one sequence and kv head after the other."""
+    q, out = cache.q64, torch.zeros(s.rows, s.nq, s.hd, dtype=torch.float64, device="cuda")
+    mag, lse, G = torch.zeros_like(out), torch.zeros(s.rows, s.nq, dtype=torch.float64, device="cuda"), s.nq // s.nkv
+    ps = cache.k.shape[2]
+    for i in range(len(s.length)):
+        a, b, n = int(s.start[i]), int(s.start[i + 1]), int(s.length[i])
+        pages = cache.table[i, :-(-n // ps)].long()
+        for h in range(s.nkv):
+            k, v, pos = (t[pages, h].flatten(0, 1)[:n] for t in (cache.k, cache.v, cache.pos))
+            t = torch.einsum("ngd,ld->ngl", q[a:b, h * G:(h + 1) * G], k.double()) * s.scale
+            t = t.masked_fill((pos[None] > s.q_pos[a:b].cuda()[:, None])[:, None], -math.inf)
+            lse[a:b, h * G:(h + 1) * G] = t.logsumexp(-1)
+            p = t.softmax(-1)
+            out[a:b, h * G:(h + 1) * G], mag[a:b, h * G:(h + 1) * G] = p @ v.double(), p @ v.double().abs()
+    return host(out), host(lse), host(mag)
+
+
+@pytest.mark.parametrize("n,lens,nq,nkv,hd,dtype", [
+    (1, [9000 - 150 * i for i in range(44)], 32, 8, 128, "bf16"),        # more tiles to a CTA, and CTAs to the GPU, than stages
+    (30, [5000 - 300 * i for i in range(12)], 16, 8, 64, "bf16"),
+    (500, [6000, 500, 4321], 32, 8, 128, "bf16"),
+    (300, [6000, 2500, 300], 8, 1, 64, "bf16"),
+    (7, [6000 - 500 * i for i in range(10)], 16, 8, 128, "f32"),
+])
+def test_a_loaded_gpu(B, n, lens, nq, nkv, hd, dtype):
+    """Long sequences on every SM at once, the same call many times in a row."""
+    g = torch.Generator(device="cuda").manual_seed(len(lens))
+    s = Setup.__new__(Setup)
+    s.B, s.dtype, s.hd, s.nq, s.nkv, s.scale = B, dtype, hd, nq, nkv, hd ** -0.5
+    s.dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    ps, width, S = 64, -(-max(lens) // 64), len(lens)
+    s.rows, s.length, s.start = n * S, torch.tensor(lens, dtype=torch.int32), torch.arange(0, n * S + 1, n, dtype=torch.int32)
+    s.q_pos = torch.cat([torch.arange(l - n, l) for l in lens]).to(torch.int32)
+    normal = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(s.dt)  # noqa: E731
+    s.k, s.v = normal(S * width, nkv, ps, hd), normal(S * width, nkv, ps, hd)
+    s.table = torch.randperm(S * width, generator=torch.Generator().manual_seed(1)).reshape(S, width).to(torch.int32)
+    s.pos = torch.zeros(S * width, nkv, ps, dtype=torch.int32)
+    s.pos[s.table.long()] = torch.arange(width * ps, dtype=torch.int32).reshape(1, width, 1, ps).expand(S, width, nkv, ps)
+    s.weight = torch.zeros(S * width, nkv, ps)
+    s.q = normal(s.rows, nq, hd)
+    cache = s.device()
+    cache.q64 = s.q.double()
+    want, want_lse, mag = dense64(s, cache)
+    outs = []
+    for _ in range(20):
+        out, lse = torch.full((s.rows, nq, hd), 77.0, dtype=s.dt, device="cuda"), torch.full((s.rows, nq), 77.0, device="cuda")
+        cache.attention(s.q, s.q_pos.cuda(), s.start.cuda(), out, lse=lse)
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    assert int(s.status) == 0
+    s.compare(host(outs[0][0]), host(outs[0][1]), want, want_lse, mag, 0.0, None)
+    assert all(torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1]) for o in outs)
+    w = torch.zeros(s.pos.shape, device="cuda")
+    cache.key_weight(s.q, s.q_pos.cuda(), s.start.cuda(), outs[0][1], weight=w, weight_out=w)
+    # each query gives every kv head's rows as much as it has heads there, in all
+    per = w[cache.table.long()].sum((1, 3)).double()
+    assert (per - n * (nq // nkv)).abs().max() <= n * (nq // nkv) * 2 * (s.score_error(0.0, None) + 2.0 ** -18)
+
+
 def test_offsets_beyond_32_bits(B):
     """A pool of more than 2^31 elements (5 GB): rows in its last pages."""
     pages, nkv, ps, hd = 1100, 8, 1024, 256
