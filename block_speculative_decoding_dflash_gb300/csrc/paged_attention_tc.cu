@@ -77,8 +77,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   uint8_t* sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
   constexpr int wLoad = QT * 4, wMma = QT * 4 + 1;
 
-  pdl_launch_dependents();
-  if (warp == wMma) tmem_alloc(&tmem_holder, 512);
   if (threadIdx.x == wLoad * 32) {
     mbar_init(&q_full, 1);
     mbar_init(&o_final, 1);
@@ -99,6 +97,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tma_prefetch_desc(&mv);
   }
   pdl_wait();
+  // TMEM only once the kernel before has given its own back, and the next
+  // kernel only once every CTA of this one has its share: neither can then
+  // wait for columns that the other holds while it waits
+  if (warp == wMma) {
+    tmem_alloc(&tmem_holder, 512);
+    pdl_launch_dependents();
+  }
   if (warp == 0) {
     const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, blockIdx.x);
     int lo = INT32_MAX, hi = INT32_MIN;
