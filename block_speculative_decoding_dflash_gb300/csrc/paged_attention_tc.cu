@@ -27,6 +27,7 @@
 // do see them add p v themselves.
 #include <math.h>
 
+#include "mma_sync.cuh"
 #include "paged_tc.cuh"
 
 namespace dfl {
@@ -54,7 +55,8 @@ struct TcShape {
   static constexpr size_t kSmem = kEnd + 1024;
 };
 
-template <int HDP, int QT>
+// EXTRA: a cap or a distance bias (their code would cost the others registers).
+template <int HDP, int QT, bool EXTRA>
 __global__ void __launch_bounds__(QT * 128 + 128, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
@@ -308,7 +310,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     int4 pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
     auto fetch = [&]() {
       pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
-      if (rel < 0 || (!a.slopes && ((all[rel >> 5] >> (rel & 31)) & 1u))) return;
+      if (rel < 0 || (!(EXTRA && a.slopes) && ((all[rel >> 5] >> (rel & 31)) & 1u))) return;
       const int slot = (sh.t0 + rel) * kPtKeys + lane * 4;
       const long long row = slot < len ? paged_row(c, t.seq, h, slot) : -1;
       if (row >= 0) {
@@ -341,34 +343,55 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       }
       const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
       const int tile = sh.t0 + rel;
-      float s[128];
-#pragma unroll
-      for (int d = 0; d < 128; d += 32) tmem_ld32(s_at + d, &s[d]);
-      tmem_ld_wait();
-      float sc = scale2;
-      if (!full || a.slopes) {
+      // First pass over S: the row's maximum. What a mask, cap or bias makes of
+      // a score is put back in its place, so that the second pass is the same
+      // for all; S is read twice because half as many registers then do.
+      const bool change = !full || (EXTRA && (a.slopes || a.softcap > 0.f));
+      if (!full || (EXTRA && a.slopes)) {
         __syncwarp();
         *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
         __syncwarp();
       }
-      if (a.softcap > 0.f) {
+      float x[2][32], top = -INFINITY;
+      tmem_ld32(s_at, x[0]);
 #pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = cap_tanh(s[j] * scale2, cap2);
-        sc = 1.f;
+      for (int n = 0; n < 4; ++n) {
+        float* v = x[n & 1];
+        tmem_ld_wait32(v);
+        if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+        if (change) {
+          const int* pk = kp + n * 32;
+          uint32_t w[32];
+          if (EXTRA && a.softcap > 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * scale2, cap2);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] *= scale2;
+          }
+          if (EXTRA && a.slopes) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope2, fabsf((float)(pq - pk[j])), v[j]);
+          }
+          if (!full) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = paged_sees(m, pq, pk[j]) ? v[j] : -INFINITY;
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+          tmem_st32(s_at + n * 32, w);
+        }
+        float t2[2] = {v[0], v[1]};
+#pragma unroll
+        for (int j = 2; j < 32; j += 4) {
+          t2[0] = j + 2 < 32 ? fmaxf(fmaxf(t2[0], v[j]), v[j + 2]) : fmaxf(t2[0], v[j]);
+          t2[1] = j + 3 < 32 ? fmaxf(fmaxf(t2[1], v[j + 1]), v[j + 3]) : fmaxf(t2[1], v[j + 1]);
+        }
+        top = fmaxf(top, fmaxf(t2[0], t2[1]));
       }
-      if (a.slopes) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = fmaf(-slope2, fabsf((float)(pq - kp[j])), s[j] * sc);
-        sc = 1.f;
-      }
-      if (!full) {
-#pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = paged_sees(m, pq, kp[j]) ? s[j] : -INFINITY;
-      }
-      float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < 128; ++j) top4[j & 3] = fmaxf(top4[j & 3], s[j]);
-      const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * sc;
+      const float sc = change ? 1.f : scale2;
+      top *= sc;
+      if (change) tmem_st_wait();
       if (__any_sync(0xffffffffu, top > mx + kLazy)) {
         const float mn = fmaxf(mx, top);
         const float f = mn == -INFINITY ? 1.f : ex2(mx - mn);
@@ -382,34 +405,41 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             tc_fence_after();
           }
 #pragma unroll
-          for (int d = 0; d < HDP; d += 32) {
-            float o[32];
-            tmem_ld32(o_at + d, o);
+          for (int d = 0; d < HDP; d += 16) {
+            float o[16];
+            tmem_ld16(o_at + d, o);
             tmem_ld_wait();
-            uint32_t w[32];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(o[j] * f);
-            tmem_st32(o_at + d, w);
+            for (int j = 0; j < 16; ++j) o[j] *= f;
+            tmem_st16(o_at + d, o);
           }
           tmem_st_wait();
         }
       }
       const float base = mx == -INFINITY ? 0.f : mx;
-      float add[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
+      uint64_t add[2] = {0, 0};
+      tmem_ld32(s_at, x[0]);
 #pragma unroll
-      for (int d = 0; d < 128; d += 64) {
-        uint32_t w[32];
+      for (int n = 0; n < 4; ++n) {
+        float* v = x[n & 1];
+        tmem_ld_wait32(v);
+        if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+        float w[16];
 #pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-          const float p0 = ex2(fmaf(s[d + j], sc, -base)), p1 = ex2(fmaf(s[d + j + 1], sc, -base));
-          add[j & 3] += p0;
-          add[(j + 1) & 3] += p1;
-          const __nv_bfloat162 b = __floats2bfloat162_rn(p0, p1);
-          w[j >> 1] = *reinterpret_cast<const uint32_t*>(&b);
+        for (int j = 0; j < 32; j += 2) {
+          float p0, p1;
+          unpack2(fma2(pack2(v[j], v[j + 1]), sc2, nb2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+          w[j >> 1] = __uint_as_float(pack_bf16(p0, p1));
         }
-        tmem_st32(s_at + (d >> 1), w);
+        tmem_st16(s_at + n * 16, w);     // columns whose scores have been read
       }
-      sum += (add[0] + add[1]) + (add[2] + add[3]);
+      float a0, a1;
+      unpack2(add2(add[0], add[1]), a0, a1);
+      sum += a0 + a1;
       tmem_st_wait();
       if (!full) {
         const unsigned* who = bad[i & 3];
@@ -429,17 +459,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             const long long row = paged_row(c, t.seq, h, slot);
             if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
             const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
-            for (int d = 0; d < HDP; d += 32) {
-              float o[32];
-              tmem_ld32(o_at + d, o);
+            for (int d = 0; d < HDP; d += 16) {
+              float o[16];
+              tmem_ld16(o_at + d, o);
               tmem_ld_wait();
-              uint32_t ow[32];
 #pragma unroll
-              for (int x = 0; x < 32; ++x) {
+              for (int x = 0; x < 16; ++x) {
                 const float v = d + x < c.hd ? to_f(vrow[d + x]) : 0.f;
-                ow[x] = __float_as_uint(p != 0.f ? fmaf(p, v, o[x]) : o[x]);
+                if (p != 0.f) o[x] = fmaf(p, v, o[x]);
               }
-              tmem_st32(o_at + d, ow);
+              tmem_st16(o_at + d, o);
             }
             tmem_st_wait();
           }
@@ -509,9 +538,11 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   if (!paged_map_rows(&mq, a.q, a, kPtKeys / a.G) || !paged_map_pages(&mk, a.c.k, a.c) || !paged_map_pages(&mv, a.c.v, a.c))
     return cudaErrorInvalidValue;
   using C = TcShape<HDP, QT>;
-  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc_kernel<HDP, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  const bool extra = a.softcap > 0.f || a.slopes;
+  auto kernel = extra ? paged_attn_tc_kernel<HDP, QT, true> : paged_attn_tc_kernel<HDP, QT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_attn_tc_kernel<HDP, QT>, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(C::kThreads), C::kSmem, st, mq, mk, mv, a);
+  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(C::kThreads), C::kSmem, st, mq, mk, mv, a);
 }
 
 }  // namespace
