@@ -184,69 +184,82 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     for (int n = issued > NS ? issued - NS : 0; n < issued; ++n) paged_wait(&kv_full[n % NS], (n / NS) & 1, landed);
     ok = ok && landed;
   } else if (warp == wMma) {
-    // ---- MMAs, all from one thread, so that they run in the order issued
-    if (lane == 0 && N > 0) {
+    // ---- MMAs, all from one lane, so that they run in the order issued; the
+    // warp stays together, so that descriptors live in uniform registers
+    if (N > 0) {
+      const bool leader = elect_one();
       const uint32_t sb = smem_u32(sm);
       const int ksteps = (c.hd + 15) >> 4;
-      const uint32_t idesc_s = idesc_bf16(128, 128), idesc_o = idesc_bf16(128, ksteps * 16) | kIdescBMnMajor;
-      auto qk = [&](int q, int buf, int i) {
-        const uint32_t ka = sb + C::kKV + ((2 * i) % NS) * C::kTileB, qa = sb + C::kQ + q * C::kTileB;
-        for (int k = 0; k < ksteps; ++k)
-          tc_mma_bf16(tmem + buf * 128, smem_desc_sw128(qa + (k >> 2) * C::kHalfB + (k & 3) * 32),
-                      smem_desc_sw128(ka + (k >> 2) * C::kHalfB + (k & 3) * 32), idesc_s, k ? 1u : 0u);
-        tc_commit(&s_full[buf]);
+      const uint32_t idesc_o = idesc_bf16(128, ksteps * 16) | kIdescBMnMajor;
+      const uint64_t q_desc = smem_desc_sw128(sb + C::kQ), k_desc = smem_desc_sw128(sb + C::kKV);
+      const uint64_t v_desc = smem_desc_sw128_mn(sb + C::kKV, C::kHalfB);
+      // scores of query tile q against key tile i into buffer buf; the last
+      // use of K frees its stage
+      auto qk = [&](int q, int buf, int i, bool last) {
+        const int s = (2 * i) % NS;
+        if (leader) {
+          tc_scores<C::kHalves>(tmem + buf * 128, q_desc + q * (C::kTileB >> 4), k_desc + s * (C::kTileB >> 4), ksteps);
+          tc_commit(&s_full[buf]);
+          if (last) tc_commit(&kv_empty[s]);
+        }
+        __syncwarp();
       };
-      auto pv = [&](int q, int buf, int i) {
-        const uint32_t va = sb + C::kKV + ((2 * i + 1) % NS) * C::kTileB;
-        for (int k = 0; k < 8; ++k)
-          tc_mma_bf16_ta(tmem + 256 + q * HDP, tmem + buf * 128 + k * 8, smem_desc_sw128_mn(va + k * 2048, C::kHalfB), idesc_o, 1u);
+      auto pv = [&](int q, int buf, int i, bool last) {
+        const int s = (2 * i + 1) % NS;
+        if (leader) {
+          const uint64_t v = v_desc + s * (C::kTileB >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256 + q * HDP, tmem + buf * 128 + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
+          if (QT == 1) tc_commit(&o_done);
+          if (last) tc_commit(&kv_empty[s]);
+        }
+        __syncwarp();
       };
       auto wait_k = [&](int i) { paged_wait(&kv_full[(2 * i) % NS], (2 * i / NS) & 1, ok); };
       auto wait_v = [&](int i) { paged_wait(&v_ok[i & 3], (i >> 2) & 1, ok); };
       paged_wait(&q_full, 0, ok);
       wait_k(0);
-      qk(0, 0, 0);
+      qk(0, 0, 0, QT == 1 || nt == 1);
       if (QT == 2) {
-        if (nt == 2) qk(1, 1, 0);
-        tc_commit(&kv_empty[0]);
-        for (int i = 0; i < N && ok; ++i) {
+        if (nt == 2) qk(1, 1, 0, true);
+        for (int i = 0; i < N; ++i) {
+          const bool more = i + 1 < N;
           wait_v(i);
-          for (int q = 0; q < nt; ++q) {
-            paged_wait(&p_ready[q], i & 1, ok);
-            if (!ok) break;
+          paged_wait(&p_ready[0], i & 1, ok);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc_fence_after();
+          pv(0, 0, i, nt == 1);
+          if (more) {
+            wait_k(i + 1);
+            qk(0, 0, i + 1, nt == 1);
+          }
+          if (nt == 2) {
+            paged_wait(&p_ready[1], i & 1, ok);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
             tc_fence_after();
-            pv(q, q, i);
-            if (q == nt - 1) tc_commit(&kv_empty[(2 * i + 1) % NS]);
-            if (i + 1 < N) {
-              if (q == 0) wait_k(i + 1);
-              qk(q, q, i + 1);
-              if (q == nt - 1) tc_commit(&kv_empty[(2 * i + 2) % NS]);
-            }
+            pv(1, 1, i, true);
+            if (more) qk(1, 1, i + 1, true);
           }
         }
       } else {
-        tc_commit(&kv_empty[0]);
         if (N > 1) {
           wait_k(1);
-          qk(0, 1, 1);
-          tc_commit(&kv_empty[2 % NS]);
+          qk(0, 1, 1, true);
         }
-        for (int i = 0; i < N && ok; ++i) {
+        for (int i = 0; i < N; ++i) {
           wait_v(i);
           paged_wait(&p_ready[i & 1], (i >> 1) & 1, ok);
-          if (!ok) break;
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
-          pv(0, i & 1, i);
-          tc_commit(&o_done);
-          tc_commit(&kv_empty[(2 * i + 1) % NS]);
+          pv(0, i & 1, i, true);
           if (i + 2 < N) {
             wait_k(i + 2);
-            qk(0, i & 1, i + 2);
-            tc_commit(&kv_empty[(2 * i + 4) % NS]);
+            qk(0, i & 1, i + 2, true);
           }
         }
       }
-      tc_commit(&o_final);
+      if (leader) tc_commit(&o_final);
+      __syncwarp();
       bool done = true;
       paged_wait(&o_final, 0, done);
       ok = ok && done;

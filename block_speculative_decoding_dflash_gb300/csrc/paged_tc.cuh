@@ -14,6 +14,7 @@ constexpr int kPtKeys = 128;               // keys (or query rows) of an operand
 __device__ __forceinline__ void paged_wait(uint64_t* bar, unsigned parity, bool& ok) {
   if (!ok) return;
   const uint32_t a = smem_u32(bar);
+#pragma unroll 1
   for (unsigned i = 0; i < (1u << 20); ++i) {
     uint32_t done;
     asm volatile(
@@ -23,6 +24,13 @@ __device__ __forceinline__ void paged_wait(uint64_t* bar, unsigned parity, bool&
     if (done) return;
   }
   ok = false;
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* m, int x, int y, int z, uint64_t* bar) {
@@ -82,6 +90,21 @@ __device__ __forceinline__ void tmem_ld_wait32(float* v) {
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// S[tmem 128 x 128] = A B^T over `steps` (<= 4 HALVES) K steps of 16: both
+// operands 128 K-major rows in tiles of 64 columns, given by the descriptors of
+// their first bytes. Whatever one lane spends between two MMAs is time the
+// tensor cores may wait, so a step adds a constant to a descriptor (its low
+// bits count 16 bytes) and nothing else.
+template <int HALVES>
+__device__ __forceinline__ void tc_scores(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, int steps) {
+  constexpr uint32_t idesc = idesc_bf16(128, 128);
+#pragma unroll
+  for (int k = 0; k < 4 * HALVES; ++k) {
+    const uint64_t off = (k >> 2) * (kPtKeys * 128 >> 4) + (k & 3) * 2;
+    if (k < steps) tc_mma_bf16(d_tmem, a_desc + off, b_desc + off, idesc, k ? 1u : 0u);
+  }
+}
 
 // D[tmem] (+)= A[tmem] * B[smem desc], bf16 inputs, fp32 accumulators. A: row
 // i in lane i, two consecutive K elements to a 32-bit column.

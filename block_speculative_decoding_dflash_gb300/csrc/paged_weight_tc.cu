@@ -169,27 +169,29 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           __syncwarp();
         }
       } else if (warp == wMma) {
-        if (lane == 0) {
-          const uint32_t sb = smem_u32(sm);
-          const int ksteps = (c.hd + 15) >> 4;
-          if (fresh && N > 0) paged_wait(&k_full, kn & 1, ok);
-          for (int i = 0; i < N && ok; ++i) {
-            const unsigned j = it + i;
-            const int s = j % NS, b = j & 1;
-            paged_wait(&q_full[s], (j / NS) & 1, ok);
-            for (int t = 0; t < KT && ok; ++t) {
-              if (j >= 2) paged_wait(&s_empty[t][b], ((j >> 1) - 1) & 1, ok);
-              if (!ok) break;
-              tc_fence_after();
-              for (int k = 0; k < ksteps; ++k)
-                tc_mma_bf16(tmem + (t * 2 + b) * 128, smem_desc_sw128(sb + C::kK + t * C::kTileB + (k >> 2) * C::kHalfB + (k & 3) * 32),
-                            smem_desc_sw128(sb + C::kQ + s * C::kTileB + (k >> 2) * C::kHalfB + (k & 3) * 32), idesc_bf16(128, 128), k ? 1u : 0u);
+        const bool leader = elect_one();
+        const uint32_t sb = smem_u32(sm);
+        const int ksteps = (c.hd + 15) >> 4;
+        const uint64_t k_desc = smem_desc_sw128(sb + C::kK), q_desc = smem_desc_sw128(sb + C::kQ);
+        if (fresh && N > 0) paged_wait(&k_full, kn & 1, ok);
+        for (int i = 0; i < N; ++i) {
+          const unsigned j = it + i;
+          const int s = j % NS, b = j & 1;
+          paged_wait(&q_full[s], (j / NS) & 1, ok);
+#pragma unroll
+          for (int t = 0; t < KT; ++t) {
+            if (j >= 2) paged_wait(&s_empty[t][b], ((j >> 1) - 1) & 1, ok);
+            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            tc_fence_after();
+            if (leader) {
+              tc_scores<C::kHalves>(tmem + (t * 2 + b) * 128, k_desc + t * (C::kTileB >> 4), q_desc + s * (C::kTileB >> 4), ksteps);
               tc_commit(&s_full[t][b]);
+              if (t == KT - 1) tc_commit(&q_empty[s]);
             }
-            tc_commit(&q_empty[s]);
+            __syncwarp();
           }
+          if (!ok) break;
         }
-        __syncwarp();
       } else if (warp >= wRows) {
         // lse, position and slope of the rows of every other tile
         for (int i = 0; i < N; ++i) {
