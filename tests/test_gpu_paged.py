@@ -430,6 +430,9 @@ def test_append_beyond_what_is_there(B):
     ([700], 2, 64, 8, "bf16", 350, 500, True),
     ([90], 2, 64, 16, "bf16", 4000, 5, False),
     ([5000, 4100, 9], 2, 8, 128, "bf16", 4096, 1000, True),
+    ([9000], 1, 64, 64, "bf16", 3000, 100, False),         # two to eight CTAs to a head
+    ([20000, 6000], 2, 8, 16, "bf16", 9999, 0, True),
+    ([40000], 1, 8, 256, "f32", 20000, 7, False),
 ])
 def test_evict(B, lens, nkv, hd, ps, dtype, budget, recent, ties, aliased):
     s = Setup(B, [(0, n) for n in lens], nkv, nkv, hd, ps, dtype, seed=40 + hd, kept=True)
@@ -459,6 +462,30 @@ def test_evict(B, lens, nkv, hd, ps, dtype, budget, recent, ties, aliased):
     assert np.array_equal(host(w_out), want_w, equal_nan=True)
     assert np.array_equal(host(cache.k), o["k"], equal_nan=True) and np.array_equal(host(cache.v), o["v"], equal_nan=True)
     assert int(s.status) == 0
+
+
+def test_evict_rows_that_no_cta_holds(B):
+    """A table of 2^20 rows, more than eight CTAs hold in shared memory, against torch's stable sort."""
+    n, ps, budget = (1 << 20) - 5, 1024, 400001
+    pages = (1 << 20) // ps
+    g = torch.Generator(device="cuda").manual_seed(3)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32)[None]
+    shape = (pages, 1, ps)
+    w = (torch.rand(shape, generator=g, device="cuda") * 1000).round()          # many equal ones
+    pos = torch.zeros(shape, dtype=torch.int32, device="cuda")
+    pos[table[0].long(), 0] = torch.arange(pages * ps, dtype=torch.int32, device="cuda").view(pages, ps)
+    k = pos[..., None].expand(-1, -1, -1, 8).to(torch.float32).contiguous()
+    c = B.PagedCache(k, -k, pos, table, torch.tensor([n], dtype=torch.int32, device="cuda"), weight=w)
+    flat = w[table[0].long(), 0].flatten()[:n]
+    keep = flat.sort(stable=True, descending=True).indices[:budget].sort().values
+    late = keep[keep >= budget]
+    holes = torch.ones(budget, dtype=torch.bool, device="cuda").index_fill(0, keep[keep < budget], False).nonzero().flatten()
+    want = torch.arange(budget, device="cuda").index_copy(0, holes, late)
+    c.evict(budget, 0, torch.tensor([n], dtype=torch.int32, device="cuda"))
+    got = pos[table[0].long(), 0].flatten()[:budget]
+    assert torch.equal(got.long(), want) and int(c.length[0]) == budget
+    assert torch.equal(w[table[0].long(), 0].flatten()[:budget], flat[want])
+    assert torch.equal(k[table[0].long(), 0].reshape(-1, 8)[:budget, 3].long(), want) and torch.equal(c.v, -k)
 
 
 # ---- together ------------------------------------------------------------------------------
