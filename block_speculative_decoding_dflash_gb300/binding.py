@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 import torch
@@ -591,41 +592,21 @@ class TargetContext(DFlashContext):
 # ---- paged KV cache ----------------------------------------------------------------
 PAGED_BAD_PAGE, PAGED_BAD_ROWS, PAGED_GAVE_UP = 1, 2, 4
 
+# The C structs of include/dflash.h, packed (a call is a few microseconds of
+# host time, of which setting ctypes fields one by one would be a good part).
+_PAGED_CACHE = struct.Struct("=6Q7i4x")
+_PAGED_APPEND = struct.Struct("=11Q3q5i2f4x")
+_PAGED_ATTENTION = struct.Struct("=7Qq5i2fi")
+_PAGED_EVICT = struct.Struct("=5Q2i")
+_PAGED_WORKSPACE = struct.Struct("=Qq")
+_NO_WORKSPACE = _PAGED_WORKSPACE.pack(0, 0)
 
-class PagedCacheC(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("k", "v", "pos", "table", "length", "status")] + [
-        (n, _i32) for n in ("n_pages", "page_rows", "kv_heads", "head_dim", "n_seq", "max_pages", "dtype")]
-
-
-class PagedAppendArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("q", "k", "v", "row_pos", "start", "rope_pos")] + [
-        ("pair_axis_host", ctypes.c_char_p)] + [(n, _vp) for n in ("q_norm", "k_norm", "q_out", "weight")] + [
-        (n, _i64) for n in ("q_stride", "k_stride", "v_stride")] + [
-        (n, _i32) for n in ("rows", "n_q_heads", "n_axes", "rot_pairs", "rope_neox")] + [
-        (n, ctypes.c_float) for n in ("rope_theta", "rms_eps")]
-
-
-class PagedAttentionArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("q", "q_pos", "start", "slopes", "prefix", "out", "lse", "workspace")] + [
-        (n, _i64) for n in ("workspace_bytes", "q_stride")] + [
-        (n, _i32) for n in ("rows", "n_q_heads", "causal", "window", "max_len")] + [
-        (n, ctypes.c_float) for n in ("scale", "softcap")]
-
-
-class PagedEvictArgs(ctypes.Structure):
-    _fields_ = [(n, _vp) for n in ("weight", "next_pos", "weight_out", "pos_out", "length_out", "workspace")] + [
-        ("workspace_bytes", _i64), ("budget", _i32), ("recent", _i32)]
-
-
-_sig("dflash_paged_append", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAppendArgs), _vp)
-_sig("dflash_paged_attention_workspace", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs),
-     ctypes.POINTER(_i64))
-_sig("dflash_paged_attention", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs), _vp)
-_sig("dflash_paged_key_weight", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedAttentionArgs), _vp,
-     ctypes.c_float, _vp, _vp)
-_sig("dflash_paged_evict_workspace", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedEvictArgs),
-     ctypes.POINTER(_i64))
-_sig("dflash_paged_evict", ctypes.c_int, ctypes.POINTER(PagedCacheC), ctypes.POINTER(PagedEvictArgs), _vp)
+_sig("dflash_paged_append", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_attention_workspace", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_attention", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_key_weight", ctypes.c_int, _vp, _vp, _vp, ctypes.c_float, _vp, _vp)
+_sig("dflash_paged_evict_workspace", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_evict", ctypes.c_int, _vp, _vp, _vp)
 
 
 class PagedCache:
@@ -644,31 +625,31 @@ class PagedCache:
     def __init__(self, k, v, pos, table, length, weight=None, status=None):
         if k.dim() != 4 or k.dtype not in (torch.bfloat16, torch.float32):
             raise DFlashError(EINVAL, "paged: k must be [n_pages, kv_heads, page_rows, head_dim] in bf16 or fp32")
-        self.device = k.device
-        self.dtype = k.dtype
-        n_pages, kv_heads, page_rows, head_dim = k.shape
+        self.device, self.dtype = k.device, k.dtype
+        self._index = k.get_device()
+        self.n_pages, self.kv_heads, self.page_rows, self.head_dim = k.shape
+        self._rows_shape = k.shape[:3]
         self._need("k", k, k.dtype, k.shape)
         self._need("v", v, k.dtype, k.shape)
-        self._need("pos", pos, torch.int32, k.shape[:3])
+        self._need("pos", pos, torch.int32, self._rows_shape)
         if table.dim() != 2:
             raise DFlashError(EINVAL, "paged: table must be [n_seq, max_pages]")
+        self.n_seq, self.max_pages = table.shape
         self._need("table", table, torch.int32, table.shape)
-        self._need("length", length, torch.int32, table.shape[:1])
+        self._need("length", length, torch.int32, (self.n_seq,))
         if weight is not None:
-            self._need("weight", weight, torch.float32, k.shape[:3])
+            self._need("weight", weight, torch.float32, self._rows_shape)
         if status is not None:
             self._need("status", status, torch.int32, (1,))
         self.k, self.v, self.pos, self.table, self.length = k, v, pos, table, length
         self.weight, self.status = weight, status
-        self._paged_shape = k.shape[:3]
-        self.c = PagedCacheC(k.data_ptr(), v.data_ptr(), pos.data_ptr(), table.data_ptr(), length.data_ptr(), _ptr(status),
-                             n_pages, page_rows, kv_heads, head_dim, table.shape[0], table.shape[1],
-                             BF16 if k.dtype == torch.bfloat16 else F32)
-        self._c = ctypes.byref(self.c)
+        self._c = _PAGED_CACHE.pack(k.data_ptr(), v.data_ptr(), pos.data_ptr(), table.data_ptr(), length.data_ptr(), _ptr(status) or 0,
+                                    self.n_pages, self.page_rows, self.kv_heads, self.head_dim, self.n_seq, self.max_pages,
+                                    BF16 if k.dtype == torch.bfloat16 else F32)
+        self._axis = b"", None                                    # the last pair_axis and its buffer
         # the C side checks sizes and alignment with every call; once here so a
         # bad cache is refused when it is made
-        probe = PagedEvictArgs(budget=1)
-        self._check(lib.dflash_paged_evict_workspace(self._c, ctypes.byref(probe), ctypes.byref(_i64())))
+        self._query(lib.dflash_paged_evict_workspace, _PAGED_EVICT.pack(0, 0, 0, 0, 0, 1, 0))
 
     @classmethod
     def allocate(cls, n_pages, page_rows, kv_heads, head_dim, n_seq, max_pages, dtype="bf16", device="cuda"):
@@ -687,107 +668,102 @@ class PagedCache:
             raise DFlashError(rc, last_error(None))
 
     def _need(self, name, t, dtype, shape):
-        """A dense tensor of the given type and shape on the cache's device."""
-        if t.dtype != dtype or t.shape != shape or t.device != self.device or not t.is_contiguous():
+        """The address of t: a dense tensor of the given type and shape on the cache's device."""
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != self._index or not t.is_contiguous():
             raise DFlashError(EINVAL, f"paged: {name} must be a dense {dtype} tensor of shape {tuple(shape)} on {self.device}, "
                                       f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _may(self, name, t, dtype, shape):
+        return 0 if t is None else self._need(name, t, dtype, shape)
 
     def _rows(self, name, t, heads=None):
-        """[rows, heads, head_dim] whose rows may be apart; its row stride."""
-        hd = self.c.head_dim
-        if (t.dim() != 3 or t.dtype != self.dtype or t.device != self.device or t.shape[2] != hd or (heads is not None and t.shape[1] != heads)
-                or t.shape[0] and (t.stride(2) != 1 or t.shape[1] > 1 and t.stride(1) != hd)):
-            raise DFlashError(EINVAL, f"paged: {name} must be [rows, heads, {hd}] in {self.dtype} on {self.device} with dense rows, "
-                                      f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * hd
+        """Address and row stride of [rows, heads, head_dim] whose rows may be apart."""
+        hd = self.head_dim
+        if t.dim() == 3 and t.dtype is self.dtype and t.get_device() == self._index:
+            n, h, d = t.shape
+            stride = t.stride()
+            if d == hd and (heads is None or h == heads) and (n == 0 or stride[2] == 1 and (h == 1 or stride[1] == hd)):
+                return t.data_ptr(), stride[0] if n > 1 else h * hd
+        raise DFlashError(EINVAL, f"paged: {name} must be [rows, heads, {hd}] in {self.dtype} on {self.device} with dense rows, "
+                                  f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
-    def _launch(self, call, stream):
-        """call(stream handle) with the cache's device current."""
-        if self.device.type != "cuda":
+    def _query(self, call, args):
+        n = _i64()
+        self._check(call(self._c, args + _NO_WORKSPACE, ctypes.byref(n)))
+        return n.value
+
+    def _launch(self, call, stream, *args):
+        """call(cache, *args, stream handle) with the cache's device current."""
+        index = self._index
+        if index < 0:
             raise DFlashError(EINVAL, "paged: the cache is not on a GPU")
-        if self.device.index is not None and self.device.index != torch.cuda.current_device():
-            with torch.cuda.device(self.device):
-                return self._launch(call, stream)
-        self._check(call((stream or torch.cuda.current_stream()).cuda_stream))
+        if torch._C._cuda_getDevice() != index:
+            with torch.cuda.device(index):
+                return self._launch(call, stream, *args)
+        handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+        self._check(call(self._c, *args, handle))
 
-    def _workspace(self, nbytes, workspace, stream):
+    def _with_workspace(self, call, query, args, workspace, stream):
+        nbytes = self._query(query, args)
         if workspace is not None:
-            if workspace.dtype != torch.uint8 or workspace.device != self.device or not workspace.is_contiguous():
+            if workspace.dtype is not torch.uint8 or workspace.get_device() != self._index or not workspace.is_contiguous():
                 raise DFlashError(EINVAL, f"paged: workspace must be a dense uint8 tensor on {self.device}")
-            return workspace
-        if not nbytes:
-            return None
-        if stream is None:
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        with torch.cuda.stream(stream):
-            return torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        elif nbytes:
+            if stream is None:
+                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+            else:
+                with torch.cuda.stream(stream):
+                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        ws = _NO_WORKSPACE if workspace is None else _PAGED_WORKSPACE.pack(workspace.data_ptr(), workspace.numel())
+        self._launch(call, stream, args + ws)
 
     def append(self, q, k, v, row_pos, start, q_out, rope_pos=None, pair_axis=b"", theta=1e6, neox=True, q_norm=None,
                k_norm=None, eps=1e-6, stream=None):
         """dflash_paged_append: the new rows q [rows, nq, hd], k, v [rows, kv_heads, hd] (rows may be apart) at positions
         row_pos [rows]; rope_pos [n_axes, rows] and pair_axis (bytes: the axis of each rotated pair) give the rotation,
         none without pairs. Their weight becomes 0 when the cache has weights."""
-        hd, n = self.c.head_dim, q.shape[0]
-        a = PagedAppendArgs()
-        a.q_stride = self._rows("q", q)
-        a.k_stride = self._rows("k", k, self.c.kv_heads)
-        a.v_stride = self._rows("v", v, self.c.kv_heads)
+        need, gain = self._need, (self.head_dim,)
+        q_at, q_stride = self._rows("q", q)
+        k_at, k_stride = self._rows("k", k, self.kv_heads)
+        v_at, v_stride = self._rows("v", v, self.kv_heads)
+        n, nq, _ = q.shape
         if k.shape[0] != n or v.shape[0] != n:
             raise DFlashError(EINVAL, f"paged: q, k and v have {n}, {k.shape[0]} and {v.shape[0]} rows")
-        self._need("row_pos", row_pos, torch.int32, (n,))
-        self._need("start", start, torch.int32, (self.c.n_seq + 1,))
-        self._need("q_out", q_out, self.dtype, q.shape)
-        pair_axis = bytes(pair_axis)
+        rope_at, axis_at, axes = 0, 0, 1
         if pair_axis:
             if rope_pos is None or rope_pos.dim() != 2:
                 raise DFlashError(EINVAL, "paged: rope_pos must be [n_axes, rows]")
-            self._need("rope_pos", rope_pos, torch.int32, (rope_pos.shape[0], n))
-            a.rope_pos = rope_pos.data_ptr()
-            a.pair_axis_host = pair_axis
-        for name, g in (("q_norm", q_norm), ("k_norm", k_norm)):
-            if g is not None:
-                self._need(name, g, self.dtype, (hd,))
-                setattr(a, name, g.data_ptr())
-        a.q, a.k, a.v, a.row_pos, a.start, a.q_out = (q.data_ptr(), k.data_ptr(), v.data_ptr(), row_pos.data_ptr(),
-                                                      start.data_ptr(), q_out.data_ptr())
-        a.weight = _ptr(self.weight)
-        a.rows, a.n_q_heads, a.n_axes, a.rot_pairs = n, q.shape[1], rope_pos.shape[0] if pair_axis else 1, len(pair_axis)
-        a.rope_neox, a.rope_theta, a.rms_eps = 1 if neox else 0, theta, eps
-        self._launch(lambda st: lib.dflash_paged_append(self._c, ctypes.byref(a), st), stream)
+            axes = rope_pos.shape[0]
+            rope_at = need("rope_pos", rope_pos, torch.int32, (axes, n))
+            held = self._axis                                     # one object: another thread may replace it
+            if held[0] != pair_axis:
+                axis = bytes(pair_axis)
+                self._axis = held = axis, ctypes.create_string_buffer(axis, len(axis))
+            axis_at = ctypes.addressof(held[1])
+        args = _PAGED_APPEND.pack(q_at, k_at, v_at, need("row_pos", row_pos, torch.int32, (n,)),
+                                  need("start", start, torch.int32, (self.n_seq + 1,)), rope_at, axis_at,
+                                  self._may("q_norm", q_norm, self.dtype, gain), self._may("k_norm", k_norm, self.dtype, gain),
+                                  need("q_out", q_out, self.dtype, q.shape), 0 if self.weight is None else self.weight.data_ptr(),
+                                  q_stride, k_stride, v_stride, n, nq, axes, len(pair_axis), 1 if neox else 0, theta, eps)
+        self._launch(lib.dflash_paged_append, stream, args)
 
-    def _attention_args(self, q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len):
-        n, nq = q.shape[0], q.shape[1]
-        a = PagedAttentionArgs()
-        a.q_stride = self._rows("q", q)
-        self._need("q_pos", q_pos, torch.int32, (n,))
-        self._need("start", start, torch.int32, (self.c.n_seq + 1,))
-        if lse is not None:
-            self._need("lse", lse, torch.float32, (n, nq))
-            a.lse = lse.data_ptr()
-        if slopes is not None:
-            self._need("slopes", slopes, torch.float32, (nq,))
-            a.slopes = slopes.data_ptr()
-        if prefix is not None:
-            self._need("prefix", prefix, torch.int32, (self.c.n_seq,))
-            a.prefix = prefix.data_ptr()
-        a.q, a.q_pos, a.start = q.data_ptr(), q_pos.data_ptr(), start.data_ptr()
-        a.rows, a.n_q_heads, a.causal, a.window, a.max_len = n, nq, 1 if causal else 0, window, max_len
-        a.scale, a.softcap = (self.c.head_dim ** -0.5 if scale is None else scale), softcap
-        return a
+    def _attention_args(self, q, q_pos, start, out_at, lse, scale, causal, window, softcap, slopes, prefix, max_len):
+        need = self._need
+        q_at, q_stride = self._rows("q", q)
+        n, nq, _ = q.shape
+        return _PAGED_ATTENTION.pack(q_at, need("q_pos", q_pos, torch.int32, (n,)), need("start", start, torch.int32, (self.n_seq + 1,)),
+                                     self._may("slopes", slopes, torch.float32, (nq,)), self._may("prefix", prefix, torch.int32, (self.n_seq,)),
+                                     out_at, self._may("lse", lse, torch.float32, (n, nq)), q_stride, n, nq, 1 if causal else 0, window,
+                                     max_len, self.head_dim ** -0.5 if scale is None else scale, softcap, 0)
 
     def attention(self, q, q_pos, start, out, lse=None, scale=None, causal=True, window=0, softcap=0.0, slopes=None,
                   prefix=None, max_len=0, workspace=None, stream=None):
         """dflash_paged_attention: out [rows, nq, hd] and lse [rows, nq] of q [rows, nq, hd] (rows may be apart) at
         positions q_pos [rows]; rows start[s] .. start[s + 1] - 1 belong to sequence s. scale None: head_dim ** -0.5."""
-        a = self._attention_args(q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len)
-        self._need("out", out, self.dtype, q.shape)
-        a.out = out.data_ptr()
-        need = _i64()
-        self._check(lib.dflash_paged_attention_workspace(self._c, ctypes.byref(a), ctypes.byref(need)))
-        ws = self._workspace(need.value, workspace, stream)
-        if ws is not None:
-            a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-        self._launch(lambda st: lib.dflash_paged_attention(self._c, ctypes.byref(a), st), stream)
+        args = self._attention_args(q, q_pos, start, self._need("out", out, self.dtype, q.shape), lse, scale, causal, window, softcap,
+                                    slopes, prefix, max_len)
+        self._with_workspace(lib.dflash_paged_attention, lib.dflash_paged_attention_workspace, args, workspace, stream)
 
     def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
                    softcap=0.0, slopes=None, prefix=None, max_len=0, stream=None):
@@ -797,32 +773,21 @@ class PagedCache:
         weight_out = self.weight if weight_out is None else weight_out
         if weight_out is None or lse is None:
             raise DFlashError(EINVAL, "paged: key_weight needs lse, and a weight_out where the cache has no weight")
-        a = self._attention_args(q, q_pos, start, lse, scale, causal, window, softcap, slopes, prefix, max_len)
-        if weight is not None:
-            self._need("weight", weight, torch.float32, self._paged_shape)
-        self._need("weight_out", weight_out, torch.float32, self._paged_shape)
-        self._launch(lambda st: lib.dflash_paged_key_weight(self._c, ctypes.byref(a), _ptr(weight), decay,
-                                                            weight_out.data_ptr(), st), stream)
+        args = self._attention_args(q, q_pos, start, 0, lse, scale, causal, window, softcap, slopes, prefix, max_len)
+        self._launch(lib.dflash_paged_key_weight, stream, args + _NO_WORKSPACE, self._may("weight", weight, torch.float32, self._rows_shape),
+                     decay, self._need("weight_out", weight_out, torch.float32, self._rows_shape))
 
     def evict(self, budget, recent, next_pos, weight=None, weight_out=None, pos_out=None, length_out=None, workspace=None,
               stream=None):
         """dflash_paged_evict: every sequence and kv head keeps its `budget` heaviest rows, those at positions >=
         next_pos[s] - recent before all others. The outputs default to the cache's own weight, pos and length."""
+        need, shape, seqs = self._need, self._rows_shape, (self.n_seq,)
         weight = self.weight if weight is None else weight
         weight_out = self.weight if weight_out is None else weight_out
-        pos_out = self.pos if pos_out is None else pos_out
-        length_out = self.length if length_out is None else length_out
         if weight is None or weight_out is None:
             raise DFlashError(EINVAL, "paged: evict needs weights")
-        self._need("weight", weight, torch.float32, self._paged_shape)
-        self._need("weight_out", weight_out, torch.float32, self._paged_shape)
-        self._need("pos_out", pos_out, torch.int32, self._paged_shape)
-        self._need("length_out", length_out, torch.int32, (self.c.n_seq,))
-        self._need("next_pos", next_pos, torch.int32, (self.c.n_seq,))
-        a = PagedEvictArgs(weight.data_ptr(), next_pos.data_ptr(), weight_out.data_ptr(), pos_out.data_ptr(),
-                           length_out.data_ptr(), None, 0, budget, recent)
-        need = _i64()
-        self._check(lib.dflash_paged_evict_workspace(self._c, ctypes.byref(a), ctypes.byref(need)))
-        ws = self._workspace(need.value, workspace, stream)
-        a.workspace, a.workspace_bytes = ws.data_ptr(), ws.numel()
-        self._launch(lambda st: lib.dflash_paged_evict(self._c, ctypes.byref(a), st), stream)
+        args = _PAGED_EVICT.pack(need("weight", weight, torch.float32, shape), need("next_pos", next_pos, torch.int32, seqs),
+                                 need("weight_out", weight_out, torch.float32, shape),
+                                 need("pos_out", self.pos if pos_out is None else pos_out, torch.int32, shape),
+                                 need("length_out", self.length if length_out is None else length_out, torch.int32, seqs), budget, recent)
+        self._with_workspace(lib.dflash_paged_evict, lib.dflash_paged_evict_workspace, args, workspace, stream)

@@ -41,107 +41,131 @@ __device__ __forceinline__ NewRow new_row(const PagedAppendArgs& a, int tok, boo
   return NewRow{t.seq, slot};
 }
 
-// Head x of a new row, counted over q, then k, then v: where it is read and
-// written, and what it is (0 q, 1 k, 2 v); dst NULL where it has no place.
+// 8 values of a head as they lie in memory.
 template <typename T>
-struct HeadPtr { const T* src; T* dst; int kind; };
-template <typename T>
-__device__ __forceinline__ HeadPtr<T> head_ptr(const PagedAppendArgs& a, const NewRow& r, int tok, int x, bool first_lane) {
-  const PagedView& c = a.c;
-  const int hd = c.hd;
-  if (x < a.nq)
-    return {static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (size_t)x * hd, static_cast<T*>(a.q_out) + ((size_t)tok * a.nq + x) * hd, 0};
-  const int kind = x < a.nq + c.nkv ? 1 : 2, h = x - a.nq - (kind == 2 ? c.nkv : 0);
-  const long long row = r.slot >= 0 ? paged_row(c, r.seq, h, r.slot) : -1;
-  const T* src = kind == 1 ? static_cast<const T*>(a.k) + (long long)tok * a.k_stride + (size_t)h * hd
-                           : static_cast<const T*>(a.v) + (long long)tok * a.v_stride + (size_t)h * hd;
-  if (row < 0) return {src, nullptr, kind};
-  if (kind == 1 && first_lane) {
-    c.pos[row] = a.row_pos[tok];
-    if (a.weight) a.weight[row] = 0.f;
+struct Raw8 {
+  static constexpr int kWords = sizeof(T) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+      w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+    }
   }
-  return {src, static_cast<T*>(kind == 1 ? c.k : c.v) + row * hd, kind};
-}
-
-__device__ __forceinline__ void store8(bf16* p, const float* v) {
-  uint4 u;
-  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords; i += 4)
+      *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if (sizeof(T) == 4) return __uint_as_float(w[i % kWords]);
+    return i & 1 ? bf_hi(w[i >> 1]) : bf_lo(w[i >> 1]);
+  }
+};
+__device__ __forceinline__ Raw8<bf16> round8(const float* v, bf16) {
+  Raw8<bf16> r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    r.w[i] = *reinterpret_cast<const uint32_t*>(&b);
   }
-  *reinterpret_cast<uint4*>(p) = u;
+  return r;
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ Raw8<float> round8(const float* v, float) {
+  Raw8<float> r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+  return r;
 }
 
-// A warp takes `per_warp` heads of one new row. A head lies in hd / 8 lanes, 8
-// dimensions to each (16-byte accesses), so 32 / (hd / 8) heads are worked on
-// side by side; the lane keeps its dimensions' (cos, sin) in registers for
-// all of them, and a rotated pair's other half is in the same
-// lane (adjacent pairs) or one shuffle away. kU heads are requested before the
-// first is used. Bound by the bytes of the rows, read once and written once.
+// A warp takes heads [x0, x1) of one new row, counted over q, then k, then v.
+// A head lies in hd / 8 lanes, 8 dimensions to each (16-byte accesses), so
+// 32 / (hd / 8) heads are worked on side by side. With r the head's 1 / rms,
+// a value becomes r (v A + w B): w the pair's other half, in the same lane
+// (adjacent pairs) or one shuffle away, A and B the gains times cos and sin,
+// which a lane holds for its dimensions. kU heads are requested before the
+// first is used, and those before the sines are computed. Bound by the bytes
+// of the rows, read once and written once, for thousands of rows; by its
+// chain of dependent loads for a few.
 // Needs pairs to fill whole lanes: a multiple of 8 (neox) or 4.
+constexpr int kU = 4;
 template <typename T>
 __global__ void __launch_bounds__(kWarps * 32, 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int per_warp, int splits) {
-  constexpr int kU = 4;
   pdl_enter();
   const PagedView& c = a.c;
-  const int lane = threadIdx.x & 31, hd = c.hd;
+  const int lane = threadIdx.x & 31, hd = c.hd, nq = a.nq, nkv = c.nkv;
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int tok = (int)(item / splits), part = (int)(item % splits);
   if (tok >= a.rows) return;
-  const NewRow r = new_row(a, tok, part == 0);
-  if (r.seq < 0) return;
+  const int x0 = part * per_warp, x1 = min(nq + 2 * nkv, x0 + per_warp);
   const int lpr = hd >> 3, side = 32 / lpr;               // lanes of a head, heads side by side
   const int sub = lane / lpr, l = lane - sub * lpr, d0 = l * 8;
   const bool in = sub < side;
-  // this lane's rotation: own = v * cs + other * sn
-  float cs[8], sn[8];
-  int other = lane;                                       // lane that holds the pairs' other halves
+  const int step = side * hd;                             // elements between a lane's heads
+  const T* qs = static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (size_t)(x0 + sub) * hd + d0;
+  Raw8<T> raw[kU];
+  const int q_left = min(x1, nq) - x0;                    // q heads of this warp
+#pragma unroll
+  for (int u = 0; u < kU; ++u)
+    if (in && u * side + sub < q_left) raw[u].load(qs + (size_t)u * step);
+  // the row's (cos, sin), two pairs or more to a lane, then this lane's
+  __shared__ __align__(16) float2 table[kWarps][kPagedMaxPairs];
+  float2* tab = table[threadIdx.x >> 5];
+  for (int i = lane; i < a.pairs; i += 32) tab[i] = turn(a, i, tok);
+  __syncwarp();
+  NewRow r{-1, -1};
+  if (x1 > nq) {
+    r = new_row(a, tok, x1 == nq + 2 * nkv);
+    if (r.seq < 0) return;
+  } else if (tok < a.start[0] || tok >= a.start[c.n_seq]) {
+    return;
+  }
+
+  int other = lane, od = d0, pair = -1;                   // where the pairs' other halves are; first pair of the lane
+  bool second = false;                                    // the lane holds second halves (neox)
   if (a.neox) {
     const int pl = a.pairs >> 3;                          // lanes of the first halves
-    const bool lo = l < pl, hi = !lo && l < 2 * pl;
-    other = lo ? lane + pl : (hi ? lane - pl : lane);
+    second = l >= pl;
+    if (l < 2 * pl) {
+      other = second ? lane - pl : lane + pl;
+      od = second ? d0 - a.pairs : d0 + a.pairs;
+      pair = second ? od : d0;
+    }
+  } else if (d0 < 2 * a.pairs) {
+    pair = d0 >> 1;
+  }
+  float A[8], B[8];
+  bool norm;
+  auto use_gain = [&](const void* g) {
+    norm = g != nullptr;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float2 t = in && (lo || hi) ? turn(a, (lo ? d0 : d0 - a.pairs) + j, tok) : make_float2(1.f, 0.f);
-      cs[j] = t.x;
-      sn[j] = lo ? -t.y : t.y;
+      float2 t = make_float2(1.f, 0.f);
+      if (in && pair >= 0) t = tab[pair + (a.neox ? j : j >> 1)];
+      A[j] = t.x;
+      B[j] = (a.neox ? second : (j & 1)) ? t.y : -t.y;
     }
-  } else {
+    if (norm && in) {
+      float own[8], oth[8];
+      load8(static_cast<const T*>(g) + d0, own);
+      load8(static_cast<const T*>(g) + od, oth);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 t = in && d0 < 2 * a.pairs ? turn(a, (d0 >> 1) + j, tok) : make_float2(1.f, 0.f);
-      cs[2 * j] = cs[2 * j + 1] = t.x;
-      sn[2 * j] = -t.y;
-      sn[2 * j + 1] = t.y;
+      for (int j = 0; j < 8; ++j) {
+        A[j] *= own[j];
+        B[j] *= a.neox ? oth[j] : own[j ^ 1];
+      }
     }
-  }
-  const int heads = a.nq + 2 * c.nkv, x1 = min(heads, (part + 1) * per_warp);
-  for (int x0 = part * per_warp; x0 < x1; x0 += side * kU) {
-    HeadPtr<T> p[kU];
-    float v[kU][8];
+  };
+  const float inv_hd = 1.f / (float)hd;
+  auto turned = [&](const Raw8<T>& x) {
+    float v[8], w[8], f = 1.f;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int x = x0 + u * side + sub;
-      p[u] = HeadPtr<T>{nullptr, nullptr, 2};
-      if (in && x < x1) p[u] = head_ptr<T>(a, r, tok, x, l == 0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[u][j] = 0.f;
-      if (p[u].dst) load8(p[u].src + d0, v[u]);
-    }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const T* gain = static_cast<const T*>(p[u].kind == 0 ? a.q_norm : p[u].kind == 1 ? a.k_norm : nullptr);
+    for (int j = 0; j < 8; ++j) v[j] = x.at(j);
+    if (norm) {
       float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[u][j], v[u][j], ss);
-      // the sum over the head's lanes: every lane adds all of them in order of
-      // a tree that needs no power of two
+      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
       float tot = ss;
       if ((lpr & (lpr - 1)) == 0) {
         for (int o = lpr >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
@@ -149,20 +173,64 @@ __global__ void __launch_bounds__(kWarps * 32, 5) paged_append_kernel(const __gr
         tot = 0.f;
         for (int o = 0; o < lpr; ++o) tot += __shfl_sync(0xffffffffu, ss, in ? sub * lpr + o : lane);
       }
-      if (in && gain) {
-        const float rs = 1.0f / sqrtf(tot / (float)hd + a.eps);
-        float g[8];
-        load8(gain + d0, g);
+      f = rsqrtf(fmaf(tot, inv_hd, a.eps));
+    }
+    if (a.neox) {
+      Raw8<T> y;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] *= rs * g[j];
+      for (int j = 0; j < Raw8<T>::kWords; ++j) y.w[j] = __shfl_sync(0xffffffffu, x.w[j], other);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = y.at(j);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = v[j ^ 1];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], A[j], w[j] * B[j]) * f;
+    return round8(v, T());
+  };
+
+  if (q_left > 0) {
+    use_gain(a.q_norm);
+    T* qd = static_cast<T*>(a.q_out) + ((size_t)tok * nq + x0 + sub) * hd + d0;
+    for (int x = 0; x < q_left; x += side * kU) {
+      const size_t at = (size_t)x * hd;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const Raw8<T> y = turned(raw[u]);
+        if (in && x + u * side + sub < q_left) y.store(qd + at + (size_t)u * step);
       }
-      float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = a.neox ? __shfl_sync(0xffffffffu, v[u][j], other) : v[u][j ^ 1];
-      if (p[u].kind != 2)
+      for (int u = 0; u < kU; ++u)
+        if (in && x + (kU + u) * side + sub < q_left) raw[u].load(qs + at + (size_t)(kU + u) * step);
+    }
+  }
+  // k and v: consecutive heads of a row lie page_rows rows apart
+  for (int kind = 1; kind <= 2; ++kind) {
+    const int base = nq + (kind - 1) * nkv, h0 = max(x0, base) - base, h1 = min(x1, base + nkv) - base;
+    if (h0 >= h1) continue;
+    const long long row0 = r.slot >= 0 ? paged_row(c, r.seq, 0, r.slot) : -1;
+    if (row0 < 0) continue;
+    if (kind == 1) use_gain(a.k_norm);
+    const T* src = kind == 1 ? static_cast<const T*>(a.k) + (long long)tok * a.k_stride : static_cast<const T*>(a.v) + (long long)tok * a.v_stride;
+    T* dst = static_cast<T*>(kind == 1 ? c.k : c.v);
+    for (int h = h0; h < h1; h += side * kU) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] = fmaf(v[u][j], cs[j], w[j] * sn[j]);
-      if (p[u].dst) store8(p[u].dst + d0, v[u]);
+      for (int u = 0; u < kU; ++u)
+        if (in && h + u * side + sub < h1) raw[u].load(src + (size_t)(h + u * side + sub) * hd + d0);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int hh = h + u * side + sub;
+        const long long row = row0 + ((long long)hh << c.lg_rows);
+        const Raw8<T> y = kind == 1 ? turned(raw[u]) : raw[u];
+        if (in && hh < h1) {
+          y.store(dst + row * hd + d0);
+          if (kind == 1 && l == 0) {
+            c.pos[row] = a.row_pos[tok];
+            if (a.weight) a.weight[row] = 0.f;
+          }
+        }
+      }
     }
   }
 }
@@ -186,21 +254,30 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_any_kernel(const __g
   const NewRow r = s_row;
   if (r.seq < 0) return;
   for (int x = warp; x < a.nq + 2 * c.nkv; x += kWarps) {
-    const HeadPtr<T> p = head_ptr<T>(a, r, tok, x, lane == 0);
-    if (!p.dst) continue;
+    const int kind = x < a.nq ? 0 : (x < a.nq + c.nkv ? 1 : 2), h = kind == 0 ? x : x - a.nq - (kind - 1) * c.nkv;
+    const long long at = kind > 0 && r.slot >= 0 ? paged_row(c, r.seq, h, r.slot) : -1;
+    if (kind > 0 && at < 0) continue;
+    const T* src = kind == 0   ? static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (size_t)h * hd
+                   : kind == 1 ? static_cast<const T*>(a.k) + (long long)tok * a.k_stride + (size_t)h * hd
+                               : static_cast<const T*>(a.v) + (long long)tok * a.v_stride + (size_t)h * hd;
+    T* dst = kind == 0 ? static_cast<T*>(a.q_out) + ((size_t)tok * a.nq + h) * hd : static_cast<T*>(kind == 1 ? c.k : c.v) + at * hd;
+    if (kind == 1 && lane == 0) {
+      c.pos[at] = a.row_pos[tok];
+      if (a.weight) a.weight[at] = 0.f;
+    }
     float ss = 0.f;
     for (int d = lane; d < hd; d += 32) {
-      const float v = to_f(p.src[d]);
+      const float v = to_f(src[d]);
       row[warp][d] = v;
       ss = fmaf(v, v, ss);
     }
-    const T* gain = static_cast<const T*>(p.kind == 0 ? a.q_norm : p.kind == 1 ? a.k_norm : nullptr);
+    const T* gain = static_cast<const T*>(kind == 0 ? a.q_norm : kind == 1 ? a.k_norm : nullptr);
     if (gain) {
       const float rs = 1.0f / sqrtf(warp_sum(ss) / (float)hd + a.eps);
       for (int d = lane; d < hd; d += 32) row[warp][d] *= rs * to_f(gain[d]);
     }
     __syncwarp();
-    if (p.kind != 2)
+    if (kind != 2)
       for (int i = lane; i < a.pairs; i += 32) {
         const int d0 = a.neox ? i : 2 * i, d1 = a.neox ? i + a.pairs : 2 * i + 1;
         const float v0 = row[warp][d0], v1 = row[warp][d1];
@@ -208,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_any_kernel(const __g
         row[warp][d1] = v1 * cs[i].x + v0 * cs[i].y;
       }
     __syncwarp();
-    for (int d = lane; d < hd; d += 32) p.dst[d] = from_f<T>(row[warp][d]);
+    for (int d = lane; d < hd; d += 32) dst[d] = from_f<T>(row[warp][d]);
     __syncwarp();
   }
 }
@@ -216,11 +293,11 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_any_kernel(const __g
 template <typename T>
 cudaError_t run(const PagedAppendArgs& a, cudaStream_t st) {
   if (a.pairs % (a.neox ? 8 : 4)) return launch_pdl(paged_append_any_kernel<T>, dim3(a.rows), dim3(kWarps * 32), 0, st, a);
-  // as many warps to a row as fill the GPU (32 warps on each of 152 SMs), each
+  // as many warps to a row as fill the GPU (16 warps on each of 152 SMs), each
   // with one round of heads at least: the rotation's sines are computed once a
   // warp
   const int heads = a.nq + 2 * a.c.nkv, side = 32 / (a.c.hd >> 3);
-  int splits = (int)(4864 / (a.rows < 4864 ? a.rows : 4864));
+  int splits = 2432 / (a.rows < 2432 ? a.rows : 2432);
   const int most = (heads + side - 1) / side;
   if (splits > most) splits = most;
   const int per_warp = (heads + splits - 1) / splits;

@@ -19,9 +19,11 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024, kWarps = 32;
-constexpr int kBins = 2048;
-constexpr int kHeld = 40960;                 // keys a CTA holds in shared memory
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBins = 2048, kBinsEach = kBins / kThreads;
+constexpr int kRanks = 8;                    // CTAs of a cluster, at most
+constexpr int kHeld = 24576;                 // keys a CTA holds in shared memory
+constexpr int kMostRows = (1 << 20) / kRanks;
 constexpr int kMovesPerWarp = 8;
 
 __device__ __forceinline__ unsigned weight_key(float w, bool keep) {
@@ -32,42 +34,35 @@ __device__ __forceinline__ unsigned weight_key(float w, bool keep) {
 }
 
 struct Shared {
-  int hist[kBins];
+  int hist[2][kBins];                        // in turns, so that a pass need not wait for the others' reads of the last
   int2 warps[kWarps];
   int2 total;                                // of this CTA, for the others of its cluster
-  int digit, left;
+  int digit, left, eq_before;
 };
 
-// Exclusive sums over the CTA's warps (lane 0's value of each) and, through
-// the cluster, over the CTAs before this one; tot: the cluster's sums.
-__device__ __forceinline__ int2 scan_warps(Shared& sh, cg::cluster_group& cl, int ranks, int2 v, int2* tot) {
+// Every CTA of the cluster (or, alone, every thread) has come here and sees
+// what the others wrote to shared memory.
+__device__ __forceinline__ void meet(cg::cluster_group& cl, int ranks) {
+  if (ranks > 1) cl.sync();
+  else __syncthreads();
+}
+
+// Exclusive sums over the CTA's warps of lane 0's values; total to all.
+__device__ __forceinline__ int2 scan_warps(Shared& sh, int2 v, int2* tot) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (lane == 0) sh.warps[warp] = v;
   __syncthreads();
-  if (warp == 0) {
-    const int2 own = sh.warps[lane];
-    int2 x = own;
+  int2 x = lane < kWarps ? sh.warps[lane] : make_int2(0, 0);
+  const int2 own = x;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
-      if (lane >= o) { x.x += a; x.y += b; }
-    }
-    sh.warps[lane] = make_int2(x.x - own.x, x.y - own.y);
-    if (lane == 31) sh.total = x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(0xffffffffu, x.x, o), b = __shfl_up_sync(0xffffffffu, x.y, o);
+    if (lane >= o) { x.x += a; x.y += b; }
   }
-  if (ranks > 1) cl.sync();
-  else __syncthreads();
-  int2 before = sh.warps[warp], all = make_int2(0, 0);
-  for (int r = 0; r < ranks; ++r) {
-    const int2 t = ranks > 1 ? *cl.map_shared_rank(&sh.total, r) : sh.total;
-    if (r < (int)cl.block_rank()) { before.x += t.x; before.y += t.y; }
-    all.x += t.x;
-    all.y += t.y;
-  }
-  *tot = all;
-  if (ranks > 1) cl.sync();
-  else __syncthreads();
-  return before;
+  *tot = make_int2(__shfl_sync(0xffffffffu, x.x, 31), __shfl_sync(0xffffffffu, x.y, 31));
+  x.x -= own.x;
+  x.y -= own.y;
+  return make_int2(__shfl_sync(0xffffffffu, x.x, warp), __shfl_sync(0xffffffffu, x.y, warp));
 }
 
 // A cluster to a (sequence, kv head), a contiguous slice of its rows to a CTA.
@@ -77,7 +72,7 @@ __device__ __forceinline__ int2 scan_warps(Shared& sh, cg::cluster_group& cl, in
 // shared memory after the first of the ranking passes. Bound by the latency of
 // its dozen dependent steps for a few thousand rows, by one SM's read of the
 // weights and positions beyond.
-__global__ void __launch_bounds__(kThreads) paged_select_kernel(PagedEvictArgs a, int ranks) {
+__global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArgs a, int ranks) {
   extern __shared__ unsigned dyn[];          // [held] keys, then the masks of kept rows
   __shared__ Shared sh;
   pdl_enter();
@@ -88,13 +83,31 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(PagedEvictArgs a
   const int n = paged_length(c, s), b = a.budget;
   const long long guard = (long long)a.next_pos[s] - a.recent;
   if (tid == 0 && h == 0 && blockIdx.x == 0 && c.status && c.length[s] != n) atomicOr(c.status, DFLASH_PAGED_BAD_ROWS);
-  // a multiple of 1024, so that a warp's share is whole words
+  // a multiple of kThreads, so that a warp's share is whole words
   const int per = (n + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;
   const int i0 = min(n, (int)cl.block_rank() * per), i1 = min(n, i0 + per), m = i1 - i0;
   const bool held = per <= kHeld;
   unsigned* keys = dyn;
   unsigned* kept_bits = dyn + (held ? per : 0);
-  const bool copies = a.weight_out != a.weight || a.pos_out != c.pos;
+  // Position and weight of a remaining row go to the outputs as they are read;
+  // a hole gets its new row's in the move, which comes after.
+  const bool new_w = a.weight_out != a.weight, new_p = a.pos_out != c.pos;
+  const int keep_n = min(n, b);
+  auto copy4 = [&](long long row, int i, const float4& w, const int4& p) {
+    if (i + 3 < keep_n) {
+      if (new_w) *reinterpret_cast<float4*>(a.weight_out + row) = w;
+      if (new_p) *reinterpret_cast<int4*>(a.pos_out + row) = p;
+    } else {
+      const float wv[4] = {w.x, w.y, w.z, w.w};
+      const int pv[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < keep_n) {
+          if (new_w) a.weight_out[row + j] = wv[j];
+          if (new_p) a.pos_out[row + j] = pv[j];
+        }
+    }
+  };
   // key of row i0 + i, from global memory (rows on no page count as NaN)
   auto fetch = [&](int i) -> unsigned {
     const long long row = paged_row(c, s, h, i0 + i);
@@ -114,6 +127,7 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(PagedEvictArgs a
         if (row >= 0) {
           const float4 w = *reinterpret_cast<const float4*>(a.weight + row);
           const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
+          copy4(row, i0 + i, w, p);
           k = make_uint4(weight_key(w.x, p.x >= guard), weight_key(w.y, p.y >= guard), weight_key(w.z, p.z >= guard), weight_key(w.w, p.w >= guard));
         } else if (c.status) {
           atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
@@ -121,61 +135,63 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(PagedEvictArgs a
         *reinterpret_cast<uint4*>(keys + i) = k;
       }
     }
-    const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
 #pragma unroll 1
     for (int d = 0; d < 3; ++d) {
-      const int shift = shifts[d], top = shift + bits[d];
-      for (int i = tid; i < kBins; i += kThreads) sh.hist[i] = 0;
+      const int shift = d == 0 ? 21 : (d == 1 ? 10 : 0), top = d == 0 ? 32 : (d == 1 ? 21 : 10), mask = (1 << (top - shift)) - 1;
+      int* hist = sh.hist[d & 1];
+      for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
       for (int i = tid; i < (m + 31) / 32 * 32; i += kThreads) {
         const unsigned k = i < m ? key(i) : 0u;
-        const bool in = i < m && (top == 32 || (k >> top) == (prefix >> top));
-        const unsigned dig = in ? (k >> shift) & ((1u << bits[d]) - 1) : 0xffffffffu;
+        const bool in = i < m && (d == 0 || (k >> top) == (prefix >> top));
+        const unsigned dig = in ? (k >> shift) & mask : 0xffffffffu;
         // equal weights are common (rows that nobody looked at): one add for a warp of them
         const unsigned one = __shfl_sync(0xffffffffu, dig, 0);
         if (__all_sync(0xffffffffu, dig == one)) {
-          if (lane == 0 && in) atomicAdd(&sh.hist[dig], 32);
+          if (lane == 0 && in) atomicAdd(&hist[dig], 32);
         } else if (in) {
-          atomicAdd(&sh.hist[dig], 1);
+          atomicAdd(&hist[dig], 1);
         }
       }
-      if (ranks > 1) cl.sync();
-      else __syncthreads();
-      // bins from the top, two to a thread: the bin in which the count reaches
-      // `left`
-      int v[2] = {0, 0};
-      for (int r = 0; r < ranks; ++r) {
-        const int* hist = ranks > 1 ? cl.map_shared_rank(sh.hist, r) : sh.hist;
-        v[0] += hist[kBins - 1 - 2 * tid];
-        v[1] += hist[kBins - 2 - 2 * tid];
+      meet(cl, ranks);
+      // bins from the top, kBinsEach to a thread: the bin in which the count
+      // reaches `left`
+      int4 v = make_int4(0, 0, 0, 0);
+      const int at = kBins - kBinsEach * (tid + 1);
+      if (ranks > 1) {
+        int4 p[kRanks];
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r)
+          p[r] = r < ranks ? *reinterpret_cast<const int4*>(cl.map_shared_rank(hist, r) + at) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int r = 0; r < kRanks; ++r) { v.x += p[r].x; v.y += p[r].y; v.z += p[r].z; v.w += p[r].w; }
+      } else {
+        v = *reinterpret_cast<const int4*>(hist + at);
       }
-      int x = v[0] + v[1];
+      const int cnt[4] = {v.w, v.z, v.y, v.x};
+      const int mine = (v.x + v.y) + (v.z + v.w);
+      int x = mine;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
       }
-      if (lane == 31) sh.warps[warp].x = x;
-      __syncthreads();
-      if (warp == 0) {
-        const int own = sh.warps[lane].x;
-        int y = own;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int w = __shfl_up_sync(0xffffffffu, y, o);
-          if (lane >= o) y += w;
+      int2 tot;
+      const int warp_total = __shfl_sync(0xffffffffu, x, 31);
+      int before = scan_warps(sh, make_int2(warp_total, 0), &tot).x + x - mine;
+      if (before < left && left <= before + mine) {
+        int j = 0;
+        while (left > before + cnt[j]) before += cnt[j++];
+        sh.digit = at + kBinsEach - 1 - j;
+        sh.left = left - before;
+        if (d == 2) {
+          // the last digit's bin counts the rows whose key is the one of rank b
+          int eq = 0;
+          for (int r = 0; r < (int)cl.block_rank(); ++r) eq += cl.map_shared_rank(hist, r)[sh.digit];
+          sh.eq_before = eq;
         }
-        sh.warps[lane].y = y - own;
       }
       __syncthreads();
-      const int after = sh.warps[warp].y + x, before = after - v[0] - v[1];
-      if (before < left && left <= after) {
-        const bool first = left <= before + v[0];
-        sh.digit = kBins - 1 - 2 * tid - (first ? 0 : 1);
-        sh.left = left - before - (first ? 0 : v[0]);
-      }
-      if (ranks > 1) cl.sync();              // the others have read this CTA's bins
-      else __syncthreads();
       prefix |= (unsigned)sh.digit << shift;
       left = sh.left;
     }
@@ -187,59 +203,68 @@ __global__ void __launch_bounds__(kThreads) paged_select_kernel(PagedEvictArgs a
     int eq = 0;
     for (int i = w0; i < w1; i += 32) eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key(i + lane) == prefix));
     int2 tot;
-    eq = scan_warps(sh, cl, ranks, make_int2(eq, 0), &tot).x;
+    eq = sh.eq_before + scan_warps(sh, make_int2(eq, 0), &tot).x;
     int2 cnt = make_int2(0, 0);              // holes below row b, kept rows from it on
     for (int i = w0; i < w1; i += 32) {
-      const unsigned k = i + lane < w1 ? key(i + lane) : 0u;
-      const unsigned same = __ballot_sync(0xffffffffu, i + lane < w1 && k == prefix);
-      const bool keep = i + lane < w1 && (k > prefix || (k == prefix && eq + __popc(same & ((1u << lane) - 1)) < left));
+      const bool there = i + lane < w1;
+      const unsigned k = there ? key(i + lane) : 0u;
+      const unsigned same = __ballot_sync(0xffffffffu, there && k == prefix);
+      const bool keep = there && (k > prefix || (k == prefix && eq + __popc(same & ((1u << lane) - 1)) < left));
       eq += __popc(same);
       const unsigned stay = __ballot_sync(0xffffffffu, keep);
-      const unsigned low = __ballot_sync(0xffffffffu, i + lane < w1 && i0 + i + lane < b);
-      const unsigned there = __ballot_sync(0xffffffffu, i + lane < w1);
+      const unsigned low = __ballot_sync(0xffffffffu, there && i0 + i + lane < b);
       cnt.x += __popc(low & ~stay);
-      cnt.y += __popc(there & ~low & stay);
+      cnt.y += __popc(~low & stay);
       if (lane == 0) kept_bits[i >> 5] = stay;
     }
-    __syncwarp();
-    int2 at = scan_warps(sh, cl, ranks, cnt, &tot);
+    __syncthreads();                         // sh.warps is free again
+    int2 at = scan_warps(sh, cnt, &tot);
+    if (tid == 0) sh.total = tot;
+    meet(cl, ranks);
+    if (ranks > 1) {
+      int2 p[kRanks];
+#pragma unroll
+      for (int r = 0; r < kRanks; ++r) p[r] = r < ranks ? *cl.map_shared_rank(&sh.total, r) : make_int2(0, 0);
+      tot = make_int2(0, 0);
+#pragma unroll
+      for (int r = 0; r < kRanks; ++r) {
+        if (r < (int)cl.block_rank()) { at.x += p[r].x; at.y += p[r].y; }
+        tot.x += p[r].x;
+        tot.y += p[r].y;
+      }
+    }
     for (int i = w0; i < w1; i += 32) {
       const unsigned stay = kept_bits[i >> 5];
       const int row = i0 + i + lane;
       const bool there = i + lane < w1, keep = (stay >> lane) & 1u;
-      const unsigned holes = __ballot_sync(0xffffffffu, there && row < b && !keep);
-      const unsigned late = __ballot_sync(0xffffffffu, there && row >= b && keep);
+      const bool hole = there && row < b && !keep, late = there && row >= b && keep;
+      const unsigned holes = __ballot_sync(0xffffffffu, hole), lates = __ballot_sync(0xffffffffu, late);
       const unsigned below = (1u << lane) - 1;
-      const int hj = at.x + __popc(holes & below), lj = at.y + __popc(late & below);
-      if ((holes >> lane) & 1u) { if (hj < a.max_moves) list[1 + hj] = row; }
-      if ((late >> lane) & 1u) { if (lj < a.max_moves) list[1 + a.max_moves + lj] = row; }
+      if (hole || late) {
+        // its place in the pool, so that the move need not look it up
+        const int j = hole ? at.x + __popc(holes & below) : a.max_moves + at.y + __popc(lates & below);
+        if (j < (hole ? a.max_moves : 2 * a.max_moves)) list[1 + j] = (int)paged_row(c, s, h, row);
+      }
       at.x += __popc(holes);
-      at.y += __popc(late);
+      at.y += __popc(lates);
     }
     if (tid == 0 && cl.block_rank() == 0) list[0] = min(tot.x, a.max_moves);
   } else if (tid == 0 && cl.block_rank() == 0) {
     list[0] = 0;
   }
-  if (copies) {
-    // position and weight of the rows that stay where they are
-    for (int i = w0; i < w1; i += 32) {
-      const int row = i0 + i + lane;
-      const unsigned stay = n > b ? kept_bits[i >> 5] : 0xffffffffu;
-      if (i + lane < w1 && row < b && ((stay >> lane) & 1u)) {
-        const long long at = paged_row(c, s, h, row);
-        if (at >= 0) {
-          if (a.weight_out != a.weight) a.weight_out[at] = a.weight[at];
-          if (a.pos_out != c.pos) a.pos_out[at] = c.pos[at];
-        }
-      }
+  if ((new_w || new_p) && !(n > b && held)) {
+    for (int i = tid * 4; i < m && i0 + i < keep_n; i += kThreads * 4) {
+      const long long row = paged_row(c, s, h, i0 + i);
+      if (row >= 0) copy4(row, i0 + i, *reinterpret_cast<const float4*>(a.weight + row), *reinterpret_cast<const int4*>(c.pos + row));
     }
   }
+  if (ranks > 1) cl.sync();                  // no CTA leaves while another reads its totals
 }
 
-// A warp to kMovesPerWarp moves: their places looked up side by side, their K
-// and V rows requested together, 16 bytes to a lane. Bound by the bytes moved.
+// A warp to kMovesPerWarp moves: their K and V rows requested together, 16
+// bytes to a lane. Bound by the bytes moved.
 template <int ES>
-__global__ void __launch_bounds__(256) paged_move_kernel(PagedEvictArgs a) {
+__global__ void __launch_bounds__(256, 3) paged_move_kernel(PagedEvictArgs a) {
   constexpr int kM = kMovesPerWarp;
   pdl_enter();
   const PagedView& c = a.c;
@@ -250,22 +275,26 @@ __global__ void __launch_bounds__(256) paged_move_kernel(PagedEvictArgs a) {
     const int n = paged_length(c, s);
     a.length_out[s] = n < a.budget ? n : a.budget;
   }
-  for (int j0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kM; j0 < count; j0 += gridDim.x * 8 * kM) {
-    long long to = -1, of = -1;
-    if (lane < kM && j0 + lane < count) {
-      to = paged_row(c, s, h, list[1 + j0 + lane]);
-      of = paged_row(c, s, h, list[1 + a.max_moves + j0 + lane]);
-      if (of < 0) to = -1;
-      if (to >= 0) {
-        a.weight_out[to] = a.weight[of];
-        a.pos_out[to] = c.pos[of];
-      }
+  const int stride = gridDim.x * 8 * kM;
+  int j0 = (blockIdx.x * 8 + (threadIdx.x >> 5)) * kM;
+  int to = -1, of = -1;
+  if (lane < kM && j0 + lane < count) {
+    to = list[1 + j0 + lane];
+    of = list[1 + a.max_moves + j0 + lane];
+  }
+  for (; j0 < count; j0 += stride) {
+    if (of < 0) to = -1;                     // a row on no page
+    const int my_to = to, my_of = of;
+    to = of = -1;
+    if (lane < kM && j0 + stride + lane < count) {
+      to = list[1 + j0 + stride + lane];
+      of = list[1 + a.max_moves + j0 + stride + lane];
     }
-    long long t[kM], f[kM];
+    int t[kM], f[kM];
 #pragma unroll
     for (int u = 0; u < kM; ++u) {
-      t[u] = __shfl_sync(0xffffffffu, to, u);
-      f[u] = __shfl_sync(0xffffffffu, of, u);
+      t[u] = __shfl_sync(0xffffffffu, my_to, u);
+      f[u] = __shfl_sync(0xffffffffu, my_of, u);
     }
     for (int i = lane * 16; i < 2 * bytes; i += 512) {
       char* base = static_cast<char*>(i < bytes ? c.k : c.v);
@@ -273,10 +302,14 @@ __global__ void __launch_bounds__(256) paged_move_kernel(PagedEvictArgs a) {
       uint4 x[kM];
 #pragma unroll
       for (int u = 0; u < kM; ++u)
-        if (t[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(base + f[u] * bytes + o);
+        if (t[u] >= 0) x[u] = *reinterpret_cast<const uint4*>(base + (long long)f[u] * bytes + o);
 #pragma unroll
       for (int u = 0; u < kM; ++u)
-        if (t[u] >= 0) *reinterpret_cast<uint4*>(base + t[u] * bytes + o) = x[u];
+        if (t[u] >= 0) *reinterpret_cast<uint4*>(base + (long long)t[u] * bytes + o) = x[u];
+    }
+    if (my_to >= 0) {
+      a.weight_out[my_to] = a.weight[my_of];
+      a.pos_out[my_to] = c.pos[my_of];
     }
   }
 }
@@ -286,12 +319,12 @@ __global__ void __launch_bounds__(256) paged_move_kernel(PagedEvictArgs a) {
 cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t st) {
   const int cap = a.c.max_pages << a.c.lg_rows, pairs = a.c.nkv * a.c.n_seq;
   // CTAs to a (sequence, kv head): more where a CTA would have more than 4096
-  // rows and SMs would be idle, and so that the masks fit
+  // rows and SMs (two CTAs to each) would be idle, and so that the masks fit
   int ranks = 1;
-  while (ranks < 8 && (cap / ranks > 131072 || (cap / ranks > 4096 && (long long)pairs * ranks * 2 <= 304))) ranks *= 2;
+  while (ranks < kRanks && (cap / ranks > kMostRows || (cap / ranks > 4096 && (long long)pairs * ranks * 2 <= 304))) ranks *= 2;
   const int per = (cap + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;
   const size_t smem = ((size_t)(per < kHeld ? per : kHeld) + per / 32) * 4;
-  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kHeld + 131072 / 32) * 4);
+  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kHeld + kMostRows / 32) * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ranks, a.c.nkv, a.c.n_seq);
@@ -309,8 +342,10 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t 
   cfg.numAttrs = 2;
   e = cudaLaunchKernelEx(&cfg, paged_select_kernel, a, ranks);
   if (e != cudaSuccess) return e;
+  // CTAs for every move there may be, at most what 152 SMs hold twice over
   int x = (a.max_moves + 8 * kMovesPerWarp - 1) / (8 * kMovesPerWarp);
-  if (x > 512) x = 512;
+  const int most = (152 * 6 + pairs - 1) / pairs;
+  if (x > most) x = most;
   if (x < 1) x = 1;
   const dim3 grid(x, a.c.nkv, a.c.n_seq);
   return dtype ? launch_pdl(paged_move_kernel<2>, grid, dim3(256), 0, st, a)

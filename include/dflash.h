@@ -709,9 +709,6 @@ typedef struct dflash_paged_attention_args {
   const int32_t* prefix;    /* [n_seq] or NULL */
   void* out;                /* [rows][n_q_heads][head_dim] dense (not read or written by key_weight) */
   float* lse;               /* [rows][n_q_heads]; NULL: not wanted (attention) */
-  void* workspace;          /* dflash_paged_attention_workspace bytes; calls that may overlap
-                               need workspaces of their own */
-  int64_t workspace_bytes;
   int64_t q_stride;         /* a multiple of 8, at least n_q_heads * head_dim */
   int32_t rows;             /* rows * n_q_heads < 2^31 */
   int32_t n_q_heads;        /* a multiple of kv_heads, at most 128 * kv_heads */
@@ -721,6 +718,10 @@ typedef struct dflash_paged_attention_args {
                                work is split, longer sequences stay right */
   float scale;              /* > 0 */
   float softcap;            /* >= 0 */
+  int32_t reserved;         /* 0 */
+  void* workspace;          /* dflash_paged_attention_workspace bytes; calls that may overlap
+                               need workspaces of their own */
+  int64_t workspace_bytes;
 } dflash_paged_attention_args;
 /* Bytes of workspace (0 for most large calls) an attention call needs; the
  * same for every content of the device arrays. */
@@ -753,10 +754,11 @@ typedef struct dflash_paged_evict_args {
   float* weight_out;
   int32_t* pos_out;
   int32_t* length_out;      /* [n_seq] */
-  void* workspace;          /* dflash_paged_evict_workspace bytes */
-  int64_t workspace_bytes;
   int32_t budget;           /* >= 1 */
   int32_t recent;           /* >= 0 */
+  void* workspace;          /* dflash_paged_evict_workspace bytes; calls that may overlap need
+                               workspaces of their own */
+  int64_t workspace_bytes;
 } dflash_paged_evict_args;
 int dflash_paged_evict_workspace(const dflash_paged_cache* cache, const dflash_paged_evict_args* args,
                                  int64_t* bytes_host);

@@ -115,7 +115,7 @@ def refused(B, call, args):
     binding's own refusal of them is left out where there is no GPU that a launch could run on."""
     with pytest.MonkeyPatch.context() as m:
         if not torch.cuda.is_available():
-            m.setattr(B.PagedCache, "_launch", lambda self, c, stream: self._check(c(None)))
+            m.setattr(B.PagedCache, "_launch", lambda self, call, stream, *args: self._check(call(self._c, *args, None)))
         with pytest.raises(B.DFlashError) as e:
             call(**args)
     assert e.value.code in (B.EINVAL, B.ERANGE) and str(e.value)
@@ -185,6 +185,40 @@ def test_evict_refuses(B, cache, over):
 def test_cache_refuses(B, over):
     with pytest.raises(B.DFlashError):
         B.PagedCache.allocate(**{**dict(n_pages=1, page_rows=16, kv_heads=1, head_dim=64, n_seq=1, max_pages=1), **over}, device="cpu")
+
+
+def test_structs_are_the_header_s(B, tmp_path):
+    """The packed layouts against the C compiler's."""
+    import shutil
+    import subprocess
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc:
+        pytest.skip("no C compiler")
+    fields = {"dflash_paged_cache": "k v pos table length status n_pages page_rows kv_heads head_dim n_seq max_pages dtype",
+              "dflash_paged_append_args": "q k v row_pos start rope_pos pair_axis_host q_norm k_norm q_out weight q_stride k_stride v_stride rows "
+                                          "n_q_heads n_axes rot_pairs rope_neox rope_theta rms_eps",
+              "dflash_paged_attention_args": "q q_pos start slopes prefix out lse q_stride rows n_q_heads causal window max_len scale softcap reserved "
+                                             "workspace workspace_bytes",
+              "dflash_paged_evict_args": "weight next_pos weight_out pos_out length_out budget recent workspace workspace_bytes"}
+    src = "#include <stdio.h>\n#include <stddef.h>\n#include \"dflash.h\"\nint main(void) {\n"
+    for t, names in fields.items():
+        src += "".join(f'printf("%zu ", offsetof({t}, {n}));' for n in names.split()) + f'printf("%zu\\n", sizeof({t}));\n'
+    (tmp_path / "o.c").write_text(src + "return 0; }\n")
+    from conftest import ROOT
+    subprocess.run([cc, "-I", f"{ROOT}/include", str(tmp_path / "o.c"), "-o", str(tmp_path / "o")], check=True)
+    got = [[int(x) for x in line.split()] for line in subprocess.run([str(tmp_path / "o")], capture_output=True, text=True, check=True).stdout.splitlines()]
+
+    def layout(*formats):
+        at, out = 0, []
+        for f in formats:
+            for n, kind in __import__("re").findall(r"(\d*)([a-zA-Z])", f.format.lstrip("=")):
+                for _ in range(int(n or 1)):
+                    if kind != "x":
+                        out.append(at)
+                    at += {"Q": 8, "q": 8, "i": 4, "f": 4, "x": 1}[kind]
+        return out + [at]
+
+    assert got == [layout(B._PAGED_CACHE), layout(B._PAGED_APPEND), layout(B._PAGED_ATTENTION, B._PAGED_WORKSPACE), layout(B._PAGED_EVICT, B._PAGED_WORKSPACE)]
 
 
 def test_c_calls_refuse_null(B):
