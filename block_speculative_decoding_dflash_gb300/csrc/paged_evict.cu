@@ -67,13 +67,11 @@ __device__ __forceinline__ int2 scan_warps(Shared& sh, int2 v, int2* tot) {
 
 // A cluster to a (sequence, kv head), a contiguous slice of its rows to a CTA.
 // Keys are read once and held in shared memory where a slice fits (otherwise
-// each pass reads them again, from L2). A warp takes contiguous rows, 32 at a
-// time, so that ranks are ballots; the kept rows of each 32 are a word in
-// shared memory after the first of the ranking passes. Bound by the latency of
-// its dozen dependent steps for a few thousand rows, by one SM's read of the
-// weights and positions beyond.
+// each pass reads them again, from L2). The ranking works on words of 32 rows,
+// one to a thread. Bound by the latency of its dozen dependent steps for a few
+// thousand rows, by one SM's passes over the keys beyond.
 __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArgs a, int ranks) {
-  extern __shared__ unsigned dyn[];          // [held] keys, then the masks of kept rows
+  extern __shared__ __align__(16) unsigned dyn[];   // keys (where held), then four words to 32 rows
   __shared__ Shared sh;
   pdl_enter();
   cg::cluster_group cl = cg::this_cluster();
@@ -87,8 +85,12 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
   const int per = (n + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;
   const int i0 = min(n, (int)cl.block_rank() * per), i1 = min(n, i0 + per), m = i1 - i0;
   const bool held = per <= kHeld;
+  // a word of 32 rows: its kept rows, its rows of the bordering key, and the
+  // number of holes and late rows before it
   unsigned* keys = dyn;
-  unsigned* kept_bits = dyn + (held ? per : 0);
+  unsigned* keep_bits = dyn + (held ? per : 0);
+  unsigned* same_bits = keep_bits + per / 32;
+  int2* offs = reinterpret_cast<int2*>(same_bits + per / 32);
   // Position and weight of a remaining row go to the outputs as they are read;
   // a hole gets its new row's in the move, which comes after.
   const bool new_w = a.weight_out != a.weight, new_p = a.pos_out != c.pos;
@@ -113,26 +115,52 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
     const long long row = paged_row(c, s, h, i0 + i);
     return row < 0 ? 0u : weight_key(a.weight[row], c.pos[row] >= guard);
   };
-  auto key = [&](int i) -> unsigned { return held ? keys[i] : fetch(i); };
+  // keys of rows i .. i + 3 (i a multiple of 4); past the end 0, the lowest
+  auto key4 = [&](int i, unsigned* k) {
+    if (held) {
+      const uint4 v = i < m ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0, 0, 0, 0);
+      k[0] = v.x; k[1] = v.y; k[2] = v.z; k[3] = v.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) k[j] = i + j < m ? fetch(i + j) : 0u;
+    }
+  };
 
   unsigned prefix = 0;                       // the key of rank b: its known top bits
   int left = b;                              // rows still to take among those with that prefix
   if (n > b) {
     if (held) {
-      // four rows to a thread: a page holds a multiple of 8
-#pragma unroll 2
-      for (int i = tid * 4; i < m; i += kThreads * 4) {
-        const long long row = paged_row(c, s, h, i0 + i);
-        uint4 k = make_uint4(0, 0, 0, 0);
-        if (row >= 0) {
-          const float4 w = *reinterpret_cast<const float4*>(a.weight + row);
-          const int4 p = *reinterpret_cast<const int4*>(c.pos + row);
-          copy4(row, i0 + i, w, p);
-          k = make_uint4(weight_key(w.x, p.x >= guard), weight_key(w.y, p.y >= guard), weight_key(w.z, p.z >= guard), weight_key(w.w, p.w >= guard));
-        } else if (c.status) {
-          atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+      // four rows to a thread (a page holds a multiple of 8), kU times at once
+      constexpr int kU = 4;
+      for (int b4 = tid * 4; b4 < m; b4 += kThreads * 4 * kU) {
+        long long row[kU];
+        float4 w[kU];
+        int4 p[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = b4 + u * kThreads * 4;
+          row[u] = i < m ? paged_row(c, s, h, i0 + i) : -1;
         }
-        *reinterpret_cast<uint4*>(keys + i) = k;
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+          if (row[u] >= 0) {
+            w[u] = *reinterpret_cast<const float4*>(a.weight + row[u]);
+            p[u] = *reinterpret_cast<const int4*>(c.pos + row[u]);
+          }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          const int i = b4 + u * kThreads * 4;
+          if (i >= m) break;
+          uint4 k = make_uint4(0, 0, 0, 0);
+          if (row[u] >= 0) {
+            copy4(row[u], i0 + i, w[u], p[u]);
+            k = make_uint4(weight_key(w[u].x, p[u].x >= guard), weight_key(w[u].y, p[u].y >= guard),
+                           weight_key(w[u].z, p[u].z >= guard), weight_key(w[u].w, p[u].w >= guard));
+          } else if (c.status) {
+            atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+          }
+          *reinterpret_cast<uint4*>(keys + i) = k;
+        }
       }
     }
 #pragma unroll 1
@@ -141,16 +169,24 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
       int* hist = sh.hist[d & 1];
       for (int i = tid; i < kBins; i += kThreads) hist[i] = 0;
       __syncthreads();
-      for (int i = tid; i < (m + 31) / 32 * 32; i += kThreads) {
-        const unsigned k = i < m ? key(i) : 0u;
-        const bool in = i < m && (d == 0 || (k >> top) == (prefix >> top));
-        const unsigned dig = in ? (k >> shift) & mask : 0xffffffffu;
+      for (int i = tid * 4; i - lane * 4 < m; i += kThreads * 4) {
+        unsigned k[4], dig[4];
+        key4(i, k);
+        bool same = true;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool in = i + j < m && (d == 0 || (k[j] >> top) == (prefix >> top));
+          dig[j] = in ? (k[j] >> shift) & mask : 0xffffffffu;
+          same = same && dig[j] == dig[0];
+        }
         // equal weights are common (rows that nobody looked at): one add for a warp of them
-        const unsigned one = __shfl_sync(0xffffffffu, dig, 0);
-        if (__all_sync(0xffffffffu, dig == one)) {
-          if (lane == 0 && in) atomicAdd(&hist[dig], 32);
-        } else if (in) {
-          atomicAdd(&hist[dig], 1);
+        const unsigned one = __shfl_sync(0xffffffffu, dig[0], 0);
+        if (__all_sync(0xffffffffu, same && dig[0] == one)) {
+          if (lane == 0 && one != 0xffffffffu) atomicAdd(&hist[one], 128);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (dig[j] != 0xffffffffu) atomicAdd(&hist[dig[j]], 1);
         }
       }
       meet(cl, ranks);
@@ -198,57 +234,100 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
   }
   // `prefix` is now the key of rank b: greater keys stay, of the equal ones
   // the first `left`
-  const int share = per / kWarps, w0 = warp * share, w1 = min(m, w0 + share);
   if (n > b) {
-    int eq = 0;
-    for (int i = w0; i < w1; i += 32) eq += __popc(__ballot_sync(0xffffffffu, i + lane < w1 && key(i + lane) == prefix));
-    int2 tot;
-    eq = sh.eq_before + scan_warps(sh, make_int2(eq, 0), &tot).x;
-    int2 cnt = make_int2(0, 0);              // holes below row b, kept rows from it on
-    for (int i = w0; i < w1; i += 32) {
-      const bool there = i + lane < w1;
-      const unsigned k = there ? key(i + lane) : 0u;
-      const unsigned same = __ballot_sync(0xffffffffu, there && k == prefix);
-      const bool keep = there && (k > prefix || (k == prefix && eq + __popc(same & ((1u << lane) - 1)) < left));
-      eq += __popc(same);
-      const unsigned stay = __ballot_sync(0xffffffffu, keep);
-      const unsigned low = __ballot_sync(0xffffffffu, there && i0 + i + lane < b);
-      cnt.x += __popc(low & ~stay);
-      cnt.y += __popc(~low & stay);
-      if (lane == 0) kept_bits[i >> 5] = stay;
+    // a bit to a row: greater and equal keys, 128 rows to a warp at a time
+    // (lane l's four rows are bits 4 (l mod 8) .. of word l / 8)
+    const int words = (m + 31) >> 5;
+    for (int i = tid * 4; i - lane * 4 < m; i += kThreads * 4) {
+      unsigned k[4], gt = 0, eq = 0;
+      key4(i, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        gt |= (unsigned)(i + j < m && k[j] > prefix) << j;
+        eq |= (unsigned)(i + j < m && k[j] == prefix) << j;
+      }
+      gt <<= 4 * (lane & 7);
+      eq <<= 4 * (lane & 7);
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) {
+        gt |= __shfl_xor_sync(0xffffffffu, gt, o);
+        eq |= __shfl_xor_sync(0xffffffffu, eq, o);
+      }
+      if ((lane & 7) == 0 && i < m) {
+        keep_bits[i >> 5] = gt;
+        same_bits[i >> 5] = eq;
+      }
     }
-    __syncthreads();                         // sh.warps is free again
-    int2 at = scan_warps(sh, cnt, &tot);
-    if (tid == 0) sh.total = tot;
+    __syncthreads();
+    // words in order, one to a thread: which equal rows stay, and the number of
+    // holes below row b and of kept rows from it on
+    int eq_run = sh.eq_before;
+    int2 run = make_int2(0, 0), tot;
+    for (int x0 = 0; x0 < words; x0 += kThreads) {
+      const int x = x0 + tid;
+      const unsigned gt = x < words ? keep_bits[x] : 0u, eq = x < words ? same_bits[x] : 0u;
+      int incl = __popc(eq);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += y;
+      }
+      int before = eq_run + scan_warps(sh, make_int2(__shfl_sync(0xffffffffu, incl, 31), 0), &tot).x + incl - __popc(eq);
+      eq_run += tot.x;
+      unsigned take = eq;
+      for (int over = before + __popc(eq) - left; over > 0 && take; --over) take &= ~(0x80000000u >> __clz(take));
+      const unsigned stay = gt | take;
+      const int r0 = i0 + x * 32;                        // rows below b: the low bits
+      const unsigned there = x < words ? (m - x * 32 >= 32 ? 0xffffffffu : (1u << (m - x * 32)) - 1) : 0u;
+      const unsigned low = b - r0 >= 32 ? 0xffffffffu : (b > r0 ? (1u << (b - r0)) - 1 : 0u);
+      const int2 cnt = make_int2(__popc(there & low & ~stay), __popc(there & ~low & stay));
+      int2 in = cnt;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, in.x, o), v = __shfl_up_sync(0xffffffffu, in.y, o);
+        if (lane >= o) { in.x += u; in.y += v; }
+      }
+      __syncthreads();                                   // sh.warps is free again
+      const int2 at = scan_warps(sh, make_int2(__shfl_sync(0xffffffffu, in.x, 31), __shfl_sync(0xffffffffu, in.y, 31)), &tot);
+      if (x < words) {
+        // a word has holes or late rows but for the one that row b - 1 lies in
+        keep_bits[x] = stay;
+        offs[x] = make_int2(run.x + at.x + in.x - cnt.x, run.y + at.y + in.y - cnt.y);
+      }
+      run.x += tot.x;
+      run.y += tot.y;
+      __syncthreads();
+    }
+    if (tid == 0) sh.total = run;
     meet(cl, ranks);
+    int2 base = make_int2(0, 0), sum = run;
     if (ranks > 1) {
       int2 p[kRanks];
 #pragma unroll
       for (int r = 0; r < kRanks; ++r) p[r] = r < ranks ? *cl.map_shared_rank(&sh.total, r) : make_int2(0, 0);
-      tot = make_int2(0, 0);
+      sum = make_int2(0, 0);
 #pragma unroll
       for (int r = 0; r < kRanks; ++r) {
-        if (r < (int)cl.block_rank()) { at.x += p[r].x; at.y += p[r].y; }
-        tot.x += p[r].x;
-        tot.y += p[r].y;
+        if (r < (int)cl.block_rank()) { base.x += p[r].x; base.y += p[r].y; }
+        sum.x += p[r].x;
+        sum.y += p[r].y;
       }
     }
-    for (int i = w0; i < w1; i += 32) {
-      const unsigned stay = kept_bits[i >> 5];
-      const int row = i0 + i + lane;
-      const bool there = i + lane < w1, keep = (stay >> lane) & 1u;
-      const bool hole = there && row < b && !keep, late = there && row >= b && keep;
-      const unsigned holes = __ballot_sync(0xffffffffu, hole), lates = __ballot_sync(0xffffffffu, late);
-      const unsigned below = (1u << lane) - 1;
+#pragma unroll 4
+    for (int x = warp; x < words; x += kWarps) {
+      const unsigned stay = keep_bits[x];
+      const int2 at = offs[x];
+      const int i = x * 32 + lane, row = i0 + i;
+      const unsigned low = b - i0 - x * 32 >= 32 ? 0xffffffffu : (b > i0 + x * 32 ? (1u << (b - i0 - x * 32)) - 1 : 0u);
+      const bool keep = (stay >> lane) & 1u, hole = i < m && row < b && !keep, late = i < m && row >= b && keep;
       if (hole || late) {
         // its place in the pool, so that the move need not look it up
-        const int j = hole ? at.x + __popc(holes & below) : a.max_moves + at.y + __popc(lates & below);
-        if (j < (hole ? a.max_moves : 2 * a.max_moves)) list[1 + j] = (int)paged_row(c, s, h, row);
+        const unsigned below = (1u << lane) - 1;
+        const int j = hole ? base.x + at.x + __popc(~stay & low & below) : base.y + at.y + __popc(stay & ~low & below);
+        if (j < a.max_moves) list[1 + (hole ? 0 : a.max_moves) + j] = (int)paged_row(c, s, h, row);
       }
-      at.x += __popc(holes);
-      at.y += __popc(lates);
     }
-    if (tid == 0 && cl.block_rank() == 0) list[0] = min(tot.x, a.max_moves);
+    if (tid == 0 && cl.block_rank() == 0) list[0] = min(sum.x, a.max_moves);
   } else if (tid == 0 && cl.block_rank() == 0) {
     list[0] = 0;
   }
@@ -323,8 +402,8 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t 
   int ranks = 1;
   while (ranks < kRanks && (cap / ranks > kMostRows || (cap / ranks > 4096 && (long long)pairs * ranks * 2 <= 304))) ranks *= 2;
   const int per = (cap + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;
-  const size_t smem = ((size_t)(per < kHeld ? per : kHeld) + per / 32) * 4;
-  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kHeld + kMostRows / 32) * 4);
+  const size_t smem = ((size_t)(per < kHeld ? per : kHeld) + per / 8) * 4;
+  cudaError_t e = cudaFuncSetAttribute(paged_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (kHeld + kMostRows / 8) * 4);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ranks, a.c.nkv, a.c.n_seq);
