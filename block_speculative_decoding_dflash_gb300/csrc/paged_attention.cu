@@ -393,12 +393,6 @@ cudaError_t run_simt(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_attn_simt_kernel<T, BM, TM, HDP>, grid, dim3(BM / TM * 16), simt_smem<BM, HDP>(), st, a);
 }
-template <typename T, int BM, int TM>
-cudaError_t run_simt_hd(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  if (a.c.hd <= 64) return run_simt<T, BM, TM, 64>(a, grid, st);
-  if (a.c.hd <= 128) return run_simt<T, BM, TM, 128>(a, grid, st);
-  return run_simt<T, BM, TM, 256>(a, grid, st);
-}
 template <typename T, int HDP>
 cudaError_t run_weight(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
   cudaError_t e = big_smem(paged_weight_simt_kernel<T, HDP>, weight_smem<HDP>());
@@ -417,22 +411,23 @@ long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
 
 }  // namespace
 
-// kind 0, 1: CUDA cores, tiles of 16 or 64 packed query rows; 2, 3: tensor
-// cores, one or two tiles of 128.
+// kind 1 and 2: tensor cores (bf16, head_dim <= 128), that many tiles of 128
+// packed query rows to a CTA; 16, 32, 64: CUDA cores, that many rows.
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
   PagedPlan p{0, 1, 0, 0};
-  const long long len = expected_len(a);
+  const long long len = expected_len(a), units = (long long)a.rows * a.G;
   long long fill, least;
   if (dtype && a.c.hd <= 128) {
     const int per = 128 / a.G;
-    p.kind = a.rows > (long long)per * a.c.n_seq ? 3 : 2;
-    p.tiles = tile_bound(a.rows, p.kind == 3 ? 2 * per : per, a);
+    p.kind = a.rows > (long long)per * a.c.n_seq ? 2 : 1;
+    p.tiles = tile_bound(a.rows, p.kind * per, a);
     fill = 152;
     least = 512;
   } else {
-    p.kind = (long long)a.rows * a.G > 24ll * a.c.n_seq ? 1 : 0;
-    p.tiles = tile_bound((long long)a.rows * a.G, p.kind ? 64 : 16, a);
-    fill = 304;
+    // the smallest tile that holds an average sequence's rows
+    p.kind = units <= 16ll * a.c.n_seq ? 16 : (units <= 32ll * a.c.n_seq && !dtype ? 32 : 64);
+    p.tiles = tile_bound(units, p.kind, a);
+    fill = 608;
     least = 256;
   }
   // as many splits as fill the SMs, of at least `least` keys each
@@ -446,9 +441,10 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
   const dim3 grid((unsigned)p.tiles, a.c.nkv, p.splits);
   cudaError_t e;
-  if (p.kind >= 2) e = launch_paged_attention_tc(a, p.kind - 1, p.tiles, st);
-  else if (p.kind == 0) e = dtype ? run_simt_hd<bf16, 16, 2>(a, grid, st) : run_simt_hd<float, 16, 2>(a, grid, st);
-  else e = dtype ? run_simt_hd<bf16, 64, 4>(a, grid, st) : run_simt_hd<float, 64, 4>(a, grid, st);
+  if (p.kind <= 2) e = launch_paged_attention_tc(a, p.kind, p.tiles, st);
+  else if (!dtype) e = launch_paged_attention_f32(a, p.kind, p.tiles, st);
+  else if (p.kind == 16) e = run_simt<bf16, 16, 2, 256>(a, grid, st);
+  else e = run_simt<bf16, 64, 4, 256>(a, grid, st);
   if (e != cudaSuccess || p.splits <= 1) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
   return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)
