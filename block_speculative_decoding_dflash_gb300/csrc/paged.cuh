@@ -64,12 +64,37 @@ __device__ __forceinline__ PagedTile paged_find_tile(const int* start, int n_seq
   return r;
 }
 
-// The mask of the header: whether a query at pq sees a row at pk.
+// The mask of the header. What one query at pq sees is a range of positions
+// and the prefix: two unsigned comparisons, both false for kPagedNoPos.
 struct PagedMask { int causal, window, prefix; };
-__device__ __forceinline__ bool paged_sees(const PagedMask& m, int pq, int pk) {
-  const int d = pq - pk;
-  const bool in = (!m.causal || d >= 0) && (m.window <= 0 || abs(d) <= m.window);
-  return pk != kPagedNoPos && (in || pk < m.prefix);
+struct PagedSees { int lo; unsigned span, prefix; };
+__device__ __forceinline__ PagedMask paged_mask(int causal, int window, const int* prefix, int seq) {
+  const int p = prefix ? prefix[seq] : 0;
+  return PagedMask{causal, window, p > 0 ? p : 0};
+}
+__device__ __forceinline__ PagedSees paged_sees_of(const PagedMask& m, int pq) {
+  long long lo = INT32_MIN + 1, hi = m.causal ? pq : INT32_MAX;
+  if (m.window > 0) {
+    if ((long long)pq - m.window > lo) lo = (long long)pq - m.window;
+    if (!m.causal && (long long)pq + m.window < hi) hi = (long long)pq + m.window;
+  }
+  // (pq = INT32_MIN with a causal mask sees nothing; a range is never empty, so
+  // its own end, kPagedNoPos, stands for that)
+  if (hi < lo) return PagedSees{(int)hi, 0u, (unsigned)m.prefix};
+  return PagedSees{(int)lo, (unsigned)(hi - lo), (unsigned)m.prefix};
+}
+__device__ __forceinline__ bool paged_sees(const PagedSees& s, int pk) {
+  return (unsigned)pk - (unsigned)s.lo <= s.span || (unsigned)pk < s.prefix;
+}
+// The other way about: the positions of the queries that see a row at pk.
+__device__ __forceinline__ PagedSees paged_seen_by(const PagedMask& m, int pk) {
+  long long lo = m.causal ? pk : INT32_MIN + 1, hi = INT32_MAX;
+  if (m.window > 0) {
+    if (!m.causal && (long long)pk - m.window > lo) lo = (long long)pk - m.window;
+    if ((long long)pk + m.window < hi) hi = (long long)pk + m.window;
+  }
+  if ((unsigned)pk < (unsigned)m.prefix) { lo = INT32_MIN + 1; hi = INT32_MAX; }
+  return PagedSees{(int)lo, (unsigned)(hi - lo), 0u};
 }
 // Queries at [qmin, qmax], rows at [kmin, kmax] (kmin > kmax: none are there):
 // 0 no query sees any row, 2 every query sees every row (of a tile whose rows
@@ -98,27 +123,31 @@ __device__ __forceinline__ void paged_classify(const PagedView& c, int s, int h,
   for (int i = threadIdx.x; i <= (t1 - t0) >> 5; i += blockDim.x) some[i] = all[i] = 0u;
   __syncthreads();
   for (int b = t0 + warp * kU; b < t1; b += nw * kU) {
-    int p[kU][kPer];
+    // loads without branches, so that they are in flight together: what is not
+    // there reads row 0 of its page or of the pool
+    int p[kU][kPer], page[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int slot = (b + u) * KEYS + lane * kPer;
-      const long long row = (b + u < t1 && slot < len) ? paged_row(c, s, h, slot) : -1;
+      page[u] = c.table[(size_t)s * c.max_pages + (slot < len ? slot >> c.lg_rows : 0)];
+    }
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) p[u][j] = kPagedNoPos;
-      if (row >= 0) {
-        if (kPer == 4) {
-          const int4 x = *reinterpret_cast<const int4*>(c.pos + row);
-          p[u][0] = x.x; p[u][1] = x.y; p[u][kPer - 2] = x.z; p[u][kPer - 1] = x.w;
-        } else {
-          const int2 x = *reinterpret_cast<const int2*>(c.pos + row);
-          p[u][0] = x.x; p[u][1] = x.y;
-        }
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (slot + j >= len) p[u][j] = kPagedNoPos;
-      } else if (b + u < t1 && slot < len && c.status) {
-        atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+    for (int u = 0; u < kU; ++u) {
+      const int slot = (b + u) * KEYS + lane * kPer;
+      const bool on = (unsigned)page[u] < (unsigned)c.n_pages;
+      const long long row = (((long long)(on ? page[u] : 0) * c.nkv + h) << c.lg_rows) + (slot & ((1 << c.lg_rows) - 1));
+      if (kPer == 4) {
+        const int4 x = *reinterpret_cast<const int4*>(c.pos + row);
+        p[u][0] = x.x; p[u][1] = x.y; p[u][kPer - 2] = x.z; p[u][kPer - 1] = x.w;
+      } else {
+        const int2 x = *reinterpret_cast<const int2*>(c.pos + row);
+        p[u][0] = x.x; p[u][1] = x.y;
       }
+      const bool in = b + u < t1;
+      if (in && slot < len && !on && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (!in || !on || slot + j >= len) p[u][j] = kPagedNoPos;
     }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {

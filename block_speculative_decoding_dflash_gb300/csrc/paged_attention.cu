@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttn
   const PagedTile t = st;
   if (t.seq < 0) return;
   const int len = paged_length(c, t.seq);
-  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[t.seq] : INT32_MIN};
+  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
   paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
 
@@ -103,11 +103,13 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttn
   }
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   int pq[TM];
+  PagedSees sees[TM];
   float slope2[TM], mx[TM], sum[TM], o[TM][NJ * 4];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int r = r0 + min(ty * TM + i, rows - 1);
     pq[i] = a.q_pos[t.first + r / G];
+    sees[i] = paged_sees_of(m, pq[i]);
     slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
     mx[i] = -INFINITY;
     sum[i] = 0.f;
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttn
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int pk = spos[tx + 16 * j];
-        const bool v = full || paged_sees(m, pq[i], pk);
+        const bool v = full || paged_sees(sees[i], pk);
         s[i][j] = v ? paged_score(a, ps, s[i][j], slope2[i], pq[i], pk) : -INFINITY;
         seen |= (unsigned)v << j;
         top = fmaxf(top, s[i][j]);
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(256) paged_weight_simt_kernel(PagedAttnArgs a)
   const int h = blockIdx.y, s = blockIdx.z, G = a.G;
   const int2 ab = paged_new_rows(a.start, s, a.rows);
   const int len = paged_length(c, s), R = (ab.y - ab.x) * G;
-  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[s] : INT32_MIN};
+  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, s);
   const PagedScore ps = paged_score_of(a);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   for (int k0 = blockIdx.x * kBN; k0 < len; k0 += gridDim.x * kBN) {
@@ -356,10 +358,11 @@ __global__ void __launch_bounds__(256) paged_weight_simt_kernel(PagedAttnArgs a)
       for (int j = 0; j < 4; ++j) {
         const float l = slse[tx + 16 * j], slope2 = sslope[tx + 16 * j];
         const int pq = sqp[tx + 16 * j];
+        const PagedSees sees = paged_sees_of(m, pq);
         if (l == -INFINITY) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if (paged_sees(m, pq, pk[i])) w[i] += exp2f(paged_score(a, ps, acc[i][j], slope2, pq, pk[i]) - l);
+          if (paged_sees(sees, pk[i])) w[i] += exp2f(paged_score(a, ps, acc[i][j], slope2, pq, pk[i]) - l);
       }
     }
 #pragma unroll

@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   const PagedTile t = st;
   if (t.seq < 0) return;
   const int len = paged_length(c, t.seq);
-  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[t.seq] : INT32_MIN};
+  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
   const int r0 = t.tile * BM, rows = min(BM, t.count * G - r0);
   // rows of Q, zeros past hd and past the last
@@ -87,12 +87,14 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   int pq[TM];
+  PagedSees sees[TM];
   float slope2[TM], mx[TM], sum[TM];
   uint64_t o[TM][NJ * 2];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int r = r0 + min(ty * TM + i, rows - 1);
     pq[i] = a.q_pos[t.first + r / G];
+    sees[i] = paged_sees_of(m, pq[i]);
     slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
     mx[i] = -INFINITY;
     sum[i] = 0.f;
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
         bool v = true;
         if (!full || a.slopes) {
           const int pk = spos[tx + 16 * j];
-          v = full || paged_sees(m, pq[i], pk);
+          v = full || paged_sees(sees[i], pk);
           if (a.slopes) u -= slope2[i] * fabsf((float)(pq[i] - pk));
         }
         s[j] = v ? u : -INFINITY;

@@ -132,7 +132,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     return;
   }
   const int len = paged_length(c, t.seq);
-  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[t.seq] : INT32_MIN};
+  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
   paged_classify<kPtKeys>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
   __syncthreads();
@@ -311,6 +311,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t o_at = tmem + lanes + 256 + q * HDP;
     const int pq = a.q_pos[tok];
+    const PagedSees sees = paged_sees_of(m, pq);
     const float slope2 = a.slopes ? a.slopes[valid ? head : h * G] * kLog2e : 0.f;
     const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
@@ -373,8 +374,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         tmem_ld_wait32(v);
         if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
         if (change) {
-          const int* pk = kp + n * 32;
           uint32_t w[32];
+          const int4* pk4 = reinterpret_cast<const int4*>(kp + n * 32);
           if (EXTRA && a.softcap > 0.f) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * scale2, cap2);
@@ -384,11 +385,23 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           }
           if (EXTRA && a.slopes) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope2, fabsf((float)(pq - pk[j])), v[j]);
+            for (int j = 0; j < 32; j += 4) {
+              const int4 k = pk4[j >> 2];
+              v[j] = fmaf(-slope2, fabsf((float)(pq - k.x)), v[j]);
+              v[j + 1] = fmaf(-slope2, fabsf((float)(pq - k.y)), v[j + 1]);
+              v[j + 2] = fmaf(-slope2, fabsf((float)(pq - k.z)), v[j + 2]);
+              v[j + 3] = fmaf(-slope2, fabsf((float)(pq - k.w)), v[j + 3]);
+            }
           }
           if (!full) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = paged_sees(m, pq, pk[j]) ? v[j] : -INFINITY;
+            for (int j = 0; j < 32; j += 4) {
+              const int4 k = pk4[j >> 2];
+              v[j] = paged_sees(sees, k.x) ? v[j] : -INFINITY;
+              v[j + 1] = paged_sees(sees, k.y) ? v[j + 1] : -INFINITY;
+              v[j + 2] = paged_sees(sees, k.z) ? v[j + 2] : -INFINITY;
+              v[j + 3] = paged_sees(sees, k.w) ? v[j + 3] : -INFINITY;
+            }
           }
 #pragma unroll
           for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);

@@ -32,9 +32,12 @@ struct WtShape {
   static constexpr size_t kSmem = kEnd + 1024;
 };
 
-struct WtRows { float lse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; };
+// Of the query rows of a tile: minus lse and the slope, in log2 units, and the
+// position (kPagedNoPos, seen by nobody, for what adds nothing).
+struct WtRows { float nlse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; };
 
-template <int HDP, int KT>
+// EXTRA: a cap or a distance bias.
+template <int HDP, int KT, bool EXTRA>
 __global__ void __launch_bounds__(KT * 128 + 128, 1)
 paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ PagedAttnArgs a) {
@@ -83,7 +86,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   const int len = paged_length(c, seq);
   const int2 ab = paged_new_rows(a.start, seq, a.rows);
   const int n_new = ab.y - ab.x, tiles = (n_new + tpt - 1) / tpt;
-  const PagedMask m{a.causal, a.window, a.prefix ? a.prefix[seq] : INT32_MIN};
+  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, seq);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -205,8 +208,8 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             const int r = x * 32 + lane, tl = r / G, tok = q * tpt + tl, head = h * G + r - tl * G;
             const bool in = tl < tpt && tok < n_new;
             const float v = in ? a.lse[(size_t)(ab.x + tok) * a.nq + head] : -INFINITY;
-            l[x] = v == -INFINITY ? INFINITY : v * kLog2e;      // adds nothing
-            p[x] = in ? a.q_pos[ab.x + tok] : 0;
+            l[x] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+            p[x] = v == -INFINITY ? kPagedNoPos : a.q_pos[ab.x + tok];
             sl[x] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
           }
           const int s = j % kNA;
@@ -215,7 +218,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int r = x * 32 + lane;
-            rows[s].lse2[r] = l[x];
+            rows[s].nlse2[r] = l[x];
             rows[s].pos[r] = p[x];
             rows[s].slope2[r] = sl[x];
           }
@@ -226,6 +229,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const int t = warp >> 2;
         const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
         const float cap2 = a.softcap * kLog2e;
+        const PagedSees by = paged_seen_by(m, pk);
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
           const int rel = cur.next(), b = j & 1, s = j % kNA;
@@ -236,40 +240,63 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
           const WtRows& rw = rows[s];
-          float add[4] = {0.f, 0.f, 0.f, 0.f};
+          uint64_t add[2] = {0, 0};
+          float x[2][32];
+          tmem_ld32(s_at, x[0]);
 #pragma unroll
-          for (int d = 0; d < 128; d += 32) {
-            float x[32];
-            tmem_ld32(s_at + d, x);
-            tmem_ld_wait();
-            if (d == 96) {
+          for (int n = 0; n < 4; ++n) {
+            float* v = x[n & 1];
+            tmem_ld_wait32(v);
+            if (n < 3) {
+              tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+            } else {
               tc_fence_before();
               mbar_arrive(&s_empty[t][b]);
             }
             float sc = scale2;
-            if (a.softcap > 0.f) {
+            if (EXTRA && a.softcap > 0.f) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = cap_tanh(x[e] * scale2, cap2);
+              for (int e = 0; e < 32; ++e) v[e] = cap_tanh(v[e] * scale2, cap2);
               sc = 1.f;
             }
-            if (a.slopes) {
+            if (EXTRA && a.slopes) {
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[e] = fmaf(-rw.slope2[d + e], fabsf((float)(rw.pos[d + e] - pk)), x[e] * sc);
-              sc = 1.f;
-            }
-            if (full) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) add[e & 3] += ex2(fmaf(x[e], sc, -rw.lse2[d + e]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                const float l = rw.lse2[d + e];
-                const float p = ex2(fmaf(x[e], sc, -l));
-                add[e & 3] += paged_sees(m, rw.pos[d + e], pk) && l != INFINITY ? p : 0.f;
+              for (int e = 0; e < 32; e += 4) {
+                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
+                const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
+                v[e] = fmaf(-sl.x, fabsf((float)(pq.x - pk)), v[e] * sc);
+                v[e + 1] = fmaf(-sl.y, fabsf((float)(pq.y - pk)), v[e + 1] * sc);
+                v[e + 2] = fmaf(-sl.z, fabsf((float)(pq.z - pk)), v[e + 2] * sc);
+                v[e + 3] = fmaf(-sl.w, fabsf((float)(pq.w - pk)), v[e + 3] * sc);
               }
+              sc = 1.f;
+            }
+            const uint64_t sc2 = pack2(sc, sc);
+            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(rw.nlse2 + n * 32);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              const ulonglong2 l = nl[e >> 2];
+              float p0, p1, p2, p3;
+              unpack2(fma2(pack2(v[e], v[e + 1]), sc2, l.x), p0, p1);
+              unpack2(fma2(pack2(v[e + 2], v[e + 3]), sc2, l.y), p2, p3);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              p2 = ex2(p2);
+              p3 = ex2(p3);
+              if (!full) {
+                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
+                p0 = paged_sees(by, pq.x) ? p0 : 0.f;
+                p1 = paged_sees(by, pq.y) ? p1 : 0.f;
+                p2 = paged_sees(by, pq.z) ? p2 : 0.f;
+                p3 = paged_sees(by, pq.w) ? p3 : 0.f;
+              }
+              add[0] = add2(add[0], pack2(p0, p1));
+              add[1] = add2(add[1], pack2(p2, p3));
             }
           }
-          w += (add[0] + add[1]) + (add[2] + add[3]);
+          float a0, a1;
+          unpack2(add2(add[0], add[1]), a0, a1);
+          w += a0 + a1;
           __syncwarp();
           if (lane == 0) mbar_arrive(&rows_empty[s]);
         }
@@ -311,10 +338,11 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
     mq = mk;
   }
   using C = WtShape<HDP, KT>;
-  cudaError_t e = cudaFuncSetAttribute(paged_weight_tc_kernel<HDP, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  auto kernel = a.softcap > 0.f || a.slopes ? paged_weight_tc_kernel<HDP, KT, true> : paged_weight_tc_kernel<HDP, KT, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   const long long x = (tiles + KT - 1) / KT;
-  return launch_pdl(paged_weight_tc_kernel<HDP, KT>, dim3((unsigned)x, a.c.nkv, a.c.n_seq), dim3(C::kThreads), C::kSmem, st, mq, mk, a);
+  return launch_pdl(kernel, dim3((unsigned)x, a.c.nkv, a.c.n_seq), dim3(C::kThreads), C::kSmem, st, mq, mk, a);
 }
 
 }  // namespace
