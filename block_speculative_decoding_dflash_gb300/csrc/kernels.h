@@ -410,13 +410,14 @@ struct PagedAttnArgs {
   float2* part_ml;             // [splits][rows * nq] (maximum in log2 units, sum)
   long long q_stride;
   int rows, nq, G, causal, window, splits, max_len;
+  int cluster;                 // the splits are a cluster's CTAs, which join their partials themselves
   float scale, softcap;
   // key weights
   const float* weight_in; float* weight_out;
   float decay;
 };
 // How an attention call is split: chosen from sizes alone.
-struct PagedPlan { int kind, splits; long long tiles, bytes; };
+struct PagedPlan { int kind, splits, cluster; long long tiles, bytes; };
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
 cudaError_t launch_paged_attention_f32(const PagedAttnArgs& a, int tile_rows, long long tiles, cudaStream_t st);

@@ -117,7 +117,7 @@ __device__ __forceinline__ int paged_class(const PagedMask& m, int qmin, int qma
 template <int KEYS>
 __device__ __forceinline__ void paged_classify(const PagedView& c, int s, int h, int len, const PagedMask& m, int qmin, int qmax,
                                                int t0, int t1, unsigned* some, unsigned* all) {
-  constexpr int kU = 4, kPer = KEYS / 32;
+  constexpr int kU = 8, kPer = KEYS / 32;
   static_assert(kPer == 2 || kPer == 4, "a lane takes 2 or 4 keys");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   for (int i = threadIdx.x; i <= (t1 - t0) >> 5; i += blockDim.x) some[i] = all[i] = 0u;
@@ -170,27 +170,26 @@ __device__ __forceinline__ void paged_classify(const PagedView& c, int s, int h,
   }
 }
 
-// The tiles that split z of n takes of the key tiles of a sequence. Without a
-// window a split classifies and takes an equal range of tiles; with one, where
-// most tiles are seen by nobody, every split classifies all tiles and takes an
-// equal share of those that are seen (skip .. skip + take - 1 in order).
-struct PagedShare { int t0, t1, skip, take; };
+// The tiles that split z of n takes of the key tiles of a sequence: an equal
+// range of them, which it classifies, or, with a window over more than
+// kDirect n tiles, where most are seen by nobody, an equal share of those that
+// are seen (skip .. skip + take - 1 in order), for which every split classifies
+// all. A range of at most kDirect tiles is not classified: the two dependent
+// loads and the meeting of the CTA would cost more than a tile too many.
+constexpr int kDirect = 3;
+struct PagedShare { int t0, t1, skip, take; bool by_share; };
 __device__ __forceinline__ PagedShare paged_range(int tiles, int window, int z, int n) {
-  if (window > 0) return PagedShare{0, tiles, 0, tiles};
+  if (window > 0 && tiles > kDirect * n) return PagedShare{0, tiles, 0, tiles, true};
   const int per = (tiles + n - 1) / n;
   const int a = min(tiles, z * per), b = min(tiles, a + per);
-  return PagedShare{a, b, 0, b - a};
+  return PagedShare{a, b, 0, b - a, false};
 }
-__device__ __forceinline__ void paged_take(PagedShare& r, const unsigned* some, int window, int z, int n) {
+__device__ __forceinline__ bool paged_direct(const PagedShare& r) { return r.t1 - r.t0 <= kDirect; }
+__device__ __forceinline__ void paged_take(PagedShare& r, const unsigned* some, int z, int n) {
   int seen = 0;
   for (int i = 0; i <= (r.t1 - r.t0) >> 5; ++i) seen += __popc(some[i]);
-  if (window > 0) {
-    r.skip = (int)((long long)seen * z / n);
-    r.take = (int)((long long)seen * (z + 1) / n) - r.skip;
-  } else {
-    r.skip = 0;
-    r.take = seen;
-  }
+  r.skip = r.by_share ? (int)((long long)seen * z / n) : 0;
+  r.take = r.by_share ? (int)((long long)seen * (z + 1) / n) - r.skip : seen;
 }
 // Walks the seen tiles of a share in ascending order.
 struct PagedCursor {

@@ -114,7 +114,7 @@ int check_attention(const dflash_paged_cache* c, const dflash_paged_attention_ar
   x->out = a->out; x->lse = a->lse;
   x->part_o = nullptr; x->part_ml = nullptr;
   x->q_stride = a->q_stride; x->rows = a->rows; x->nq = a->n_q_heads; x->G = a->n_q_heads / c->kv_heads;
-  x->causal = a->causal != 0; x->window = a->window; x->splits = 1; x->max_len = a->max_len;
+  x->causal = a->causal != 0; x->window = a->window; x->splits = 1; x->cluster = 0; x->max_len = a->max_len;
   x->scale = a->scale; x->softcap = a->softcap;
   x->weight_in = nullptr; x->weight_out = nullptr; x->decay = 0.f;
   return DFLASH_OK;
@@ -207,6 +207,7 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_a
     x.part_ml = reinterpret_cast<float2*>(x.part_o + (int64_t)p.splits * a->rows * a->n_q_heads * cache->head_dim);
   }
   x.splits = p.splits;
+  x.cluster = p.cluster;
   return launched(launch_paged_attention(cache->dtype, x, p, static_cast<cudaStream_t>(stream)), "paged attention");
 }
 

@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttn
   }
   const PagedScore ps = paged_score_of(a);
   __syncthreads();
-  paged_take(sh, some, a.window, z, a.splits);
+  paged_take(sh, some, z, a.splits);
   PagedCursor cur(some, sh);
   for (int rel = cur.next(); rel >= 0; rel = cur.next()) {
     const int k0 = (sh.t0 + rel) * kBN;
@@ -254,21 +254,30 @@ __global__ void __launch_bounds__(128) paged_attn_merge_kernel(PagedAttnArgs a) 
   M = warp_max(M);
   const float base = M == -INFINITY ? 0.f : M;
   float L = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  for (int z = 0; z < a.splits; ++z) {
-    const float2 ml = a.part_ml[z * n + at];
-    if (ml.y == 0.f) continue;
-    const float f = exp2f(ml.x - base);
-    L += ml.y * f;
-    const float* o = a.part_o + (z * n + at) * hd;
+  constexpr int kU = 4;                      // splits requested together
+  for (int z0 = 0; z0 < a.splits; z0 += kU) {
+    float2 ml[kU];
+    float4 x[kU][2];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int d = j * 128 + lane * 4;
-      if (d < hd) {
-        const float4 x = *reinterpret_cast<const float4*>(o + d);
-        acc[j * 4] = fmaf(f, x.x, acc[j * 4]);
-        acc[j * 4 + 1] = fmaf(f, x.y, acc[j * 4 + 1]);
-        acc[j * 4 + 2] = fmaf(f, x.z, acc[j * 4 + 2]);
-        acc[j * 4 + 3] = fmaf(f, x.w, acc[j * 4 + 3]);
+    for (int u = 0; u < kU; ++u) {
+      const bool in = z0 + u < a.splits;
+      ml[u] = in ? a.part_ml[(z0 + u) * n + at] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        x[u][j] = in && j * 128 + lane * 4 < hd ? *reinterpret_cast<const float4*>(a.part_o + ((z0 + u) * n + at) * hd + j * 128 + lane * 4)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (ml[u].y == 0.f) continue;          // it saw nothing
+      const float f = exp2f(ml[u].x - base);
+      L += ml[u].y * f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        acc[j * 4] = fmaf(f, x[u][j].x, acc[j * 4]);
+        acc[j * 4 + 1] = fmaf(f, x[u][j].y, acc[j * 4 + 1]);
+        acc[j * 4 + 2] = fmaf(f, x[u][j].z, acc[j * 4 + 2]);
+        acc[j * 4 + 3] = fmaf(f, x[u][j].w, acc[j * 4 + 3]);
       }
     }
   }
@@ -417,7 +426,7 @@ long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
 // kind 1 and 2: tensor cores (bf16, head_dim <= 128), that many tiles of 128
 // packed query rows to a CTA; 16, 32, 64: CUDA cores, that many rows.
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
-  PagedPlan p{0, 1, 0, 0};
+  PagedPlan p{0, 1, 0, 0, 0};
   const long long len = expected_len(a), units = (long long)a.rows * a.G;
   long long fill, least;
   if (dtype && a.c.hd <= 128) {
@@ -437,7 +446,20 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
   const long long ctas = p.tiles * a.c.nkv, by_keys = (len + least - 1) / least;
   const long long n = ctas >= fill ? 1 : (fill / ctas < by_keys ? fill / ctas : by_keys);
   p.splits = n < 1 ? 1 : (int)n;
-  if (p.splits > 1) p.bytes = (long long)p.splits * a.rows * a.nq * (a.c.hd + 2) * 4;
+  if (p.kind <= 2 && ctas < fill && (p.splits <= 8 || len <= 8 * 4096)) {
+    // Up to eight splits are a cluster that joins its partials in shared
+    // memory: no second kernel and no workspace. A cluster is of CTAs of one
+    // GPC (18 SMs or more), so what fits at once goes by its size; its splits may
+    // be as short as a tile.
+    static const struct { int size, most; } kFit[5] = {{8, 16}, {6, 24}, {4, 32}, {3, 48}, {2, 72}};
+    const long long key_tiles = (len + 127) / 128;
+    p.splits = 1;
+    for (const auto& f : kFit)
+      if (p.splits == 1 && ctas <= f.most && f.size <= key_tiles) p.splits = f.size;
+    p.cluster = p.splits > 1;
+  } else if (p.splits > 1) {
+    p.bytes = (long long)p.splits * a.rows * a.nq * (a.c.hd + 2) * 4;
+  }
   return p;
 }
 
@@ -448,7 +470,7 @@ cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const Page
   else if (!dtype) e = launch_paged_attention_f32(a, p.kind, p.tiles, st);
   else if (p.kind == 16) e = run_simt<bf16, 16, 2, 256>(a, grid, st);
   else e = run_simt<bf16, 64, 4, 256>(a, grid, st);
-  if (e != cudaSuccess || p.splits <= 1) return e;
+  if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
   return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)
                : launch_pdl(paged_attn_merge_kernel<float>, mg, dim3(128), 0, st, a);

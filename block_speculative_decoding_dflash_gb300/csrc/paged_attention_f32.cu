@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   // a score in log2 units: dot * scale2, or cap2 * tanh(dot * scale2)
   const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
   __syncthreads();
-  paged_take(sh, some, a.window, z, a.splits);
+  paged_take(sh, some, z, a.splits);
   PagedCursor cur(some, sh);
 
   // thread e copies 16 bytes e % kChunks of rows e / kChunks, + NT / kChunks, ..

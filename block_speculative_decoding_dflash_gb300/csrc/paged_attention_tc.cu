@@ -25,6 +25,7 @@
 // NaN. So in every tile that is not wholly seen by all its queries two warps
 // look for such rows of V and zero them in shared memory, and the queries that
 // do see them add p v themselves.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "mma_sync.cuh"
@@ -34,6 +35,9 @@ namespace dfl {
 
 namespace {
 
+namespace cg = cooperative_groups;
+
+constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kMaxTiles = (1 << 20) / kPtKeys;
@@ -62,11 +66,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
                      const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
   using C = TcShape<HDP, QT>;
   constexpr int NS = C::kStages;
+  constexpr int kClusterLd = HDP + 4;                   // row stride of O in shared memory: rows a bank quad apart
+  static_assert(QT * 128 * kClusterLd * 4 <= C::kEnd, "O over the Q, K and V tiles");
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t q_full, o_final, kv_full[NS], kv_empty[NS], v_ok[4], s_full[2], p_ready[2], o_done;
   __shared__ uint32_t tmem_holder;
-  __shared__ PagedTile s_tile;
-  __shared__ int s_qmin, s_qmax;
+  __shared__ float2 s_ml[QT * 128];                     // a row's maximum and sum, for the cluster
   __shared__ unsigned some[kBitWords], all[kBitWords];
   __shared__ unsigned bad[4][4];                        // of V tile i: [i & 3]
   __shared__ __align__(16) int kpos[QT * 4][kPtKeys];
@@ -106,37 +111,39 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tmem_alloc(&tmem_holder, 512);
     pdl_launch_dependents();
   }
-  if (warp == 0) {
-    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, blockIdx.x);
-    int lo = INT32_MAX, hi = INT32_MIN;
-    if (t.seq >= 0) {
-      const int r0 = t.tile * QT * tpt, r1 = min(t.count, r0 + QT * tpt);
-      for (int i = r0 + lane; i < r1; i += 32) {
-        const int p = a.q_pos[t.first + i];
-        lo = min(lo, p);
-        hi = max(hi, p);
-      }
+  // every warp looks for the tile itself: no one waits for another's answer
+  const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, blockIdx.x);
+  int qmin = INT32_MAX, qmax = INT32_MIN, len = 0;
+  PagedMask m{};
+  if (t.seq >= 0) {
+    len = paged_length(c, t.seq);
+    m = paged_mask(a.causal, a.window, a.prefix, t.seq);
+    const int r0 = t.tile * QT * tpt, r1 = min(t.count, r0 + QT * tpt);
+    for (int i = r0 + lane; i < r1; i += 32) {
+      const int p = a.q_pos[t.first + i];
+      qmin = min(qmin, p);
+      qmax = max(qmax, p);
     }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) { s_tile = t; s_qmin = lo; s_qmax = hi; }
+    qmin = __reduce_min_sync(0xffffffffu, qmin);
+    qmax = __reduce_max_sync(0xffffffffu, qmax);
+  }
+  PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
+  const bool direct = paged_direct(sh);
+  if (direct) {
+    if (threadIdx.x == 0) { some[0] = (1u << sh.take) - 1; all[0] = 0u; }
+  } else {
+    paged_classify<kPtKeys>(c, t.seq, h, len, m, qmin, qmax, sh.t0, sh.t1, some, all);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const PagedTile t = s_tile;
   const uint32_t tmem = tmem_holder;
   if (t.seq < 0) {
     __syncthreads();
     if (warp == wMma) tmem_dealloc(tmem, 512);
     return;
   }
-  const int len = paged_length(c, t.seq);
-  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
-  PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
-  paged_classify<kPtKeys>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
-  __syncthreads();
-  paged_take(sh, some, a.window, z, a.splits);
+  paged_take(sh, some, z, a.splits);
   const int N = sh.take;                                 // tiles this CTA works on
   const int row0 = t.tile * QT * tpt;                    // its first new row, within the sequence
   const int nt = (QT == 2 && row0 + tpt < t.count) ? 2 : 1;
@@ -160,6 +167,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       if (lane < boxes && slot < len) {
         const long long row = paged_row(c, t.seq, h, slot);
         if (row >= 0) y = (int)row;
+        else if (c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
       }
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
@@ -312,6 +320,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const uint32_t o_at = tmem + lanes + 256 + q * HDP;
     const int pq = a.q_pos[tok];
     const PagedSees sees = paged_sees_of(m, pq);
+    const int wmin = __reduce_min_sync(0xffffffffu, valid ? pq : INT32_MAX), wmax = __reduce_max_sync(0xffffffffu, valid ? pq : INT32_MIN);
     const float slope2 = a.slopes ? a.slopes[valid ? head : h * G] * kLog2e : 0.f;
     const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
@@ -360,8 +369,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       // First pass over S: the row's maximum. What a mask, cap or bias makes of
       // a score is put back in its place, so that the second pass is the same
       // for all; S is read twice because half as many registers then do.
-      const bool change = !full || (EXTRA && (a.slopes || a.softcap > 0.f));
-      if (!full || (EXTRA && a.slopes)) {
+      // (a tile that other warps see in part, or that was not classified, may be
+      // wholly seen by this warp's rows)
+      bool masked = !full;
+      if (masked) {
+        const bool there = pos4.x != kPagedNoPos && pos4.y != kPagedNoPos && pos4.z != kPagedNoPos && pos4.w != kPagedNoPos;
+        const int kmin = __reduce_min_sync(0xffffffffu, min(min(pos4.x, pos4.y), min(pos4.z, pos4.w)));
+        const int kmax = __reduce_max_sync(0xffffffffu, max(max(pos4.x, pos4.y), max(pos4.z, pos4.w)));
+        masked = !__all_sync(0xffffffffu, there) || paged_class(m, wmin, wmax, kmin, kmax, true) != 2;
+      }
+      const bool change = masked || (EXTRA && (a.slopes || a.softcap > 0.f));
+      if (masked || (EXTRA && a.slopes)) {
         __syncwarp();
         *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
         __syncwarp();
@@ -393,7 +411,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
               v[j + 3] = fmaf(-slope2, fabsf((float)(pq - k.w)), v[j + 3]);
             }
           }
-          if (!full) {
+          if (masked) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const int4 k = pk4[j >> 2];
@@ -504,7 +522,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       rel = cur.next();
       fetch();
     }
-    // ---- the row's output, or its split's partial
+    // ---- the row's output, or its split's partial (to shared memory for the
+    // cluster, else to the workspace)
     if (N > 0) {
       paged_wait(&o_final, 0, ok);
       tc_fence_after();
@@ -512,20 +531,27 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const size_t at = (size_t)tok * a.nq + head;
     const bool none = sum == 0.f;                        // nothing seen (a NaN score makes the sum NaN)
     const float inv = none ? 0.f : 1.f / sum;
+    if (a.cluster) {
+      // every copy into this memory has landed and been used by an MMA that is done
+      fence_proxy_async_shared();
+      s_ml[q * 128 + r] = make_float2(mx, valid ? sum : 0.f);
+    }
     if (work) {
 #pragma unroll
       for (int d = 0; d < HDP; d += 32) {
         float o[32];
         if (N > 0) {
           tmem_ld32(o_at + d, o);
-          tmem_ld_wait();
+          tmem_ld_wait32(o);
         }
-        if (valid && a.splits > 1) {
-          float* po = a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
+        if (!valid) continue;
+        if (a.splits > 1) {
+          float* po = a.cluster ? reinterpret_cast<float*>(sm) + (q * 128 + r) * kClusterLd + d
+                                : a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
 #pragma unroll
           for (int x = 0; x < 32; x += 4)
             if (d + x < c.hd && !none) *reinterpret_cast<float4*>(po + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
-        } else if (valid) {
+        } else {
           bf16* out = static_cast<bf16*>(a.out) + at * c.hd + d;
 #pragma unroll
           for (int x = 0; x < 32; x += 8) {
@@ -533,20 +559,55 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             if (!none) {
               uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
-                w[y] = *reinterpret_cast<const uint32_t*>(&b);
-              }
+              for (int y = 0; y < 4; ++y) w[y] = pack_bf16(o[x + 2 * y] * inv, o[x + 2 * y + 1] * inv);
             }
             if (d + x < c.hd) *reinterpret_cast<uint4*>(out + x) = u;
           }
         }
       }
-      if (valid) {
+      if (valid && !a.cluster) {
         if (a.splits > 1) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx, sum);
         else if (a.lse) a.lse[at] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
+  }
+  if (a.cluster) {
+    // The splits are the cluster's CTAs: each joins its share of the rows' 4
+    // dimensions at a time, o = sum_z o_z exp2(m_z - M) / sum_z l_z exp2(m_z - M),
+    // out of the others' shared memory.
+    cg::cluster_group cl = cg::this_cluster();
+    cl.sync();
+    const int rows = nt * 128, quads = c.hd >> 2;
+    for (int e = z * C::kThreads + (int)threadIdx.x; e < rows * quads; e += a.splits * C::kThreads) {
+      const int R = e / quads, d = (e - R * quads) * 4, r = R & 127, tl = r / G, at_row = row0 + (R >> 7) * tpt + tl;
+      if (tl >= tpt || at_row >= t.count) continue;
+      float2 ml[kMaxCluster];
+      float4 o[kMaxCluster];
+      float M = -INFINITY, L = 0.f;
+#pragma unroll
+      for (int x = 0; x < kMaxCluster; ++x) {
+        ml[x] = x < a.splits ? *cl.map_shared_rank(&s_ml[R], x) : make_float2(-INFINITY, 0.f);
+        if (x < a.splits) o[x] = *reinterpret_cast<const float4*>(cl.map_shared_rank(reinterpret_cast<float*>(sm) + R * kClusterLd + d, x));
+        M = fmaxf(M, ml[x].x);
+      }
+      const float base = M == -INFINITY ? 0.f : M;
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int x = 0; x < kMaxCluster; ++x) {
+        if (ml[x].y == 0.f) continue;                    // it saw nothing: its o was not written
+        const float f = ex2(ml[x].x - base);
+        L = fmaf(ml[x].y, f, L);
+        v.x = fmaf(o[x].x, f, v.x);
+        v.y = fmaf(o[x].y, f, v.y);
+        v.z = fmaf(o[x].z, f, v.z);
+        v.w = fmaf(o[x].w, f, v.w);
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      const size_t at = (size_t)(t.first + at_row) * a.nq + h * G + r - tl * G;
+      *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + at * c.hd + d) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
+      if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    }
+    cl.sync();                                           // no CTA leaves while another reads it
   }
   if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
   tc_fence_before();
@@ -568,7 +629,21 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   auto kernel = extra ? paged_attn_tc_kernel<HDP, QT, true> : paged_attn_tc_kernel<HDP, QT, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(C::kThreads), C::kSmem, st, mq, mk, mv, a);
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)tiles, a.c.nkv, a.splits);
+  cfg.blockDim = dim3(C::kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = a.splits;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
 }
 
 }  // namespace

@@ -154,8 +154,8 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         }
       }
       __syncthreads();
-      PagedShare sh{0, cn, 0, 0};
-      paged_take(sh, some, 0, 0, 1);
+      PagedShare sh{0, cn, 0, 0, false};
+      paged_take(sh, some, 0, 1);
       PagedCursor cur(some, sh);
       const int N = sh.take;
       if (warp == wLoad) {
