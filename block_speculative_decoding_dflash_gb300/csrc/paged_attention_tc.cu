@@ -385,15 +385,31 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         __syncwarp();
       }
       float x[2][32], top = -INFINITY;
-      tmem_ld32(s_at, x[0]);
+      auto rise = [&](const float* v) {
+        float t2[2] = {v[0], v[1]};
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        float* v = x[n & 1];
-        tmem_ld_wait32(v);
-        if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-        if (change) {
+        for (int j = 2; j < 32; j += 4) {
+          t2[0] = j + 2 < 32 ? fmaxf(fmaxf(t2[0], v[j]), v[j + 2]) : fmaxf(t2[0], v[j]);
+          t2[1] = j + 3 < 32 ? fmaxf(fmaxf(t2[1], v[j + 1]), v[j + 3]) : fmaxf(t2[1], v[j + 1]);
+        }
+        top = fmaxf(top, fmaxf(t2[0], t2[1]));
+      };
+      if (!change) {
+        tmem_ld32(s_at, x[0]);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          tmem_ld_wait32(x[n & 1]);
+          if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+          rise(x[n & 1]);
+        }
+      } else {
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+          float* v = x[0];
           uint32_t w[32];
           const int4* pk4 = reinterpret_cast<const int4*>(kp + n * 32);
+          tmem_ld32(s_at + n * 32, v);
+          tmem_ld_wait32(v);
           if (EXTRA && a.softcap > 0.f) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * scale2, cap2);
@@ -424,14 +440,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
           for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
           tmem_st32(s_at + n * 32, w);
+          rise(v);
         }
-        float t2[2] = {v[0], v[1]};
-#pragma unroll
-        for (int j = 2; j < 32; j += 4) {
-          t2[0] = j + 2 < 32 ? fmaxf(fmaxf(t2[0], v[j]), v[j + 2]) : fmaxf(t2[0], v[j]);
-          t2[1] = j + 3 < 32 ? fmaxf(fmaxf(t2[1], v[j + 1]), v[j + 3]) : fmaxf(t2[1], v[j + 1]);
-        }
-        top = fmaxf(top, fmaxf(t2[0], t2[1]));
       }
       const float sc = change ? 1.f : scale2;
       top *= sc;

@@ -241,57 +241,68 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           tc_fence_after();
           const WtRows& rw = rows[s];
           uint64_t add[2] = {0, 0};
-          float x[2][32];
-          tmem_ld32(s_at, x[0]);
+          if (full && !EXTRA) {
+            const uint64_t sc2 = pack2(scale2, scale2);
+            float x[2][32];
+            tmem_ld32(s_at, x[0]);
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            float* v = x[n & 1];
-            tmem_ld_wait32(v);
-            if (n < 3) {
-              tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-            } else {
-              tc_fence_before();
-              mbar_arrive(&s_empty[t][b]);
-            }
-            float sc = scale2;
-            if (EXTRA && a.softcap > 0.f) {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] = cap_tanh(v[e] * scale2, cap2);
-              sc = 1.f;
-            }
-            if (EXTRA && a.slopes) {
+            for (int n = 0; n < 4; ++n) {
+              float* v = x[n & 1];
+              tmem_ld_wait32(v);
+              if (n < 3) {
+                tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+              } else {
+                tc_fence_before();
+                mbar_arrive(&s_empty[t][b]);
+              }
+              const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(rw.nlse2 + n * 32);
 #pragma unroll
               for (int e = 0; e < 32; e += 4) {
-                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
-                const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
-                v[e] = fmaf(-sl.x, fabsf((float)(pq.x - pk)), v[e] * sc);
-                v[e + 1] = fmaf(-sl.y, fabsf((float)(pq.y - pk)), v[e + 1] * sc);
-                v[e + 2] = fmaf(-sl.z, fabsf((float)(pq.z - pk)), v[e + 2] * sc);
-                v[e + 3] = fmaf(-sl.w, fabsf((float)(pq.w - pk)), v[e + 3] * sc);
+                const ulonglong2 l = nl[e >> 2];
+                float p0, p1, p2, p3;
+                unpack2(fma2(pack2(v[e], v[e + 1]), sc2, l.x), p0, p1);
+                unpack2(fma2(pack2(v[e + 2], v[e + 3]), sc2, l.y), p2, p3);
+                add[0] = add2(add[0], pack2(ex2(p0), ex2(p1)));
+                add[1] = add2(add[1], pack2(ex2(p2), ex2(p3)));
               }
-              sc = 1.f;
             }
-            const uint64_t sc2 = pack2(sc, sc);
-            const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(rw.nlse2 + n * 32);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const ulonglong2 l = nl[e >> 2];
-              float p0, p1, p2, p3;
-              unpack2(fma2(pack2(v[e], v[e + 1]), sc2, l.x), p0, p1);
-              unpack2(fma2(pack2(v[e + 2], v[e + 3]), sc2, l.y), p2, p3);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-              p2 = ex2(p2);
-              p3 = ex2(p3);
-              if (!full) {
-                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
-                p0 = paged_sees(by, pq.x) ? p0 : 0.f;
-                p1 = paged_sees(by, pq.y) ? p1 : 0.f;
-                p2 = paged_sees(by, pq.z) ? p2 : 0.f;
-                p3 = paged_sees(by, pq.w) ? p3 : 0.f;
+          } else {
+#pragma unroll 1
+            for (int n = 0; n < 4; ++n) {
+              float v[32];
+              tmem_ld32(s_at + n * 32, v);
+              tmem_ld_wait32(v);
+              if (n == 3) {
+                tc_fence_before();
+                mbar_arrive(&s_empty[t][b]);
               }
-              add[0] = add2(add[0], pack2(p0, p1));
-              add[1] = add2(add[1], pack2(p2, p3));
+              float sc = scale2;
+              if (EXTRA && a.softcap > 0.f) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = cap_tanh(v[e] * scale2, cap2);
+                sc = 1.f;
+              }
+              if (EXTRA && a.slopes) {
+#pragma unroll
+                for (int e = 0; e < 32; e += 4) {
+                  const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
+                  const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
+                  v[e] = fmaf(-sl.x, fabsf((float)(pq.x - pk)), v[e] * sc);
+                  v[e + 1] = fmaf(-sl.y, fabsf((float)(pq.y - pk)), v[e + 1] * sc);
+                  v[e + 2] = fmaf(-sl.z, fabsf((float)(pq.z - pk)), v[e + 2] * sc);
+                  v[e + 3] = fmaf(-sl.w, fabsf((float)(pq.w - pk)), v[e + 3] * sc);
+                }
+                sc = 1.f;
+              }
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(rw.nlse2 + n * 32 + e);
+                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
+                const float p0 = ex2(fmaf(v[e], sc, l.x)), p1 = ex2(fmaf(v[e + 1], sc, l.y));
+                const float p2 = ex2(fmaf(v[e + 2], sc, l.z)), p3 = ex2(fmaf(v[e + 3], sc, l.w));
+                add[0] = add2(add[0], pack2(full || paged_sees(by, pq.x) ? p0 : 0.f, full || paged_sees(by, pq.y) ? p1 : 0.f));
+                add[1] = add2(add[1], pack2(full || paged_sees(by, pq.z) ? p2 : 0.f, full || paged_sees(by, pq.w) ? p3 : 0.f));
+              }
             }
           }
           float a0, a1;
