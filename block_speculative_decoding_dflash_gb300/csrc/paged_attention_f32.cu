@@ -34,17 +34,18 @@ __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0
 template <int BM, int HDP>
 struct F32Shape {
   static constexpr int LD = HDP + 4;          // row stride: 16-byte loads of 8 rows touch all banks
-  static constexpr int kQ = 0, kK = BM * LD, kV = kK + kBN * LD, kP = kV + kBN * LD, kPos = kP + BM * (kBN + 4), kEnd = kPos + kBN;
+  static constexpr int kQ = 0, kK = BM * LD, kV = kK + kBN * LD, kP = kV + kBN * LD, kPos = kP + BM * (kBN + 4), kRow = kPos + kBN, kEnd = kRow + 2 * kBN;
   static constexpr size_t kSmem = (size_t)kEnd * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
 };
 
 template <int BM, int TM, int HDP>
-__global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
+__global__ void __launch_bounds__(BM / TM * 16, HDP > 128 || BM > 32 ? 1 : 2) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
   using C = F32Shape<BM, HDP>;
   constexpr int NT = BM / TM * 16, LD = C::LD, NJ = HDP / 64;
   extern __shared__ __align__(16) float smf[];
   float *sq = smf + C::kQ, *sk = smf + C::kK, *sv = smf + C::kV, *sp = smf + C::kP;
   int* spos = reinterpret_cast<int*>(smf + C::kPos);
+  int* srow = reinterpret_cast<int*>(smf + C::kRow);      // [2][kBN] places of a tile's rows, -1 for none
   unsigned* some = reinterpret_cast<unsigned*>(smf + C::kEnd);
   unsigned* all = some + kMaxTiles / 32 + 1;
   __shared__ PagedTile st;
@@ -73,12 +74,12 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   const int len = paged_length(c, t.seq);
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
-  const int r0 = t.tile * BM, rows = min(BM, t.count * G - r0);
+  const int r0 = t.tile * BM, n_rows = min(BM, t.count * G - r0);
   // rows of Q, zeros past hd and past the last
   constexpr int kChunks = HDP / 4;
   for (int e = threadIdx.x; e < BM * kChunks; e += NT) {
     const int r = e / kChunks, d = e % kChunks * 4;
-    const bool in = r < rows && d < hd;
+    const bool in = r < n_rows && d < hd;
     const float* src = static_cast<const float*>(a.q);
     if (in) src += (size_t)(t.first + (r0 + r) / G) * a.q_stride + (size_t)(h * G + (r0 + r) % G) * hd + d;
     cp_async16(sq + r * LD + d, src, in);
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   uint64_t o[TM][NJ * 2];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
-    const int r = r0 + min(ty * TM + i, rows - 1);
+    const int r = r0 + min(ty * TM + i, n_rows - 1);
     pq[i] = a.q_pos[t.first + r / G];
     sees[i] = paged_sees_of(m, pq[i]);
     slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
@@ -111,28 +112,37 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
   static_assert(NT % kChunks == 0, "whole rows at a time");
   constexpr int kStep = NT / kChunks, kRows = kBN / kStep;
   const int lr = threadIdx.x / kChunks, ld = threadIdx.x % kChunks * 4;
-  auto copy = [&](float* dst, const void* base, int tile) {
-#pragma unroll 4
+  const bool cols = ld < hd;
+  auto find = [&](int* rows, int tile) {
+    if (threadIdx.x < kBN) {
+      const int slot = tile * kBN + threadIdx.x;
+      rows[threadIdx.x] = slot < len ? (int)paged_row(c, t.seq, h, slot) : -1;
+    }
+  };
+  auto copy = [&](float* dst, const void* base, const int* rows) {
+    const float* src = static_cast<const float*>(base) + ld;
+#pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      const int j = lr + i * kStep, slot = tile * kBN + j;
-      const long long row = slot < len ? paged_row(c, t.seq, h, slot) : -1;
-      const bool in = row >= 0 && ld < hd;
-      cp_async16(dst + j * LD + ld, static_cast<const float*>(base) + (in ? row * hd + ld : 0), in);
+      const int j = lr + i * kStep, row = rows[j];
+      const bool in = row >= 0 && cols;
+      cp_async16(dst + j * LD + ld, src + (in ? (long long)row * hd : 0ll), in);
     }
     cp_commit();
   };
-  int rel = cur.next();
-  if (rel >= 0) copy(sk, c.k, sh.t0 + rel);
-  while (rel >= 0) {
-    const int tile = sh.t0 + rel;
+  int rel = cur.next(), buf = 0;
+  if (rel >= 0) find(srow, sh.t0 + rel);
+  __syncthreads();
+  if (rel >= 0) copy(sk, c.k, srow);
+  for (; rel >= 0; buf ^= 1) {
     const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
     const int next = cur.next();
-    copy(sv, c.v, tile);
+    const int* rows = srow + buf * kBN;
+    copy(sv, c.v, rows);
     if (threadIdx.x < kBN && (!full || a.slopes)) {
-      const int slot = tile * kBN + threadIdx.x;
-      const long long row = slot < len ? paged_row(c, t.seq, h, slot) : -1;
+      const int row = rows[threadIdx.x];
       spos[threadIdx.x] = row >= 0 ? c.pos[row] : kPagedNoPos;
     }
+    if (next >= 0) find(srow + (buf ^ 1) * kBN, sh.t0 + next);
     cp_wait<1>();                            // K
     __syncthreads();
     uint64_t s2[TM][4];
@@ -140,7 +150,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2[i][j] = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int d = 0; d < HDP; d += 4) {
       ulonglong2 q[TM], k[4];
 #pragma unroll
@@ -156,7 +166,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
         }
     }
     __syncthreads();                         // K is free
-    if (next >= 0) copy(sk, c.k, sh.t0 + next);
+    if (next >= 0) copy(sk, c.k, srow + (buf ^ 1) * kBN);
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
       unsigned seen = 0;
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
       careful = __syncthreads_or(bad);
     }
     if (!careful) {
-#pragma unroll 2
+#pragma unroll 4
       for (int j = 0; j < kBN; j += 4) {
         float4 p[TM];
 #pragma unroll
@@ -261,7 +271,7 @@ __global__ void __launch_bounds__(BM / TM * 16) paged_attn_f32_kernel(const __gr
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int r = ty * TM + i;
-    if (r >= rows) continue;
+    if (r >= n_rows) continue;
     const size_t at = (size_t)(t.first + (r0 + r) / G) * a.nq + h * G + (r0 + r) % G;
     const bool none = sum[i] == 0.f;         // nothing seen (a NaN score makes the sum NaN)
     const bool split = a.splits > 1;
