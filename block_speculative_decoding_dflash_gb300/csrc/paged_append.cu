@@ -8,7 +8,7 @@
 // argument reduction.
 #include <math.h>
 
-#include "paged.cuh"
+#include "paged_tc.cuh"
 
 namespace dfl {
 
@@ -85,46 +85,39 @@ __device__ __forceinline__ Raw8<float> round8(const float* v, float) {
 // a value becomes r (v A + w B): w the pair's other half, in the same lane
 // (adjacent pairs) or one shuffle away, A and B the gains times cos and sin,
 // which a lane holds for its dimensions. kU heads are requested before the
-// first is used, and those before the sines are computed. Bound by the bytes
-// of the rows, read once and written once, for thousands of rows; by its
-// chain of dependent loads for a few.
-// Needs pairs to fill whole lanes: a multiple of 8 (neox) or 4.
-constexpr int kU = 4;
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32, 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int per_warp, int splits) {
+// first is used, and the next ones as soon as one is in its registers. Bound by
+// the bytes of the rows, read once and written once, for thousands of rows; by
+// its chain of dependent loads for a few.
+// Needs pairs to fill whole lanes: a multiple of 8 (NEOX) or 4. LPR: hd / 8
+// where it is 8 or 16 (head_dim 64 and 128), else 0.
+constexpr int kU = 2;
+template <typename T, int LPR, bool NEOX>
+__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int per_warp, int splits) {
   pdl_enter();
   const PagedView& c = a.c;
-  const int lane = threadIdx.x & 31, hd = c.hd, nq = a.nq, nkv = c.nkv;
+  const int lane = threadIdx.x & 31, nq = a.nq, nkv = c.nkv;
+  const int hd = LPR ? LPR * 8 : c.hd, lpr = hd >> 3, side = 32 / lpr;   // lanes of a head, heads side by side
   const long long item = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int tok = (int)(item / splits), part = (int)(item % splits);
   if (tok >= a.rows) return;
   const int x0 = part * per_warp, x1 = min(nq + 2 * nkv, x0 + per_warp);
-  const int lpr = hd >> 3, side = 32 / lpr;               // lanes of a head, heads side by side
   const int sub = lane / lpr, l = lane - sub * lpr, d0 = l * 8;
-  const bool in = sub < side;
+  const bool in = LPR || sub < side;
   const int step = side * hd;                             // elements between a lane's heads
   const T* qs = static_cast<const T*>(a.q) + (long long)tok * a.q_stride + (size_t)(x0 + sub) * hd + d0;
   Raw8<T> raw[kU];
   const int q_left = min(x1, nq) - x0;                    // q heads of this warp
 #pragma unroll
   for (int u = 0; u < kU; ++u)
-    if (in && u * side + sub < q_left) raw[u].load(qs + (size_t)u * step);
+    if (in && u * side + sub < q_left) raw[u].load(qs + u * step);
   // the row's (cos, sin), two pairs or more to a lane, then this lane's
   __shared__ __align__(16) float2 table[kWarps][kPagedMaxPairs];
   float2* tab = table[threadIdx.x >> 5];
   for (int i = lane; i < a.pairs; i += 32) tab[i] = turn(a, i, tok);
   __syncwarp();
-  NewRow r{-1, -1};
-  if (x1 > nq) {
-    r = new_row(a, tok, x1 == nq + 2 * nkv);
-    if (r.seq < 0) return;
-  } else if (tok < a.start[0] || tok >= a.start[c.n_seq]) {
-    return;
-  }
-
   int other = lane, od = d0, pair = -1;                   // where the pairs' other halves are; first pair of the lane
-  bool second = false;                                    // the lane holds second halves (neox)
-  if (a.neox) {
+  bool second = false;                                    // the lane holds second halves
+  if (NEOX) {
     const int pl = a.pairs >> 3;                          // lanes of the first halves
     second = l >= pl;
     if (l < 2 * pl) {
@@ -135,74 +128,99 @@ __global__ void __launch_bounds__(kWarps * 32, 5) paged_append_kernel(const __gr
   } else if (d0 < 2 * a.pairs) {
     pair = d0 >> 1;
   }
-  float A[8], B[8];
+  Raw8<T> g_own, g_oth;                                   // the gains, requested before they are needed
+  auto get_gain = [&](const void* g) {
+    if (g && in) {
+      g_own.load(static_cast<const T*>(g) + d0);
+      if (NEOX) g_oth.load(static_cast<const T*>(g) + od);
+    }
+  };
+  get_gain(q_left > 0 ? a.q_norm : a.k_norm);
+  NewRow r{-1, -1};
+  if (x1 > nq) {
+    r = new_row(a, tok, x1 == nq + 2 * nkv);
+    if (r.seq < 0) return;
+  } else if (tok < a.start[0] || tok >= a.start[c.n_seq]) {
+    return;
+  }
+
+  uint64_t A[4], B[4];
   bool norm;
   auto use_gain = [&](const void* g) {
     norm = g != nullptr;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float2 t = make_float2(1.f, 0.f);
-      if (in && pair >= 0) t = tab[pair + (a.neox ? j : j >> 1)];
-      A[j] = t.x;
-      B[j] = (a.neox ? second : (j & 1)) ? t.y : -t.y;
-    }
-    if (norm && in) {
-      float own[8], oth[8];
-      load8(static_cast<const T*>(g) + d0, own);
-      load8(static_cast<const T*>(g) + od, oth);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        A[j] *= own[j];
-        B[j] *= a.neox ? oth[j] : own[j ^ 1];
+    for (int j = 0; j < 8; j += 2) {
+      float2 t0 = make_float2(1.f, 0.f), t1 = t0;
+      if (in && pair >= 0) {
+        t0 = tab[pair + (NEOX ? j : j >> 1)];
+        t1 = NEOX ? tab[pair + j + 1] : t0;
       }
+      float b0 = (NEOX ? second : false) ? t0.y : -t0.y, b1 = (NEOX ? second : true) ? t1.y : -t1.y;
+      if (norm && in) {
+        t0.x *= g_own.at(j);
+        t1.x *= g_own.at(j + 1);
+        b0 *= NEOX ? g_oth.at(j) : g_own.at(j + 1);
+        b1 *= NEOX ? g_oth.at(j + 1) : g_own.at(j);
+      }
+      A[j >> 1] = pack2(t0.x, t1.x);
+      B[j >> 1] = pack2(b0, b1);
     }
   };
   const float inv_hd = 1.f / (float)hd;
-  auto turned = [&](const Raw8<T>& x) {
-    float v[8], w[8], f = 1.f;
+  // x turned; `next` is called as soon as x's registers are free
+  auto turned = [&](Raw8<T>& x, auto next) {
+    uint64_t v[4], w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = x.at(j);
-    if (norm) {
-      float ss = 0.f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
-      float tot = ss;
-      if ((lpr & (lpr - 1)) == 0) {
-        for (int o = lpr >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-      } else {
-        tot = 0.f;
-        for (int o = 0; o < lpr; ++o) tot += __shfl_sync(0xffffffffu, ss, in ? sub * lpr + o : lane);
-      }
-      f = rsqrtf(fmaf(tot, inv_hd, a.eps));
-    }
-    if (a.neox) {
+    for (int j = 0; j < 4; ++j) v[j] = pack2(x.at(2 * j), x.at(2 * j + 1));
+    if (NEOX) {
       Raw8<T> y;
 #pragma unroll
       for (int j = 0; j < Raw8<T>::kWords; ++j) y.w[j] = __shfl_sync(0xffffffffu, x.w[j], other);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = y.at(j);
+      for (int j = 0; j < 4; ++j) w[j] = pack2(y.at(2 * j), y.at(2 * j + 1));
     } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = v[j ^ 1];
+      for (int j = 0; j < 4; ++j) w[j] = pack2(x.at(2 * j + 1), x.at(2 * j));
     }
+    next();
+    float f = 1.f;
+    if (norm) {
+      uint64_t s2 = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], A[j], w[j] * B[j]) * f;
-    return round8(v, T());
+      for (int j = 0; j < 4; ++j) s2 = fma2(v[j], v[j], s2);
+      float s0, s1;
+      unpack2(s2, s0, s1);
+      float tot = s0 + s1;
+      if (LPR) {
+#pragma unroll
+        for (int o = LPR >> 1; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+      } else {
+        const float own = tot;
+        tot = 0.f;
+        for (int o = 0; o < lpr; ++o) tot += __shfl_sync(0xffffffffu, own, in ? sub * lpr + o : lane);
+      }
+      f = rsqrtf(fmaf(tot, inv_hd, a.eps));
+    }
+    float y[8];
+    const uint64_t f2 = pack2(f, f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) unpack2(fma2(fma2(v[j], A[j], fma2(w[j], B[j], 0)), f2, 0), y[2 * j], y[2 * j + 1]);
+    return round8(y, T());
   };
 
   if (q_left > 0) {
     use_gain(a.q_norm);
     T* qd = static_cast<T*>(a.q_out) + ((size_t)tok * nq + x0 + sub) * hd + d0;
-    for (int x = 0; x < q_left; x += side * kU) {
-      const size_t at = (size_t)x * hd;
+    int left = in ? q_left - sub : 0;                     // heads from this lane's on
+    for (int x = q_left; x > 0; x -= side * kU, left -= side * kU, qs += kU * step, qd += kU * step) {
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
-        const Raw8<T> y = turned(raw[u]);
-        if (in && x + u * side + sub < q_left) y.store(qd + at + (size_t)u * step);
+        if (u * side >= x) break;
+        const Raw8<T> y = turned(raw[u], [&] {
+          if ((kU + u) * side < left) raw[u].load(qs + (kU + u) * step);
+        });
+        if (u * side < left) y.store(qd + u * step);
       }
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (in && x + (kU + u) * side + sub < q_left) raw[u].load(qs + at + (size_t)(kU + u) * step);
     }
   }
   // k and v: consecutive heads of a row lie page_rows rows apart
@@ -211,21 +229,35 @@ __global__ void __launch_bounds__(kWarps * 32, 5) paged_append_kernel(const __gr
     if (h0 >= h1) continue;
     const long long row0 = r.slot >= 0 ? paged_row(c, r.seq, 0, r.slot) : -1;
     if (row0 < 0) continue;
-    if (kind == 1) use_gain(a.k_norm);
-    const T* src = kind == 1 ? static_cast<const T*>(a.k) + (long long)tok * a.k_stride : static_cast<const T*>(a.v) + (long long)tok * a.v_stride;
-    T* dst = static_cast<T*>(kind == 1 ? c.k : c.v);
+    if (kind == 1) {
+      if (q_left > 0) get_gain(a.k_norm);
+      use_gain(a.k_norm);
+    }
+    const T* src = (kind == 1 ? static_cast<const T*>(a.k) + (long long)tok * a.k_stride : static_cast<const T*>(a.v) + (long long)tok * a.v_stride) + d0;
+    T* dst = static_cast<T*>(kind == 1 ? c.k : c.v) + row0 * hd + d0;
+    const size_t apart = (size_t)hd << c.lg_rows;         // elements between heads in a page
+#pragma unroll
+    for (int u = 0; u < kU; ++u)
+      if (in && h0 + u * side + sub < h1) raw[u].load(src + (h0 + u * side + sub) * hd);
     for (int h = h0; h < h1; h += side * kU) {
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (in && h + u * side + sub < h1) raw[u].load(src + (size_t)(h + u * side + sub) * hd + d0);
-#pragma unroll
       for (int u = 0; u < kU; ++u) {
+        if (h + u * side >= h1) break;
         const int hh = h + u * side + sub;
-        const long long row = row0 + ((long long)hh << c.lg_rows);
-        const Raw8<T> y = kind == 1 ? turned(raw[u]) : raw[u];
+        auto next = [&] {
+          if (in && hh + kU * side < h1) raw[u].load(src + (hh + kU * side) * hd);
+        };
+        Raw8<T> y;
+        if (kind == 1) {
+          y = turned(raw[u], next);
+        } else {
+          y = raw[u];
+          next();
+        }
         if (in && hh < h1) {
-          y.store(dst + row * hd + d0);
+          y.store(dst + hh * apart);
           if (kind == 1 && l == 0) {
+            const long long row = row0 + ((long long)hh << c.lg_rows);
             c.pos[row] = a.row_pos[tok];
             if (a.weight) a.weight[row] = 0.f;
           }
@@ -290,6 +322,12 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_any_kernel(const __g
   }
 }
 
+template <typename T, int LPR>
+cudaError_t run_whole(const PagedAppendArgs& a, unsigned grid, int per_warp, int splits, cudaStream_t st) {
+  return a.neox ? launch_pdl(paged_append_kernel<T, LPR, true>, dim3(grid), dim3(kWarps * 32), 0, st, a, per_warp, splits)
+                : launch_pdl(paged_append_kernel<T, LPR, false>, dim3(grid), dim3(kWarps * 32), 0, st, a, per_warp, splits);
+}
+
 template <typename T>
 cudaError_t run(const PagedAppendArgs& a, cudaStream_t st) {
   if (a.pairs % (a.neox ? 8 : 4)) return launch_pdl(paged_append_any_kernel<T>, dim3(a.rows), dim3(kWarps * 32), 0, st, a);
@@ -303,7 +341,10 @@ cudaError_t run(const PagedAppendArgs& a, cudaStream_t st) {
   const int per_warp = (heads + splits - 1) / splits;
   splits = (heads + per_warp - 1) / per_warp;
   const long long warps = (long long)a.rows * splits;
-  return launch_pdl(paged_append_kernel<T>, dim3((unsigned)((warps + kWarps - 1) / kWarps)), dim3(kWarps * 32), 0, st, a, per_warp, splits);
+  const unsigned grid = (unsigned)((warps + kWarps - 1) / kWarps);
+  if (a.c.hd == 128) return run_whole<T, 16>(a, grid, per_warp, splits, st);
+  if (a.c.hd == 64) return run_whole<T, 8>(a, grid, per_warp, splits, st);
+  return run_whole<T, 0>(a, grid, per_warp, splits, st);
 }
 
 }  // namespace
