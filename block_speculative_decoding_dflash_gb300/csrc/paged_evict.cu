@@ -418,7 +418,7 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t 
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = ranks > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, paged_select_kernel, a, ranks);
   if (e != cudaSuccess) return e;
   // CTAs for every move there may be, at most what 152 SMs hold twice over

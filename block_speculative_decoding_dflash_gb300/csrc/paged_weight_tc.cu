@@ -26,7 +26,7 @@ struct WtShape {
   static constexpr int kHalves = HDP / 64;
   static constexpr int kTileB = kPtKeys * HDP * 2;
   static constexpr int kHalfB = kPtKeys * 128;
-  static constexpr int kStages = 4;
+  static constexpr int kStages = KT == 1 ? 2 : 4;       // one key tile: two CTAs to an SM
   static constexpr int kThreads = KT * 128 + 128;
   static constexpr int kK = 0, kQ = KT * kTileB, kEnd = kQ + kStages * kTileB;
   static constexpr size_t kSmem = kEnd + 1024;
@@ -38,7 +38,7 @@ struct WtRows { float nlse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; }
 
 // EXTRA: a cap or a distance bias.
 template <int HDP, int KT, bool EXTRA>
-__global__ void __launch_bounds__(KT * 128 + 128, 1)
+__global__ void __launch_bounds__(KT * 128 + 128, KT == 1 ? 2 : 1)
 paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ PagedAttnArgs a) {
   using C = WtShape<HDP, KT>;
@@ -105,9 +105,11 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
       if (slot < len) my_row = paged_row(c, seq, h, slot);
       if (my_row >= 0) pk = c.pos[my_row];
       if (slot < len && my_row < 0 && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
-      const int lo = __reduce_min_sync(0xffffffffu, pk == kPagedNoPos ? INT32_MAX : pk);
-      const int hi = __reduce_max_sync(0xffffffffu, pk);
-      if (lane == 0) { atomicMin(&s_kmin, lo); atomicMax(&s_kmax, hi); }
+      if (tiles > kDirect) {
+        const int lo = __reduce_min_sync(0xffffffffu, pk == kPagedNoPos ? INT32_MAX : pk);
+        const int hi = __reduce_max_sync(0xffffffffu, pk);
+        if (lane == 0) { atomicMin(&s_kmin, lo); atomicMax(&s_kmax, hi); }
+      }
     } else if (warp == wLoad) {
       // K, a box per page (or per 128 rows of one)
       const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
@@ -127,30 +129,37 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             tma_load_2d(sm + C::kK + t * C::kTileB + x * C::kHalfB + lane * box * 128, &mk, x * 64, y, &k_full);
       }
     }
-    __syncthreads();
+    // few query tiles are not classified: that would cost more than a tile
+    // too many
+    const bool direct = tiles <= kDirect;
+    if (!direct) __syncthreads();
     const int kmin = s_kmin, kmax = s_kmax;
     float w = 0.f;
     bool fresh = true;                      // K not yet waited for
     for (int c0 = 0; c0 < tiles; c0 += kChunk) {
       // which query tiles see any key here, and which see all of them
       const int cn = min(kChunk, tiles - c0);
-      __syncthreads();
-      for (int i = threadIdx.x; i <= cn >> 5; i += C::kThreads) some[i] = all[i] = 0u;
-      __syncthreads();
-      for (int q = warp; q < cn; q += C::kThreads / 32) {
-        int lo = INT32_MAX, hi = INT32_MIN;
-        const int r0 = (c0 + q) * tpt, r1 = min(n_new, r0 + tpt);
-        for (int i = r0 + lane; i < r1; i += 32) {
-          const int p = a.q_pos[ab.x + i];
-          lo = min(lo, p);
-          hi = max(hi, p);
-        }
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (lane == 0) {
-          const int k = paged_class(m, lo, hi, kmin, kmax, r1 - r0 == tpt);
-          if (k >= 1) atomicOr(&some[q >> 5], 1u << (q & 31));
-          if (k == 2) atomicOr(&all[q >> 5], 1u << (q & 31));
+      if (direct) {
+        if (threadIdx.x == 0) { some[0] = (1u << cn) - 1; all[0] = 0u; }
+      } else {
+        __syncthreads();
+        for (int i = threadIdx.x; i <= cn >> 5; i += C::kThreads) some[i] = all[i] = 0u;
+        __syncthreads();
+        for (int q = warp; q < cn; q += C::kThreads / 32) {
+          int lo = INT32_MAX, hi = INT32_MIN;
+          const int r0 = (c0 + q) * tpt, r1 = min(n_new, r0 + tpt);
+          for (int i = r0 + lane; i < r1; i += 32) {
+            const int p = a.q_pos[ab.x + i];
+            lo = min(lo, p);
+            hi = max(hi, p);
+          }
+          lo = __reduce_min_sync(0xffffffffu, lo);
+          hi = __reduce_max_sync(0xffffffffu, hi);
+          if (lane == 0) {
+            const int k = paged_class(m, lo, hi, kmin, kmax, r1 - r0 == tpt);
+            if (k >= 1) atomicOr(&some[q >> 5], 1u << (q & 31));
+            if (k == 2) atomicOr(&all[q >> 5], 1u << (q & 31));
+          }
         }
       }
       __syncthreads();
@@ -359,9 +368,10 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
-  // two key tiles to a CTA halve the passes over the query rows; one where
-  // two would leave SMs without work
-  const bool two = tiles / 2 * a.c.nkv * a.c.n_seq >= 152;
+  // Two key tiles to a CTA halve the passes over the query rows; one, with two
+  // CTAs to an SM, where two would leave SMs without work or where there are
+  // so few query rows that a CTA's life is its latency.
+  const bool two = tiles / 2 * a.c.nkv * a.c.n_seq >= 152 && (long long)a.rows * a.G > 3ll * kPtKeys * a.c.n_seq;
   if (a.c.hd <= 64) return two ? run<64, 2>(a, tiles, st) : run<64, 1>(a, tiles, st);
   return two ? run<128, 2>(a, tiles, st) : run<128, 1>(a, tiles, st);
 }
