@@ -74,7 +74,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   __shared__ float2 s_ml[QT * 128];                     // a row's maximum and sum, for the cluster
   __shared__ unsigned some[kBitWords], all[kBitWords];
   __shared__ unsigned bad[4][4];                        // of V tile i: [i & 3]
-  __shared__ __align__(16) int kpos[QT * 4][kPtKeys];
+  __shared__ __align__(16) int kpos[QT * 4][kPtKeys];    // a warp's key positions, and
+  __shared__ __align__(16) float kdist[EXTRA ? QT * 4 : 1][kPtKeys];   // their distances from wmin
 
   const PagedView& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,6 +326,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
     const float cap2 = a.softcap * kLog2e;
     int* kp = kpos[warp];
+    // A distance is the difference of two distances from the warp's first
+    // query, converted once a key and not once a score (a conversion takes the
+    // pipe of the exponentials); exact while the warp's queries are near each
+    // other, otherwise taken from the integers.
+    float* kd = kdist[EXTRA ? warp : 0];
+    const bool near = (long long)wmax - wmin < (1 << 23);
+    const float pqf = (float)(pq - wmin);
     float mx = -INFINITY, sum = 0.f;
 
     // positions of the tile's keys, four to a lane, loaded a tile ahead where
@@ -382,6 +390,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       if (masked || (EXTRA && a.slopes)) {
         __syncwarp();
         *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
+        if (EXTRA && a.slopes)
+          *reinterpret_cast<float4*>(kd + lane * 4) =
+              make_float4((float)(pos4.x - wmin), (float)(pos4.y - wmin), (float)(pos4.z - wmin), (float)(pos4.w - wmin));
         __syncwarp();
       }
       float x[2][32], top = -INFINITY;
@@ -417,15 +428,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= scale2;
           }
-          if (EXTRA && a.slopes) {
+          if (EXTRA && a.slopes && near) {
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
-              const int4 k = pk4[j >> 2];
-              v[j] = fmaf(-slope2, fabsf((float)(pq - k.x)), v[j]);
-              v[j + 1] = fmaf(-slope2, fabsf((float)(pq - k.y)), v[j + 1]);
-              v[j + 2] = fmaf(-slope2, fabsf((float)(pq - k.z)), v[j + 2]);
-              v[j + 3] = fmaf(-slope2, fabsf((float)(pq - k.w)), v[j + 3]);
+              const float4 k = *reinterpret_cast<const float4*>(kd + n * 32 + j);
+              v[j] = fmaf(-slope2, fabsf(pqf - k.x), v[j]);
+              v[j + 1] = fmaf(-slope2, fabsf(pqf - k.y), v[j + 1]);
+              v[j + 2] = fmaf(-slope2, fabsf(pqf - k.z), v[j + 2]);
+              v[j + 3] = fmaf(-slope2, fabsf(pqf - k.w), v[j + 3]);
             }
+          } else if (EXTRA && a.slopes) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope2, fabsf((float)(pq - kp[n * 32 + j])), v[j]);
           }
           if (masked) {
 #pragma unroll

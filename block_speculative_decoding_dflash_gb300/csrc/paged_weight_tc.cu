@@ -34,7 +34,9 @@ struct WtShape {
 
 // Of the query rows of a tile: minus lse and the slope, in log2 units, and the
 // position (kPagedNoPos, seen by nobody, for what adds nothing).
-struct WtRows { float nlse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; };
+// `base`: the first row's position, and the others' distances from it (see
+// the attention kernel), `near` whether all are exact.
+struct alignas(16) WtRows { float nlse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; float dist[kPtKeys]; int base, near; };
 
 // EXTRA: a cap or a distance bias.
 template <int HDP, int KT, bool EXTRA>
@@ -221,6 +223,17 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             p[x] = v == -INFINITY ? kPagedNoPos : a.q_pos[ab.x + tok];
             sl[x] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
           }
+          int base = 0, near = 1;
+          if (EXTRA && a.slopes) {
+            int lo = INT32_MAX, hi = INT32_MIN;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              lo = min(lo, p[x] == kPagedNoPos ? INT32_MAX : p[x]);
+              hi = max(hi, p[x]);
+            }
+            base = __reduce_min_sync(0xffffffffu, lo);
+            near = (long long)__reduce_max_sync(0xffffffffu, hi) - base < (1 << 23);
+          }
           const int s = j % kNA;
           if (j >= kNA) paged_wait(&rows_empty[s], (j / kNA - 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -230,6 +243,11 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
             rows[s].nlse2[r] = l[x];
             rows[s].pos[r] = p[x];
             rows[s].slope2[r] = sl[x];
+            if (EXTRA && a.slopes) rows[s].dist[r] = (float)(p[x] - base);
+          }
+          if (EXTRA && lane == 0) {
+            rows[s].base = base;
+            rows[s].near = near;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&rows_full[s]);
@@ -292,14 +310,20 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                 sc = 1.f;
               }
               if (EXTRA && a.slopes) {
+                if (rw.near) {
+                  const float pkf = (float)(pk - rw.base);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) {
-                  const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
-                  const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
-                  v[e] = fmaf(-sl.x, fabsf((float)(pq.x - pk)), v[e] * sc);
-                  v[e + 1] = fmaf(-sl.y, fabsf((float)(pq.y - pk)), v[e + 1] * sc);
-                  v[e + 2] = fmaf(-sl.z, fabsf((float)(pq.z - pk)), v[e + 2] * sc);
-                  v[e + 3] = fmaf(-sl.w, fabsf((float)(pq.w - pk)), v[e + 3] * sc);
+                  for (int e = 0; e < 32; e += 4) {
+                    const float4 pq = *reinterpret_cast<const float4*>(rw.dist + n * 32 + e);
+                    const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
+                    v[e] = fmaf(-sl.x, fabsf(pq.x - pkf), v[e] * sc);
+                    v[e + 1] = fmaf(-sl.y, fabsf(pq.y - pkf), v[e + 1] * sc);
+                    v[e + 2] = fmaf(-sl.z, fabsf(pq.z - pkf), v[e + 2] * sc);
+                    v[e + 3] = fmaf(-sl.w, fabsf(pq.w - pkf), v[e + 3] * sc);
+                  }
+                } else {
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = fmaf(-rw.slope2[n * 32 + e], fabsf((float)(rw.pos[n * 32 + e] - pk)), v[e] * sc);
                 }
                 sc = 1.f;
               }

@@ -240,6 +240,20 @@ def test_queries_that_see_nothing(B, dtype, hd, nq, n):
         s.check_weight(cache, lse, **m)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_positions_far_apart_and_far_out(B, dtype):
+    """Distances of queries 2^30 positions apart in one tile, and of neighbours at 2^30."""
+    s = Setup(B, [(4, 300), (3, 140)], 4, 2, 64, 16, dtype, seed=7)
+    far = 1 << 30
+    s.q_pos[:4] = torch.tensor([299, far, far + 5, 299 + (1 << 23)])
+    s.q_pos[4:] += far
+    for i in range(140):
+        s.pos[int(s.table[1, i // 16]), :, i % 16] += far
+    cache = s.device()
+    _, lse = s.check_attention(cache, slopes=torch.tensor([2.0 ** -30, 2.0 ** -29, 0.01, 2.0 ** -8]), window=1 << 30)
+    s.check_weight(cache, lse, slopes=torch.tensor([2.0 ** -30, 2.0 ** -29, 0.01, 2.0 ** -8]), window=1 << 30)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 32), ("f32", 128, 8), ("bf16", 136, 4)])
 @pytest.mark.parametrize("n", [6, 80, 300])
