@@ -109,63 +109,60 @@ __device__ __forceinline__ int paged_class(const PagedMask& m, int qmin, int qma
   return all && whole ? 2 : 1;
 }
 
-// Classifies the key tiles [t0, t1) of `keys` rows of (s, h) against queries
+// Classifies the key tiles [t0, t1) of `KEYS` rows of (s, h) against queries
 // at [qmin, qmax]: bit t - t0 of `some` / `all` in shared memory (zeroed here)
-// for classes >= 1 / 2. Called by every thread of the CTA; a warp takes kU
-// tiles at a time so that its loads are in flight together. The caller
-// synchronises afterwards.
+// for classes >= 1 / 2. Called by every thread of the CTA, which synchronises
+// afterwards. A lane takes 16 rows, so a warp 512 / KEYS tiles at a time, with
+// its loads in flight together: without branches, what is not there reads row
+// 0 of the pool. (Short code on purpose: it runs once a CTA, as fast as its
+// instructions arrive.)
 template <int KEYS>
 __device__ __forceinline__ void paged_classify(const PagedView& c, int s, int h, int len, const PagedMask& m, int qmin, int qmax,
                                                int t0, int t1, unsigned* some, unsigned* all) {
-  constexpr int kU = 8, kPer = KEYS / 32;
-  static_assert(kPer == 2 || kPer == 4, "a lane takes 2 or 4 keys");
+  constexpr int kLanes = KEYS / 16, kTiles = 32 / kLanes;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
   for (int i = threadIdx.x; i <= (t1 - t0) >> 5; i += blockDim.x) some[i] = all[i] = 0u;
   __syncthreads();
-  for (int b = t0 + warp * kU; b < t1; b += nw * kU) {
-    // loads without branches, so that they are in flight together: what is not
-    // there reads row 0 of its page or of the pool
-    int p[kU][kPer], page[kU];
+#pragma unroll 1
+  for (int b = t0 + warp * kTiles; b < t1; b += nw * kTiles) {
+    const int tile = b + lane / kLanes, slot = tile * KEYS + (lane & (kLanes - 1)) * 16;
+    const int end = tile < t1 ? len : 0;                  // rows from here on are not there
+    int page[2];
+    int4 p[4];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int slot = (b + u) * KEYS + lane * kPer;
-      page[u] = c.table[(size_t)s * c.max_pages + (slot < len ? slot >> c.lg_rows : 0)];
+    for (int u = 0; u < 2; ++u) page[u] = c.table[(size_t)s * c.max_pages + (slot + 8 * u < end ? (slot + 8 * u) >> c.lg_rows : 0)];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const bool on = (unsigned)page[u >> 1] < (unsigned)c.n_pages;
+      const long long row = on ? (((long long)page[u >> 1] * c.nkv + h) << c.lg_rows) + ((slot + 4 * u) & ((1 << c.lg_rows) - 1)) : 0;
+      p[u] = *reinterpret_cast<const int4*>(c.pos + row);
+      if (!on) p[u] = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
+      if (!on && slot + 4 * u < end && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
     }
+    int lo = INT32_MAX, hi = INT32_MIN;
+    bool whole = slot + 16 <= end;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int slot = (b + u) * KEYS + lane * kPer;
-      const bool on = (unsigned)page[u] < (unsigned)c.n_pages;
-      const long long row = (((long long)(on ? page[u] : 0) * c.nkv + h) << c.lg_rows) + (slot & ((1 << c.lg_rows) - 1));
-      if (kPer == 4) {
-        const int4 x = *reinterpret_cast<const int4*>(c.pos + row);
-        p[u][0] = x.x; p[u][1] = x.y; p[u][kPer - 2] = x.z; p[u][kPer - 1] = x.w;
-      } else {
-        const int2 x = *reinterpret_cast<const int2*>(c.pos + row);
-        p[u][0] = x.x; p[u][1] = x.y;
+    for (int u = 0; u < 4; ++u) {
+      const int v[4] = {p[u].x, p[u].y, p[u].z, p[u].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool there = v[j] != kPagedNoPos && slot + 4 * u + j < end;
+        whole = whole && there;
+        lo = min(lo, there ? v[j] : INT32_MAX);
+        hi = max(hi, there ? v[j] : INT32_MIN);
       }
-      const bool in = b + u < t1;
-      if (in && slot < len && !on && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
-#pragma unroll
-      for (int j = 0; j < kPer; ++j)
-        if (!in || !on || slot + j >= len) p[u][j] = kPagedNoPos;
     }
+    int w = whole;
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      int lo = INT32_MAX, hi = INT32_MIN;
-      bool whole = true;
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        if (p[u][j] == kPagedNoPos) whole = false;
-        else { lo = min(lo, p[u][j]); hi = max(hi, p[u][j]); }
-      }
-      lo = __reduce_min_sync(0xffffffffu, lo);
-      hi = __reduce_max_sync(0xffffffffu, hi);
-      whole = __all_sync(0xffffffffu, whole);
-      if (lane == 0 && b + u < t1) {
-        const int k = paged_class(m, qmin, qmax, lo, hi, whole);
-        if (k >= 1) atomicOr(&some[(b + u - t0) >> 5], 1u << ((b + u - t0) & 31));
-        if (k == 2) atomicOr(&all[(b + u - t0) >> 5], 1u << ((b + u - t0) & 31));
-      }
+    for (int o = 1; o < kLanes; o <<= 1) {
+      lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      w &= __shfl_xor_sync(0xffffffffu, w, o);
+    }
+    if ((lane & (kLanes - 1)) == 0 && tile < t1) {
+      const int k = paged_class(m, qmin, qmax, lo, hi, w != 0);
+      if (k >= 1) atomicOr(&some[(tile - t0) >> 5], 1u << ((tile - t0) & 31));
+      if (k == 2) atomicOr(&all[(tile - t0) >> 5], 1u << ((tile - t0) & 31));
     }
   }
 }

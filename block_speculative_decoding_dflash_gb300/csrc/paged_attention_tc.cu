@@ -323,8 +323,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const PagedSees sees = paged_sees_of(m, pq);
     const int wmin = __reduce_min_sync(0xffffffffu, valid ? pq : INT32_MAX), wmax = __reduce_max_sync(0xffffffffu, valid ? pq : INT32_MIN);
     const float slope2 = a.slopes ? a.slopes[valid ? head : h * G] * kLog2e : 0.f;
-    const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
-    const float cap2 = a.softcap * kLog2e;
+    const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+    const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
     int* kp = kpos[warp];
     // A distance is the difference of two distances from the warp's first
     // query, converted once a key and not once a score (a conversion takes the
@@ -422,8 +422,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           tmem_ld32(s_at + n * 32, v);
           tmem_ld_wait32(v);
           if (EXTRA && a.softcap > 0.f) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * scale2, cap2);
+            cap_tanh32(v, cap);
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= scale2;

@@ -151,12 +151,57 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 // cap2 * tanh(x / 2 / log2(e)) for x in log2 units of e^(2 z): 1 - 2 / (1 + e^2z),
 // whose error is a few 2^-24 of cap2 everywhere (a hardware tanh has 2^-11).
 __device__ __forceinline__ float cap_tanh(float x, float cap2) {
   float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(x)));
   return fmaf(-2.f * cap2, r, cap2);
+}
+
+// v = cap2 * tanh(v * scale) for 32 values of every lane of a warp. Where all of
+// them are at most half the cap, as most scores are, tanh(y) / y is a polynomial
+// of degree 4 in y^2 (interpolated at the Chebyshev nodes of [0, 1/4]; within
+// 2^-23 of it in fp32), with scale and cap2 in its coefficients: six packed
+// instructions to two values, where the exponential and the reciprocal would
+// bound capped attention.
+struct CapPoly { uint64_t c[5]; float scale, cap2; };
+__device__ __forceinline__ CapPoly cap_poly(float scale, float cap2) {
+  const float c[5] = {1.0f, -0.3333306908607483f, 0.133247509598732f, -0.05298423767089844f, 0.017131345346570015f};
+  CapPoly p;
+  p.scale = scale;
+  p.cap2 = cap2;
+  float f = scale * cap2;
+#pragma unroll
+  for (int k = 0; k < 5; ++k) {
+    p.c[k] = pack2(c[k] * f, c[k] * f);
+    f *= scale * scale;
+  }
+  return p;
+}
+__device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
+  float top = 0.f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) top = fmaxf(fmaxf(top, fabsf(v[j])), fabsf(v[j + 1]));
+  if (__all_sync(0xffffffffu, top * p.scale <= 0.5f)) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) {
+      const uint64_t y = pack2(v[j], v[j + 1]), z = mul2(y, y);
+      uint64_t r = p.c[4];
+#pragma unroll
+      for (int k = 3; k >= 0; --k) r = fma2(r, z, p.c[k]);
+      unpack2(mul2(r, y), v[j], v[j + 1]);
+    }
+  } else {
+    const float twice = p.scale * 2.8853900817779268f;   // 2 log2(e)
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * twice, p.cap2);
+  }
 }
 
 // Maps of K or V as rows of head_dim (boxes of 64 elements x up to 128 rows)

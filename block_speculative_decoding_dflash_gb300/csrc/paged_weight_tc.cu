@@ -254,8 +254,8 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         }
       } else {
         const int t = warp >> 2;
-        const float scale2 = a.softcap > 0.f ? a.scale / a.softcap * (2.f * kLog2e) : a.scale * kLog2e;
-        const float cap2 = a.softcap * kLog2e;
+        const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+        const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
         const PagedSees by = paged_seen_by(m, pk);
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
@@ -305,8 +305,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
               }
               float sc = scale2;
               if (EXTRA && a.softcap > 0.f) {
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = cap_tanh(v[e] * scale2, cap2);
+                cap_tanh32(v, cap);
                 sc = 1.f;
               }
               if (EXTRA && a.slopes) {
