@@ -17,9 +17,19 @@
 // fp32 sums nor bf16 products any relative accuracy, and after the first tiles
 // nearly no tile needs it.
 //
-// P's rounding to bf16 (half a step, 2^-8 relative at most, independent from
-// key to key) adds about as much error to an output as the output's own
-// rounding to bf16 does; the sum of p is taken before it, in fp32.
+// A tile of at most 32 (64) rows, a decode or verify block's, is held 4 (2) times
+// in the tile's lanes: each warp then takes a quarter (half) of the keys, its
+// lanes' P is zero for the others', and the warps' outputs are joined at the end
+// like those of splits. The softmax of a tile takes a quarter of the time, and
+// all four warps have work.
+//
+// P as a product's operand is bf16. For those few rows, where K and V's bytes
+// are the bound, it is two bf16 parts (16 bits of p, two products), the second
+// in the half of S's columns that the first leaves free. For many, where the
+// products are the bound, it is rounded: half a step, 2^-8 relative at most
+// and independent from key to key, adds as much error to an output as the
+// output's own rounding to bf16 does (measured against fp64: 0.0023 of the norm
+// instead of 0.0017). The sum of p is taken before, in fp32.
 //
 // Rows that a query does not see get p = 0, but 0 times an infinite or NaN V is
 // NaN. So in every tile that is not wholly seen by all its queries two warps
@@ -62,8 +72,8 @@ struct TcShape {
 // EXTRA: a cap or a distance bias (their code would cost the others registers).
 template <int HDP, int QT, bool EXTRA>
 __global__ void __launch_bounds__(QT * 128 + 128, 1)
-paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
-                     const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
+paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mq32,
+                     const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
   using C = TcShape<HDP, QT>;
   constexpr int NS = C::kStages;
   constexpr int kClusterLd = HDP + 4;                   // row stride of O in shared memory: rows a bank quad apart
@@ -150,14 +160,26 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int nt = (QT == 2 && row0 + tpt < t.count) ? 2 : 1;
   PagedCursor cur(some, sh);
   bool ok = true;
+  // With one query tile of at most 64 (32) rows, its rows are there 2 (4) times,
+  // in quarters of 32 lanes, and a warp takes a half (a quarter) of the keys.
+  const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
+  const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
+  const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
 
   if (warp == wLoad) {
     // ---- loads: Q, then K and V of every tile, a box per page (or per 128 rows of one)
     if (N > 0 && lane == 0) {
-      mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
-      for (int i = 0; i < nt; ++i)
-        for (int x = 0; x < C::kHalves; ++x)
-          tma_load_3d(sm + C::kQ + i * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, t.first + row0 + i * tpt, &q_full);
+      if (rep == 1) {
+        mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
+        for (int i = 0; i < nt; ++i)
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(sm + C::kQ + i * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, t.first + row0 + i * tpt, &q_full);
+      } else {
+        mbar_expect_tx(&q_full, 4 * C::kHalves * t32 * G * 128);
+        for (int i = 0; i < 4; ++i)
+          for (int x = 0; x < C::kHalves; ++x)
+            tma_load_3d(sm + C::kQ + x * C::kHalfB + i * 32 * 128, &mq32, x * 64, h * G, t.first + row0 + (i & (4 / rep - 1)) * t32, &q_full);
+      }
     }
     const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
     const int beyond = (c.n_pages * c.nkv) << c.lg_rows;   // a row past the pool reads as zeros
@@ -219,7 +241,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           const uint64_t v = v_desc + s * (C::kTileB >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256 + q * HDP, tmem + buf * 128 + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
-          if (QT == 1) tc_commit(&o_done);
+          if (QT == 1) {
+            if (rep > 1)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256, tmem + buf * 128 + 64 + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
+            tc_commit(&o_done);
+          }
           if (last) tc_commit(&kv_empty[s]);
         }
         __syncwarp();
@@ -312,9 +339,12 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   } else if (QT == 1 || (warp >> 2) < nt) {
     // ---- softmax: one query row to a thread
     const int q = warp >> 2, quad = warp & 3, r = quad * 32 + lane;
-    const int tl = r / G, g = r - tl * G, head = h * G + g;
+    const int distinct = 4 / rep;                        // quarters of different rows
+    const int lr = rep > 1 ? lane : r;
+    const int tl = lr / G + (rep > 1 ? (quad & (distinct - 1)) * t32 : 0), g = lr % G, head = h * G + g;
     const int at_row = row0 + q * tpt + tl;
-    const bool valid = tl < tpt && at_row < t.count;
+    const bool valid = (rep > 1 ? lane < t32 * G : tl < tpt) && at_row < t.count;
+    const int n0 = rep > 1 ? quad / distinct * distinct : 0, n1 = rep > 1 ? n0 + distinct : 4;   // its chunks of 32 keys
     const int tok = t.first + (valid ? at_row : row0);
     const bool work = __any_sync(0xffffffffu, valid);
     const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
@@ -405,7 +435,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         }
         top = fmaxf(top, fmaxf(t2[0], t2[1]));
       };
-      if (!change) {
+      if (QT == 2 && !change) {
         tmem_ld32(s_at, x[0]);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -413,9 +443,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
           rise(x[n & 1]);
         }
+      } else if (!change) {
+#pragma unroll 1
+        for (int n = n0; n < n1; ++n) {
+          tmem_ld32(s_at + n * 32, x[0]);
+          tmem_ld_wait32(x[0]);
+          rise(x[0]);
+        }
       } else {
 #pragma unroll 1
-        for (int n = 0; n < 4; ++n) {
+        for (int n = n0; n < n1; ++n) {
           float* v = x[0];
           uint32_t w[32];
           const int4* pk4 = reinterpret_cast<const int4*>(kp + n * 32);
@@ -486,23 +523,62 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       const float base = mx == -INFINITY ? 0.f : mx;
       const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
       uint64_t add[2] = {0, 0};
-      tmem_ld32(s_at, x[0]);
+      // two values' p, and the bf16 pair that they are stored as
+      auto weigh = [&](const float* v, float& p0, float& p1) {
+        unpack2(fma2(pack2(v[0], v[1]), sc2, nb2), p0, p1);
+        p0 = ex2(p0);
+        p1 = ex2(p1);
+        return pack_bf16(p0, p1);
+      };
+      if (QT == 2) {
+        tmem_ld32(s_at, x[0]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        float* v = x[n & 1];
-        tmem_ld_wait32(v);
-        if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-        float w[16];
+        for (int n = 0; n < 4; ++n) {
+          float* v = x[n & 1];
+          tmem_ld_wait32(v);
+          if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+          float w[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float p0, p1;
-          unpack2(fma2(pack2(v[j], v[j + 1]), sc2, nb2), p0, p1);
-          p0 = ex2(p0);
-          p1 = ex2(p1);
-          add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
-          w[j >> 1] = __uint_as_float(pack_bf16(p0, p1));
+          for (int j = 0; j < 32; j += 2) {
+            float p0, p1;
+            w[j >> 1] = __uint_as_float(weigh(v + j, p0, p1));
+            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+          }
+          tmem_st16(s_at + n * 16, w);                   // columns whose scores have been read
         }
-        tmem_st16(s_at + n * 16, w);     // columns whose scores have been read
+      } else {
+        // P's first part goes into columns 0 .. 63, its second into 64 .. 127; in
+        // this order no chunk's parts fall on scores of the warp not yet read
+        const bool down = rep == 2 && n0 == 2;
+#pragma unroll 1
+        for (int k = n0; k < n1; ++k) {
+          const int n = down ? n0 + n1 - 1 - k : k;
+          if (rep < 4) {
+            tmem_ld32(s_at + n * 32, x[0]);
+            tmem_ld_wait32(x[0]);
+          }
+          float w[16], lo[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float p0, p1;
+            const uint32_t hi = weigh(x[0] + j, p0, p1);
+            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+            w[j >> 1] = __uint_as_float(hi);
+            lo[j >> 1] = __uint_as_float(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
+          }
+          tmem_st16(s_at + n * 16, w);
+          if (rep > 1) tmem_st16(s_at + 64 + n * 16, lo);
+        }
+        if (rep > 1) {
+          // the other warps' keys have no weight in these lanes
+          const float zero[16] = {};
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            if (n >= n0 && n < n1) continue;
+            tmem_st16(s_at + n * 16, zero);
+            tmem_st16(s_at + 64 + n * 16, zero);
+          }
+        }
       }
       float a0, a1;
       unpack2(add2(add[0], add[1]), a0, a1);
@@ -520,9 +596,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           for (unsigned b = who[w]; b; b &= b - 1) {
             const int j = w * 32 + __ffs(b) - 1, slot = tile * kPtKeys + j;
             if (slot >= len) continue;
-            const uint32_t pp = tmem_ld1(s_at + (j >> 1));
+            const uint32_t ph = tmem_ld1(s_at + (j >> 1)), pl = rep > 1 ? tmem_ld1(s_at + 64 + (j >> 1)) : 0u;
             tmem_ld_wait();
-            const float p = j & 1 ? bf_hi(pp) : bf_lo(pp);
+            const float p = j & 1 ? bf_hi(ph) + bf_hi(pl) : bf_lo(ph) + bf_lo(pl);
             const long long row = paged_row(c, t.seq, h, slot);
             if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
             const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
@@ -554,7 +630,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const size_t at = (size_t)tok * a.nq + head;
     const bool none = sum == 0.f;                        // nothing seen (a NaN score makes the sum NaN)
     const float inv = none ? 0.f : 1.f / sum;
-    if (a.cluster) {
+    if (joins) {
       // every copy into this memory has landed and been used by an MMA that is done
       fence_proxy_async_shared();
       s_ml[q * 128 + r] = make_float2(mx, valid ? sum : 0.f);
@@ -568,9 +644,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           tmem_ld_wait32(o);
         }
         if (!valid) continue;
-        if (a.splits > 1) {
-          float* po = a.cluster ? reinterpret_cast<float*>(sm) + (q * 128 + r) * kClusterLd + d
-                                : a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
+        if (joins || a.splits > 1) {
+          float* po = joins ? reinterpret_cast<float*>(sm) + (q * 128 + r) * kClusterLd + d
+                            : a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
 #pragma unroll
           for (int x = 0; x < 32; x += 4)
             if (d + x < c.hd && !none) *reinterpret_cast<float4*>(po + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
@@ -588,49 +664,70 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           }
         }
       }
-      if (valid && !a.cluster) {
+      if (valid && !joins) {
         if (a.splits > 1) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx, sum);
         else if (a.lse) a.lse[at] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
   }
-  if (a.cluster) {
-    // The splits are the cluster's CTAs: each joins its share of the rows' 4
-    // dimensions at a time, o = sum_z o_z exp2(m_z - M) / sum_z l_z exp2(m_z - M),
-    // out of the others' shared memory.
+  if (joins) {
+    // The parts of a row, `rep` in each CTA and the CTAs of the cluster where
+    // those are the splits, are joined out of shared memory 4 dimensions at a
+    // time: o = sum_x o_x exp2(m_x - M) / sum_x l_x exp2(m_x - M).
     cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
-    const int rows = nt * 128, quads = c.hd >> 2;
-    for (int e = z * C::kThreads + (int)threadIdx.x; e < rows * quads; e += a.splits * C::kThreads) {
-      const int R = e / quads, d = (e - R * quads) * 4, r = R & 127, tl = r / G, at_row = row0 + (R >> 7) * tpt + tl;
-      if (tl >= tpt || at_row >= t.count) continue;
-      float2 ml[kMaxCluster];
-      float4 o[kMaxCluster];
+    if (a.cluster) cl.sync();
+    else __syncthreads();
+    const int ctas = a.cluster ? a.splits : 1, rows = nt * 128 / rep, quads = c.hd >> 2;
+    for (int e = (a.cluster ? z : 0) * C::kThreads + (int)threadIdx.x; e < rows * quads; e += ctas * C::kThreads) {
+      const int R = e / quads, d = (e - R * quads) * 4, lr = rep > 1 ? R & 31 : R & 127;
+      const int tl = lr / G + (rep > 1 ? (R >> 5) * t32 : 0), at_row = row0 + (rep > 1 ? 0 : (R >> 7) * tpt) + tl;
+      if ((rep > 1 ? lr >= t32 * G : tl >= tpt) || at_row >= t.count) continue;
       float M = -INFINITY, L = 0.f;
-#pragma unroll
-      for (int x = 0; x < kMaxCluster; ++x) {
-        ml[x] = x < a.splits ? *cl.map_shared_rank(&s_ml[R], x) : make_float2(-INFINITY, 0.f);
-        if (x < a.splits) o[x] = *reinterpret_cast<const float4*>(cl.map_shared_rank(reinterpret_cast<float*>(sm) + R * kClusterLd + d, x));
-        M = fmaxf(M, ml[x].x);
-      }
-      const float base = M == -INFINITY ? 0.f : M;
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+      for (int y = 0; y < rep; ++y) {
+        const int at = R + y * rows;
+        float2 ml[kMaxCluster];
+        float4 o[kMaxCluster];
+        float top = M;
 #pragma unroll
-      for (int x = 0; x < kMaxCluster; ++x) {
-        if (ml[x].y == 0.f) continue;                    // it saw nothing: its o was not written
-        const float f = ex2(ml[x].x - base);
-        L = fmaf(ml[x].y, f, L);
-        v.x = fmaf(o[x].x, f, v.x);
-        v.y = fmaf(o[x].y, f, v.y);
-        v.z = fmaf(o[x].z, f, v.z);
-        v.w = fmaf(o[x].w, f, v.w);
+        for (int x = 0; x < kMaxCluster; ++x) {
+          ml[x] = make_float2(-INFINITY, 0.f);
+          if (x < ctas) {
+            const float2* pm = &s_ml[at];
+            const float* po = reinterpret_cast<const float*>(sm) + at * kClusterLd + d;
+            ml[x] = *(a.cluster ? cl.map_shared_rank(pm, x) : pm);
+            o[x] = *reinterpret_cast<const float4*>(a.cluster ? cl.map_shared_rank(po, x) : po);
+          }
+          top = fmaxf(top, ml[x].x);
+        }
+        const float base = top == -INFINITY ? 0.f : top, old = ex2(M - base);
+        M = top;
+        L *= old;
+        v.x *= old; v.y *= old; v.z *= old; v.w *= old;
+#pragma unroll
+        for (int x = 0; x < kMaxCluster; ++x) {
+          if (ml[x].y == 0.f) continue;                  // it saw nothing: its o was not written
+          const float f = ex2(ml[x].x - base);
+          L = fmaf(ml[x].y, f, L);
+          v.x = fmaf(o[x].x, f, v.x);
+          v.y = fmaf(o[x].y, f, v.y);
+          v.z = fmaf(o[x].z, f, v.z);
+          v.w = fmaf(o[x].w, f, v.w);
+        }
+      }
+      const size_t at = (size_t)(t.first + at_row) * a.nq + h * G + lr % G;
+      if (a.splits > 1 && !a.cluster) {
+        const size_t part = (size_t)z * a.rows * a.nq + at;
+        *reinterpret_cast<float4*>(a.part_o + part * c.hd + d) = v;
+        if (d == 0) a.part_ml[part] = make_float2(M, L);
+        continue;
       }
       const float inv = L == 0.f ? 0.f : 1.f / L;
-      const size_t at = (size_t)(t.first + at_row) * a.nq + h * G + r - tl * G;
       *reinterpret_cast<uint2*>(static_cast<bf16*>(a.out) + at * c.hd + d) = make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv));
       if (d == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     }
-    cl.sync();                                           // no CTA leaves while another reads it
+    if (a.cluster) cl.sync();                            // no CTA leaves while another reads it
   }
   if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
   tc_fence_before();
@@ -644,8 +741,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 
 template <int HDP, int QT>
 cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
-  CUtensorMap mq, mk, mv;
-  if (!paged_map_rows(&mq, a.q, a, kPtKeys / a.G) || !paged_map_pages(&mk, a.c.k, a.c) || !paged_map_pages(&mv, a.c.v, a.c))
+  CUtensorMap mq, mq32, mk, mv;
+  if (!paged_map_rows(&mq, a.q, a, kPtKeys / a.G) || !paged_map_rows(&mq32, a.q, a, a.G <= 32 ? 32 / a.G : 1) || !paged_map_pages(&mk, a.c.k, a.c) || !paged_map_pages(&mv, a.c.v, a.c))
     return cudaErrorInvalidValue;
   using C = TcShape<HDP, QT>;
   const bool extra = a.softcap > 0.f || a.slopes;
@@ -666,7 +763,7 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   attr[1].val.clusterDim.z = a.splits;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, mq, mk, mv, a);
+  return cudaLaunchKernelEx(&cfg, kernel, mq, mq32, mk, mv, a);
 }
 
 }  // namespace
