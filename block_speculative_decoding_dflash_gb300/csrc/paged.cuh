@@ -37,29 +37,38 @@ __device__ __forceinline__ long long paged_row(const PagedView& c, int s, int h,
 // the last tile.
 struct PagedTile { int seq, tile, first, count; };
 __device__ __forceinline__ PagedTile paged_find_tile(const int* start, int n_seq, int rows, int G, int per, int t) {
+  constexpr int kU = 4;                      // sequences of a lane requested together
   const int lane = threadIdx.x & 31;
   PagedTile r{-1, 0, 0, 0};
-  for (int s0 = 0; s0 < n_seq; s0 += 32) {
-    const int s = s0 + lane;
-    int2 ab = make_int2(0, 0);
-    if (s < n_seq) ab = paged_new_rows(start, s, rows);
-    const int tiles = (int)(((long long)(ab.y - ab.x) * G + per - 1) / per);
-    int incl = tiles;
+  for (int s0 = 0; s0 < n_seq; s0 += 32 * kU) {
+    int2 ab[kU];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
+    for (int u = 0; u < kU; ++u) {
+      const int s = s0 + u * 32 + lane;
+      ab[u] = s < n_seq ? make_int2(start[s], start[s + 1]) : make_int2(0, 0);
     }
-    const unsigned hit = __ballot_sync(0xffffffffu, t < incl);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      r.seq = s0 + l;
-      r.tile = t - __shfl_sync(0xffffffffu, incl - tiles, l);
-      r.first = __shfl_sync(0xffffffffu, ab.x, l);
-      r.count = __shfl_sync(0xffffffffu, ab.y - ab.x, l);
-      return r;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (s0 + u * 32 >= n_seq) break;
+      const int a = min(max(ab[u].x, 0), rows), b = min(max(ab[u].y, a), rows);
+      const int tiles = (int)(((long long)(b - a) * G + per - 1) / per);
+      int incl = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const unsigned hit = __ballot_sync(0xffffffffu, t < incl);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        r.seq = s0 + u * 32 + l;
+        r.tile = t - __shfl_sync(0xffffffffu, incl - tiles, l);
+        r.first = __shfl_sync(0xffffffffu, a, l);
+        r.count = __shfl_sync(0xffffffffu, b - a, l);
+        return r;
+      }
+      t -= __shfl_sync(0xffffffffu, incl, 31);
     }
-    t -= __shfl_sync(0xffffffffu, incl, 31);
   }
   return r;
 }

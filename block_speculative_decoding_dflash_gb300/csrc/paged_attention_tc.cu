@@ -139,9 +139,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     qmax = __reduce_max_sync(0xffffffffu, qmax);
   }
   PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
-  const bool direct = paged_direct(sh);
+  // One query tile without a window sees nearly every row there is: no
+  // classification beforehand, the warps that need to know look at a tile's
+  // positions, which they request a tile ahead.
+  const bool direct = paged_direct(sh) || (QT == 1 && !sh.by_share);
   if (direct) {
-    if (threadIdx.x == 0) { some[0] = (1u << sh.take) - 1; all[0] = 0u; }
+    for (int i = threadIdx.x; i <= sh.take >> 5; i += C::kThreads) {
+      const int left = sh.take - i * 32;
+      some[i] = left >= 32 ? 0xffffffffu : (1u << left) - 1;
+      all[i] = 0u;
+    }
   } else {
     paged_classify<kPtKeys>(c, t.seq, h, len, m, qmin, qmax, sh.t0, sh.t1, some, all);
   }
@@ -165,6 +172,32 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
   const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
   const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
+
+  // The page of a lane's four keys of a tile (-1: none) and their positions; a
+  // page is requested two tiles ahead and positions one, so that neither load
+  // waits for the other.
+  auto page_of = [&](int rel) {
+    const int slot = (sh.t0 + rel) * kPtKeys + lane * 4;
+    return rel >= 0 && slot < len ? c.table[(size_t)t.seq * c.max_pages + (slot >> c.lg_rows)] : -1;
+  };
+  auto positions = [&](int rel, int page) {
+    int4 p = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
+    const int slot = (sh.t0 + rel) * kPtKeys + lane * 4;
+    if (rel >= 0 && (unsigned)page < (unsigned)c.n_pages) {
+      p = *reinterpret_cast<const int4*>(c.pos + ((((long long)page * c.nkv + h) << c.lg_rows) + (slot & ((1 << c.lg_rows) - 1))));
+      if (slot + 1 >= len) p.y = kPagedNoPos;
+      if (slot + 2 >= len) p.z = kPagedNoPos;
+      if (slot + 3 >= len) p.w = kPagedNoPos;
+    }
+    return p;
+  };
+  struct Span { int lo, hi; bool whole; };
+  auto span = [&](const int4& p) {
+    const bool there = p.x != kPagedNoPos && p.y != kPagedNoPos && p.z != kPagedNoPos && p.w != kPagedNoPos;
+    return Span{__reduce_min_sync(0xffffffffu, min(min(p.x, p.y), min(p.z, p.w))),
+                __reduce_max_sync(0xffffffffu, max(max(p.x, p.y), max(p.z, p.w))), __all_sync(0xffffffffu, there) != 0};
+  };
+  auto classified = [&](int rel) { return !direct && ((all[rel >> 5] >> (rel & 31)) & 1u); };
 
   if (warp == wLoad) {
     // ---- loads: Q, then K and V of every tile, a box per page (or per 128 rows of one)
@@ -303,14 +336,31 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   } else if (warp > wMma) {
     // ---- V's non-finite rows, in tiles that some query sees only in part
     const int half = warp - wMma - 1;
+    const bool look = QT == 1 && direct;
+    int rel = cur.next(), rel1 = cur.next(), page1 = -1;
+    int4 pos4 = make_int4(0, 0, 0, 0);
+    if (look) {
+      const int page = page_of(rel);
+      page1 = page_of(rel1);
+      pos4 = positions(rel, page);
+    }
     for (int i = 0; i < N; ++i) {
-      const int rel = cur.next(), n = 2 * i + 1, s = n % NS;
+      const int n = 2 * i + 1, s = n % NS;
+      bool full = classified(rel);
+      if (look) {
+        const Span k = span(pos4);
+        full = k.whole && paged_class(m, qmin, qmax, k.lo, k.hi, true) == 2;
+        pos4 = positions(rel1, page1);
+      }
+      rel = rel1;
+      rel1 = cur.next();
+      if (look) page1 = page_of(rel1);
       paged_wait(&kv_full[s], (n / NS) & 1, ok);
       if (!__all_sync(0xffffffffu, ok)) {
         ok = false;
         break;
       }
-      if (!((all[rel >> 5] >> (rel & 31)) & 1u)) {
+      if (!full) {
         uint8_t* v = sm + C::kKV + s * C::kTileB;
         for (int x = 0; x < 2; ++x) {
           const int r = half * 64 + x * 32 + lane;
@@ -367,21 +417,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 
     // positions of the tile's keys, four to a lane, loaded a tile ahead where
     // they will be needed
-    int rel = cur.next();
-    int4 pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
-    auto fetch = [&]() {
-      pos4 = make_int4(kPagedNoPos, kPagedNoPos, kPagedNoPos, kPagedNoPos);
-      if (rel < 0 || (!(EXTRA && a.slopes) && ((all[rel >> 5] >> (rel & 31)) & 1u))) return;
-      const int slot = (sh.t0 + rel) * kPtKeys + lane * 4;
-      const long long row = slot < len ? paged_row(c, t.seq, h, slot) : -1;
-      if (row >= 0) {
-        pos4 = *reinterpret_cast<const int4*>(c.pos + row);
-        if (slot + 1 >= len) pos4.y = kPagedNoPos;
-        if (slot + 2 >= len) pos4.z = kPagedNoPos;
-        if (slot + 3 >= len) pos4.w = kPagedNoPos;
-      }
+    int rel = cur.next(), rel1 = cur.next(), page1 = page_of(rel1);
+    int4 pos4 = positions(rel, page_of(rel));
+    auto advance = [&]() {
+      rel = rel1;
+      if (rel >= 0 && ((EXTRA && a.slopes) || !classified(rel))) pos4 = positions(rel, page1);
+      rel1 = cur.next();
+      page1 = page_of(rel1);
     };
-    if (work) fetch();
     if (N > 0 && work) {
       const uint32_t zero[32] = {};
 #pragma unroll
@@ -398,11 +441,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       }
       tc_fence_after();
       if (!work) {                                       // rows of nobody: their P may be anything
-        cur.next();
         mbar_arrive(&p_ready[buf]);
         continue;
       }
-      const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
+      bool full = classified(rel);
       const int tile = sh.t0 + rel;
       // First pass over S: the row's maximum. What a mask, cap or bias makes of
       // a score is put back in its place, so that the second pass is the same
@@ -411,10 +453,9 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       // wholly seen by this warp's rows)
       bool masked = !full;
       if (masked) {
-        const bool there = pos4.x != kPagedNoPos && pos4.y != kPagedNoPos && pos4.z != kPagedNoPos && pos4.w != kPagedNoPos;
-        const int kmin = __reduce_min_sync(0xffffffffu, min(min(pos4.x, pos4.y), min(pos4.z, pos4.w)));
-        const int kmax = __reduce_max_sync(0xffffffffu, max(max(pos4.x, pos4.y), max(pos4.z, pos4.w)));
-        masked = !__all_sync(0xffffffffu, there) || paged_class(m, wmin, wmax, kmin, kmax, true) != 2;
+        const Span k = span(pos4);
+        masked = !k.whole || paged_class(m, wmin, wmax, k.lo, k.hi, true) != 2;
+        if (QT == 1 && direct) full = k.whole && paged_class(m, qmin, qmax, k.lo, k.hi, true) == 2;
       }
       const bool change = masked || (EXTRA && (a.slopes || a.softcap > 0.f));
       if (masked || (EXTRA && a.slopes)) {
@@ -618,8 +659,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       }
       tc_fence_before();
       mbar_arrive(&p_ready[buf]);
-      rel = cur.next();
-      fetch();
+      advance();
     }
     // ---- the row's output, or its split's partial (to shared memory for the
     // cluster, else to the workspace)
