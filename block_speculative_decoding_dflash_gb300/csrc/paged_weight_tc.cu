@@ -1,13 +1,16 @@
 // Key weights on the tensor cores (bf16, head_dim <= 128): for every cached row
 // of a (sequence, kv head) the sum over the query rows of exp(t - lse).
 //
-// S^T = K Q^T: a CTA holds KT tiles of 128 keys as the A operands and passes
-// the query rows by as B, 128 at a time. A key is a TMEM lane, so one thread
-// owns it for the whole pass and adds up its row of S^T in registers: no
-// exchange between threads, no atomics, and a fixed order. S has two buffers
-// per key tile; the exponentials of one run while the next is computed.
-// Bounded by them: one ex2 to a score (three with a cap), against 2 head_dim
-// flops on the tensor cores.
+// S^T = K Q^T: a CTA holds a tile of 128 keys as the A operand and passes the
+// query rows by as B, 128 at a time. A key is a TMEM lane, so one thread owns it
+// for the whole pass and adds up its row of S^T in registers: no exchange
+// between threads, no atomics, and a fixed order. S has two buffers; the
+// exponentials of one run while the next is computed, and a second CTA on the SM
+// works while this one starts or ends. Bounded by the exponentials, one ex2 to a
+// score, against 2 head_dim flops on the tensor cores, for many query rows, and
+// by a CTA's start and end for few.
+// (Two key tiles to a CTA, which would halve the passes over the query rows, and
+// one CTA to an SM took 166 us instead of 154 us for 512 rows over 32768 keys.)
 #include <math.h>
 
 #include "paged_tc.cuh"
@@ -21,14 +24,14 @@ constexpr int kChunk = 8192;               // query tiles classified at a time
 constexpr int kBitWords = kChunk / 32 + 1;
 constexpr int kNA = 4;                     // rows' lse, position and slope: ring stages
 
-template <int HDP, int KT>
+template <int HDP>
 struct WtShape {
   static constexpr int kHalves = HDP / 64;
   static constexpr int kTileB = kPtKeys * HDP * 2;
   static constexpr int kHalfB = kPtKeys * 128;
-  static constexpr int kStages = KT == 1 ? 2 : 4;       // one key tile: two CTAs to an SM
-  static constexpr int kThreads = KT * 128 + 128;
-  static constexpr int kK = 0, kQ = KT * kTileB, kEnd = kQ + kStages * kTileB;
+  static constexpr int kStages = 2;
+  static constexpr int kThreads = 256;
+  static constexpr int kK = 0, kQ = kTileB, kEnd = kQ + kStages * kTileB;
   static constexpr size_t kSmem = kEnd + 1024;
 };
 
@@ -39,14 +42,14 @@ struct WtShape {
 struct alignas(16) WtRows { float nlse2[kPtKeys]; float slope2[kPtKeys]; int pos[kPtKeys]; float dist[kPtKeys]; int base, near; };
 
 // EXTRA: a cap or a distance bias.
-template <int HDP, int KT, bool EXTRA>
-__global__ void __launch_bounds__(KT * 128 + 128, KT == 1 ? 2 : 1)
+template <int HDP, bool EXTRA>
+__global__ void __launch_bounds__(256, 2)
 paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ PagedAttnArgs a) {
-  using C = WtShape<HDP, KT>;
+  using C = WtShape<HDP>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t k_full, q_full[NS], q_empty[NS], rows_full[kNA], rows_empty[kNA], s_full[KT][2], s_empty[KT][2];
+  __shared__ uint64_t k_full, q_full[NS], q_empty[NS], rows_full[kNA], rows_empty[kNA], s_full[2], s_empty[2];
   __shared__ uint32_t tmem_holder;
   __shared__ int s_kmin, s_kmax;
   __shared__ unsigned some[kBitWords], all[kBitWords];
@@ -57,15 +60,14 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   const int h = blockIdx.y, seq = blockIdx.z, G = a.G, tpt = kPtKeys / G;
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
-  constexpr int wMma = KT * 4, wLoad = KT * 4 + 1, wRows = KT * 4 + 2;
-  constexpr unsigned kTmemCols = KT * 256;
+  constexpr int wMma = 4, wLoad = 5, wRows = 6;
+  constexpr unsigned kTmemCols = 256;
 
   if (threadIdx.x == wLoad * 32) {
     mbar_init(&k_full, 1);
     for (int i = 0; i < NS; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
-    for (int i = 0; i < kNA; ++i) { mbar_init(&rows_full[i], 1); mbar_init(&rows_empty[i], KT * 4); }
-    for (int i = 0; i < KT; ++i)
-      for (int b = 0; b < 2; ++b) { mbar_init(&s_full[i][b], 1); mbar_init(&s_empty[i][b], 128); }
+    for (int i = 0; i < kNA; ++i) { mbar_init(&rows_full[i], 1); mbar_init(&rows_empty[i], 4); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_empty[b], 128); }
     fence_mbar_init();
     tma_prefetch_desc(&mq);
     tma_prefetch_desc(&mk);
@@ -97,7 +99,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   unsigned it = 0;                         // query tiles passed by, over the whole kernel
   unsigned kn = 0;                         // key tiles loaded
 
-  for (int k0 = blockIdx.x * KT * kPtKeys; k0 < len; k0 += gridDim.x * KT * kPtKeys, ++kn) {
+  for (int k0 = blockIdx.x * kPtKeys; k0 < len; k0 += gridDim.x * kPtKeys, ++kn) {
     if (threadIdx.x == 0) { s_kmin = INT32_MAX; s_kmax = INT32_MIN; }
     __syncthreads();
     const int slot = k0 + (int)threadIdx.x;
@@ -116,20 +118,18 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
       // K, a box per page (or per 128 rows of one)
       const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
       const int beyond = (c.n_pages * c.nkv) << c.lg_rows;
-      if (lane == 0) mbar_expect_tx(&k_full, KT * C::kTileB);
+      if (lane == 0) mbar_expect_tx(&k_full, C::kTileB);
       __syncwarp();
-      for (int t = 0; t < KT; ++t) {
-        const int at = k0 + t * kPtKeys + lane * box;
-        int y = beyond;
-        if (lane < boxes && at < len) {
-          const long long row = paged_row(c, seq, h, at);
-          if (row >= 0) y = (int)row;
-        }
-        if (lane < boxes)
-#pragma unroll
-          for (int x = 0; x < C::kHalves; ++x)
-            tma_load_2d(sm + C::kK + t * C::kTileB + x * C::kHalfB + lane * box * 128, &mk, x * 64, y, &k_full);
+      const int at = k0 + lane * box;
+      int y = beyond;
+      if (lane < boxes && at < len) {
+        const long long row = paged_row(c, seq, h, at);
+        if (row >= 0) y = (int)row;
       }
+      if (lane < boxes)
+#pragma unroll
+        for (int x = 0; x < C::kHalves; ++x)
+          tma_load_2d(sm + C::kK + x * C::kHalfB + lane * box * 128, &mk, x * 64, y, &k_full);
     }
     // few query tiles are not classified: that would cost more than a tile
     // too many
@@ -192,19 +192,15 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           const unsigned j = it + i;
           const int s = j % NS, b = j & 1;
           paged_wait(&q_full[s], (j / NS) & 1, ok);
-#pragma unroll
-          for (int t = 0; t < KT; ++t) {
-            if (j >= 2) paged_wait(&s_empty[t][b], ((j >> 1) - 1) & 1, ok);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            tc_fence_after();
-            if (leader) {
-              tc_scores<C::kHalves>(tmem + (t * 2 + b) * 128, k_desc + t * (C::kTileB >> 4), q_desc + s * (C::kTileB >> 4), ksteps);
-              tc_commit(&s_full[t][b]);
-              if (t == KT - 1) tc_commit(&q_empty[s]);
-            }
-            __syncwarp();
+          if (j >= 2) paged_wait(&s_empty[b], ((j >> 1) - 1) & 1, ok);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc_fence_after();
+          if (leader) {
+            tc_scores<C::kHalves>(tmem + b * 128, k_desc, q_desc + s * (C::kTileB >> 4), ksteps);
+            tc_commit(&s_full[b]);
+            tc_commit(&q_empty[s]);
           }
-          if (!ok) break;
+          __syncwarp();
         }
       } else if (warp >= wRows) {
         // lse, position and slope of the rows of every other tile
@@ -253,7 +249,6 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           if (lane == 0) mbar_arrive(&rows_full[s]);
         }
       } else {
-        const int t = warp >> 2;
         const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
         const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
         const PagedSees by = paged_seen_by(m, pk);
@@ -261,9 +256,9 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           const unsigned j = it + i;
           const int rel = cur.next(), b = j & 1, s = j % kNA;
           const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
-          const uint32_t s_at = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + (t * 2 + b) * 128;
+          const uint32_t s_at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * 128;
           paged_wait(&rows_full[s], (j / kNA) & 1, ok);
-          paged_wait(&s_full[t][b], (j >> 1) & 1, ok);
+          paged_wait(&s_full[b], (j >> 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
           const WtRows& rw = rows[s];
@@ -280,7 +275,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                 tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
               } else {
                 tc_fence_before();
-                mbar_arrive(&s_empty[t][b]);
+                mbar_arrive(&s_empty[b]);
               }
               const ulonglong2* nl = reinterpret_cast<const ulonglong2*>(rw.nlse2 + n * 32);
 #pragma unroll
@@ -301,7 +296,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
               tmem_ld_wait32(v);
               if (n == 3) {
                 tc_fence_before();
-                mbar_arrive(&s_empty[t][b]);
+                mbar_arrive(&s_empty[b]);
               }
               float sc = scale2;
               if (EXTRA && a.softcap > 0.f) {
@@ -370,7 +365,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   }
 }
 
-template <int HDP, int KT>
+template <int HDP>
 cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   CUtensorMap mq, mk;
   // without new rows there is nothing to map: K's map stands in, unread
@@ -380,23 +375,17 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   } else {
     mq = mk;
   }
-  using C = WtShape<HDP, KT>;
-  auto kernel = a.softcap > 0.f || a.slopes ? paged_weight_tc_kernel<HDP, KT, true> : paged_weight_tc_kernel<HDP, KT, false>;
+  using C = WtShape<HDP>;
+  auto kernel = a.softcap > 0.f || a.slopes ? paged_weight_tc_kernel<HDP, true> : paged_weight_tc_kernel<HDP, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
-  const long long x = (tiles + KT - 1) / KT;
-  return launch_pdl(kernel, dim3((unsigned)x, a.c.nkv, a.c.n_seq), dim3(C::kThreads), C::kSmem, st, mq, mk, a);
+  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.c.n_seq), dim3(C::kThreads), C::kSmem, st, mq, mk, a);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
-  // Two key tiles to a CTA halve the passes over the query rows; one, with two
-  // CTAs to an SM, where two would leave SMs without work or where there are
-  // so few query rows that a CTA's life is its latency.
-  const bool two = tiles / 2 * a.c.nkv * a.c.n_seq >= 152 && (long long)a.rows * a.G > 3ll * kPtKeys * a.c.n_seq;
-  if (a.c.hd <= 64) return two ? run<64, 2>(a, tiles, st) : run<64, 1>(a, tiles, st);
-  return two ? run<128, 2>(a, tiles, st) : run<128, 1>(a, tiles, st);
+  return a.c.hd <= 64 ? run<64>(a, tiles, st) : run<128>(a, tiles, st);
 }
 
 }  // namespace dfl
