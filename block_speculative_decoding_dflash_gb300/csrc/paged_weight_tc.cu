@@ -49,7 +49,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   using C = WtShape<HDP>;
   constexpr int NS = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t k_full, q_full[NS], q_empty[NS], rows_full[kNA], rows_empty[kNA], s_full[2], s_empty[2];
+  __shared__ uint64_t k_full[2], k_empty[2], q_full[NS], q_empty[NS], rows_full[kNA], rows_empty[kNA], s_full[2], s_empty[2];
   __shared__ uint32_t tmem_holder;
   __shared__ int s_kmin, s_kmax;
   __shared__ unsigned some[kBitWords], all[kBitWords];
@@ -64,7 +64,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   constexpr unsigned kTmemCols = 256;
 
   if (threadIdx.x == wLoad * 32) {
-    mbar_init(&k_full, 1);
+    for (int i = 0; i < 2; ++i) { mbar_init(&k_full[i], 1); mbar_init(&k_empty[i], 1); }
     for (int i = 0; i < NS; ++i) { mbar_init(&q_full[i], 1); mbar_init(&q_empty[i], 1); }
     for (int i = 0; i < kNA; ++i) { mbar_init(&rows_full[i], 1); mbar_init(&rows_empty[i], 4); }
     for (int b = 0; b < 2; ++b) { mbar_init(&s_full[b], 1); mbar_init(&s_empty[b], 128); }
@@ -96,6 +96,203 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   tc_fence_after();
   const uint32_t tmem = tmem_holder;
   bool ok = true;
+
+  // lse, position and slope of the query rows of tile q, four to a lane
+  struct RowData { float l[4], sl[4]; int p[4], base, near; };
+  auto row_data = [&](int q) {
+    RowData d;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = x * 32 + lane, tl = r / G, tok = q * tpt + tl, head = h * G + r - tl * G;
+      const bool in = tl < tpt && tok < n_new;
+      const float v = in ? a.lse[(size_t)(ab.x + tok) * a.nq + head] : -INFINITY;
+      d.l[x] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+      d.p[x] = v == -INFINITY ? kPagedNoPos : a.q_pos[ab.x + tok];
+      d.sl[x] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+    }
+    d.base = 0;
+    d.near = 1;
+    if (EXTRA && a.slopes) {
+      int lo = INT32_MAX, hi = INT32_MIN;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        lo = min(lo, d.p[x] == kPagedNoPos ? INT32_MAX : d.p[x]);
+        hi = max(hi, d.p[x]);
+      }
+      d.base = __reduce_min_sync(0xffffffffu, lo);
+      d.near = (long long)__reduce_max_sync(0xffffffffu, hi) - d.base < (1 << 23);
+    }
+    return d;
+  };
+  auto put_rows = [&](WtRows& to, const RowData& d) {
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int r = x * 32 + lane;
+      to.nlse2[r] = d.l[x];
+      to.pos[r] = d.p[x];
+      to.slope2[r] = d.sl[x];
+      if (EXTRA && a.slopes) to.dist[r] = (float)(d.p[x] - d.base);
+    }
+    if (EXTRA && lane == 0) {
+      to.base = d.base;
+      to.near = d.near;
+    }
+  };
+  // adds the exponentials of 32 query rows (from row n * 32 of `rw`) to two sums
+  const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
+  const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
+  auto add_chunk = [&](float* v, const WtRows& rw, int n, const PagedSees& by, int pk, bool full, uint64_t* add) {
+    float sc = scale2;
+    if (EXTRA && a.softcap > 0.f) {
+      cap_tanh32(v, cap);
+      sc = 1.f;
+    }
+    if (EXTRA && a.slopes) {
+      if (rw.near) {
+        const float pkf = (float)(pk - rw.base);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 pq = *reinterpret_cast<const float4*>(rw.dist + n * 32 + e);
+          const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
+          v[e] = fmaf(-sl.x, fabsf(pq.x - pkf), v[e] * sc);
+          v[e + 1] = fmaf(-sl.y, fabsf(pq.y - pkf), v[e + 1] * sc);
+          v[e + 2] = fmaf(-sl.z, fabsf(pq.z - pkf), v[e + 2] * sc);
+          v[e + 3] = fmaf(-sl.w, fabsf(pq.w - pkf), v[e + 3] * sc);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = fmaf(-rw.slope2[n * 32 + e], fabsf((float)(rw.pos[n * 32 + e] - pk)), v[e] * sc);
+      }
+      sc = 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 4) {
+      const float4 l = *reinterpret_cast<const float4*>(rw.nlse2 + n * 32 + e);
+      const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
+      const float p0 = ex2(fmaf(v[e], sc, l.x)), p1 = ex2(fmaf(v[e + 1], sc, l.y));
+      const float p2 = ex2(fmaf(v[e + 2], sc, l.z)), p3 = ex2(fmaf(v[e + 3], sc, l.w));
+      add[0] = add2(add[0], pack2(full || paged_sees(by, pq.x) ? p0 : 0.f, full || paged_sees(by, pq.y) ? p1 : 0.f));
+      add[1] = add2(add[1], pack2(full || paged_sees(by, pq.z) ? p2 : 0.f, full || paged_sees(by, pq.w) ? p3 : 0.f));
+    }
+  };
+  const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;   // K arrives a page (or 128 rows of one) at a time
+  const int beyond = (c.n_pages * c.nkv) << c.lg_rows;                   // a row past the pool reads as zeros
+  auto k_row = [&](int k0) {
+    const int at = k0 + lane * box;
+    const long long row = lane < boxes && at < len ? paged_row(c, seq, h, at) : -1;
+    return row >= 0 ? (int)row : beyond;
+  };
+  auto load_k = [&](uint8_t* to, int y, uint64_t* bar) {
+    if (lane == 0) mbar_expect_tx(bar, C::kTileB);
+    __syncwarp();
+    if (lane < boxes)
+#pragma unroll
+      for (int x = 0; x < C::kHalves; ++x) tma_load_2d(to + x * C::kHalfB + lane * box * 128, &mk, x * 64, y, bar);
+  };
+  auto load_q = [&](int q, int s) {
+    mbar_expect_tx(&q_full[s], C::kHalves * tpt * G * 128);
+    for (int x = 0; x < C::kHalves; ++x)
+      tma_load_3d(sm + C::kQ + s * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, ab.x + q * tpt, &q_full[s]);
+  };
+
+  if (tiles == 1) {
+    // One tile of query rows, a decode or verify block's: it stays, and the
+    // CTA's key tiles pass by, two buffers of K (the second where the other
+    // stage of Q would be) and of S ahead of the threads that own the keys.
+    const int all_k = (len + kPtKeys - 1) / kPtKeys, x0 = blockIdx.x, dx = gridDim.x;
+    const int nk = x0 < all_k ? (all_k - x0 + dx - 1) / dx : 0, chunks = (n_new * G + 31) >> 5;
+    if (warp == wLoad) {
+      if (nk > 0 && lane == 0) load_q(0, 0);
+      int y = k_row(x0 * kPtKeys);
+      int i = 0;
+      for (; i < nk; ++i) {
+        const int b = i & 1, next = k_row((x0 + (i + 1) * dx) * kPtKeys);
+        if (i >= 2) paged_wait(&k_empty[b], ((i >> 1) - 1) & 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        load_k(sm + (b ? C::kQ + C::kTileB : C::kK), y, &k_full[b]);
+        y = next;
+      }
+      // no copy may be in flight when the CTA ends
+      bool landed = true;
+      if (nk > 0) paged_wait(&q_full[0], 0, landed);
+      for (int j = i > 2 ? i - 2 : 0; j < i; ++j) paged_wait(&k_full[j & 1], (j >> 1) & 1, landed);
+      ok = ok && landed;
+    } else if (warp == wMma) {
+      const bool leader = elect_one();
+      const uint32_t sb = smem_u32(sm);
+      const int ksteps = (c.hd + 15) >> 4;
+      const uint64_t q_desc = smem_desc_sw128(sb + C::kQ), k_desc = smem_desc_sw128(sb + C::kK), k2_desc = smem_desc_sw128(sb + C::kQ + C::kTileB);
+      if (nk > 0) paged_wait(&q_full[0], 0, ok);
+      for (int i = 0; i < nk; ++i) {
+        const int b = i & 1;
+        paged_wait(&k_full[b], (i >> 1) & 1, ok);
+        if (i >= 2) paged_wait(&s_empty[b], ((i >> 1) - 1) & 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        if (leader) {
+          tc_scores<C::kHalves>(tmem + b * 128, b ? k2_desc : k_desc, q_desc, ksteps);
+          tc_commit(&s_full[b]);
+          tc_commit(&k_empty[b]);
+        }
+        __syncwarp();
+      }
+    } else if (warp == wRows) {
+      if (nk > 0) {
+        put_rows(rows[0], row_data(0));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rows_full[0]);
+      }
+    } else if (warp < wMma) {
+      // the key's place, position and weight are requested a tile ahead
+      auto place = [&](int i) {
+        const int slot = (x0 + i * dx) * kPtKeys + (int)threadIdx.x;
+        const long long row = slot < len ? paged_row(c, seq, h, slot) : -1;
+        if (slot < len && row < 0 && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+        return row;
+      };
+      long long row = nk > 0 ? place(0) : -1;
+      int pk = row >= 0 ? c.pos[row] : kPagedNoPos;
+      float old = row >= 0 && a.weight_in ? a.weight_in[row] : 0.f;
+      if (nk > 0) paged_wait(&rows_full[0], 0, ok);
+      for (int i = 0; i < nk; ++i) {
+        const int b = i & 1;
+        const uint32_t s_at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * 128;
+        const long long next = i + 1 < nk ? place(i + 1) : -1;
+        const PagedSees by = paged_seen_by(m, pk);
+        paged_wait(&s_full[b], (i >> 1) & 1, ok);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        tc_fence_after();
+        const int pk1 = next >= 0 ? c.pos[next] : kPagedNoPos;
+        const float old1 = next >= 0 && a.weight_in ? a.weight_in[next] : 0.f;
+        uint64_t add[2] = {0, 0};
+#pragma unroll 1
+        for (int n = 0; n < chunks; ++n) {
+          float v[32];
+          tmem_ld32(s_at + n * 32, v);
+          tmem_ld_wait32(v);
+          add_chunk(v, rows[0], n, by, pk, false, add);
+        }
+        tc_fence_before();
+        mbar_arrive(&s_empty[b]);
+        float a0, a1;
+        unpack2(add2(add[0], add[1]), a0, a1);
+        if (row >= 0) a.weight_out[row] = (a.weight_in ? a.decay * old : 0.f) + (a0 + a1);
+        row = next;
+        pk = pk1;
+        old = old1;
+      }
+    }
+    if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == wMma) {
+      __syncwarp();
+      tc_fence_after();
+      tmem_dealloc(tmem, kTmemCols);
+    }
+    return;
+  }
+
   unsigned it = 0;                         // query tiles passed by, over the whole kernel
   unsigned kn = 0;                         // key tiles loaded
 
@@ -115,21 +312,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         if (lane == 0) { atomicMin(&s_kmin, lo); atomicMax(&s_kmax, hi); }
       }
     } else if (warp == wLoad) {
-      // K, a box per page (or per 128 rows of one)
-      const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
-      const int beyond = (c.n_pages * c.nkv) << c.lg_rows;
-      if (lane == 0) mbar_expect_tx(&k_full, C::kTileB);
-      __syncwarp();
-      const int at = k0 + lane * box;
-      int y = beyond;
-      if (lane < boxes && at < len) {
-        const long long row = paged_row(c, seq, h, at);
-        if (row >= 0) y = (int)row;
-      }
-      if (lane < boxes)
-#pragma unroll
-        for (int x = 0; x < C::kHalves; ++x)
-          tma_load_2d(sm + C::kK + x * C::kHalfB + lane * box * 128, &mk, x * 64, y, &k_full);
+      load_k(sm + C::kK, k_row(k0), &k_full[0]);
     }
     // few query tiles are not classified: that would cost more than a tile
     // too many
@@ -175,11 +358,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           const int s = j % NS, q = c0 + cur.next();
           if (j >= NS) paged_wait(&q_empty[s], (j / NS - 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-          if (lane == 0) {
-            mbar_expect_tx(&q_full[s], C::kHalves * tpt * G * 128);
-            for (int x = 0; x < C::kHalves; ++x)
-              tma_load_3d(sm + C::kQ + s * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, ab.x + q * tpt, &q_full[s]);
-          }
+          if (lane == 0) load_q(q, s);
           __syncwarp();
         }
       } else if (warp == wMma) {
@@ -187,7 +366,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         const uint32_t sb = smem_u32(sm);
         const int ksteps = (c.hd + 15) >> 4;
         const uint64_t k_desc = smem_desc_sw128(sb + C::kK), q_desc = smem_desc_sw128(sb + C::kQ);
-        if (fresh && N > 0) paged_wait(&k_full, kn & 1, ok);
+        if (fresh && N > 0) paged_wait(&k_full[0], kn & 1, ok);
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
           const int s = j % NS, b = j & 1;
@@ -208,49 +387,15 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           const unsigned j = it + i;
           const int q = c0 + cur.next();
           if ((int)(j & 1) != warp - wRows) continue;
-          float l[4], sl[4];
-          int p[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = x * 32 + lane, tl = r / G, tok = q * tpt + tl, head = h * G + r - tl * G;
-            const bool in = tl < tpt && tok < n_new;
-            const float v = in ? a.lse[(size_t)(ab.x + tok) * a.nq + head] : -INFINITY;
-            l[x] = v == -INFINITY ? -INFINITY : -v * kLog2e;
-            p[x] = v == -INFINITY ? kPagedNoPos : a.q_pos[ab.x + tok];
-            sl[x] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
-          }
-          int base = 0, near = 1;
-          if (EXTRA && a.slopes) {
-            int lo = INT32_MAX, hi = INT32_MIN;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              lo = min(lo, p[x] == kPagedNoPos ? INT32_MAX : p[x]);
-              hi = max(hi, p[x]);
-            }
-            base = __reduce_min_sync(0xffffffffu, lo);
-            near = (long long)__reduce_max_sync(0xffffffffu, hi) - base < (1 << 23);
-          }
+          RowData d = row_data(q);
           const int s = j % kNA;
           if (j >= kNA) paged_wait(&rows_empty[s], (j / kNA - 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int r = x * 32 + lane;
-            rows[s].nlse2[r] = l[x];
-            rows[s].pos[r] = p[x];
-            rows[s].slope2[r] = sl[x];
-            if (EXTRA && a.slopes) rows[s].dist[r] = (float)(p[x] - base);
-          }
-          if (EXTRA && lane == 0) {
-            rows[s].base = base;
-            rows[s].near = near;
-          }
+          put_rows(rows[s], d);
           __syncwarp();
           if (lane == 0) mbar_arrive(&rows_full[s]);
         }
       } else {
-        const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
-        const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
         const PagedSees by = paged_seen_by(m, pk);
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
@@ -298,38 +443,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
                 tc_fence_before();
                 mbar_arrive(&s_empty[b]);
               }
-              float sc = scale2;
-              if (EXTRA && a.softcap > 0.f) {
-                cap_tanh32(v, cap);
-                sc = 1.f;
-              }
-              if (EXTRA && a.slopes) {
-                if (rw.near) {
-                  const float pkf = (float)(pk - rw.base);
-#pragma unroll
-                  for (int e = 0; e < 32; e += 4) {
-                    const float4 pq = *reinterpret_cast<const float4*>(rw.dist + n * 32 + e);
-                    const float4 sl = *reinterpret_cast<const float4*>(rw.slope2 + n * 32 + e);
-                    v[e] = fmaf(-sl.x, fabsf(pq.x - pkf), v[e] * sc);
-                    v[e + 1] = fmaf(-sl.y, fabsf(pq.y - pkf), v[e + 1] * sc);
-                    v[e + 2] = fmaf(-sl.z, fabsf(pq.z - pkf), v[e + 2] * sc);
-                    v[e + 3] = fmaf(-sl.w, fabsf(pq.w - pkf), v[e + 3] * sc);
-                  }
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) v[e] = fmaf(-rw.slope2[n * 32 + e], fabsf((float)(rw.pos[n * 32 + e] - pk)), v[e] * sc);
-                }
-                sc = 1.f;
-              }
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(rw.nlse2 + n * 32 + e);
-                const int4 pq = *reinterpret_cast<const int4*>(rw.pos + n * 32 + e);
-                const float p0 = ex2(fmaf(v[e], sc, l.x)), p1 = ex2(fmaf(v[e + 1], sc, l.y));
-                const float p2 = ex2(fmaf(v[e + 2], sc, l.z)), p3 = ex2(fmaf(v[e + 3], sc, l.w));
-                add[0] = add2(add[0], pack2(full || paged_sees(by, pq.x) ? p0 : 0.f, full || paged_sees(by, pq.y) ? p1 : 0.f));
-                add[1] = add2(add[1], pack2(full || paged_sees(by, pq.z) ? p2 : 0.f, full || paged_sees(by, pq.w) ? p3 : 0.f));
-              }
+              add_chunk(v, rw, n, by, pk, full, add);
             }
           }
           float a0, a1;
@@ -344,7 +458,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
     }
     if (warp < wMma && my_row >= 0) a.weight_out[my_row] = (a.weight_in ? a.decay * a.weight_in[my_row] : 0.f) + w;
     // K has landed before its tile is loaded again or the CTA ends
-    if (warp == wLoad) paged_wait(&k_full, kn & 1, ok);
+    if (warp == wLoad) paged_wait(&k_full[0], kn & 1, ok);
     if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
     if (__syncthreads_or(!ok)) { ok = false; break; }
   }
@@ -385,6 +499,14 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  // Few query rows: CTAs, two to an SM, that pass several key tiles each, two
+  // waves of them for sequences of different lengths. (The kernel decides by each
+  // sequence's own rows what it does; a grid for the other case only starts more
+  // CTAs.)
+  if ((long long)a.rows * a.G <= 128ll * a.c.n_seq) {
+    const long long pairs = (long long)a.c.nkv * a.c.n_seq, most = (608 + pairs - 1) / pairs;
+    if (tiles > most) tiles = most;
+  }
   return a.c.hd <= 64 ? run<64>(a, tiles, st) : run<128>(a, tiles, st);
 }
 
