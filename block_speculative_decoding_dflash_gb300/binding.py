@@ -688,6 +688,12 @@ class PagedCache:
         raise DFlashError(EINVAL, f"paged: {name} must be [rows, heads, {hd}] in {self.dtype} on {self.device} with dense rows, "
                                   f"got {t.dtype} {tuple(t.shape)} with strides {t.stride()} on {t.device}")
 
+    def _pack(self, layout, *values):
+        try:
+            return layout.pack(*values)
+        except (struct.error, OverflowError) as e:
+            raise DFlashError(EINVAL, f"paged: an argument is not a number of the C call's type ({e})") from None
+
     def _query(self, call, args):
         n = _i64()
         self._check(call(self._c, args + _NO_WORKSPACE, ctypes.byref(n)))
@@ -741,7 +747,7 @@ class PagedCache:
                 axis = bytes(pair_axis)
                 self._axis = held = axis, ctypes.create_string_buffer(axis, len(axis))
             axis_at = ctypes.addressof(held[1])
-        args = _PAGED_APPEND.pack(q_at, k_at, v_at, need("row_pos", row_pos, torch.int32, (n,)),
+        args = self._pack(_PAGED_APPEND, q_at, k_at, v_at, need("row_pos", row_pos, torch.int32, (n,)),
                                   need("start", start, torch.int32, (self.n_seq + 1,)), rope_at, axis_at,
                                   self._may("q_norm", q_norm, self.dtype, gain), self._may("k_norm", k_norm, self.dtype, gain),
                                   need("q_out", q_out, self.dtype, q.shape), 0 if self.weight is None else self.weight.data_ptr(),
@@ -752,7 +758,7 @@ class PagedCache:
         need = self._need
         q_at, q_stride = self._rows("q", q)
         n, nq, _ = q.shape
-        return _PAGED_ATTENTION.pack(q_at, need("q_pos", q_pos, torch.int32, (n,)), need("start", start, torch.int32, (self.n_seq + 1,)),
+        return self._pack(_PAGED_ATTENTION, q_at, need("q_pos", q_pos, torch.int32, (n,)), need("start", start, torch.int32, (self.n_seq + 1,)),
                                      self._may("slopes", slopes, torch.float32, (nq,)), self._may("prefix", prefix, torch.int32, (self.n_seq,)),
                                      out_at, self._may("lse", lse, torch.float32, (n, nq)), q_stride, n, nq, 1 if causal else 0, window,
                                      max_len, self.head_dim ** -0.5 if scale is None else scale, softcap, 0)
@@ -786,7 +792,7 @@ class PagedCache:
         weight_out = self.weight if weight_out is None else weight_out
         if weight is None or weight_out is None:
             raise DFlashError(EINVAL, "paged: evict needs weights")
-        args = _PAGED_EVICT.pack(need("weight", weight, torch.float32, shape), need("next_pos", next_pos, torch.int32, seqs),
+        args = self._pack(_PAGED_EVICT, need("weight", weight, torch.float32, shape), need("next_pos", next_pos, torch.int32, seqs),
                                  need("weight_out", weight_out, torch.float32, shape),
                                  need("pos_out", self.pos if pos_out is None else pos_out, torch.int32, shape),
                                  need("length_out", self.length if length_out is None else length_out, torch.int32, seqs), budget, recent)

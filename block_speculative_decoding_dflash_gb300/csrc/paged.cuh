@@ -87,9 +87,9 @@ __device__ __forceinline__ PagedSees paged_sees_of(const PagedMask& m, int pq) {
     if ((long long)pq - m.window > lo) lo = (long long)pq - m.window;
     if (!m.causal && (long long)pq + m.window < hi) hi = (long long)pq + m.window;
   }
-  // (pq = INT32_MIN with a causal mask sees nothing; a range is never empty, so
-  // its own end, kPagedNoPos, stands for that)
-  if (hi < lo) return PagedSees{(int)hi, 0u, (unsigned)m.prefix};
+  // (pq = INT32_MIN with a causal mask: a range is never empty, so it gets one of
+  // a negative position, which no row has)
+  if (hi < lo) return PagedSees{INT32_MIN + 1, 0u, (unsigned)m.prefix};
   return PagedSees{(int)lo, (unsigned)(hi - lo), (unsigned)m.prefix};
 }
 __device__ __forceinline__ bool paged_sees(const PagedSees& s, int pk) {

@@ -484,7 +484,11 @@ cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const Page
 
 cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st) {
   if (dtype && a.c.hd <= 128) return launch_paged_weight_tc(a, (expected_len(a) + 127) / 128, st);
+  // at most so many CTAs that a table far longer than its sequences does not
+  // start one for every tile
   long long x = (expected_len(a) + kBN - 1) / kBN;
+  const long long limit = 65536 / ((long long)a.c.nkv * a.c.n_seq) + 1;
+  if (x > limit) x = limit;
   const dim3 grid((unsigned)x, a.c.nkv, a.c.n_seq);
   if (a.c.hd <= 64) return dtype ? run_weight<bf16, 64>(a, grid, st) : run_weight<float, 64>(a, grid, st);
   if (a.c.hd <= 128) return dtype ? run_weight<bf16, 128>(a, grid, st) : run_weight<float, 128>(a, grid, st);

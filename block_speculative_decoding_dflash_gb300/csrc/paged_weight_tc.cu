@@ -507,6 +507,9 @@ cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cuda
     const long long pairs = (long long)a.c.nkv * a.c.n_seq, most = (608 + pairs - 1) / pairs;
     if (tiles > most) tiles = most;
   }
+  // a table far longer than its sequences need not start a CTA for every tile
+  const long long limit = 65536 / ((long long)a.c.nkv * a.c.n_seq) + 1;
+  if (tiles > limit) tiles = limit;
   return a.c.hd <= 64 ? run<64>(a, tiles, st) : run<128>(a, tiles, st);
 }
 

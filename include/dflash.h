@@ -699,7 +699,8 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
  * cap); t -= slopes[h] * |pq - pk|. out = sum softmax(t) v, lse = log sum
  * exp(t) (natural log); a query that sees nothing gives out = 0 and lse =
  * -inf. What a query does not see has no influence on it, infinities and NaN
- * included. Softmax statistics and sums are fp32. Rows outside [start[0],
+ * included; infinities and NaN that it does see make what they reach infinite
+ * or NaN. Softmax statistics and sums are fp32. out and lse overlap no input. Rows outside [start[0],
  * start[n_seq]) of out and lse are left as they are. */
 typedef struct dflash_paged_attention_args {
   const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */

@@ -158,12 +158,17 @@ def attention_args(**over):
     dict(q=torch.zeros(5, 4, 64)), dict(q=torch.zeros(5, 5, 64, dtype=torch.bfloat16)), dict(out=torch.zeros(5, 4, 64)), dict(q_pos=torch.zeros(4, dtype=torch.int32)),
     dict(start=torch.zeros(4, dtype=torch.int64)), dict(lse=torch.zeros(5, 3)), dict(lse=torch.zeros(4, 5).T), dict(slopes=torch.zeros(2)), dict(prefix=torch.zeros(2, dtype=torch.int32)),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(max_len=-1),
-    dict(workspace=torch.zeros(4, dtype=torch.uint8), q=torch.zeros(1, 4, 64, dtype=torch.bfloat16), out=torch.zeros(1, 4, 64, dtype=torch.bfloat16), q_pos=torch.zeros(1, dtype=torch.int32)),
-    dict(workspace=torch.zeros(1 << 20)),
+    dict(workspace=torch.zeros(1 << 20)), dict(window=1 << 40), dict(scale="wide"), dict(softcap=1e300),
 ])
 def test_attention_refuses(B, over):
     c = B.PagedCache.allocate(80, 64, 2, 64, 3, 20, device="cpu")
     refused(B, c.attention, attention_args(**over))
+
+
+def test_attention_refuses_a_small_workspace(B):
+    c = B.PagedCache.allocate(80, 64, 2, 64, 3, 20, dtype="f32", device="cpu")
+    args = attention_args(q=torch.zeros(5, 4, 64), out=torch.zeros(5, 4, 64), workspace=torch.zeros(4, dtype=torch.uint8))
+    refused(B, c.attention, args)
 
 
 @pytest.mark.parametrize("over", [dict(lse=None), dict(lse=torch.zeros(5, 2)), dict(weight=torch.zeros(8, 2, 8)), dict(weight_out=torch.zeros(8, 2, 16, dtype=torch.float64)),
@@ -174,7 +179,7 @@ def test_key_weight_refuses(B, cache, over):
     refused(B, cache.key_weight, {**a, **over})
 
 
-@pytest.mark.parametrize("over", [dict(budget=0), dict(recent=-1), dict(next_pos=torch.zeros(2, dtype=torch.int32)), dict(weight_out=torch.zeros(1)),
+@pytest.mark.parametrize("over", [dict(budget=0), dict(recent=-1), dict(budget=1 << 32), dict(recent=0.5), dict(next_pos=torch.zeros(2, dtype=torch.int32)), dict(weight_out=torch.zeros(1)),
                                   dict(length_out=torch.zeros(3, dtype=torch.int64)), dict(workspace=torch.zeros(3, dtype=torch.uint8))])
 def test_evict_refuses(B, cache, over):
     refused(B, cache.evict, {**dict(budget=4, recent=1, next_pos=torch.zeros(3, dtype=torch.int32)), **over})
