@@ -107,8 +107,10 @@ int check_attention(const dflash_paged_cache* c, const dflash_paged_attention_ar
   PG(may(a->slopes, "slopes"));
   PG(may(a->prefix, "prefix"));
   PG(may(a->lse, "lse"));
-  if (!(a->scale > 0.f) || isinf(a->scale)) return refuse(DFLASH_EINVAL, "paged attention: scale must be positive and finite");
-  if (!(a->softcap >= 0.f) || isinf(a->softcap)) return refuse(DFLASH_EINVAL, "paged attention: softcap must be finite and not negative");
+  // (within these no product or quotient of the two leaves fp32)
+  if (!(a->scale > 0.f && a->scale <= 1e18f)) return refuse(DFLASH_EINVAL, "paged attention: scale must be positive and at most 1e18");
+  if (a->softcap != 0.f && !(a->softcap >= 1e-18f && a->softcap <= 1e18f))
+    return refuse(DFLASH_EINVAL, "paged attention: softcap must be 0 or in [1e-18, 1e18]");
   if (a->max_len < 0) return refuse(DFLASH_EINVAL, "paged attention: max_len is negative");
   x->q = a->q; x->q_pos = a->q_pos; x->start = a->start; x->slopes = a->slopes; x->prefix = a->prefix;
   x->out = a->out; x->lse = a->lse;

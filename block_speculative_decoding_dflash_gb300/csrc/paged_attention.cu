@@ -1,6 +1,6 @@
-// Attention over the paged cache on CUDA cores, for fp32 and for the shapes
-// the tensor-core kernel does not take, the merge of split partials, and the
-// key weights for the same shapes.
+// How an attention call over the paged cache is divided; attention for bf16 heads
+// of more than 128 dimensions, which the tensor-core kernel does not take; the
+// merge of split partials; key weights for fp32 and for those heads.
 //
 // Per (query tile, kv head, split): an online softmax over key tiles. The
 // scores are kept in log2 units, u = t * log2(e), so p = exp2(u - m).
@@ -18,12 +18,11 @@ constexpr int kBN = 64;                    // keys of a tile
 constexpr int kMaxTiles = (1 << 20) / kBN; // of the longest table
 
 // Score of a raw dot product in log2 units.
-struct PagedScore { float scale2, cap2, inv_cap; };
+struct PagedScore { float scale2, cap2; };
 __device__ __forceinline__ PagedScore paged_score_of(const PagedAttnArgs& a) {
   PagedScore s;
   s.scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
   s.cap2 = a.softcap * kLog2e;
-  s.inv_cap = 0.f;
   return s;
 }
 __device__ __forceinline__ float paged_score(const PagedAttnArgs& a, const PagedScore& s, float dot, float slope2, int pq, int pk) {
@@ -55,9 +54,10 @@ __device__ __forceinline__ bool load_row(float* dst, const T* src, int hd, int l
 // 16 lanes share a row, so row statistics are shuffles within half a warp.
 // K and V tiles are read from HBM once per query tile; for few query rows
 // that read bounds the kernel, for many the fp32 FMA rate.
-template <typename T, int BM, int TM, int HDP>
+template <int BM, int TM>
 __global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttnArgs a) {
-  constexpr int NT = BM / TM * 16, LD = HDP + 4, NJ = HDP / 64;
+  using T = bf16;
+  constexpr int HDP = 256, NT = BM / TM * 16, LD = HDP + 4, NJ = HDP / 64;
   pdl_enter();
   extern __shared__ float smf[];
   float* sq = smf;                          // [BM][LD]
@@ -387,9 +387,9 @@ __global__ void __launch_bounds__(256) paged_weight_simt_kernel(PagedAttnArgs a)
   }
 }
 
-template <int BM, int HDP>
+template <int BM>
 constexpr size_t simt_smem() {
-  return ((size_t)(BM + 2 * kBN) * (HDP + 4) + BM * (kBN + 4) + kBN) * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
+  return ((size_t)(BM + 2 * kBN) * (256 + 4) + BM * (kBN + 4) + kBN) * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
 }
 template <int HDP>
 constexpr size_t weight_smem() { return (size_t)2 * kBN * (HDP + 4) * 4; }
@@ -399,11 +399,11 @@ cudaError_t big_smem(K* kernel, size_t bytes) {
   return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <typename T, int BM, int TM, int HDP>
+template <int BM, int TM>
 cudaError_t run_simt(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  cudaError_t e = big_smem(paged_attn_simt_kernel<T, BM, TM, HDP>, simt_smem<BM, HDP>());
+  cudaError_t e = big_smem(paged_attn_simt_kernel<BM, TM>, simt_smem<BM>());
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_attn_simt_kernel<T, BM, TM, HDP>, grid, dim3(BM / TM * 16), simt_smem<BM, HDP>(), st, a);
+  return launch_pdl(paged_attn_simt_kernel<BM, TM>, grid, dim3(BM / TM * 16), simt_smem<BM>(), st, a);
 }
 template <typename T, int HDP>
 cudaError_t run_weight(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
@@ -474,8 +474,8 @@ cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const Page
   cudaError_t e;
   if (p.kind <= 2) e = launch_paged_attention_tc(a, p.kind, p.tiles, st);
   else if (!dtype) e = launch_paged_attention_f32(a, p.kind, p.tiles, st);
-  else if (p.kind == 16) e = run_simt<bf16, 16, 2, 256>(a, grid, st);
-  else e = run_simt<bf16, 64, 4, 256>(a, grid, st);
+  else if (p.kind == 16) e = run_simt<16, 2>(a, grid, st);
+  else e = run_simt<64, 4>(a, grid, st);
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
   return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)
@@ -490,9 +490,9 @@ cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStrea
   const long long limit = 65536 / ((long long)a.c.nkv * a.c.n_seq) + 1;
   if (x > limit) x = limit;
   const dim3 grid((unsigned)x, a.c.nkv, a.c.n_seq);
-  if (a.c.hd <= 64) return dtype ? run_weight<bf16, 64>(a, grid, st) : run_weight<float, 64>(a, grid, st);
-  if (a.c.hd <= 128) return dtype ? run_weight<bf16, 128>(a, grid, st) : run_weight<float, 128>(a, grid, st);
-  return dtype ? run_weight<bf16, 256>(a, grid, st) : run_weight<float, 256>(a, grid, st);
+  if (dtype) return run_weight<bf16, 256>(a, grid, st);
+  if (a.c.hd <= 64) return run_weight<float, 64>(a, grid, st);
+  return a.c.hd <= 128 ? run_weight<float, 128>(a, grid, st) : run_weight<float, 256>(a, grid, st);
 }
 
 }  // namespace dfl

@@ -114,6 +114,14 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
   }
+  // query rows that no load fills: zeros, so that nothing depends on what was there
+  for (int e = threadIdx.x; e < QT * C::kHalves * kPtKeys; e += C::kThreads) {
+    const int r = e & (kPtKeys - 1);
+    if (r < tpt * G && (QT == 2 || (r & 31) < 32 / G * G || G > 32)) continue;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) *reinterpret_cast<uint4*>(sm + C::kQ + (e >> 7) * C::kHalfB + r * 128 + d * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async_shared();
   pdl_wait();
   // TMEM only once the kernel before has given its own back, and the next
   // kernel only once every CTA of this one has its share: neither can then

@@ -164,18 +164,25 @@ __device__ __forceinline__ float cap_tanh(float x, float cap2) {
   return fmaf(-2.f * cap2, r, cap2);
 }
 
-// v = cap2 * tanh(v * scale) for 32 values of every lane of a warp. Where all of
-// them are at most half the cap, as most scores are, tanh(y) / y is a polynomial
-// of degree 4 in y^2 (interpolated at the Chebyshev nodes of [0, 1/4]; within
-// 2^-23 of it in fp32), with scale and cap2 in its coefficients: six packed
+// v = cap2 * tanh(v * scale) for 32 values of every lane of a warp. For a value
+// of at most half the cap, as most scores are, tanh(y) / y is a polynomial of
+// degree 4 in y^2 (interpolated at the Chebyshev nodes of [0, 1/4]; within 2^-23
+// of it in fp32), with scale and cap2 in its coefficients: six packed
 // instructions to two values, where the exponential and the reciprocal would
-// bound capped attention.
-struct CapPoly { uint64_t c[5]; float scale, cap2; };
+// bound capped attention (512 rows' key weights over 32768 keys, cap 20: 335 us
+// with it, 459 us without). Where some value of the warp is larger, all take the
+// exponential, whose error of a few 2^-24 of the cap is nothing beside scores of
+// half of it; under a cap so vast that it could be (cap2 > 1024) each value takes
+// its own. (Each its own under every cap: 2048 rows over 32768 keys under a cap
+// of 2 took 3.40 ms instead of 1.98 ms.) limit: the largest |v| for the
+// polynomial, none where a power of the scale would leave fp32.
+struct CapPoly { uint64_t c[5]; float scale, cap2, limit; };
 __device__ __forceinline__ CapPoly cap_poly(float scale, float cap2) {
   const float c[5] = {1.0f, -0.3333306908607483f, 0.133247509598732f, -0.05298423767089844f, 0.017131345346570015f};
   CapPoly p;
   p.scale = scale;
   p.cap2 = cap2;
+  p.limit = scale <= 1024.f ? 0.5f / scale : -1.f;
   float f = scale * cap2;
 #pragma unroll
   for (int k = 0; k < 5; ++k) {
@@ -188,19 +195,30 @@ __device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) top = fmaxf(fmaxf(top, fabsf(v[j])), fabsf(v[j + 1]));
-  if (__all_sync(0xffffffffu, top * p.scale <= 0.5f)) {
+  auto poly = [&](float v0, float v1, float& r0, float& r1) {
+    const uint64_t y = pack2(v0, v1), z = mul2(y, y);
+    uint64_t r = p.c[4];
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const uint64_t y = pack2(v[j], v[j + 1]), z = mul2(y, y);
-      uint64_t r = p.c[4];
+    for (int k = 3; k >= 0; --k) r = fma2(r, z, p.c[k]);
+    unpack2(mul2(r, y), r0, r1);
+  };
+  if (__all_sync(0xffffffffu, top <= p.limit)) {
 #pragma unroll
-      for (int k = 3; k >= 0; --k) r = fma2(r, z, p.c[k]);
-      unpack2(mul2(r, y), v[j], v[j + 1]);
-    }
+    for (int j = 0; j < 32; j += 2) poly(v[j], v[j + 1], v[j], v[j + 1]);
   } else {
     const float twice = p.scale * 2.8853900817779268f;   // 2 log2(e)
+    if (p.cap2 <= 1024.f) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * twice, p.cap2);
+      for (int j = 0; j < 32; ++j) v[j] = cap_tanh(v[j] * twice, p.cap2);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        float r0, r1;
+        poly(v[j], v[j + 1], r0, r1);
+        v[j] = fabsf(v[j]) <= p.limit ? r0 : cap_tanh(v[j] * twice, p.cap2);
+        v[j + 1] = fabsf(v[j + 1]) <= p.limit ? r1 : cap_tanh(v[j + 1] * twice, p.cap2);
+      }
+    }
   }
 }
 

@@ -700,8 +700,9 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
  * exp(t) (natural log); a query that sees nothing gives out = 0 and lse =
  * -inf. What a query does not see has no influence on it, infinities and NaN
  * included; infinities and NaN that it does see make what they reach infinite
- * or NaN. Softmax statistics and sums are fp32. out and lse overlap no input. Rows outside [start[0],
- * start[n_seq]) of out and lse are left as they are. */
+ * or NaN. Softmax statistics and sums are fp32. out and lse
+ * overlap no input. Rows outside [start[0], start[n_seq]) of out and lse are
+ * left as they are. */
 typedef struct dflash_paged_attention_args {
   const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */
   const int32_t* q_pos;     /* [rows] */
@@ -717,8 +718,8 @@ typedef struct dflash_paged_attention_args {
   int32_t window;
   int32_t max_len;          /* longest length the caller expects, 0: the table's; sets how the
                                work is split, longer sequences stay right */
-  float scale;              /* > 0 */
-  float softcap;            /* >= 0 */
+  float scale;              /* > 0, at most 1e18 */
+  float softcap;            /* 0, or in [1e-18, 1e18] */
   int32_t reserved;         /* 0 */
   void* workspace;          /* dflash_paged_attention_workspace bytes; calls that may overlap
                                need workspaces of their own */

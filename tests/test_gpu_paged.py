@@ -254,6 +254,22 @@ def test_positions_far_apart_and_far_out(B, dtype):
     s.check_weight(cache, lse, slopes=torch.tensor([2.0 ** -30, 2.0 ** -29, 0.01, 2.0 ** -8]), window=1 << 30)
 
 
+@pytest.mark.parametrize("softcap", [1e-18, 1e-6, 1e-3, 1e18])
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 64, 4), ("bf16", 256, 2)])
+@pytest.mark.parametrize("n", [1, 40, 200])
+def test_caps_far_from_the_scores(B, dtype, hd, nq, n, softcap):
+    """Zero scores under a cap stay zero, however small it is; a vast cap leaves scores as they are."""
+    s = Setup(B, [(n, n + 150)], nq, 2, hd, 16, dtype, seed=n)
+    s.q[: n - n // 2] = 0
+    cache = s.device()
+    # the scores' error in the formula counts 8 roundings of a cap that a vast one does not reach
+    reach = min(softcap, 1e3)
+    s_error = s.score_error
+    s.score_error = lambda cap, slopes: s_error(reach, slopes)
+    _, lse = s.check_attention(cache, softcap=softcap)
+    s.check_weight(cache, lse, softcap=softcap)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
 @pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 32), ("f32", 128, 8), ("bf16", 136, 4)])
 @pytest.mark.parametrize("n", [6, 80, 300])

@@ -159,6 +159,7 @@ def attention_args(**over):
     dict(start=torch.zeros(4, dtype=torch.int64)), dict(lse=torch.zeros(5, 3)), dict(lse=torch.zeros(4, 5).T), dict(slopes=torch.zeros(2)), dict(prefix=torch.zeros(2, dtype=torch.int32)),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=math.inf), dict(scale=math.nan), dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(max_len=-1),
     dict(workspace=torch.zeros(1 << 20)), dict(window=1 << 40), dict(scale="wide"), dict(softcap=1e300),
+    dict(scale=1e19), dict(softcap=1e-19), dict(softcap=1e19),
 ])
 def test_attention_refuses(B, over):
     c = B.PagedCache.allocate(80, 64, 2, 64, 3, 20, device="cpu")
