@@ -454,9 +454,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       }
       bool full = classified(rel);
       const int tile = sh.t0 + rel;
-      // First pass over S: the row's maximum. What a mask, cap or bias makes of
-      // a score is put back in its place, so that the second pass is the same
-      // for all; S is read twice because half as many registers then do.
+      // First pass over S: the row's maximum. What a mask or bias makes of a score
+      // is put back in its place, so that the second pass is the same for all; S
+      // is read twice because half as many registers then do. A cap alone keeps
+      // the order of scores: the maximum's is enough here, and the second pass
+      // caps the others.
       // (a tile that other warps see in part, or that was not classified, may be
       // wholly seen by this warp's rows)
       bool masked = !full;
@@ -465,7 +467,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         masked = !k.whole || paged_class(m, wmin, wmax, k.lo, k.hi, true) != 2;
         if (QT == 1 && direct) full = k.whole && paged_class(m, qmin, qmax, k.lo, k.hi, true) == 2;
       }
-      const bool change = masked || (EXTRA && (a.slopes || a.softcap > 0.f));
+      const bool late = EXTRA && a.softcap > 0.f && !masked && !a.slopes;
+      const bool change = masked || (EXTRA && a.slopes);
       if (masked || (EXTRA && a.slopes)) {
         __syncwarp();
         *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
@@ -542,8 +545,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           rise(v);
         }
       }
-      const float sc = change ? 1.f : scale2;
-      top *= sc;
+      const float sc = change || late ? 1.f : scale2;
+      top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
       if (change) tmem_st_wait();
       if (__any_sync(0xffffffffu, top > mx + kLazy)) {
         const float mn = fmaxf(mx, top);
@@ -579,7 +582,22 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         p1 = ex2(p1);
         return pack_bf16(p0, p1);
       };
-      if (QT == 2) {
+      if (QT == 2 && EXTRA && late) {
+#pragma unroll 1
+        for (int n = 0; n < 4; ++n) {
+          float w[16];
+          tmem_ld32(s_at + n * 32, x[0]);
+          tmem_ld_wait32(x[0]);
+          cap_tanh32(x[0], cap);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float p0, p1;
+            w[j >> 1] = __uint_as_float(weigh(x[0] + j, p0, p1));
+            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+          }
+          tmem_st16(s_at + n * 16, w);
+        }
+      } else if (QT == 2) {
         tmem_ld32(s_at, x[0]);
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
@@ -606,6 +624,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             tmem_ld32(s_at + n * 32, x[0]);
             tmem_ld_wait32(x[0]);
           }
+          if (EXTRA && late) cap_tanh32(x[0], cap);
           float w[16], lo[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {

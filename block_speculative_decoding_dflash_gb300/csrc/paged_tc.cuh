@@ -191,6 +191,18 @@ __device__ __forceinline__ CapPoly cap_poly(float scale, float cap2) {
   }
   return p;
 }
+// The same of one value.
+__device__ __forceinline__ float cap_tanh1(float v, const CapPoly& p) {
+  if (!(fabsf(v) <= p.limit)) return cap_tanh(v * (p.scale * 2.8853900817779268f), p.cap2);
+  float r = 0.f, unused;
+#pragma unroll
+  for (int k = 4; k >= 0; --k) {
+    float c;
+    unpack2(p.c[k], c, unused);
+    r = fmaf(r, v * v, c);
+  }
+  return r * v;
+}
 __device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
   float top = 0.f;
 #pragma unroll
