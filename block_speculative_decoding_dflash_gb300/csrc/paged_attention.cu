@@ -436,8 +436,8 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
     fill = 152;
     least = 512;
   } else {
-    // the smallest tile that holds an average sequence's rows
-    p.kind = units <= 16ll * a.c.n_seq ? 16 : (units <= 32ll * a.c.n_seq && !dtype ? 32 : 64);
+    // the smallest tile that holds an average sequence's rows (fp32: 16 always)
+    p.kind = !dtype || units <= 16ll * a.c.n_seq ? 16 : 64;
     p.tiles = tile_bound(units, p.kind, a);
     fill = 608;
     least = 256;
@@ -473,7 +473,7 @@ cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const Page
   const dim3 grid((unsigned)p.tiles, a.c.nkv, p.splits);
   cudaError_t e;
   if (p.kind <= 2) e = launch_paged_attention_tc(a, p.kind, p.tiles, st);
-  else if (!dtype) e = launch_paged_attention_f32(a, p.kind, p.tiles, st);
+  else if (!dtype) e = launch_paged_attention_f32(a, p.tiles, st);
   else if (p.kind == 16) e = run_simt<16, 2>(a, grid, st);
   else e = run_simt<64, 4>(a, grid, st);
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;

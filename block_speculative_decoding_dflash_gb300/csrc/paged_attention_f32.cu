@@ -1,20 +1,29 @@
-// Attention over the paged cache in fp32 on CUDA cores.
+// Attention over the paged cache in fp32.
 //
-// BM packed query rows (row r = token r / G, head r % G of the group) against
-// 64 keys at a time. Thread (ty, tx) holds TM rows ty * TM .. and keys tx,
-// tx + 16, .. of the scores, then dims tx * 4 + 64 j of the same rows' output:
-// 16 lanes share a row, so row statistics are shuffles within half a warp. A
-// 4 x 4 tile of scores takes 8 16-byte shared loads for 64 multiplications
-// (two to an instruction), which keeps the FMA pipes, not shared memory, the
-// bound. K and V have one buffer each: the next K arrives while P V runs, the
-// next V while Q K^T does, and a second CTA on the SM fills the rest.
+// The products run on the tensor cores in tf32 with every factor in two parts,
+// x = hi + lo: x y = hi hi + hi lo + lo hi, whose missing lo lo is 2^-22 of x y, as
+// much as lo's own rounding. Few query rows read K and V once, which the HBM
+// bounds; on CUDA cores the same rows read them from shared memory many times
+// over (8 sequences of up to 10 rows over up to 4099 keys, 8 heads: 84 us).
 //
-// Three bf16 or two tf32 parts of every factor on the tensor cores would give
-// fp32's accuracy too, at 6 or 3 products; for the few rows of a decode or
-// verify block that is no less time than this.
+// A CTA has 16 packed query rows (row r = token r / G, head r % G of the group)
+// against 64 keys at a time. For the scores each of its 8 warps takes 8 of the
+// keys; for P V an eighth of the dimensions. In both a lane's rows are the same,
+// so the running maximum rescales the output where it lies. Which dimension (key)
+// is which of an instruction's eight K elements is free as long as both operands
+// agree, and so is the order of its columns: they are chosen so that a lane's
+// elements are neighbours and shared loads are free of bank conflicts.
+//
+// A tensor core's sums are fp32 but not rounded to nearest: the large products of a
+// tile are summed apart from the small ones, at most 16 of them in a chain, and
+// tiles are joined by ordinary additions.
+//
+// K and V come by TMA, a box per page, 32 dimensions wide, into one buffer each:
+// the next K arrives while P V runs, the next V while Q K^T does, and a second CTA
+// on the SM fills the rest. (With cp.async, 16 to a thread and tile, half of a
+// tile's time went into their instructions: 61 us.)
 #include <math.h>
 
-#include "mma_sync.cuh"
 #include "paged_tc.cuh"
 
 namespace dfl {
@@ -26,38 +35,82 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBN = 64;
 constexpr int kMaxTiles = (1 << 20) / kBN;
 
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-// All but the newest N groups of this thread's copies have landed.
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// D += A B: 16 x 8 of A, row g or g + 8 and element c or c + 4 of lane 4 g + c; 8 x 8 of B, its element c or c + 4 and column g.
+__device__ __forceinline__ void mma_tf32(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The two parts of K's and V's values: hi is cut, not rounded, so that the
+// largest finite value stays finite; what tf32 drops of lo is 2^-21 of x.
+__device__ __forceinline__ void cut2(float x, uint32_t& hi, uint32_t& lo) {
+  hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// Of Q's and P's: hi rounded, so that lo has a bit less to hold. -0 is (-0, 0).
+__device__ __forceinline__ void round2(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+// W neighbours in one load.
+template <int W>
+struct Few {
+  float v[W];
+  __device__ __forceinline__ explicit Few(const float* p) {
+    if constexpr (W == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+    else if constexpr (W == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p);
+    else v[0] = *p;
+  }
+};
+__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.4028234663852886e38f); }
 
-template <int BM, int HDP>
+constexpr int kBM = 16, kWarps = 8;
+
+template <int HDP>
 struct F32Shape {
-  static constexpr int LD = HDP + 4;          // row stride: 16-byte loads of 8 rows touch all banks
-  static constexpr int kQ = 0, kK = BM * LD, kV = kK + kBN * LD, kP = kV + kBN * LD, kPos = kP + BM * (kBN + 4), kRow = kPos + kBN, kEnd = kRow + 2 * kBN;
-  static constexpr size_t kSmem = (size_t)kEnd * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
+  static constexpr int kSub = HDP / 32;                   // K and V tiles lie in parts of 32 dimensions, 128-byte swizzled
+  static constexpr int kTileB = kBN * HDP * 4, kSubB = kBN * 128;
+  static constexpr int LDP = kBN + 8, LDQ = HDP + 16;
+  static constexpr bool kQRegs = HDP <= 128;              // Q in registers, otherwise in shared memory
+  static constexpr int kK = 0, kV = kTileB, kP = 2 * kTileB, kQ = kP + kBM * LDP * 4, kMax = kQ + (kQRegs ? 0 : kBM * LDQ * 4),
+                       kRow = kMax + kWarps * kBM * 4, kBits = kRow + 2 * kBN * 4, kEnd = kBits + 2 * (kMaxTiles / 32 + 1) * 4;
+  static constexpr size_t kSmem = kEnd + 1024;
 };
 
-template <int BM, int TM, int HDP>
-__global__ void __launch_bounds__(BM / TM * 16, HDP > 128 || BM > 32 ? 1 : 2) paged_attn_f32_kernel(const __grid_constant__ PagedAttnArgs a) {
-  using C = F32Shape<BM, HDP>;
-  constexpr int NT = BM / TM * 16, LD = C::LD, NJ = HDP / 64;
-  extern __shared__ __align__(16) float smf[];
-  float *sq = smf + C::kQ, *sk = smf + C::kK, *sv = smf + C::kV, *sp = smf + C::kP;
-  int* spos = reinterpret_cast<int*>(smf + C::kPos);
-  int* srow = reinterpret_cast<int*>(smf + C::kRow);      // [2][kBN] places of a tile's rows, -1 for none
-  unsigned* some = reinterpret_cast<unsigned*>(smf + C::kEnd);
-  unsigned* all = some + kMaxTiles / 32 + 1;
+template <int HDP>
+__global__ void __launch_bounds__(kWarps * 32, HDP > 128 ? 1 : 2)
+paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
+  using C = F32Shape<HDP>;
+  constexpr int NT = kWarps * 32, LDP = C::LDP;
+  constexpr int kSteps = HDP / 16;            // of 16 dimensions, two instructions each
+  constexpr int W = HDP / 64;                 // a warp's tiles of 8 dimensions, all from one load
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t k_full, v_full;
   __shared__ PagedTile st;
   __shared__ int s_qmin, s_qmax;
+  __shared__ unsigned s_bad[kBN / 32];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
+  float *sp = reinterpret_cast<float*>(sm + C::kP), *sq = reinterpret_cast<float*>(sm + C::kQ), *smax = reinterpret_cast<float*>(sm + C::kMax);
+  int* srow = reinterpret_cast<int*>(sm + C::kRow);       // [2][kBN] places of a tile's rows, -1 for none
+  unsigned* some = reinterpret_cast<unsigned*>(sm + C::kBits);
+  unsigned* all = some + kMaxTiles / 32 + 1;
+  if (threadIdx.x == 0) {
+    mbar_init(&k_full, 1);
+    mbar_init(&v_full, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&mk);
+    tma_prefetch_desc(&mv);
+  }
   pdl_enter();
   const PagedView& c = a.c;
   const int h = blockIdx.y, z = blockIdx.z, G = a.G, hd = c.hd;
   if (threadIdx.x < 32) {
-    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, G, BM, blockIdx.x);
+    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, G, kBM, blockIdx.x);
     int lo = INT32_MAX, hi = INT32_MIN;
     if (t.seq >= 0) {
-      const int r0 = t.tile * BM, r1 = min(t.count * G, r0 + BM);
+      const int r0 = t.tile * kBM, r1 = min(t.count * G, r0 + kBM);
       for (int i = r0 / G + (int)threadIdx.x; i <= (r1 - 1) / G; i += 32) {
         const int p = a.q_pos[t.first + i];
         lo = min(lo, p);
@@ -74,245 +127,323 @@ __global__ void __launch_bounds__(BM / TM * 16, HDP > 128 || BM > 32 ? 1 : 2) pa
   const int len = paged_length(c, t.seq);
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
-  const int r0 = t.tile * BM, n_rows = min(BM, t.count * G - r0);
-  // rows of Q, zeros past hd and past the last
-  constexpr int kChunks = HDP / 4;
-  for (int e = threadIdx.x; e < BM * kChunks; e += NT) {
-    const int r = e / kChunks, d = e % kChunks * 4;
-    const bool in = r < n_rows && d < hd;
-    const float* src = static_cast<const float*>(a.q);
-    if (in) src += (size_t)(t.first + (r0 + r) / G) * a.q_stride + (size_t)(h * G + (r0 + r) % G) * hd + d;
-    cp_async16(sq + r * LD + d, src, in);
-  }
-  cp_commit();
-  paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  int pq[TM];
-  PagedSees sees[TM];
-  float slope2[TM], mx[TM], sum[TM];
-  uint64_t o[TM][NJ * 2];
+  const int r0 = t.tile * kBM, n_rows = min(kBM, t.count * G - r0);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, e4 = lane & 3;
+  // Q, zeros past hd and past the last row
+  auto q_at = [&](int r, int d) {
+    return r < n_rows && d < hd ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (size_t)(t.first + (r0 + r) / G) * a.q_stride +
+                                                                   (size_t)(h * G + (r0 + r) % G) * hd + d)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  float4 q[C::kQRegs ? kSteps : 1][2];
+  if constexpr (C::kQRegs) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = r0 + min(ty * TM + i, n_rows - 1);
+    for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) q[s][i] = q_at(g + 8 * i, s * 16 + e4 * 4);
+  } else {
+    for (int e = threadIdx.x; e < kBM * HDP / 4; e += NT) *reinterpret_cast<float4*>(sq + e / (HDP / 4) * C::LDQ + e % (HDP / 4) * 4) = q_at(e / (HDP / 4), e % (HDP / 4) * 4);
+  }
+  paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
+  // of the lane's two rows, g and g + 8
+  int pq[2];
+  PagedSees sees[2];
+  float slope2[2], mx[2], sum[2], o[W][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = r0 + min(g + 8 * i, n_rows - 1);
     pq[i] = a.q_pos[t.first + r / G];
     sees[i] = paged_sees_of(m, pq[i]);
     slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
     mx[i] = -INFINITY;
     sum[i] = 0.f;
-#pragma unroll
-    for (int d = 0; d < NJ * 2; ++d) o[i][d] = 0;
   }
+#pragma unroll
+  for (int n = 0; n < W; ++n)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) o[n][x] = 0.f;
   // a score in log2 units: dot * scale2, or cap2 * tanh(dot * scale2)
   const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
   __syncthreads();
   paged_take(sh, some, z, a.splits);
   PagedCursor cur(some, sh);
 
-  // thread e copies 16 bytes e % kChunks of rows e / kChunks, + NT / kChunks, ..
-  static_assert(NT % kChunks == 0, "whole rows at a time");
-  constexpr int kStep = NT / kChunks, kRows = kBN / kStep;
-  const int lr = threadIdx.x / kChunks, ld = threadIdx.x % kChunks * 4;
-  const bool cols = ld < hd;
-  auto find = [&](int* rows, int tile) {
-    if (threadIdx.x < kBN) {
-      const int slot = tile * kBN + threadIdx.x;
-      rows[threadIdx.x] = slot < len ? (int)paged_row(c, t.seq, h, slot) : -1;
-    }
+  // A row's place: its page is requested a tile before it is needed.
+  const int my_slot = threadIdx.x & (kBN - 1);
+  auto page_of = [&](int rel) {
+    const int slot = (sh.t0 + rel) * kBN + my_slot;
+    return threadIdx.x < kBN && rel >= 0 && slot < len ? c.table[(size_t)t.seq * c.max_pages + (slot >> c.lg_rows)] : -1;
   };
-  auto copy = [&](float* dst, const void* base, const int* rows) {
-    const float* src = static_cast<const float*>(base) + ld;
+  auto put_row = [&](int* rows, int rel, int page) {
+    const int slot = (sh.t0 + rel) * kBN + my_slot;
+    if (threadIdx.x < kBN)
+      rows[my_slot] = (unsigned)page < (unsigned)c.n_pages ? ((page * c.nkv + h) << c.lg_rows) + (slot & ((1 << c.lg_rows) - 1)) : -1;
+  };
+  const int box = min(1 << c.lg_rows, kBN), boxes = kBN / box;
+  const int beyond = (c.n_pages * c.nkv) << c.lg_rows;     // a row past the pool reads as zeros
+  // warp 0: the boxes of a tile
+  auto copy = [&](int off, const CUtensorMap* map, const int* rows, uint64_t* bar) {
+    if (lane == 0) mbar_expect_tx(bar, C::kTileB);
+    __syncwarp();
+    if (lane >= boxes) return;
+    const int row = rows[lane * box], y = row >= 0 ? row : beyond;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const int j = lr + i * kStep, row = rows[j];
-      const bool in = row >= 0 && cols;
-      cp_async16(dst + j * LD + ld, src + (in ? (long long)row * hd : 0ll), in);
-    }
-    cp_commit();
+    for (int x = 0; x < C::kSub; ++x) tma_load_2d(sm + off + x * C::kSubB + lane * box * 128, map, x * 64, y, bar);
   };
-  int rel = cur.next(), buf = 0;
-  if (rel >= 0) find(srow, sh.t0 + rel);
+  bool ok = true;
+  unsigned phase = 0;
+  int rel = cur.next(), next = cur.next(), buf = 0, page = page_of(next);
+  if (rel >= 0) put_row(srow, rel, page_of(rel));
   __syncthreads();
-  if (rel >= 0) copy(sk, c.k, srow);
-  for (; rel >= 0; buf ^= 1) {
+  if (rel >= 0 && warp == 0) {
+    copy(C::kK, &mk, srow, &k_full);
+    copy(C::kV, &mv, srow, &v_full);
+  }
+  // where this lane's K and V elements lie: K's row 8 warp + perm(g) (column g of the
+  // instruction is that key), V's rows 2 e4, + 1, + 8, + 9 of every 16
+  const int k_row = warp * 8 + (g >> 1) + 4 * (g & 1);
+  const uint8_t* k_at = sm + C::kK + k_row * 128;
+  const uint8_t* v_at = sm + C::kV + (warp * 8 * W >> 5) * C::kSubB;
+  const int v_col = warp * 8 * W + g * W & 31;
+  for (; rel >= 0; buf ^= 1, phase ^= 1) {
     const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
-    const int next = cur.next();
     const int* rows = srow + buf * kBN;
-    copy(sv, c.v, rows);
-    if (threadIdx.x < kBN && (!full || a.slopes)) {
-      const int row = rows[threadIdx.x];
-      spos[threadIdx.x] = row >= 0 ? c.pos[row] : kPagedNoPos;
-    }
-    if (next >= 0) find(srow + (buf ^ 1) * kBN, sh.t0 + next);
-    cp_wait<1>();                            // K
-    __syncthreads();
-    uint64_t s2[TM][4];
+    if (next >= 0) put_row(srow + (buf ^ 1) * kBN, next, page);
+    const int after = cur.next();
+    page = page_of(after);
+    int pk[2] = {kPagedNoPos, kPagedNoPos};               // of keys 8 warp + e4, + 4
+    if (!full || a.slopes)
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s2[i][j] = 0;
-#pragma unroll 8
-    for (int d = 0; d < HDP; d += 4) {
-      ulonglong2 q[TM], k[4];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) q[i] = *reinterpret_cast<const ulonglong2*>(sq + (ty * TM + i) * LD + d);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const ulonglong2*>(sk + (tx + 16 * j) * LD + d);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s2[i][j] = fma2(q[i].x, k[j].x, s2[i][j]);
-          s2[i][j] = fma2(q[i].y, k[j].y, s2[i][j]);
-        }
-    }
-    __syncthreads();                         // K is free
-    if (next >= 0) copy(sk, c.k, srow + (buf ^ 1) * kBN);
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      unsigned seen = 0;
-      float s[4], top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float x, y;
-        unpack2(s2[i][j], x, y);
-        float u = (x + y) * scale2;
-        if (a.softcap > 0.f) u = cap2 * tanhf(u);
-        bool v = true;
-        if (!full || a.slopes) {
-          const int pk = spos[tx + 16 * j];
-          v = full || paged_sees(sees[i], pk);
-          if (a.slopes) u -= slope2[i] * fabsf((float)(pq[i] - pk));
-        }
-        s[j] = v ? u : -INFINITY;
-        seen |= (unsigned)v << j;
-        top = fmaxf(top, s[j]);
+      for (int x = 0; x < 2; ++x) {
+        const int row = rows[warp * 8 + e4 + 4 * x];
+        if (row >= 0) pk[x] = c.pos[row];
       }
+    paged_wait(&k_full, phase, ok);
+    // scores of rows g, g + 8 and keys 8 warp + e4, + 4
+    float s4[4], odd[4], low[2][4];
 #pragma unroll
-      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float mn = fmaxf(mx[i], top);
+    for (int x = 0; x < 4; ++x) s4[x] = odd[x] = low[0][x] = low[1][x] = 0.f;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      uint32_t qh[2][4], ql[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4 v = C::kQRegs ? q[C::kQRegs ? s : 0][i] : *reinterpret_cast<const float4*>(sq + (g + 8 * i) * C::LDQ + s * 16 + e4 * 4);
+        // (not to be taken out of the loop: the parts of all of Q do not fit the registers)
+        asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w));
+        round2(v.x, qh[i][0], ql[i][0]);
+        round2(v.y, qh[i][1], ql[i][1]);
+        round2(v.z, qh[i][2], ql[i][2]);
+        round2(v.w, qh[i][3], ql[i][3]);
+      }
+      const float4 k = *reinterpret_cast<const float4*>(k_at + (s >> 1) * C::kSubB + ((((s & 1) * 4 + e4) ^ (k_row & 7)) << 4));
+      uint32_t kh[4], kl[4];
+      cut2(k.x, kh[0], kl[0]);
+      cut2(k.y, kh[1], kl[1]);
+      cut2(k.z, kh[2], kl[2]);
+      cut2(k.w, kh[3], kl[3]);
+      float* big = s & 1 ? odd : s4;
+#pragma unroll
+      for (int x = 0; x < 4; x += 2) {
+        mma_tf32(big, qh[0][x], qh[1][x], qh[0][x + 1], qh[1][x + 1], kh[x], kh[x + 1]);
+        mma_tf32(low[0], qh[0][x], qh[1][x], qh[0][x + 1], qh[1][x + 1], kl[x], kl[x + 1]);
+        mma_tf32(low[1], ql[0][x], ql[1][x], ql[0][x + 1], ql[1][x + 1], kh[x], kh[x + 1]);
+      }
+    }
+    unsigned seen = 0;
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int i = x >> 1;
+      float u = (s4[x] + odd[x] + (low[0][x] + low[1][x])) * scale2;
+      if (a.softcap > 0.f) u = cap2 * tanhf(u);
+      if (a.slopes) u -= slope2[i] * fabsf((float)(pq[i] - pk[x & 1]));
+      const bool v = full || paged_sees(sees[i], pk[x & 1]);
+      s4[x] = v ? u : -INFINITY;
+      seen |= (unsigned)v << x;
+      top[i] = fmaxf(top[i], s4[x]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
+      top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
+      if (e4 == 0) smax[warp * kBM + g + 8 * i] = top[i];
+    }
+    __syncthreads();                         // maxima of all warps; K is free
+    if (warp == 0 && next >= 0) copy(C::kK, &mk, srow + (buf ^ 1) * kBN, &k_full);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float mn = mx[i];
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) mn = fmaxf(mn, smax[w * kBM + g + 8 * i]);
       const float base = mn == -INFINITY ? 0.f : mn;
-      float add = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[j] - base);
-        add += p;
-        // a hidden row's weight is -0, a seen one's that underflowed +0
-        sp[(ty * TM + i) * (kBN + 4) + tx + 16 * j] = (seen >> j) & 1u ? p : -0.f;
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
       if (mn != mx[i]) {
         const float f = exp2f(mx[i] - base);
         sum[i] *= f;
         mx[i] = mn;
-        const uint64_t f2 = pack2(f, f);
 #pragma unroll
-        for (int d = 0; d < NJ * 2; ++d) o[i][d] = fma2(o[i][d], f2, 0);
+        for (int n = 0; n < W; ++n) {
+          o[n][2 * i] *= f;
+          o[n][2 * i + 1] *= f;
+        }
       }
-      sum[i] += add;
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const float p = exp2f(s4[2 * i + x] - base);
+        sum[i] += p;
+        // a hidden row's weight is -0, a seen one's that underflowed +0
+        sp[(g + 8 * i) * LDP + warp * 8 + e4 + 4 * x] = (seen >> (2 * i + x)) & 1u ? p : -0.f;
+      }
     }
-    if (next >= 0) cp_wait<1>();             // V; the next K stays in flight
-    else cp_wait<0>();
+    if (threadIdx.x < kBN / 32) s_bad[threadIdx.x] = 0u;
+    paged_wait(&v_full, phase, ok);
     __syncthreads();
-    // infinite or NaN values of V in a tile that some query sees only in part:
-    // its hidden rows must not be multiplied by their zero weight
+    // Infinite or NaN values of V in a tile that some query sees only in part:
+    // its hidden rows must not be multiplied by their zero weight. Such rows are
+    // made zeros, and added where they are seen.
     bool careful = false;
     if (!full) {
-      bool bad = false;
-      for (int e = threadIdx.x; e < kBN * kChunks; e += NT) {
-        const float4 v = *reinterpret_cast<const float4*>(sv + e / kChunks * LD + e % kChunks * 4);
-        bad = bad || !(fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))) <= 3.4028234663852886e38f) || v.x != v.x || v.y != v.y ||
-              v.z != v.z || v.w != v.w;
+      unsigned bad = 0;
+      constexpr int kEach = kBN * HDP / 4 / NT;            // 16-byte pieces of a thread
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(sm + C::kV + (i * NT + threadIdx.x) * 16);
+        bad |= (unsigned)(not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w)) << i;
       }
-      careful = __syncthreads_or(bad);
+      careful = __syncthreads_or(bad != 0);
+      if (careful) {
+        for (int i = 0; i < kEach; ++i) {
+          const int j = ((i * NT + (int)threadIdx.x) >> 3) & (kBN - 1);
+          if ((bad >> i) & 1u) atomicOr(&s_bad[j >> 5], 1u << (j & 31));
+        }
+        __syncthreads();
+        for (int i = 0; i < kEach; ++i) {
+          const int e = i * NT + threadIdx.x, j = (e >> 3) & (kBN - 1);
+          if ((s_bad[j >> 5] >> (j & 31)) & 1u) *reinterpret_cast<float4*>(sm + C::kV + e * 16) = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        fence_proxy_async_shared();          // the next copy comes after these writes
+        __syncthreads();
+      }
     }
-    if (!careful) {
-#pragma unroll 4
-      for (int j = 0; j < kBN; j += 4) {
-        float4 p[TM];
+    // rows g, g + 8 and dimensions 8 W warp + W (2 e4 + x) + n
+    float big[W][4], small[W][4];
 #pragma unroll
-        for (int i = 0; i < TM; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * TM + i) * (kBN + 4) + j);
+    for (int n = 0; n < W; ++n)
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          ulonglong2 v[NJ];
+      for (int x = 0; x < 4; ++x) big[n][x] = small[n][x] = 0.f;
 #pragma unroll
-          for (int n = 0; n < NJ; ++n) v[n] = *reinterpret_cast<const ulonglong2*>(sv + (j + jj) * LD + n * 64 + tx * 4);
+    for (int s = 0; s < kBN / 16; ++s) {
 #pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
-            const uint64_t w2 = pack2(w, w);
+      for (int y = 0; y < 2; ++y) {
+        const int key = s * 16 + y * 8 + e4 * 2;           // and the next
+        uint32_t ph[2][2], pl[2][2];
 #pragma unroll
-            for (int n = 0; n < NJ; ++n) {
-              o[i][n * 2] = fma2(w2, v[n].x, o[i][n * 2]);
-              o[i][n * 2 + 1] = fma2(w2, v[n].y, o[i][n * 2 + 1]);
+        for (int i = 0; i < 2; ++i) {
+          const float2 p = *reinterpret_cast<const float2*>(sp + (g + 8 * i) * LDP + key);
+          round2(p.x, ph[i][0], pl[i][0]);
+          round2(p.y, ph[i][1], pl[i][1]);
+        }
+        const Few<W> v0(reinterpret_cast<const float*>(v_at + key * 128 + (((v_col >> 2) ^ (key & 7)) << 4)) + (v_col & 3));
+        const Few<W> v1(reinterpret_cast<const float*>(v_at + (key + 1) * 128 + (((v_col >> 2) ^ (key + 1 & 7)) << 4)) + (v_col & 3));
+#pragma unroll
+        for (int n = 0; n < W; ++n) {
+          uint32_t h0, l0, h1, l1;
+          cut2(v0.v[n], h0, l0);
+          cut2(v1.v[n], h1, l1);
+          mma_tf32(big[n], ph[0][0], ph[1][0], ph[0][1], ph[1][1], h0, h1);
+          mma_tf32(small[n], ph[0][0], ph[1][0], ph[0][1], ph[1][1], l0, l1);
+          mma_tf32(small[n], pl[0][0], pl[1][0], pl[0][1], pl[1][1], h0, h1);
+        }
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < W; ++n)
+#pragma unroll
+      for (int x = 0; x < 4; ++x) o[n][x] += big[n][x] + small[n][x];
+    if (careful) {
+      for (int j = 0; j < kBN; ++j) {
+        if (!((s_bad[j >> 5] >> (j & 31)) & 1u) || rows[j] < 0) continue;
+        const float* v = static_cast<const float*>(c.v) + (long long)rows[j] * hd;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float p = sp[(g + 8 * i) * LDP + j];
+          if (__float_as_uint(p) == 0x80000000u) continue;
+#pragma unroll
+          for (int n = 0; n < W; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int d = (warp * 8 + 2 * e4 + x) * W + n;
+              if (d < hd) o[n][2 * i + x] = fmaf(p, v[d], o[n][2 * i + x]);
             }
-          }
         }
       }
-    } else {
-      for (int j = 0; j < kBN; ++j)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          const float w = sp[(ty * TM + i) * (kBN + 4) + j];
-          if (__float_as_uint(w) == 0x80000000u) continue;
-          const uint64_t w2 = pack2(w, w);
-#pragma unroll
-          for (int n = 0; n < NJ; ++n) {
-            const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(sv + j * LD + n * 64 + tx * 4);
-            o[i][n * 2] = fma2(w2, v.x, o[i][n * 2]);
-            o[i][n * 2 + 1] = fma2(w2, v.y, o[i][n * 2 + 1]);
-          }
-        }
     }
-    __syncthreads();                         // V, P and the positions are free
+    const bool stop = __syncthreads_or(!ok);   // V and P are free
+    if (warp == 0 && next >= 0 && !stop) copy(C::kV, &mv, srow + (buf ^ 1) * kBN, &v_full);
+    if (stop) {
+      // a wait gave up: the K on its way, and what V there was, land before the CTA ends
+      ok = false;
+      bool landed = true;
+      paged_wait(&v_full, phase, landed);
+      if (next >= 0) paged_wait(&k_full, phase ^ 1, landed);
+      if (threadIdx.x == 0 && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
+      break;
+    }
     rel = next;
+    next = after;
   }
-  cp_wait<0>();
+  // the sums over the warps' keys
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = ty * TM + i;
+  for (int i = 0; i < 2; ++i) {
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+    if (e4 == 0) smax[warp * kBM + g + 8 * i] = sum[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = g + 8 * i;
     if (r >= n_rows) continue;
+    float total = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += smax[w * kBM + r];
     const size_t at = (size_t)(t.first + (r0 + r) / G) * a.nq + h * G + (r0 + r) % G;
-    const bool none = sum[i] == 0.f;         // nothing seen (a NaN score makes the sum NaN)
+    const bool none = total == 0.f;          // nothing seen (a NaN score makes the sum NaN)
     const bool split = a.splits > 1;
-    const float inv = none ? 0.f : (split ? 1.f : 1.f / sum[i]);
+    const float inv = none ? 0.f : (split ? 1.f : 1.f / total);
     float* out = split ? a.part_o + ((size_t)z * a.rows * a.nq + at) * hd : static_cast<float*>(a.out) + at * hd;
 #pragma unroll
-    for (int n = 0; n < NJ; ++n) {
-      float4 v;
-      unpack2(o[i][n * 2], v.x, v.y);
-      unpack2(o[i][n * 2 + 1], v.z, v.w);
-      if (n * 64 + tx * 4 < hd)
-        *reinterpret_cast<float4*>(out + n * 64 + tx * 4) =
-            none ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    for (int x = 0; x < 2; ++x) {
+      const int d = (warp * 8 + 2 * e4 + x) * W;
+      if (d >= hd) continue;
+#pragma unroll
+      for (int n = 0; n < W; ++n) out[d + n] = none ? 0.f : o[n][2 * i + x] * inv;
     }
-    if (tx) continue;
-    if (split) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], sum[i]);
-    else if (a.lse) a.lse[at] = none ? -INFINITY : (mx[i] + log2f(sum[i])) * kLn2;
+    if (warp || e4) continue;
+    if (split) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], total);
+    else if (a.lse) a.lse[at] = none ? -INFINITY : (mx[i] + log2f(total)) * kLn2;
   }
 }
 
-template <int BM, int TM, int HDP>
-cudaError_t run(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  auto kernel = paged_attn_f32_kernel<BM, TM, HDP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F32Shape<BM, HDP>::kSmem);
+template <int HDP>
+cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  // (the maps of bf16 rows of twice the columns: the bytes are what counts)
+  PagedView c = a.c;
+  c.hd *= 2;
+  CUtensorMap mk, mv;
+  if (!paged_map_pages(&mk, c.k, c, kBN) || !paged_map_pages(&mv, c.v, c, kBN)) return cudaErrorInvalidValue;
+  auto kernel = paged_attn_f32_kernel<HDP>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F32Shape<HDP>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, grid, dim3(BM / TM * 16), F32Shape<BM, HDP>::kSmem, st, a);
-}
-template <int BM, int TM>
-cudaError_t run_hd(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  if (a.c.hd <= 64) return run<BM, TM, 64>(a, grid, st);
-  if (a.c.hd <= 128) return run<BM, TM, 128>(a, grid, st);
-  return run<BM, TM, 256>(a, grid, st);
+  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), F32Shape<HDP>::kSmem, st, mk, mv, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attention_f32(const PagedAttnArgs& a, int tile_rows, long long tiles, cudaStream_t st) {
-  const dim3 grid((unsigned)tiles, a.c.nkv, a.splits);
-  if (tile_rows == 16) return run_hd<16, 2>(a, grid, st);
-  if (tile_rows == 32) return run_hd<32, 4>(a, grid, st);
-  return run_hd<64, 4>(a, grid, st);
+cudaError_t launch_paged_attention_f32(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  if (a.c.hd <= 64) return run<64>(a, tiles, st);
+  if (a.c.hd <= 128) return run<128>(a, tiles, st);
+  return run<256>(a, tiles, st);
 }
 
 }  // namespace dfl

@@ -835,10 +835,10 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
 
 }  // namespace
 
-bool paged_map_pages(CUtensorMap* m, const void* base, const PagedView& c) {
+bool paged_map_pages(CUtensorMap* m, const void* base, const PagedView& c, int most) {
   const int rows = 1 << c.lg_rows;
   return tc_encode_map(m, base, c.hd, ((uint64_t)c.n_pages * c.nkv) << c.lg_rows, (uint64_t)c.hd * 2, 64,
-                       rows < kPtKeys ? rows : kPtKeys);
+                       rows < most ? rows : most);
 }
 
 bool paged_map_rows(CUtensorMap* m, const void* base, const PagedAttnArgs& a, int per) {

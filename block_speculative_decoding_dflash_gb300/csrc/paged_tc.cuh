@@ -234,10 +234,10 @@ __device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
   }
 }
 
-// Maps of K or V as rows of head_dim (boxes of 64 elements x up to 128 rows)
+// Maps of K or V as rows of head_dim (boxes of 64 elements x up to `most` rows)
 // and of the query rows as [rows][n_q_heads][head_dim] (boxes of 64 elements x
 // G heads x per rows). Columns past head_dim and rows past the end read as 0.
-bool paged_map_pages(CUtensorMap* m, const void* base, const PagedView& c);
+bool paged_map_pages(CUtensorMap* m, const void* base, const PagedView& c, int most = kPtKeys);
 bool paged_map_rows(CUtensorMap* m, const void* base, const PagedAttnArgs& a, int per);
 
 }  // namespace dfl
