@@ -21,7 +21,10 @@
 // K and V come by TMA, a box per page, 32 dimensions wide, into one buffer each:
 // the next K arrives while P V runs, the next V while Q K^T does, and a second CTA
 // on the SM fills the rest. (With cp.async, 16 to a thread and tile, half of a
-// tile's time went into their instructions: 61 us.)
+// tile's time went into their instructions: 61 us.) Those blocks take 56 us, 2.3
+// TB/s, 64 such sequences 384 us, 2.8 TB/s: nothing waits for memory any more; the
+// time goes into taking values apart and into the products' latency (a warp
+// issues every fifth cycle; tensor pipe 31%, integer pipe 31%).
 #include <math.h>
 
 #include "paged_tc.cuh"

@@ -8,7 +8,7 @@
 // exponentials of one run while the next is computed, and a second CTA on the SM
 // works while this one starts or ends. Bounded by the exponentials, one ex2 to a
 // score, against 2 head_dim flops on the tensor cores, for many query rows, and
-// by a CTA's start and end for few.
+// by a CTA's start and end for few (16 rows over 6000 keys: 7.5 us).
 // (Two key tiles to a CTA, which would halve the passes over the query rows, and
 // one CTA to an SM took 166 us instead of 154 us for 512 rows over 32768 keys.)
 #include <math.h>
@@ -500,7 +500,8 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
 
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   // Few query rows: CTAs, two to an SM, that pass several key tiles each, two
-  // waves of them for sequences of different lengths. (The kernel decides by each
+  // waves of them for sequences of different lengths (32 rows of decode over 12000
+  // keys: 83 us, with a CTA to every key tile 292 us). (The kernel decides by each
   // sequence's own rows what it does; a grid for the other case only starts more
   // CTAs.)
   if ((long long)a.rows * a.G <= 128ll * a.c.n_seq) {
