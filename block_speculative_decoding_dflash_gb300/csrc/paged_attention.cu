@@ -439,8 +439,9 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
     fill = 152;
     least = 512;
   } else {
-    // the smallest tile that holds an average sequence's rows (fp32: 16 always;
-    // 40 rows of 2 heads to a kv head: 148 us in tiles of 16, 155 us of 32)
+    // the smallest tile that holds an average sequence's rows (100 rows of 4
+    // sequences, 4 heads to a kv head: 670 us in tiles of 64, 2163 us of 16; one
+    // row each of 8: 719 us and 710 us); fp32: 16 always
     p.kind = !dtype || units <= 16ll * a.c.n_seq ? 16 : 64;
     p.tiles = tile_bound(units, p.kind, a);
     fill = 608;

@@ -9,9 +9,9 @@
 // those. Sources lie at or beyond row `budget` and destinations below it, so
 // the moves are independent, and nothing that stays is touched.
 //
-// 2304 rows to 2048 in 8 heads: 11.6 us, the two kernels' dependent steps; 12
-// sequences of up to 32768 rows to 16000: 79 us, of which the selection takes 32 us
-// and the moves 40 us (rows of 256 bytes, read and written at 4 TB/s).
+// 2304 rows to 2048 in 8 heads: 10.9 us, the two kernels' dependent steps; 12
+// sequences of up to 32768 rows to 16000: 76 us, of which the moves take 40 us (rows
+// of 256 bytes, read and written at 4 TB/s).
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -41,7 +41,7 @@ struct Shared {
   int hist[2][kBins];                        // in turns, so that a pass need not wait for the others' reads of the last
   int2 warps[kWarps];
   int2 total;                                // of this CTA, for the others of its cluster
-  int digit, left, eq_before;
+  int digit, left, eq_before, all_stay;
 };
 
 // Every CTA of the cluster (or, alone, every thread) has come here and sees
@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
         while (left > before + cnt[j]) before += cnt[j++];
         sh.digit = at + kBinsEach - 1 - j;
         sh.left = left - before;
+        sh.all_stay = left - before == cnt[j];
         if (d == 2) {
           // the last digit's bin counts the rows whose key is the one of rank b
           int eq = 0;
@@ -234,6 +235,15 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
       __syncthreads();
       prefix |= (unsigned)sh.digit << shift;
       left = sh.left;
+      if (d < 2 && sh.all_stay) {
+        // every row with these top bits stays (weights seldom agree in 22 bits):
+        // the border lies below them, and the digits left need no pass (2304
+        // rows: 10.9 us, with all three passes 11.6 us). Not zero: with the lowest
+        // digit n <= b rows would stay.
+        prefix -= 1;
+        left = 0;
+        break;
+      }
     }
   }
   // `prefix` is now the key of rank b: greater keys stay, of the equal ones
@@ -265,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
     __syncthreads();
     // words in order, one to a thread: which equal rows stay, and the number of
     // holes below row b and of kept rows from it on
-    int eq_run = sh.eq_before;
+    int eq_run = left ? sh.eq_before : 0;
     int2 run = make_int2(0, 0), tot;
     for (int x0 = 0; x0 < words; x0 += kThreads) {
       const int x = x0 + tid;
@@ -403,7 +413,8 @@ cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t 
   const int cap = a.c.max_pages << a.c.lg_rows, pairs = a.c.nkv * a.c.n_seq;
   // CTAs to a (sequence, kv head): more where a CTA would have more than 4096
   // rows and SMs (two CTAs to each) would be idle, and so that the masks fit (12
-  // sequences of up to 32768 rows: 79 us, with one CTA to each 136 us)
+  // sequences of up to 32768 rows: 79 us, with one CTA to each 136 us, both with
+  // all three passes)
   int ranks = 1;
   while (ranks < kRanks && (cap / ranks > kMostRows || (cap / ranks > 4096 && (long long)pairs * ranks * 2 <= 304))) ranks *= 2;
   const int per = (cap + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;

@@ -500,8 +500,8 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
 
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   // Few query rows: CTAs, two to an SM, that pass several key tiles each, two
-  // waves of them for sequences of different lengths (32 rows of decode over 12000
-  // keys: 83 us, with a CTA to every key tile 292 us). (The kernel decides by each
+  // waves of them for sequences of different lengths (32 sequences of one row over
+  // 12000 keys: 83 us, with a CTA to every key tile 292 us). (The kernel decides by each
   // sequence's own rows what it does; a grid for the other case only starts more
   // CTAs.)
   if ((long long)a.rows * a.G <= 128ll * a.c.n_seq) {
