@@ -769,6 +769,14 @@ class PagedCache:
         positions q_pos [rows]; rows start[s] .. start[s + 1] - 1 belong to sequence s. scale None: head_dim ** -0.5."""
         args = self._attention_args(q, q_pos, start, self._need("out", out, self.dtype, q.shape), lse, scale, causal, window, softcap,
                                     slopes, prefix, max_len)
+        if workspace is None:
+            # most calls need none and are done with this one; a refused one asks
+            # (and hears of anything else that is wrong)
+            try:
+                return self._launch(lib.dflash_paged_attention, stream, args + _NO_WORKSPACE)
+            except DFlashError as e:
+                if e.code != EINVAL:
+                    raise
         self._with_workspace(lib.dflash_paged_attention, lib.dflash_paged_attention_workspace, args, workspace, stream)
 
     def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
