@@ -7,6 +7,7 @@
 #include <math.h>
 
 #include "paged.cuh"
+#include "paged_tf32.cuh"
 
 namespace dfl {
 
@@ -291,98 +292,132 @@ __global__ void __launch_bounds__(128) paged_attn_merge_kernel(PagedAttnArgs a) 
   if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-// Key weights: a CTA holds kBN keys of one (sequence, kv head) and passes over
-// the sequence's query rows, 64 at a time; thread (ty, tx) has keys ty * 4 ..
-// and query rows tx, tx + 16, .., and adds exp2(u - lse) over its rows. One CTA
-// owns a key, so the sum's order is fixed. Bounded by the FMA rate for more
-// than a few query rows.
+// Key weights for fp32, and for bf16 heads of more than 128 dimensions: S^T = K Q^T
+// on the tensor cores in tf32, fp32's factors in two parts (see paged_tf32.cuh;
+// bf16 is a tf32 as it stands). A warp has 16 keys in registers, read once, and
+// the CTA passes the sequence's query rows by in shared memory, kWRows at a time; a
+// lane adds exp2(u - lse) over its columns for its two keys, the four lanes of a key
+// are summed at the end: no atomics, and a fixed order. (On CUDA cores, 16
+// sequences of up to 10 rows and 6000 keys, 8 heads, fp32: 220 us; so: 81 us.)
+constexpr int kWRows = 64;
+
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const bf16* p) {
+  const uint2 u = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
+}
+
 template <typename T, int HDP>
-__global__ void __launch_bounds__(256) paged_weight_simt_kernel(PagedAttnArgs a) {
-  constexpr int LD = HDP + 4;
+__global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kernel(const __grid_constant__ PagedAttnArgs a) {
+  constexpr bool kParts = sizeof(T) == 4;
+  constexpr int LD = HDP + 16, kSteps = HDP / 16;
   pdl_enter();
-  extern __shared__ float smf[];
-  float* sk = smf;                          // [kBN][LD]
-  float* sq = sk + kBN * LD;                // [64][LD]
-  __shared__ int sqp[64], spos[kBN];
-  __shared__ float slse[64], sslope[64];
+  extern __shared__ __align__(16) float sq[];     // [kWRows][LD]
+  __shared__ int sqp[kWRows];
+  __shared__ float snl[kWRows], sslope[kWRows];   // minus lse and the slope, in log2 units; -inf for what adds nothing
   const PagedView& c = a.c;
-  const int h = blockIdx.y, s = blockIdx.z, G = a.G;
+  const int h = blockIdx.y, s = blockIdx.z, G = a.G, hd = c.hd;
   const int2 ab = paged_new_rows(a.start, s, a.rows);
   const int len = paged_length(c, s), R = (ab.y - ab.x) * G;
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, s);
   const PagedScore ps = paged_score_of(a);
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, e4 = lane & 3;
   for (int k0 = blockIdx.x * kBN; k0 < len; k0 += gridDim.x * kBN) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kBN * 16; e += 256) {
-      const int j = e >> 4;
-      const long long row = k0 + j < len ? paged_row(c, s, h, k0 + j) : -1;
-      load_row<T, HDP>(sk + j * LD, row >= 0 ? static_cast<const T*>(c.k) + row * c.hd : nullptr, c.hd, e & 15, 16);
-      if ((e & 15) == 0) spos[j] = row >= 0 ? c.pos[row] : kPagedNoPos;
-    }
-    __syncthreads();
-    int pk[4];
-    float w[4] = {0.f, 0.f, 0.f, 0.f};
+    // the lane's keys, g and g + 8 of the warp's
+    long long row[2];
+    int pk[2];
+    PagedSees by[2];
+    float w[2] = {0.f, 0.f};
+    float4 k[kSteps][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) pk[i] = spos[ty * 4 + i];
-    for (int q0 = 0; q0 < R; q0 += 64) {
+    for (int i = 0; i < 2; ++i) {
+      const int slot = k0 + warp * 16 + g + 8 * i;
+      row[i] = slot < len ? paged_row(c, s, h, slot) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const T* src = static_cast<const T*>(c.k) + (row[i] >= 0 ? row[i] : 0) * hd;
+      pk[i] = row[i] >= 0 ? c.pos[row[i]] : kPagedNoPos;
+      by[i] = paged_seen_by(m, pk[i]);
+#pragma unroll
+      for (int t = 0; t < kSteps; ++t)
+        k[t][i] = row[i] >= 0 && t * 16 + e4 * 4 < hd ? load4(src + t * 16 + e4 * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int q0 = 0; q0 < R; q0 += kWRows) {
+      const int n = min(kWRows, R - q0), n16 = (n + 15) & ~15;
       __syncthreads();
-      for (int e = threadIdx.x; e < 64 * 16; e += 256) {
-        const int r = e >> 4, rr = q0 + r;
-        const bool in = rr < R;
-        const size_t tok = in ? ab.x + rr / G : 0;
-        const int head = in ? h * G + rr % G : 0;
-        load_row<T, HDP>(sq + r * LD, in ? static_cast<const T*>(a.q) + tok * a.q_stride + (size_t)head * c.hd : nullptr, c.hd, e & 15, 16);
-        if ((e & 15) == 0) {
-          const float l = in ? a.lse[tok * a.nq + head] : -INFINITY;
-          sqp[r] = in ? a.q_pos[tok] : 0;
-          slse[r] = l * kLog2e;
-          sslope[r] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
-        }
+      for (int e = threadIdx.x; e < n16 * (HDP / 4); e += 128) {
+        const int r = e / (HDP / 4), d = e % (HDP / 4) * 4, rr = q0 + r;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < n && d < hd) v = load4(static_cast<const T*>(a.q) + (size_t)(ab.x + rr / G) * a.q_stride + (size_t)(h * G + rr % G) * hd + d);
+        *reinterpret_cast<float4*>(sq + r * LD + d) = v;
+      }
+      for (int r = threadIdx.x; r < n16; r += 128) {
+        const bool in = r < n;
+        const size_t tok = in ? ab.x + (q0 + r) / G : 0;
+        const int head = in ? h * G + (q0 + r) % G : 0;
+        const float l = in ? a.lse[tok * a.nq + head] : -INFINITY;
+        sqp[r] = in ? a.q_pos[tok] : 0;
+        snl[r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        sslope[r] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
       }
       __syncthreads();
-      float acc[4][4];
+#pragma unroll 1
+      for (int n0 = 0; n0 < n; n0 += 16) {
+        // scores of keys g, g + 8 and rows n0 + 8 y + 2 e4, + 1
+        float big[2][4], odd[2][4], low[2][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < HDP; d += 4) {
-        float4 k[4], q[4];
+          for (int x = 0; x < 4; ++x) big[y][x] = odd[y][x] = low[y][x] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) k[i] = *reinterpret_cast<const float4*>(sk + (ty * 4 + i) * LD + d);
+        for (int t = 0; t < kSteps; ++t) {
+          uint32_t kh[2][4], kl[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) q[j] = *reinterpret_cast<const float4*>(sq + (tx + 16 * j) * LD + d);
+          for (int i = 0; i < 2; ++i) {
+            float4 v = k[t][i];
+            // (not to be taken out of the loop: the parts of all of K do not fit the registers)
+            if (kParts) asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w));
+            cut2(v.x, kh[i][0], kl[i][0]);
+            cut2(v.y, kh[i][1], kl[i][1]);
+            cut2(v.z, kh[i][2], kl[i][2]);
+            cut2(v.w, kh[i][3], kl[i][3]);
+          }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+          for (int y = 0; y < 2; ++y) {
+            const float4 q = *reinterpret_cast<const float4*>(sq + (n0 + y * 8 + g) * LD + t * 16 + e4 * 4);
+            uint32_t qh[4], ql[4];
+            round2(q.x, qh[0], ql[0]);
+            round2(q.y, qh[1], ql[1]);
+            round2(q.z, qh[2], ql[2]);
+            round2(q.w, qh[3], ql[3]);
+            float* to = t & 1 ? odd[y] : big[y];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            acc[i][j] = fmaf(k[i].x, q[j].x, acc[i][j]);
-            acc[i][j] = fmaf(k[i].y, q[j].y, acc[i][j]);
-            acc[i][j] = fmaf(k[i].z, q[j].z, acc[i][j]);
-            acc[i][j] = fmaf(k[i].w, q[j].w, acc[i][j]);
+            for (int x = 0; x < 4; x += 2) {
+              mma_tf32(to, kh[0][x], kh[1][x], kh[0][x + 1], kh[1][x + 1], qh[x], qh[x + 1]);
+              if (kParts) {
+                mma_tf32(low[y], kl[0][x], kl[1][x], kl[0][x + 1], kl[1][x + 1], qh[x], qh[x + 1]);
+                mma_tf32(low[y], kh[0][x], kh[1][x], kh[0][x + 1], kh[1][x + 1], ql[x], ql[x + 1]);
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int i = x >> 1, r = n0 + y * 8 + e4 * 2 + (x & 1);
+            const float nl = snl[r];
+            const float u = paged_score(a, ps, big[y][x] + odd[y][x] + low[y][x], sslope[r], sqp[r], pk[i]);
+            if (nl != -INFINITY && paged_sees(by[i], sqp[r])) w[i] += exp2f(u + nl);
           }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float l = slse[tx + 16 * j], slope2 = sslope[tx + 16 * j];
-        const int pq = sqp[tx + 16 * j];
-        const PagedSees sees = paged_sees_of(m, pq);
-        if (l == -INFINITY) continue;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (paged_sees(sees, pk[i])) w[i] += exp2f(paged_score(a, ps, acc[i][j], slope2, pq, pk[i]) - l);
-      }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) w[i] += __shfl_xor_sync(0xffffffffu, w[i], x);
-      const int slot = k0 + ty * 4 + i;
-      if (tx == 0 && slot < len) {
-        const long long row = paged_row(c, s, h, slot);
-        if (row >= 0) a.weight_out[row] = (a.weight_in ? a.decay * a.weight_in[row] : 0.f) + w[i];
-      }
+    for (int i = 0; i < 2; ++i) {
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 1);
+      w[i] += __shfl_xor_sync(0xffffffffu, w[i], 2);
+      if (e4 == 0 && row[i] >= 0) a.weight_out[row[i]] = (a.weight_in ? a.decay * a.weight_in[row[i]] : 0.f) + w[i];
     }
   }
 }
@@ -391,8 +426,6 @@ template <int BM>
 constexpr size_t simt_smem() {
   return ((size_t)(BM + 2 * kBN) * (256 + 4) + BM * (kBN + 4) + kBN) * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
 }
-template <int HDP>
-constexpr size_t weight_smem() { return (size_t)2 * kBN * (HDP + 4) * 4; }
 
 template <typename K>
 cudaError_t big_smem(K* kernel, size_t bytes) {
@@ -407,9 +440,10 @@ cudaError_t run_simt(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
 }
 template <typename T, int HDP>
 cudaError_t run_weight(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  cudaError_t e = big_smem(paged_weight_simt_kernel<T, HDP>, weight_smem<HDP>());
+  constexpr size_t smem = (size_t)kWRows * (HDP + 16) * 4;
+  cudaError_t e = big_smem(paged_weight_tf32_kernel<T, HDP>, smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_weight_simt_kernel<T, HDP>, grid, dim3(256), weight_smem<HDP>(), st, a);
+  return launch_pdl(paged_weight_tf32_kernel<T, HDP>, grid, dim3(128), smem, st, a);
 }
 
 int expected_len(const PagedAttnArgs& a) {

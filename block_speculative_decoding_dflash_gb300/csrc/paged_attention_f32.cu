@@ -28,6 +28,7 @@
 #include <math.h>
 
 #include "paged_tc.cuh"
+#include "paged_tf32.cuh"
 
 namespace dfl {
 
@@ -38,24 +39,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBN = 64;
 constexpr int kMaxTiles = (1 << 20) / kBN;
 
-// D += A B: 16 x 8 of A, row g or g + 8 and element c or c + 4 of lane 4 g + c; 8 x 8 of B, its element c or c + 4 and column g.
-__device__ __forceinline__ void mma_tf32(float* d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// The two parts of K's and V's values: hi is cut, not rounded, so that the
-// largest finite value stays finite; what tf32 drops of lo is 2^-21 of x.
-__device__ __forceinline__ void cut2(float x, uint32_t& hi, uint32_t& lo) {
-  hi = __float_as_uint(x) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
-// Of Q's and P's: hi rounded, so that lo has a bit less to hold. -0 is (-0, 0).
-__device__ __forceinline__ void round2(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
-}
 // W neighbours in one load.
 template <int W>
 struct Few {

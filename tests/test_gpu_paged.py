@@ -732,6 +732,9 @@ def test_offsets_beyond_32_bits(B):
     want = (t.softmax(-1) @ vv).transpose(0, 1)
     assert (out.float() - want).abs().max() < 0.05
     c.key_weight(q, at, start, lse)
-    assert abs(float(weight[pages - 1, :, :40].sum()) - 40 * 16) < 0.1 and float(weight.sum()) == float(weight[pages - 1, :, :40].sum())
+    # nothing elsewhere: counted, as the two sums of the same 320 values may differ by their order's roundings (one
+    # step of 640 is 2^-14)
+    assert abs(float(weight[pages - 1, :, :40].sum()) - 40 * 16) < 0.1
+    assert int(weight.count_nonzero()) == int(weight[pages - 1, :, :40].count_nonzero())
     c.evict(20, 5, torch.tensor([40], dtype=torch.int32, device="cuda"))
     assert int(length[0]) == 20 and (pos[pages - 1, :, :20].sort(-1).values[:, -5:] == at[35:]).all()
