@@ -420,7 +420,7 @@ struct PagedAttnArgs {
 struct PagedPlan { int kind, splits, cluster; long long tiles, bytes; };
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
-cudaError_t launch_paged_attention_f32(const PagedAttnArgs& a, long long tiles, cudaStream_t st);
+cudaError_t launch_paged_attention_tf32(int dtype, const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st);

@@ -1,9 +1,6 @@
-// How an attention call over the paged cache is divided; attention for bf16 heads
-// of more than 128 dimensions, which the tensor-core kernel does not take; the
-// merge of split partials; key weights for fp32 and for those heads.
-//
-// Per (query tile, kv head, split): an online softmax over key tiles. The
-// scores are kept in log2 units, u = t * log2(e), so p = exp2(u - m).
+// How an attention call over the paged cache is divided, the merge of split
+// partials, and key weights for fp32 and for bf16 heads of more than 128
+// dimensions. Scores are kept in log2 units, u = t * log2(e).
 #include <math.h>
 
 #include "paged.cuh"
@@ -15,8 +12,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kBN = 64;                    // keys of a tile
-constexpr int kMaxTiles = (1 << 20) / kBN; // of the longest table
+constexpr int kBN = 64;                    // keys of a key-weight tile
 
 // Score of a raw dot product in log2 units.
 struct PagedScore { float scale2, cap2; };
@@ -31,213 +27,6 @@ __device__ __forceinline__ float paged_score(const PagedAttnArgs& a, const Paged
   if (a.softcap > 0.f) u = s.cap2 * tanhf(u);
   if (slope2 != 0.f) u -= slope2 * fabsf((float)(pq - pk));
   return u;
-}
-
-// Rows of `n` values at src into shared rows of HDP + 4 floats, zero past hd
-// and where src is NULL; 16-byte loads, `lanes` threads to a row.
-template <typename T, int HDP>
-__device__ __forceinline__ bool load_row(float* dst, const T* src, int hd, int lane, int lanes) {
-  bool bad = false;
-  for (int d = lane * 8; d < HDP; d += lanes * 8) {
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (src && d < hd) load8(src + d, x);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bad |= !(fabsf(x[i]) <= 3.4028234663852886e38f);
-    *reinterpret_cast<float4*>(dst + d) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4*>(dst + d + 4) = make_float4(x[4], x[5], x[6], x[7]);
-  }
-  return bad;
-}
-
-// BM packed query rows (row r = token r / G, head r % G of the group) against
-// kBN keys at a time. Thread (ty, tx) holds TM rows ty * TM .. and keys tx,
-// tx + 16, .. of the scores, then dims tx * 4 + 64 j of the same rows' output:
-// 16 lanes share a row, so row statistics are shuffles within half a warp.
-// K and V tiles are read from HBM once per query tile; for few query rows
-// that read bounds the kernel, for many the fp32 FMA rate.
-template <int BM, int TM>
-__global__ void __launch_bounds__(BM / TM * 16) paged_attn_simt_kernel(PagedAttnArgs a) {
-  using T = bf16;
-  constexpr int HDP = 256, NT = BM / TM * 16, LD = HDP + 4, NJ = HDP / 64;
-  pdl_enter();
-  extern __shared__ float smf[];
-  float* sq = smf;                          // [BM][LD]
-  float* sk = sq + BM * LD;                 // [kBN][LD]
-  float* sv = sk + kBN * LD;                // [kBN][LD]
-  float* sp = sv + kBN * LD;                // [BM][kBN + 4]
-  int* spos = reinterpret_cast<int*>(sp + BM * (kBN + 4));     // [kBN]
-  unsigned* some = reinterpret_cast<unsigned*>(spos + kBN);
-  unsigned* all = some + kMaxTiles / 32 + 1;
-  __shared__ PagedTile st;
-  __shared__ int s_qmin, s_qmax;
-  const PagedView& c = a.c;
-  const int h = blockIdx.y, z = blockIdx.z, G = a.G;
-  if (threadIdx.x < 32) {
-    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, G, BM, blockIdx.x);
-    int lo = INT32_MAX, hi = INT32_MIN;
-    if (t.seq >= 0) {
-      const int r0 = t.tile * BM, r1 = min(t.count * G, r0 + BM);
-      for (int i = r0 / G + (int)threadIdx.x; i <= (r1 - 1) / G; i += 32) {
-        const int p = a.q_pos[t.first + i];
-        lo = min(lo, p);
-        hi = max(hi, p);
-      }
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (threadIdx.x == 0) { st = t; s_qmin = lo; s_qmax = hi; }
-  }
-  __syncthreads();
-  const PagedTile t = st;
-  if (t.seq < 0) return;
-  const int len = paged_length(c, t.seq);
-  const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
-  PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
-  paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
-
-  const int r0 = t.tile * BM, rows = min(BM, t.count * G - r0);
-  for (int e = threadIdx.x; e < BM * 16; e += NT) {
-    const int r = e >> 4;
-    const T* src = r < rows ? static_cast<const T*>(a.q) + (size_t)(t.first + (r0 + r) / G) * a.q_stride +
-                                  (size_t)(h * G + (r0 + r) % G) * c.hd : nullptr;
-    load_row<T, HDP>(sq + r * LD, src, c.hd, e & 15, 16);
-  }
-  const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-  int pq[TM];
-  PagedSees sees[TM];
-  float slope2[TM], mx[TM], sum[TM], o[TM][NJ * 4];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = r0 + min(ty * TM + i, rows - 1);
-    pq[i] = a.q_pos[t.first + r / G];
-    sees[i] = paged_sees_of(m, pq[i]);
-    slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
-    mx[i] = -INFINITY;
-    sum[i] = 0.f;
-#pragma unroll
-    for (int d = 0; d < NJ * 4; ++d) o[i][d] = 0.f;
-  }
-  const PagedScore ps = paged_score_of(a);
-  __syncthreads();
-  paged_take(sh, some, z, a.splits);
-  PagedCursor cur(some, sh);
-  for (int rel = cur.next(); rel >= 0; rel = cur.next()) {
-    const int k0 = (sh.t0 + rel) * kBN;
-    const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
-    bool bad = false;
-    for (int e = threadIdx.x; e < kBN * 8; e += NT) {
-      const int j = e >> 3, l8 = e & 7;
-      const long long row = k0 + j < len ? paged_row(c, t.seq, h, k0 + j) : -1;
-      load_row<T, HDP>(sk + j * LD, row >= 0 ? static_cast<const T*>(c.k) + row * c.hd : nullptr, c.hd, l8, 8);
-      bad |= load_row<T, HDP>(sv + j * LD, row >= 0 ? static_cast<const T*>(c.v) + row * c.hd : nullptr, c.hd, l8, 8);
-      if (l8 == 0) spos[j] = row >= 0 ? c.pos[row] : kPagedNoPos;
-    }
-    // a tile that some query sees only in part and whose V holds infinities or
-    // NaN: the hidden rows must not be multiplied by their zero weight
-    const bool careful = __syncthreads_or(bad && !full);
-    float s[TM][4];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
-#pragma unroll 4
-    for (int d = 0; d < HDP; d += 4) {
-      float4 q[TM], k[4];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) q[i] = *reinterpret_cast<const float4*>(sq + (ty * TM + i) * LD + d);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * LD + d);
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(q[i].x, k[j].x, s[i][j]);
-          s[i][j] = fmaf(q[i].y, k[j].y, s[i][j]);
-          s[i][j] = fmaf(q[i].z, k[j].z, s[i][j]);
-          s[i][j] = fmaf(q[i].w, k[j].w, s[i][j]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < TM; ++i) {
-      unsigned seen = 0;
-      float top = -INFINITY;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int pk = spos[tx + 16 * j];
-        const bool v = full || paged_sees(sees[i], pk);
-        s[i][j] = v ? paged_score(a, ps, s[i][j], slope2[i], pq[i], pk) : -INFINITY;
-        seen |= (unsigned)v << j;
-        top = fmaxf(top, s[i][j]);
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float mn = fmaxf(mx[i], top);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(mx[i] - base);
-      float add = 0.f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p = exp2f(s[i][j] - base);
-        add += p;
-        // a hidden row's weight is -0, a seen one's that underflowed +0
-        sp[(ty * TM + i) * (kBN + 4) + tx + 16 * j] = (seen >> j) & 1u ? p : -0.f;
-      }
-#pragma unroll
-      for (int x = 8; x > 0; x >>= 1) add += __shfl_xor_sync(0xffffffffu, add, x);
-      sum[i] = sum[i] * f + add;
-      mx[i] = mn;
-#pragma unroll
-      for (int d = 0; d < NJ * 4; ++d) o[i][d] *= f;
-    }
-    __syncwarp();
-#pragma unroll 2
-    for (int j = 0; j < kBN; j += 4) {
-      float4 p[TM];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) p[i] = *reinterpret_cast<const float4*>(sp + (ty * TM + i) * (kBN + 4) + j);
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-#pragma unroll
-        for (int n = 0; n < NJ; ++n) {
-          const float4 v = *reinterpret_cast<const float4*>(sv + (j + jj) * LD + n * 64 + tx * 4);
-#pragma unroll
-          for (int i = 0; i < TM; ++i) {
-            const float w = jj == 0 ? p[i].x : jj == 1 ? p[i].y : jj == 2 ? p[i].z : p[i].w;
-            if (careful && __float_as_uint(w) == 0x80000000u) continue;
-            o[i][n * 4 + 0] = fmaf(w, v.x, o[i][n * 4 + 0]);
-            o[i][n * 4 + 1] = fmaf(w, v.y, o[i][n * 4 + 1]);
-            o[i][n * 4 + 2] = fmaf(w, v.z, o[i][n * 4 + 2]);
-            o[i][n * 4 + 3] = fmaf(w, v.w, o[i][n * 4 + 3]);
-          }
-        }
-      }
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int r = ty * TM + i;
-    if (r >= rows) continue;
-    const size_t at = (size_t)(t.first + (r0 + r) / G) * a.nq + h * G + (r0 + r) % G;
-    if (a.splits > 1) {
-      float* po = a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd;
-#pragma unroll
-      for (int n = 0; n < NJ; ++n)
-        if (n * 64 + tx * 4 < c.hd)
-          *reinterpret_cast<float4*>(po + n * 64 + tx * 4) = make_float4(o[i][n * 4], o[i][n * 4 + 1], o[i][n * 4 + 2], o[i][n * 4 + 3]);
-      if (tx == 0) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], sum[i]);
-      continue;
-    }
-    const bool none = sum[i] == 0.f;           // nothing seen (a NaN score makes the sum NaN)
-    const float inv = none ? 0.f : 1.f / sum[i];
-    T* out = static_cast<T*>(a.out) + at * c.hd;
-#pragma unroll
-    for (int n = 0; n < NJ; ++n)
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-        if (n * 64 + tx * 4 + d < c.hd) out[n * 64 + tx * 4 + d] = from_f<T>(none ? 0.f : o[i][n * 4 + d] * inv);
-    if (tx == 0 && a.lse) a.lse[at] = none ? -INFINITY : (mx[i] + log2f(sum[i])) * kLn2;
-  }
 }
 
 // Joins the splits of one (row, head), a warp to each: o = sum_z o_z
@@ -300,12 +89,6 @@ __global__ void __launch_bounds__(128) paged_attn_merge_kernel(PagedAttnArgs a) 
 // are summed at the end: no atomics, and a fixed order. (On CUDA cores, 16
 // sequences of up to 10 rows and 6000 keys, 8 heads, fp32: 220 us; so: 81 us.)
 constexpr int kWRows = 64;
-
-__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const bf16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf_lo(u.x), bf_hi(u.x), bf_lo(u.y), bf_hi(u.y));
-}
 
 template <typename T, int HDP>
 __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kernel(const __grid_constant__ PagedAttnArgs a) {
@@ -422,22 +205,11 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
   }
 }
 
-template <int BM>
-constexpr size_t simt_smem() {
-  return ((size_t)(BM + 2 * kBN) * (256 + 4) + BM * (kBN + 4) + kBN) * 4 + 2 * (kMaxTiles / 32 + 1) * 4;
-}
-
 template <typename K>
 cudaError_t big_smem(K* kernel, size_t bytes) {
   return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
-template <int BM, int TM>
-cudaError_t run_simt(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
-  cudaError_t e = big_smem(paged_attn_simt_kernel<BM, TM>, simt_smem<BM>());
-  if (e != cudaSuccess) return e;
-  return launch_pdl(paged_attn_simt_kernel<BM, TM>, grid, dim3(BM / TM * 16), simt_smem<BM>(), st, a);
-}
 template <typename T, int HDP>
 cudaError_t run_weight(const PagedAttnArgs& a, dim3 grid, cudaStream_t st) {
   constexpr size_t smem = (size_t)kWRows * (HDP + 16) * 4;
@@ -457,8 +229,8 @@ long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
 
 }  // namespace
 
-// kind 1 and 2: tensor cores (bf16, head_dim <= 128), that many tiles of 128
-// packed query rows to a CTA; 16, 32, 64: CUDA cores, that many rows.
+// kind 1 and 2: tcgen05 (bf16, head_dim <= 128), that many tiles of 128 packed
+// query rows to a CTA; 16: mma.sync in tf32, that many rows.
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
   PagedPlan p{0, 1, 0, 0, 0};
   const long long len = expected_len(a), units = (long long)a.rows * a.G;
@@ -473,10 +245,7 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
     fill = 152;
     least = 512;
   } else {
-    // the smallest tile that holds an average sequence's rows (100 rows of 4
-    // sequences, 4 heads to a kv head: 670 us in tiles of 64, 2163 us of 16; one
-    // row each of 8: 719 us and 710 us); fp32: 16 always
-    p.kind = !dtype || units <= 16ll * a.c.n_seq ? 16 : 64;
+    p.kind = 16;
     p.tiles = tile_bound(units, p.kind, a);
     fill = 608;
     least = 256;
@@ -511,12 +280,9 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
 }
 
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
-  const dim3 grid((unsigned)p.tiles, a.c.nkv, p.splits);
   cudaError_t e;
   if (p.kind <= 2) e = launch_paged_attention_tc(a, p.kind, p.tiles, st);
-  else if (!dtype) e = launch_paged_attention_f32(a, p.tiles, st);
-  else if (p.kind == 16) e = run_simt<16, 2>(a, grid, st);
-  else e = run_simt<64, 4>(a, grid, st);
+  else e = launch_paged_attention_tf32(dtype, a, p.tiles, st);
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
   return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)

@@ -1,10 +1,12 @@
-// Attention over the paged cache in fp32.
+// Attention over the paged cache in fp32, and in bf16 for heads of more than 128
+// dimensions.
 //
 // The products run on the tensor cores in tf32 with every factor in two parts,
 // x = hi + lo: x y = hi hi + hi lo + lo hi, whose missing lo lo is 2^-22 of x y, as
 // much as lo's own rounding. Few query rows read K and V once, which the HBM
 // bounds; on CUDA cores the same rows read them from shared memory many times
-// over (8 sequences of up to 10 rows over up to 4099 keys, 8 heads: 84 us).
+// over (8 sequences of up to 10 rows over up to 4099 keys, 8 heads: 84 us). A bf16
+// value is a tf32 as it stands, so of bf16's factors only P has two parts.
 //
 // A CTA has 16 packed query rows (row r = token r / G, head r % G of the group)
 // against 64 keys at a time. For the scores each of its 8 warps takes 8 of the
@@ -44,19 +46,28 @@ template <int W>
 struct Few {
   float v[W];
   __device__ __forceinline__ explicit Few(const float* p) {
-    if constexpr (W == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(p);
+    if constexpr (W == 4) *reinterpret_cast<float4*>(v) = load4(p);
     else if constexpr (W == 2) *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(p);
     else v[0] = *p;
   }
+  __device__ __forceinline__ explicit Few(const bf16* p) {
+    static_assert(W == 4, "four bf16 to a load");
+    *reinterpret_cast<float4*>(v) = load4(p);
+  }
 };
-__device__ __forceinline__ bool not_finite(float x) { return !(fabsf(x) <= 3.4028234663852886e38f); }
+// Whether 16 bytes hold an infinity or NaN: an exponent of all ones carries into the sign's place.
+template <typename T>
+__device__ __forceinline__ bool not_finite(const uint4& u) {
+  constexpr uint32_t kExp = sizeof(T) == 4 ? 0x7f800000u : 0x7f807f80u, kOne = sizeof(T) == 4 ? 0x00800000u : 0x00800080u;
+  return ((((u.x & kExp) + kOne) | ((u.y & kExp) + kOne) | ((u.z & kExp) + kOne) | ((u.w & kExp) + kOne)) & (kOne << 8)) != 0;
+}
 
 constexpr int kBM = 16, kWarps = 8;
 
-template <int HDP>
-struct F32Shape {
-  static constexpr int kSub = HDP / 32;                   // K and V tiles lie in parts of 32 dimensions, 128-byte swizzled
-  static constexpr int kTileB = kBN * HDP * 4, kSubB = kBN * 128;
+template <typename T, int HDP>
+struct Tf32Shape {
+  static constexpr int kCols = 128 / sizeof(T), kSub = HDP / kCols;   // K and V tiles lie in parts of 128 bytes a row, swizzled
+  static constexpr int kTileB = kBN * HDP * sizeof(T), kSubB = kBN * 128;
   static constexpr int LDP = kBN + 8, LDQ = HDP + 16;
   static constexpr bool kQRegs = HDP <= 128;              // Q in registers, otherwise in shared memory
   static constexpr int kK = 0, kV = kTileB, kP = 2 * kTileB, kQ = kP + kBM * LDP * 4, kMax = kQ + (kQRegs ? 0 : kBM * LDQ * 4),
@@ -64,10 +75,11 @@ struct F32Shape {
   static constexpr size_t kSmem = kEnd + 1024;
 };
 
-template <int HDP>
-__global__ void __launch_bounds__(kWarps * 32, HDP > 128 ? 1 : 2)
-paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
-  using C = F32Shape<HDP>;
+template <typename T, int HDP>
+__global__ void __launch_bounds__(kWarps * 32, HDP * sizeof(T) > 512 ? 1 : 2)
+paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
+  using C = Tf32Shape<T, HDP>;
+  constexpr bool kParts = sizeof(T) == 4;
   constexpr int NT = kWarps * 32, LDP = C::LDP;
   constexpr int kSteps = HDP / 16;            // of 16 dimensions, two instructions each
   constexpr int W = HDP / 64;                 // a warp's tiles of 8 dimensions, all from one load
@@ -117,8 +129,7 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, e4 = lane & 3;
   // Q, zeros past hd and past the last row
   auto q_at = [&](int r, int d) {
-    return r < n_rows && d < hd ? *reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + (size_t)(t.first + (r0 + r) / G) * a.q_stride +
-                                                                   (size_t)(h * G + (r0 + r) % G) * hd + d)
+    return r < n_rows && d < hd ? load4(static_cast<const T*>(a.q) + (size_t)(t.first + (r0 + r) / G) * a.q_stride + (size_t)(h * G + (r0 + r) % G) * hd + d)
                                 : make_float4(0.f, 0.f, 0.f, 0.f);
   };
   float4 q[C::kQRegs ? kSteps : 1][2];
@@ -189,8 +200,8 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
   // instruction is that key), V's rows 2 e4, + 1, + 8, + 9 of every 16
   const int k_row = warp * 8 + (g >> 1) + 4 * (g & 1);
   const uint8_t* k_at = sm + C::kK + k_row * 128;
-  const uint8_t* v_at = sm + C::kV + (warp * 8 * W >> 5) * C::kSubB;
-  const int v_col = warp * 8 * W + g * W & 31;
+  const uint8_t* v_at = sm + C::kV + warp * 8 * W / C::kCols * C::kSubB;
+  const int v_byte = (warp * 8 * W + g * W) % C::kCols * (int)sizeof(T);
   for (; rel >= 0; buf ^= 1, phase ^= 1) {
     const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
     const int* rows = srow + buf * kBN;
@@ -222,7 +233,8 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
         round2(v.z, qh[i][2], ql[i][2]);
         round2(v.w, qh[i][3], ql[i][3]);
       }
-      const float4 k = *reinterpret_cast<const float4*>(k_at + (s >> 1) * C::kSubB + ((((s & 1) * 4 + e4) ^ (k_row & 7)) << 4));
+      const int k_byte = (s * 16 + e4 * 4) % C::kCols * (int)sizeof(T);
+      const float4 k = load4(reinterpret_cast<const T*>(k_at + s * 16 / C::kCols * C::kSubB + (((k_byte >> 4) ^ (k_row & 7)) << 4) + (k_byte & 15)));
       uint32_t kh[4], kl[4];
       cut2(k.x, kh[0], kl[0]);
       cut2(k.y, kh[1], kl[1]);
@@ -232,6 +244,7 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
 #pragma unroll
       for (int x = 0; x < 4; x += 2) {
         mma_tf32(big, qh[0][x], qh[1][x], qh[0][x + 1], qh[1][x + 1], kh[x], kh[x + 1]);
+        if (!kParts) continue;
         mma_tf32(low[0], qh[0][x], qh[1][x], qh[0][x + 1], qh[1][x + 1], kl[x], kl[x + 1]);
         mma_tf32(low[1], ql[0][x], ql[1][x], ql[0][x + 1], ql[1][x + 1], kh[x], kh[x + 1]);
       }
@@ -290,11 +303,10 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     bool careful = false;
     if (!full) {
       unsigned bad = 0;
-      constexpr int kEach = kBN * HDP / 4 / NT;            // 16-byte pieces of a thread
+      constexpr int kEach = C::kTileB / 16 / NT;            // 16-byte pieces of a thread
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(sm + C::kV + (i * NT + threadIdx.x) * 16);
-        bad |= (unsigned)(not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w)) << i;
+        bad |= (unsigned)not_finite<T>(*reinterpret_cast<const uint4*>(sm + C::kV + (i * NT + threadIdx.x) * 16)) << i;
       }
       careful = __syncthreads_or(bad != 0);
       if (careful) {
@@ -329,15 +341,15 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
           round2(p.x, ph[i][0], pl[i][0]);
           round2(p.y, ph[i][1], pl[i][1]);
         }
-        const Few<W> v0(reinterpret_cast<const float*>(v_at + key * 128 + (((v_col >> 2) ^ (key & 7)) << 4)) + (v_col & 3));
-        const Few<W> v1(reinterpret_cast<const float*>(v_at + (key + 1) * 128 + (((v_col >> 2) ^ (key + 1 & 7)) << 4)) + (v_col & 3));
+        const Few<W> v0(reinterpret_cast<const T*>(v_at + key * 128 + (((v_byte >> 4) ^ (key & 7)) << 4) + (v_byte & 15)));
+        const Few<W> v1(reinterpret_cast<const T*>(v_at + (key + 1) * 128 + (((v_byte >> 4) ^ (key + 1 & 7)) << 4) + (v_byte & 15)));
 #pragma unroll
         for (int n = 0; n < W; ++n) {
           uint32_t h0, l0, h1, l1;
           cut2(v0.v[n], h0, l0);
           cut2(v1.v[n], h1, l1);
           mma_tf32(big[n], ph[0][0], ph[1][0], ph[0][1], ph[1][1], h0, h1);
-          mma_tf32(small[n], ph[0][0], ph[1][0], ph[0][1], ph[1][1], l0, l1);
+          if (kParts) mma_tf32(small[n], ph[0][0], ph[1][0], ph[0][1], ph[1][1], l0, l1);
           mma_tf32(small[n], pl[0][0], pl[1][0], pl[0][1], pl[1][1], h0, h1);
         }
       }
@@ -349,7 +361,7 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     if (careful) {
       for (int j = 0; j < kBN; ++j) {
         if (!((s_bad[j >> 5] >> (j & 31)) & 1u) || rows[j] < 0) continue;
-        const float* v = static_cast<const float*>(c.v) + (long long)rows[j] * hd;
+        const T* v = static_cast<const T*>(c.v) + (long long)rows[j] * hd;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const float p = sp[(g + 8 * i) * LDP + j];
@@ -359,7 +371,7 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               const int d = (warp * 8 + 2 * e4 + x) * W + n;
-              if (d < hd) o[n][2 * i + x] = fmaf(p, v[d], o[n][2 * i + x]);
+              if (d < hd) o[n][2 * i + x] = fmaf(p, to_f(v[d]), o[n][2 * i + x]);
             }
         }
       }
@@ -397,13 +409,18 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
     const bool none = total == 0.f;          // nothing seen (a NaN score makes the sum NaN)
     const bool split = a.splits > 1;
     const float inv = none ? 0.f : (split ? 1.f : 1.f / total);
-    float* out = split ? a.part_o + ((size_t)z * a.rows * a.nq + at) * hd : static_cast<float*>(a.out) + at * hd;
+    float* part = a.part_o + ((size_t)z * a.rows * a.nq + at) * hd;
+    T* out = static_cast<T*>(a.out) + at * hd;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int d = (warp * 8 + 2 * e4 + x) * W;
       if (d >= hd) continue;
 #pragma unroll
-      for (int n = 0; n < W; ++n) out[d + n] = none ? 0.f : o[n][2 * i + x] * inv;
+      for (int n = 0; n < W; ++n) {
+        const float v = none ? 0.f : o[n][2 * i + x] * inv;
+        if (split) part[d + n] = v;
+        else out[d + n] = from_f<T>(v);
+      }
     }
     if (warp || e4) continue;
     if (split) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], total);
@@ -411,25 +428,26 @@ paged_attn_f32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_const
   }
 }
 
-template <int HDP>
+template <typename T, int HDP>
 cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
-  // (the maps of bf16 rows of twice the columns: the bytes are what counts)
+  // (fp32 rows are mapped as bf16 rows of twice the columns: the bytes are what counts)
   PagedView c = a.c;
-  c.hd *= 2;
+  c.hd *= sizeof(T) / 2;
   CUtensorMap mk, mv;
   if (!paged_map_pages(&mk, c.k, c, kBN) || !paged_map_pages(&mv, c.v, c, kBN)) return cudaErrorInvalidValue;
-  auto kernel = paged_attn_f32_kernel<HDP>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)F32Shape<HDP>::kSmem);
+  auto kernel = paged_attn_tf32_kernel<T, HDP>;
+  constexpr size_t smem = Tf32Shape<T, HDP>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), F32Shape<HDP>::kSmem, st, mk, mv, a);
+  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), smem, st, mk, mv, a);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attention_f32(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
-  if (a.c.hd <= 64) return run<64>(a, tiles, st);
-  if (a.c.hd <= 128) return run<128>(a, tiles, st);
-  return run<256>(a, tiles, st);
+cudaError_t launch_paged_attention_tf32(int dtype, const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  if (dtype) return run<bf16, 256>(a, tiles, st);
+  if (a.c.hd <= 64) return run<float, 64>(a, tiles, st);
+  return a.c.hd <= 128 ? run<float, 128>(a, tiles, st) : run<float, 256>(a, tiles, st);
 }
 
 }  // namespace dfl
