@@ -647,6 +647,8 @@ class PagedCache:
                                     self.n_pages, self.page_rows, self.kv_heads, self.head_dim, self.n_seq, self.max_pages,
                                     BF16 if k.dtype == torch.bfloat16 else F32)
         self._axis = b"", None                                    # the last pair_axis and its buffer
+        self._evict_bytes = 0, 0                                  # the last budget and its workspace
+        self._no_bytes = torch.empty(0, dtype=torch.uint8, device=self.device)
         # the C side checks sizes and alignment with every call; once here so a
         # bad cache is refused when it is made
         self._query(lib.dflash_paged_evict_workspace, _PAGED_EVICT.pack(0, 0, 0, 0, 0, 1, 0))
@@ -710,17 +712,16 @@ class PagedCache:
         handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
         self._check(call(self._c, *args, handle))
 
-    def _with_workspace(self, call, query, args, workspace, stream):
-        nbytes = self._query(query, args)
+    def _with_workspace(self, call, nbytes, args, workspace, stream):
         if workspace is not None:
             if workspace.dtype is not torch.uint8 or workspace.get_device() != self._index or not workspace.is_contiguous():
                 raise DFlashError(EINVAL, f"paged: workspace must be a dense uint8 tensor on {self.device}")
         elif nbytes:
             if stream is None:
-                workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                workspace = self._no_bytes.new_empty(nbytes)
             else:
                 with torch.cuda.stream(stream):
-                    workspace = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+                    workspace = self._no_bytes.new_empty(nbytes)
         ws = _NO_WORKSPACE if workspace is None else _PAGED_WORKSPACE.pack(workspace.data_ptr(), workspace.numel())
         self._launch(call, stream, args + ws)
 
@@ -777,7 +778,7 @@ class PagedCache:
             except DFlashError as e:
                 if e.code != EINVAL:
                     raise
-        self._with_workspace(lib.dflash_paged_attention, lib.dflash_paged_attention_workspace, args, workspace, stream)
+        self._with_workspace(lib.dflash_paged_attention, self._query(lib.dflash_paged_attention_workspace, args), args, workspace, stream)
 
     def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
                    softcap=0.0, slopes=None, prefix=None, max_len=0, stream=None):
@@ -804,4 +805,7 @@ class PagedCache:
                                  need("weight_out", weight_out, torch.float32, shape),
                                  need("pos_out", self.pos if pos_out is None else pos_out, torch.int32, shape),
                                  need("length_out", self.length if length_out is None else length_out, torch.int32, seqs), budget, recent)
-        self._with_workspace(lib.dflash_paged_evict, lib.dflash_paged_evict_workspace, args, workspace, stream)
+        held = self._evict_bytes                                  # of the cache's sizes and the budget
+        if held[0] != budget:
+            self._evict_bytes = held = budget, self._query(lib.dflash_paged_evict_workspace, args)
+        self._with_workspace(lib.dflash_paged_evict, held[1], args, workspace, stream)
