@@ -95,8 +95,10 @@ __device__ __forceinline__ PagedSees paged_sees_of(const PagedMask& m, int pq) {
 __device__ __forceinline__ bool paged_sees(const PagedSees& s, int pk) {
   return (unsigned)pk - (unsigned)s.lo <= s.span || (unsigned)pk < s.prefix;
 }
-// The other way about: the positions of the queries that see a row at pk.
+// The other way about: the positions of the queries that see a row at pk (none,
+// and no query has a negative one, for a row that is not there).
 __device__ __forceinline__ PagedSees paged_seen_by(const PagedMask& m, int pk) {
+  if (pk == kPagedNoPos) return PagedSees{INT32_MIN + 1, 0u, 0u};
   long long lo = m.causal ? pk : INT32_MIN + 1, hi = INT32_MAX;
   if (m.window > 0) {
     if (!m.causal && (long long)pk - m.window > lo) lo = (long long)pk - m.window;

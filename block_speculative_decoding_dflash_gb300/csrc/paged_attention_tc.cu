@@ -517,7 +517,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           tmem_ld32(s_at + n * 32, v);
           tmem_ld_wait32(v);
           if (EXTRA && a.softcap > 0.f) {
-            cap_tanh32(v, cap);
+            cap_tanh32(v, cap, masked, [&]() {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = paged_sees(sees, kp[n * 32 + j]) ? v[j] : 0.f;
+            });
           } else {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] *= scale2;
@@ -594,7 +597,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           float w[16];
           tmem_ld32(s_at + n * 32, x[0]);
           tmem_ld_wait32(x[0]);
-          cap_tanh32(x[0], cap);
+          cap_tanh32(x[0], cap, false, []() {});
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {
             float p0, p1;
@@ -630,7 +633,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             tmem_ld32(s_at + n * 32, x[0]);
             tmem_ld_wait32(x[0]);
           }
-          if (EXTRA && late) cap_tanh32(x[0], cap);
+          if (EXTRA && late) cap_tanh32(x[0], cap, false, []() {});
           float w[16], lo[16];
 #pragma unroll
           for (int j = 0; j < 32; j += 2) {

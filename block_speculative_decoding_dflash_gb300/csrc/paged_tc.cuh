@@ -170,7 +170,7 @@ __device__ __forceinline__ float cap_tanh(float x, float cap2) {
 // of it in fp32), with scale and cap2 in its coefficients: six packed
 // instructions to two values, where the exponential and the reciprocal would
 // bound capped attention (512 rows' key weights over 32768 keys, cap 20: 335 us
-// with it, 459 us without). Where some value of the warp is larger, all take the
+// with it, 459 us without; 364 us since hidden scores have no say in the choice). Where some value of the warp is larger, all take the
 // exponential, whose error of a few 2^-24 of the cap is nothing beside scores of
 // half of it; under a cap so vast that it could be (cap2 > 1024) each value takes
 // its own. (Each its own under every cap: 2048 rows over 32768 keys under a cap
@@ -203,10 +203,21 @@ __device__ __forceinline__ float cap_tanh1(float v, const CapPoly& p) {
   }
   return r * v;
 }
-__device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
+__device__ __forceinline__ bool cap_fits(const float* v, const CapPoly& p) {
   float top = 0.f;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) top = fmaxf(fmaxf(top, fabsf(v[j])), fabsf(v[j + 1]));
+  return __all_sync(0xffffffffu, top <= p.limit);
+}
+// hide() makes zeros of the scores that are not seen: they must not decide how
+// the others are computed. It is called only where they might.
+template <typename F>
+__device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p, bool some_hidden, F&& hide) {
+  bool fits = cap_fits(v, p);
+  if (!fits && some_hidden) {
+    hide();
+    fits = cap_fits(v, p);
+  }
   auto poly = [&](float v0, float v1, float& r0, float& r1) {
     const uint64_t y = pack2(v0, v1), z = mul2(y, y);
     uint64_t r = p.c[4];
@@ -214,7 +225,7 @@ __device__ __forceinline__ void cap_tanh32(float* v, const CapPoly& p) {
     for (int k = 3; k >= 0; --k) r = fma2(r, z, p.c[k]);
     unpack2(mul2(r, y), r0, r1);
   };
-  if (__all_sync(0xffffffffu, top <= p.limit)) {
+  if (fits) {
 #pragma unroll
     for (int j = 0; j < 32; j += 2) poly(v[j], v[j + 1], v[j], v[j + 1]);
   } else {

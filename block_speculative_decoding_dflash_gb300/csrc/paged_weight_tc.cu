@@ -144,7 +144,10 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   auto add_chunk = [&](float* v, const WtRows& rw, int n, const PagedSees& by, int pk, bool full, uint64_t* add) {
     float sc = scale2;
     if (EXTRA && a.softcap > 0.f) {
-      cap_tanh32(v, cap);
+      cap_tanh32(v, cap, !full, [&]() {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = paged_sees(by, rw.pos[n * 32 + e]) ? v[e] : 0.f;
+      });
       sc = 1.f;
     }
     if (EXTRA && a.slopes) {

@@ -289,6 +289,35 @@ def test_hidden_rows_may_hold_anything(B, dtype, hd, nq, n, bad):
     s.check_attention(cache)
 
 
+@pytest.mark.parametrize("mask", [dict(), dict(softcap=20.0), dict(softcap=20.0, slopes=True), dict(window=50)], ids=lambda m: "-".join(m) or "plain")
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 128, 4), ("bf16", 200, 4)])
+@pytest.mark.parametrize("n", [3, 70, 200])
+def test_hidden_rows_leave_every_bit(B, dtype, hd, nq, n, mask):
+    """The same bits whatever stands in the rows behind the length and in those that no query sees."""
+    results = []
+    for fill in (0.0, 1e4, math.inf, math.nan):
+        s = Setup(B, [(n, n + 77)], nq, 2, hd, 16, dtype, seed=5)
+        length = n + 77
+        hidden = list(range(10, 77, 7))
+        page, j = s.table[0, torch.tensor(hidden) // 16].long(), torch.tensor(hidden) % 16
+        for x in (s.k, s.v):
+            x[torch.isnan(x)] = fill
+            x[page, :, j] = fill
+        s.pos[page, :, j] = 1 << 20                     # later than every query
+        cache = s.device()
+        out = torch.zeros(s.rows, nq, hd, dtype=s.dt, device="cuda")
+        lse = torch.zeros(s.rows, nq, device="cuda")
+        w = torch.zeros(s.pos.shape, device="cuda")
+        m = {k: v.cuda() if torch.is_tensor(v) else v for k, v in mask_of(mask, nq, 1).items()}
+        args = s.q.cuda(), s.q_pos.cuda(), s.start.cuda()
+        cache.attention(*args, out, lse=lse, **m)
+        cache.key_weight(*args, lse, weight_out=w, weight=torch.zeros_like(w), **m)
+        assert torch.isfinite(out).all() and torch.isfinite(w).all() and length == int(s.length[0])
+        results.append((out, lse, w))
+    for r in results[1:]:
+        assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 3
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, dtype, seed=8)
