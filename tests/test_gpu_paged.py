@@ -7,6 +7,9 @@ Tolerances count roundings. eps = 2^-24 is fp32's half step, u = 2^-8 (bf16) or
 * A score t is a dot product of hd terms in fp32, a scaling, a cap and a bias:
   dt = (hd + 8) eps sum |q k| scale + 8 eps (cap + |bias| + |t|), the largest over
   the call. The cap's slope is at most 1.
+  fp32's products in two tf32 parts add 2^-21 of |q k| for what the parts drop and
+  2^-22 for their smallest product, 12 eps at the worst, with both of one sign in
+  every term; Cauchy-Schwarz's bound on sum |q k| leaves more than that.
 * A weight p = exp(t - m) then is off by a factor of dt + 2^-20 (exp2's own error
   and the change to log2 units at |t| < 16), the sum l by as much.
 * out: u |out| for its rounding, and 2 (dt + 2^-20) + n eps, for n summed keys,
