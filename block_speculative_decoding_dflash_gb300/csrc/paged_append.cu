@@ -87,7 +87,9 @@ __device__ __forceinline__ Raw8<float> round8(const float* v, float) {
 // 32 / (hd / 8) heads are worked on side by side. With r the head's 1 / rms,
 // a value becomes r (v A + w B): w the pair's other half, in the same lane
 // (adjacent pairs) or one shuffle away, A and B the gains times cos and sin,
-// which a lane holds for its dimensions. kU heads are requested before the
+// which a lane holds for its dimensions. A lane whose dimensions are not rotated
+// takes w = +0 and B = -0, which leaves v A as it is to the sign of a zero,
+// whatever its neighbours hold. kU heads are requested before the
 // first is used, and the next ones as soon as one is in its registers. Bound by
 // the bytes of the rows, read once and written once, for thousands of rows; by
 // its chain of dependent loads for a few.
@@ -131,6 +133,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
   } else if (d0 < 2 * a.pairs) {
     pair = d0 >> 1;
   }
+  const uint32_t turns = pair >= 0 ? ~0u : 0u;            // keeps or clears the pairs' other halves
   Raw8<T> g_own, g_oth;                                   // the gains, requested before they are needed
   auto get_gain = [&](const void* g) {
     if (g && in) {
@@ -165,6 +168,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
         b0 *= NEOX ? g_oth.at(j) : g_own.at(j + 1);
         b1 *= NEOX ? g_oth.at(j + 1) : g_own.at(j);
       }
+      if (pair < 0) b0 = b1 = -0.f;
       A[j >> 1] = pack2(t0.x, t1.x);
       B[j >> 1] = pack2(b0, b1);
     }
@@ -175,16 +179,11 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
     uint64_t v[4], w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = pack2(x.at(2 * j), x.at(2 * j + 1));
-    if (NEOX) {
-      Raw8<T> y;
+    Raw8<T> y;
 #pragma unroll
-      for (int j = 0; j < Raw8<T>::kWords; ++j) y.w[j] = __shfl_sync(0xffffffffu, x.w[j], other);
+    for (int j = 0; j < Raw8<T>::kWords; ++j) y.w[j] = (NEOX ? __shfl_sync(0xffffffffu, x.w[j], other) : x.w[j]) & turns;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack2(y.at(2 * j), y.at(2 * j + 1));
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = pack2(x.at(2 * j + 1), x.at(2 * j));
-    }
+    for (int j = 0; j < 4; ++j) w[j] = NEOX ? pack2(y.at(2 * j), y.at(2 * j + 1)) : pack2(y.at(2 * j + 1), y.at(2 * j));
     next();
     float f = 1.f;
     if (norm) {
@@ -204,11 +203,11 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
       }
       f = rsqrtf(fmaf(tot, inv_hd, a.eps));
     }
-    float y[8];
+    float z[8];
     const uint64_t f2 = pack2(f, f);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) unpack2(fma2(fma2(v[j], A[j], fma2(w[j], B[j], 0)), f2, 0), y[2 * j], y[2 * j + 1]);
-    return round8(y, T());
+    for (int j = 0; j < 4; ++j) unpack2(mul2(fma2(v[j], A[j], mul2(w[j], B[j])), f2), z[2 * j], z[2 * j + 1]);
+    return round8(z, T());
   };
 
   if (q_left > 0) {

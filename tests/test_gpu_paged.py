@@ -445,6 +445,45 @@ def test_append(B, lens, nq, nkv, hd, ps, dtype, axes, pairs, norm, neox):
     assert int(s.status) == 0
 
 
+@pytest.mark.parametrize("neox", [True, False])
+@pytest.mark.parametrize("norm", [True, False])
+@pytest.mark.parametrize("hd,pairs,dtype", [(64, 0, "bf16"), (128, 16, "bf16"), (128, 16, "f32"), (80, 8, "f32"), (96, 24, "bf16"), (64, 5, "bf16"), (128, 33, "f32")])
+def test_append_leaves_what_is_not_rotated(B, hd, pairs, dtype, norm, neox):
+    """Infinities, NaN and -0 in dimensions that are not rotated stay where they are, in both kernels."""
+    s = Setup(B, [(6, 20)], 4, 2, hd, 16, dtype, seed=32)
+    x = torch.randn(6, 8, hd, generator=torch.Generator().manual_seed(pairs))
+    x[0, :, -3:] = -0.0
+    x[1, :, -1] = math.inf
+    x[2, :, -2] = -math.inf
+    x[3, :, -2:] = math.inf
+    x[4, :, -1] = math.nan
+    x[5, :, 2 * pairs] = math.inf
+    x = x.to(s.dt)
+    gains = [(1 + 0.2 * torch.randn(hd, generator=torch.Generator().manual_seed(i))).to(s.dt) if norm else None for i in (1, 2)]
+    rope_pos = torch.tensor([[3, 10, 200, 7, 5000, 1]], dtype=torch.int32)
+    cache, dev = s.device(), x.cuda()
+    q_out = torch.full((6, 4, hd), 77.0, dtype=s.dt, device="cuda")
+    cache.append(dev[:, :4], dev[:, 4:6], dev[:, 6:], s.q_pos.cuda(), s.start.cuda(), q_out, rope_pos=rope_pos.cuda(), pair_axis=bytes(pairs), theta=1e4, neox=neox,
+                 q_norm=None if gains[0] is None else gains[0].cuda(), k_norm=None if gains[1] is None else gains[1].cuda())
+    o, y = s.oracle(), host(x)
+    g = [None if t is None else host(t) for t in gains]
+    with np.errstate(invalid="ignore"):
+        want = P.append(o, y[:, :4], y[:, 4:6], y[:, 6:], s.q_pos.numpy(), s.start.numpy(), rope_pos.numpy(), bytes(pairs), 1e4, neox, g[0], g[1], 1e-6)
+    rows = [(int(s.table[0, r // 16]), r % 16) for r in range(14, 20)]
+    keys = np.stack([o["k"][p, :, j] for p, j in rows])
+    got = [host(q_out), np.stack([host(cache.k[p, :, j]) for p, j in rows])]
+    for a, b, given in ((got[0], want, y[:, :4]), (got[1], keys, y[:, 4:6])):
+        assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.isinf(a), np.isinf(b))
+        assert (a[np.isinf(b)] == b[np.isinf(b)]).all()
+        near = np.abs(np.where(np.isfinite(b), b, 0)).max(-1, keepdims=True) * 2
+        fine = np.isfinite(b)
+        assert (np.abs(a[fine] - b[fine]) <= (unit(dtype) * np.abs(b) + (hd + 16) * EPS * near)[fine]).all()
+        if not norm:
+            still, was = a[..., 2 * pairs:], given[..., 2 * pairs:]
+            assert np.array_equal(still, was, equal_nan=True) and np.array_equal(np.signbit(still)[~np.isnan(was)], np.signbit(was)[~np.isnan(was)])
+    assert np.array_equal(host(cache.v), o["v"], equal_nan=True)
+
+
 def test_append_in_place_and_far_positions(B):
     """q_out = q, and angles of positions up to 2^31 - 1: turns of pair 0 there are exact to 2^-24 of a turn."""
     s = Setup(B, [(3, 3)], 2, 1, 64, 8, "f32", seed=30)
