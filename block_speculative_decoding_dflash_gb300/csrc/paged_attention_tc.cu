@@ -418,7 +418,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     const int wmin = __reduce_min_sync(0xffffffffu, valid ? pq : INT32_MAX), wmax = __reduce_max_sync(0xffffffffu, valid ? pq : INT32_MIN);
     const float slope2 = a.slopes ? a.slopes[valid ? head : h * G] * kLog2e : 0.f;
     const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
-    const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
+    CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
+    // (rows of the next sequence, which a load brings along, have no say in how
+    // the warp's caps are computed)
+    if (!valid) cap.limit = INFINITY;
     int* kp = kpos[warp];
     // A distance is the difference of two distances from the warp's first
     // query, converted once a key and not once a score (a conversion takes the
@@ -557,11 +560,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       const float sc = change || late ? 1.f : scale2;
       top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
       if (change) tmem_st_wait();
-      if (__any_sync(0xffffffffu, top > mx + kLazy)) {
-        const float mn = fmaxf(mx, top);
-        const float f = mn == -INFINITY ? 1.f : ex2(mx - mn);
+      // (every row by its own maximum: other rows' only decide whether the warp
+      // comes here, where theirs are multiplied by 1)
+      const bool up = top > mx + kLazy;
+      if (__any_sync(0xffffffffu, up)) {
+        const float f = up ? ex2(mx - top) : 1.f;
         sum *= f;
-        mx = mn;
+        if (up) mx = top;
         if (i > 0) {
           // O holds the tiles before this one: their P V is done (with two
           // query tiles because S of this tile was issued after it)

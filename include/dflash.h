@@ -698,8 +698,9 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
  * and its score is t = scale * q.k; t = c * tanh(t / c) (c = softcap, 0 = no
  * cap); t -= slopes[h] * |pq - pk|. out = sum softmax(t) v, lse = log sum
  * exp(t) (natural log); a query that sees nothing gives out = 0 and lse =
- * -inf. What a query does not see has no influence on it, infinities and NaN
- * included; infinities and NaN that it does see make what they reach infinite
+ * -inf. What a query does not see, other sequences' queries among it, has no
+ * influence on it, infinities and NaN included (the sizes of a batch have, on
+ * how sums are split); infinities and NaN that it does see make what they reach infinite
  * or NaN. Softmax statistics and sums are fp32. out and lse
  * overlap no input. Rows outside [start[0], start[n_seq]) of out and lse are
  * left as they are. */

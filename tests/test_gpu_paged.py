@@ -321,6 +321,30 @@ def test_hidden_rows_leave_every_bit(B, dtype, hd, nq, n, mask):
         assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 3
 
 
+@pytest.mark.parametrize("mask", [dict(), dict(softcap=20.0), dict(softcap=3.0, slopes=True), dict(window=600)], ids=lambda m: "-".join(m) or "plain")
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 64, 4), ("bf16", 200, 4)])
+@pytest.mark.parametrize("n", [1, 3, 70, 200])
+def test_the_next_sequence_leaves_every_bit(B, dtype, hd, nq, n, mask):
+    """out, lse and key weights of a sequence are the same bits whatever the queries of the next one are, and those of no
+    sequence at all: a load brings them into its tile, and its warps vote on how scores are computed."""
+    s = Setup(B, [(n, 1500), (5, 60)], nq, 2, hd, 16, dtype, seed=9, tail=4)
+    m = {k: v.cuda() if torch.is_tensor(v) else v for k, v in mask_of(mask, nq, 2).items()}
+    cache, q = s.device(), s.q.cuda()
+    pages = s.table[0, :-(-1500 // 16)].long().cuda()
+    results = []
+    for fill in (None, 0.0, 1e4, math.inf, math.nan):
+        if fill is not None:
+            q[n:] = fill
+        out, lse = torch.zeros_like(q), torch.zeros(s.rows, nq, device="cuda")
+        w = torch.zeros(s.pos.shape, device="cuda")
+        cache.attention(q, s.q_pos.cuda(), s.start.cuda(), out, lse=lse, **m)
+        cache.key_weight(q, s.q_pos.cuda(), s.start.cuda(), lse, weight_out=w, weight=torch.zeros_like(w), **m)
+        results.append((out[:n], lse[:n], w[pages]))
+    assert torch.isfinite(results[0][0]).all()
+    for r in results[1:]:
+        assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 3
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, dtype, seed=8)
