@@ -18,18 +18,22 @@
 // nearly no tile needs it.
 //
 // A tile of at most 32 (64) rows, a decode or verify block's, is held 4 (2) times
-// in the tile's lanes: each warp then takes a quarter (half) of the keys, its
-// lanes' P is zero for the others', and the warps' outputs are joined at the end
-// like those of splits. The softmax of a tile takes a quarter of the time, and
-// all four warps have work, which pays for the second part of P (below).
+// in the tile's lanes (where a token's heads are 32 at most): each warp then takes
+// a quarter (half) of the keys, its lanes' P is zero for the others', and the
+// warps' outputs are joined at the end like those of splits. The softmax of a
+// tile takes a quarter of the time, and all four warps have work, which pays for
+// the second part of P (below).
 //
 // P as a product's operand is bf16. For those few rows, where K and V's bytes
 // are the bound, it is two bf16 parts (16 bits of p, two products), the second
-// in the half of S's columns that the first leaves free. For many, where the
-// products are the bound, it is rounded: half a step, 2^-8 relative at most
-// and independent from key to key, adds as much error to an output as the
-// output's own rounding to bf16 does (measured against fp64: 0.0023 of the norm
-// instead of 0.0017). The sum of p is taken before, in fp32.
+// in the half of S's columns that the first leaves free, or, of a sequence that
+// a batch with prompts gives to the two-tile kernel, in the S of the tile that
+// it does not have: what a batch holds beside a decode row does not change how
+// exact the row is. For many rows, where the products are the bound, it is
+// rounded: half a step, 2^-8 relative at most and independent from key to key,
+// adds as much error to an output as the output's own rounding to bf16 does
+// (measured against fp64: 0.0023 of the norm instead of 0.0017). The sum of p is
+// taken before, in fp32.
 //
 // Rows that a query does not see get p = 0, but 0 times an infinite or NaN V is
 // NaN. So in every tile that is not wholly seen by all its queries two warps
@@ -186,6 +190,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
   const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
   const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
+  const bool two_parts = QT == 2 ? nt == 1 && n_tok <= 2 * t32 : rep > 1;   // of P, the second `low` columns on
+  constexpr int low = QT == 2 ? 128 : 64;
 
   // The page of a lane's four keys of a tile (-1: none) and their positions; a
   // page is requested two tiles ahead and positions one, so that neither load
@@ -282,18 +288,19 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         }
         __syncwarp();
       };
+      // the second part of P
+      auto low_pv = [&](int buf, uint64_t v) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256, tmem + buf * 128 + low + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
+      };
       auto pv = [&](int q, int buf, int i, bool last) {
         const int s = (2 * i + 1) % NS;
         if (leader) {
           const uint64_t v = v_desc + s * (C::kTileB >> 4);
 #pragma unroll
           for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256 + q * HDP, tmem + buf * 128 + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
-          if (QT == 1) {
-            if (rep > 1)
-#pragma unroll
-              for (int k = 0; k < 8; ++k) tc_mma_bf16_ta(tmem + 256, tmem + buf * 128 + 64 + k * 8, v + k * (2048 >> 4), idesc_o, 1u);
-            tc_commit(&o_done);
-          }
+          if (QT == 1 && rep > 1) low_pv(buf, v);
+          if (QT == 1) tc_commit(&o_done);
           if (last) tc_commit(&kv_empty[s]);
         }
         __syncwarp();
@@ -303,7 +310,25 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       paged_wait(&q_full, 0, ok);
       wait_k(0);
       qk(0, 0, 0, QT == 1 || nt == 1);
-      if (QT == 2) {
+      if (QT == 2 && two_parts) {
+        for (int i = 0; i < N; ++i) {
+          wait_v(i);
+          paged_wait(&p_ready[0], i & 1, ok);
+          if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+          tc_fence_after();
+          const int s = (2 * i + 1) % NS;
+          pv(0, 0, i, false);
+          if (leader) {
+            low_pv(0, v_desc + s * (C::kTileB >> 4));
+            tc_commit(&kv_empty[s]);
+          }
+          __syncwarp();
+          if (i + 1 < N) {
+            wait_k(i + 1);
+            qk(0, 0, i + 1, true);
+          }
+        }
+      } else if (QT == 2) {
         if (nt == 2) qk(1, 1, 0, true);
         for (int i = 0; i < N; ++i) {
           const bool more = i + 1 < N;
@@ -448,259 +473,272 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       for (int d = 0; d < HDP; d += 32) tmem_st32(o_at + d, zero);
       tmem_st_wait();
     }
-    for (int i = 0; i < N; ++i) {
-      const int buf = QT == 2 ? q : (i & 1);
-      const uint32_t s_at = tmem + lanes + buf * 128;
-      paged_wait(&s_full[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1), ok);
-      if (!__all_sync(0xffffffffu, ok)) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      if (!work) {                                       // rows of nobody: their P may be anything
-        mbar_arrive(&p_ready[buf]);
-        continue;
-      }
-      bool full = classified(rel);
-      const int tile = sh.t0 + rel;
-      // First pass over S: the row's maximum. What a mask or bias makes of a score
-      // is put back in its place, so that the second pass is the same for all; S
-      // is read twice because half as many registers then do. A cap alone keeps
-      // the order of scores: the maximum's is enough here, and the second pass
-      // caps the others.
-      // (a tile that other warps see in part, or that was not classified, may be
-      // wholly seen by this warp's rows)
-      bool masked = !full;
-      if (masked) {
-        const Span k = span(pos4);
-        masked = !k.whole || paged_class(m, wmin, wmax, k.lo, k.hi, true) != 2;
-        if (QT == 1 && direct) full = k.whole && paged_class(m, qmin, qmax, k.lo, k.hi, true) == 2;
-      }
-      const bool late = EXTRA && a.softcap > 0.f && !masked && !a.slopes;
-      const bool change = masked || (EXTRA && a.slopes);
-      if (masked || (EXTRA && a.slopes)) {
-        __syncwarp();
-        *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
-        if (EXTRA && a.slopes)
-          *reinterpret_cast<float4*>(kd + lane * 4) =
-              make_float4((float)(pos4.x - wmin), (float)(pos4.y - wmin), (float)(pos4.z - wmin), (float)(pos4.w - wmin));
-        __syncwarp();
-      }
-      float x[2][32], top = -INFINITY;
-      auto rise = [&](const float* v) {
-        float t2[2] = {v[0], v[1]};
+    // The two-tile kernel's few rows have a loop of their own: their branch within
+    // that of all others costs a prompt 3% (2048 rows over 32768 keys: 820 us, with
+    // it 843 us). With a cap or bias it costs nothing, and a second loop 4%.
 #pragma unroll
-        for (int j = 2; j < 32; j += 4) {
-          t2[0] = j + 2 < 32 ? fmaxf(fmaxf(t2[0], v[j]), v[j + 2]) : fmaxf(t2[0], v[j]);
-          t2[1] = j + 3 < 32 ? fmaxf(fmaxf(t2[1], v[j + 1]), v[j + 3]) : fmaxf(t2[1], v[j + 1]);
+    for (int alone = 0; alone < (QT == 2 && !EXTRA ? 2 : 1); ++alone) {
+      const bool two = QT == 2 && !EXTRA ? alone == 1 : two_parts;
+      if (two != two_parts) continue;
+      for (int i = 0; i < N; ++i) {
+        const int buf = QT == 2 ? q : (i & 1);
+        const uint32_t s_at = tmem + lanes + buf * 128;
+        paged_wait(&s_full[buf], QT == 2 ? (i & 1) : ((i >> 1) & 1), ok);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
-        top = fmaxf(top, fmaxf(t2[0], t2[1]));
-      };
-      if (QT == 2 && !change) {
-        tmem_ld32(s_at, x[0]);
+        tc_fence_after();
+        if (!work) {                                       // rows of nobody: their P may be anything
+          mbar_arrive(&p_ready[buf]);
+          continue;
+        }
+        bool full = classified(rel);
+        const int tile = sh.t0 + rel;
+        // First pass over S: the row's maximum. What a mask or bias makes of a score
+        // is put back in its place, so that the second pass is the same for all; S
+        // is read twice because half as many registers then do. A cap alone keeps
+        // the order of scores: the maximum's is enough here, and the second pass
+        // caps the others.
+        // (a tile that other warps see in part, or that was not classified, may be
+        // wholly seen by this warp's rows)
+        bool masked = !full;
+        if (masked) {
+          const Span k = span(pos4);
+          masked = !k.whole || paged_class(m, wmin, wmax, k.lo, k.hi, true) != 2;
+          if (QT == 1 && direct) full = k.whole && paged_class(m, qmin, qmax, k.lo, k.hi, true) == 2;
+        }
+        const bool late = EXTRA && a.softcap > 0.f && !masked && !a.slopes;
+        const bool change = masked || (EXTRA && a.slopes);
+        if (masked || (EXTRA && a.slopes)) {
+          __syncwarp();
+          *reinterpret_cast<int4*>(kp + lane * 4) = pos4;
+          if (EXTRA && a.slopes)
+            *reinterpret_cast<float4*>(kd + lane * 4) =
+                make_float4((float)(pos4.x - wmin), (float)(pos4.y - wmin), (float)(pos4.z - wmin), (float)(pos4.w - wmin));
+          __syncwarp();
+        }
+        float x[2][32], top = -INFINITY;
+        auto rise = [&](const float* v) {
+          float t2[2] = {v[0], v[1]};
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          tmem_ld_wait32(x[n & 1]);
-          if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-          rise(x[n & 1]);
-        }
-      } else if (!change) {
+          for (int j = 2; j < 32; j += 4) {
+            t2[0] = j + 2 < 32 ? fmaxf(fmaxf(t2[0], v[j]), v[j + 2]) : fmaxf(t2[0], v[j]);
+            t2[1] = j + 3 < 32 ? fmaxf(fmaxf(t2[1], v[j + 1]), v[j + 3]) : fmaxf(t2[1], v[j + 1]);
+          }
+          top = fmaxf(top, fmaxf(t2[0], t2[1]));
+        };
+        if (QT == 2 && !change) {
+          tmem_ld32(s_at, x[0]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            tmem_ld_wait32(x[n & 1]);
+            if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+            rise(x[n & 1]);
+          }
+        } else if (!change) {
 #pragma unroll 1
-        for (int n = n0; n < n1; ++n) {
-          tmem_ld32(s_at + n * 32, x[0]);
-          tmem_ld_wait32(x[0]);
-          rise(x[0]);
-        }
-      } else {
-#pragma unroll 1
-        for (int n = n0; n < n1; ++n) {
-          float* v = x[0];
-          uint32_t w[32];
-          const int4* pk4 = reinterpret_cast<const int4*>(kp + n * 32);
-          tmem_ld32(s_at + n * 32, v);
-          tmem_ld_wait32(v);
-          if (EXTRA && a.softcap > 0.f) {
-            cap_tanh32(v, cap, masked, [&]() {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = paged_sees(sees, kp[n * 32 + j]) ? v[j] : 0.f;
-            });
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] *= scale2;
-          }
-          if (EXTRA && a.slopes && near) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 k = *reinterpret_cast<const float4*>(kd + n * 32 + j);
-              v[j] = fmaf(-slope2, fabsf(pqf - k.x), v[j]);
-              v[j + 1] = fmaf(-slope2, fabsf(pqf - k.y), v[j + 1]);
-              v[j + 2] = fmaf(-slope2, fabsf(pqf - k.z), v[j + 2]);
-              v[j + 3] = fmaf(-slope2, fabsf(pqf - k.w), v[j + 3]);
-            }
-          } else if (EXTRA && a.slopes) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope2, fabsf((float)(pq - kp[n * 32 + j])), v[j]);
-          }
-          if (masked) {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const int4 k = pk4[j >> 2];
-              v[j] = paged_sees(sees, k.x) ? v[j] : -INFINITY;
-              v[j + 1] = paged_sees(sees, k.y) ? v[j + 1] : -INFINITY;
-              v[j + 2] = paged_sees(sees, k.z) ? v[j + 2] : -INFINITY;
-              v[j + 3] = paged_sees(sees, k.w) ? v[j + 3] : -INFINITY;
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
-          tmem_st32(s_at + n * 32, w);
-          rise(v);
-        }
-      }
-      const float sc = change || late ? 1.f : scale2;
-      top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
-      if (change) tmem_st_wait();
-      // (every row by its own maximum: other rows' only decide whether the warp
-      // comes here, where theirs are multiplied by 1)
-      const bool up = top > mx + kLazy;
-      if (__any_sync(0xffffffffu, up)) {
-        const float f = up ? ex2(mx - top) : 1.f;
-        sum *= f;
-        if (up) mx = top;
-        if (i > 0) {
-          // O holds the tiles before this one: their P V is done (with two
-          // query tiles because S of this tile was issued after it)
-          if (QT == 1) {
-            paged_wait(&o_done, (i - 1) & 1, ok);
-            tc_fence_after();
-          }
-#pragma unroll
-          for (int d = 0; d < HDP; d += 16) {
-            float o[16];
-            tmem_ld16(o_at + d, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] *= f;
-            tmem_st16(o_at + d, o);
-          }
-          tmem_st_wait();
-        }
-      }
-      const float base = mx == -INFINITY ? 0.f : mx;
-      const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
-      uint64_t add[2] = {0, 0};
-      // two values' p, and the bf16 pair that they are stored as
-      auto weigh = [&](const float* v, float& p0, float& p1) {
-        unpack2(fma2(pack2(v[0], v[1]), sc2, nb2), p0, p1);
-        p0 = ex2(p0);
-        p1 = ex2(p1);
-        return pack_bf16(p0, p1);
-      };
-      if (QT == 2 && EXTRA && late) {
-#pragma unroll 1
-        for (int n = 0; n < 4; ++n) {
-          float w[16];
-          tmem_ld32(s_at + n * 32, x[0]);
-          tmem_ld_wait32(x[0]);
-          cap_tanh32(x[0], cap, false, []() {});
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float p0, p1;
-            w[j >> 1] = __uint_as_float(weigh(x[0] + j, p0, p1));
-            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
-          }
-          tmem_st16(s_at + n * 16, w);
-        }
-      } else if (QT == 2) {
-        tmem_ld32(s_at, x[0]);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-          float* v = x[n & 1];
-          tmem_ld_wait32(v);
-          if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-          float w[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float p0, p1;
-            w[j >> 1] = __uint_as_float(weigh(v + j, p0, p1));
-            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
-          }
-          tmem_st16(s_at + n * 16, w);                   // columns whose scores have been read
-        }
-      } else {
-        // P's first part goes into columns 0 .. 63, its second into 64 .. 127; in
-        // this order no chunk's parts fall on scores of the warp not yet read
-        const bool down = rep == 2 && n0 == 2;
-#pragma unroll 1
-        for (int k = n0; k < n1; ++k) {
-          const int n = down ? n0 + n1 - 1 - k : k;
-          if (rep < 4) {
+          for (int n = n0; n < n1; ++n) {
             tmem_ld32(s_at + n * 32, x[0]);
             tmem_ld_wait32(x[0]);
+            rise(x[0]);
           }
-          if (EXTRA && late) cap_tanh32(x[0], cap, false, []() {});
-          float w[16], lo[16];
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float p0, p1;
-            const uint32_t hi = weigh(x[0] + j, p0, p1);
-            add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
-            w[j >> 1] = __uint_as_float(hi);
-            lo[j >> 1] = __uint_as_float(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi)));
-          }
-          tmem_st16(s_at + n * 16, w);
-          if (rep > 1) tmem_st16(s_at + 64 + n * 16, lo);
-        }
-        if (rep > 1) {
-          // the other warps' keys have no weight in these lanes
-          const float zero[16] = {};
+        } else {
 #pragma unroll 1
-          for (int n = 0; n < 4; ++n) {
-            if (n >= n0 && n < n1) continue;
-            tmem_st16(s_at + n * 16, zero);
-            tmem_st16(s_at + 64 + n * 16, zero);
+          for (int n = n0; n < n1; ++n) {
+            float* v = x[0];
+            uint32_t w[32];
+            const int4* pk4 = reinterpret_cast<const int4*>(kp + n * 32);
+            tmem_ld32(s_at + n * 32, v);
+            tmem_ld_wait32(v);
+            if (EXTRA && a.softcap > 0.f) {
+              cap_tanh32(v, cap, masked, [&]() {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = paged_sees(sees, kp[n * 32 + j]) ? v[j] : 0.f;
+              });
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] *= scale2;
+            }
+            if (EXTRA && a.slopes && near) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const float4 k = *reinterpret_cast<const float4*>(kd + n * 32 + j);
+                v[j] = fmaf(-slope2, fabsf(pqf - k.x), v[j]);
+                v[j + 1] = fmaf(-slope2, fabsf(pqf - k.y), v[j + 1]);
+                v[j + 2] = fmaf(-slope2, fabsf(pqf - k.z), v[j + 2]);
+                v[j + 3] = fmaf(-slope2, fabsf(pqf - k.w), v[j + 3]);
+              }
+            } else if (EXTRA && a.slopes) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = fmaf(-slope2, fabsf((float)(pq - kp[n * 32 + j])), v[j]);
+            }
+            if (masked) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 4) {
+                const int4 k = pk4[j >> 2];
+                v[j] = paged_sees(sees, k.x) ? v[j] : -INFINITY;
+                v[j + 1] = paged_sees(sees, k.y) ? v[j + 1] : -INFINITY;
+                v[j + 2] = paged_sees(sees, k.z) ? v[j + 2] : -INFINITY;
+                v[j + 3] = paged_sees(sees, k.w) ? v[j + 3] : -INFINITY;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+            tmem_st32(s_at + n * 32, w);
+            rise(v);
           }
         }
-      }
-      float a0, a1;
-      unpack2(add2(add[0], add[1]), a0, a1);
-      sum += a0 + a1;
-      tmem_st_wait();
-      if (!full) {
-        const unsigned* who = bad[i & 3];
-        paged_wait(&v_ok[i & 3], (i >> 2) & 1, ok);
-        const unsigned any = who[0] | who[1] | who[2] | who[3];
-        if (any && QT == 1 && i > 0) {
-          paged_wait(&o_done, (i - 1) & 1, ok);
-          tc_fence_after();
-        }
-        for (int w = 0; any && w < 4; ++w)
-          for (unsigned b = who[w]; b; b &= b - 1) {
-            const int j = w * 32 + __ffs(b) - 1, slot = tile * kPtKeys + j;
-            if (slot >= len) continue;
-            const uint32_t ph = tmem_ld1(s_at + (j >> 1)), pl = rep > 1 ? tmem_ld1(s_at + 64 + (j >> 1)) : 0u;
-            tmem_ld_wait();
-            const float p = j & 1 ? bf_hi(ph) + bf_hi(pl) : bf_lo(ph) + bf_lo(pl);
-            const long long row = paged_row(c, t.seq, h, slot);
-            if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
-            const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
+        const float sc = change || late ? 1.f : scale2;
+        top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
+        if (change) tmem_st_wait();
+        // (every row by its own maximum: other rows' only decide whether the warp
+        // comes here, where theirs are multiplied by 1)
+        const bool up = top > mx + kLazy;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = up ? ex2(mx - top) : 1.f;
+          sum *= f;
+          if (up) mx = top;
+          if (i > 0) {
+            // O holds the tiles before this one: their P V is done (with two
+            // query tiles because S of this tile was issued after it)
+            if (QT == 1) {
+              paged_wait(&o_done, (i - 1) & 1, ok);
+              tc_fence_after();
+            }
+#pragma unroll
             for (int d = 0; d < HDP; d += 16) {
               float o[16];
               tmem_ld16(o_at + d, o);
               tmem_ld_wait();
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const float v = d + x < c.hd ? to_f(vrow[d + x]) : 0.f;
-                if (p != 0.f) o[x] = fmaf(p, v, o[x]);
-              }
+              for (int j = 0; j < 16; ++j) o[j] *= f;
               tmem_st16(o_at + d, o);
             }
             tmem_st_wait();
           }
+        }
+        const float base = mx == -INFINITY ? 0.f : mx;
+        const uint64_t sc2 = pack2(sc, sc), nb2 = pack2(-base, -base);
+        uint64_t add[2] = {0, 0};
+        // two values' p, and the bf16 pair that they are stored as
+        auto weigh = [&](const float* v, float& p0, float& p1) {
+          unpack2(fma2(pack2(v[0], v[1]), sc2, nb2), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          return pack_bf16(p0, p1);
+        };
+        // what a stored pair leaves of them
+        auto rest = [&](uint32_t hi, float p0, float p1) { return __uint_as_float(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi))); };
+        if (QT == 2 && (two || (EXTRA && late))) {
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            float w[16], lo[16];
+            tmem_ld32(s_at + n * 32, x[0]);
+            tmem_ld_wait32(x[0]);
+            if (EXTRA && late) cap_tanh32(x[0], cap, false, []() {});
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float p0, p1;
+              const uint32_t hi = weigh(x[0] + j, p0, p1);
+              w[j >> 1] = __uint_as_float(hi);
+              lo[j >> 1] = rest(hi, p0, p1);
+              add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+            }
+            tmem_st16(s_at + n * 16, w);
+            if (two) tmem_st16(s_at + low + n * 16, lo);
+          }
+        } else if (QT == 2) {
+          tmem_ld32(s_at, x[0]);
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            float* v = x[n & 1];
+            tmem_ld_wait32(v);
+            if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
+            float w[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float p0, p1;
+              w[j >> 1] = __uint_as_float(weigh(v + j, p0, p1));
+              add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+            }
+            tmem_st16(s_at + n * 16, w);                   // columns whose scores have been read
+          }
+        } else {
+          // P's first part goes into columns 0 .. 63, its second into 64 .. 127; in
+          // this order no chunk's parts fall on scores of the warp not yet read
+          const bool down = rep == 2 && n0 == 2;
+#pragma unroll 1
+          for (int k = n0; k < n1; ++k) {
+            const int n = down ? n0 + n1 - 1 - k : k;
+            if (rep < 4) {
+              tmem_ld32(s_at + n * 32, x[0]);
+              tmem_ld_wait32(x[0]);
+            }
+            if (EXTRA && late) cap_tanh32(x[0], cap, false, []() {});
+            float w[16], lo[16];
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float p0, p1;
+              const uint32_t hi = weigh(x[0] + j, p0, p1);
+              add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+              w[j >> 1] = __uint_as_float(hi);
+              lo[j >> 1] = rest(hi, p0, p1);
+            }
+            tmem_st16(s_at + n * 16, w);
+            if (two) tmem_st16(s_at + low + n * 16, lo);
+          }
+          if (rep > 1) {
+            // the other warps' keys have no weight in these lanes
+            const float zero[16] = {};
+#pragma unroll 1
+            for (int n = 0; n < 4; ++n) {
+              if (n >= n0 && n < n1) continue;
+              tmem_st16(s_at + n * 16, zero);
+              tmem_st16(s_at + low + n * 16, zero);
+            }
+          }
+        }
+        float a0, a1;
+        unpack2(add2(add[0], add[1]), a0, a1);
+        sum += a0 + a1;
+        tmem_st_wait();
+        if (!full) {
+          const unsigned* who = bad[i & 3];
+          paged_wait(&v_ok[i & 3], (i >> 2) & 1, ok);
+          const unsigned any = who[0] | who[1] | who[2] | who[3];
+          if (any && QT == 1 && i > 0) {
+            paged_wait(&o_done, (i - 1) & 1, ok);
+            tc_fence_after();
+          }
+          for (int w = 0; any && w < 4; ++w)
+            for (unsigned b = who[w]; b; b &= b - 1) {
+              const int j = w * 32 + __ffs(b) - 1, slot = tile * kPtKeys + j;
+              if (slot >= len) continue;
+              const uint32_t ph = tmem_ld1(s_at + (j >> 1)), pl = two ? tmem_ld1(s_at + low + (j >> 1)) : 0u;
+              tmem_ld_wait();
+              const float p = j & 1 ? bf_hi(ph) + bf_hi(pl) : bf_lo(ph) + bf_lo(pl);
+              const long long row = paged_row(c, t.seq, h, slot);
+              if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
+              const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
+              for (int d = 0; d < HDP; d += 16) {
+                float o[16];
+                tmem_ld16(o_at + d, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                  const float v = d + x < c.hd ? to_f(vrow[d + x]) : 0.f;
+                  if (p != 0.f) o[x] = fmaf(p, v, o[x]);
+                }
+                tmem_st16(o_at + d, o);
+              }
+              tmem_st_wait();
+            }
+        }
+        tc_fence_before();
+        mbar_arrive(&p_ready[buf]);
+        advance();
       }
-      tc_fence_before();
-      mbar_arrive(&p_ready[buf]);
-      advance();
     }
     // ---- the row's output, or its split's partial (to shared memory for the
     // cluster, else to the workspace)

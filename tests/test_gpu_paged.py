@@ -345,6 +345,26 @@ def test_the_next_sequence_leaves_every_bit(B, dtype, hd, nq, n, mask):
         assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 3
 
 
+@pytest.mark.parametrize("nq,hd", [(8, 128), (6, 64), (32, 128)])
+@pytest.mark.parametrize("prompt", [0, 300])
+def test_few_rows_beside_a_prompt_are_as_exact_as_alone(B, nq, hd, prompt):
+    """A sequence of at most 64 packed rows has its weights in two bf16 parts, 2^-16 of each at most, whatever else is in the
+    batch: values +1 and -1 nearly cancel, so that an output's own rounding is no cover for one part's 2^-8."""
+    lens = [(1, 9), (1, 14), (2, 12), (3, 11)]
+    s = Setup(B, ([(prompt, 320)] if prompt else []) + lens, nq, 2, hd, 16, seed=12, scale=0.3)
+    s.v = torch.where(torch.isnan(s.v), s.v, torch.where(s.v > 0, 1.0, -1.0).to(s.dt))
+    cache = s.device()
+    out, lse = torch.zeros(s.rows, nq, hd, dtype=s.dt, device="cuda"), torch.zeros(s.rows, nq, device="cuda")
+    cache.attention(s.q.cuda(), s.q_pos.cuda(), s.start.cuda(), out, lse=lse)
+    few = slice(prompt, s.rows)
+    want, want_lse, mag = (x[few] for x in P.attention(s.oracle(), host(s.q), s.q_pos.numpy(), s.start.numpy(), s.scale))
+    dt = s.score_error(0.0, None)
+    tol = unit("bf16") * np.abs(want) + (2 * (dt + 2.0 ** -20) + 14 * EPS + 2.0 ** -16) * mag
+    off = np.abs(host(out)[few] - want) / tol
+    assert off.max() <= 1.0, f"off by {off.max():.3g} of the tolerance"
+    assert (np.abs(host(lse)[few] - want_lse) <= dt + 2.0 ** -20 + 4 * EPS * np.abs(want_lse)).all()
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, dtype, seed=8)
