@@ -140,7 +140,8 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   };
   // adds the exponentials of 32 query rows (from row n * 32 of `rw`) to two sums
   const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e;
-  const CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
+  CapPoly cap = cap_poly(scale2, a.softcap * kLog2e);
+  const float cap_limit = cap.limit;
   auto add_chunk = [&](float* v, const WtRows& rw, int n, const PagedSees& by, int pk, bool full, uint64_t* add) {
     float sc = scale2;
     if (EXTRA && a.softcap > 0.f) {
@@ -400,6 +401,9 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         }
       } else {
         const PagedSees by = paged_seen_by(m, pk);
+        // a lane without a row holds scores of whatever its page has there, which
+        // have no say in how the warp's caps are computed
+        cap.limit = my_row >= 0 ? cap_limit : INFINITY;
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
           const int rel = cur.next(), b = j & 1, s = j % kNA;

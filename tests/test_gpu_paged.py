@@ -365,6 +365,26 @@ def test_few_rows_beside_a_prompt_are_as_exact_as_alone(B, nq, hd, prompt):
     assert (np.abs(host(lse)[few] - want_lse) <= dt + 2.0 ** -20 + 4 * EPS * np.abs(want_lse)).all()
 
 
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 128, 4), ("bf16", 200, 4)])
+@pytest.mark.parametrize("n", [200, 270])
+def test_rows_behind_the_length_leave_every_bit_of_key_weights(B, dtype, hd, nq, n):
+    """Every query sees every row there is, and the last tile of keys ends inside a page: what that page holds behind the length
+    has no say in how the others' caps are computed."""
+    results = []
+    for fill in (0.0, 1e4, math.inf, math.nan):
+        s = Setup(B, [(n, 277)], nq, 2, hd, 16, dtype, seed=5)
+        s.k[torch.isnan(s.k)] = fill
+        cache, args = s.device(), (s.q.cuda(), s.q_pos.cuda(), s.start.cuda())
+        out, lse = torch.zeros(n, nq, hd, dtype=s.dt, device="cuda"), torch.zeros(n, nq, device="cuda")
+        w = torch.zeros(s.pos.shape, device="cuda")
+        cache.attention(*args, out, lse=lse, causal=False, softcap=20.0)
+        cache.key_weight(*args, lse, weight_out=w, weight=torch.zeros_like(w), causal=False, softcap=20.0)
+        assert torch.isfinite(w).all()
+        results.append((lse, w))
+    for r in results[1:]:
+        assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 2
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, dtype, seed=8)
