@@ -98,9 +98,10 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
   bool ok = true;
 
   // lse, position and slope of the query rows of tile q, four to a lane
-  struct RowData { float l[4], sl[4]; int p[4], base, near; };
+  struct RowData { float l[4], sl[4]; int p[4], base, near; bool whole; };
   auto row_data = [&](int q) {
     RowData d;
+    bool whole = true;                     // every row has an lse
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int r = x * 32 + lane, tl = r / G, tok = q * tpt + tl, head = h * G + r - tl * G;
@@ -109,7 +110,9 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
       d.l[x] = v == -INFINITY ? -INFINITY : -v * kLog2e;
       d.p[x] = v == -INFINITY ? kPagedNoPos : a.q_pos[ab.x + tok];
       d.sl[x] = in && a.slopes ? a.slopes[head] * kLog2e : 0.f;
+      whole = whole && (!in || v != -INFINITY);
     }
+    d.whole = __all_sync(0xffffffffu, whole);
     d.base = 0;
     d.near = 1;
     if (EXTRA && a.slopes) {
@@ -396,6 +399,10 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
           if (j >= kNA) paged_wait(&rows_empty[s], (j / kNA - 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           put_rows(rows[s], d);
+          // a row without an lse (padding, perhaps) adds nothing, but its score may
+          // be NaN, which minus infinity does not hide: its tile is looked at row by
+          // row (512 rows over 32768 keys: 155 us, without this 152 us)
+          if (!d.whole && lane == 0) atomicAnd(&all[(q - c0) >> 5], ~(1u << ((q - c0) & 31)));
           __syncwarp();
           if (lane == 0) mbar_arrive(&rows_full[s]);
         }
@@ -407,13 +414,13 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
         for (int i = 0; i < N; ++i) {
           const unsigned j = it + i;
           const int rel = cur.next(), b = j & 1, s = j % kNA;
-          const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
           const uint32_t s_at = tmem + (static_cast<uint32_t>(warp * 32) << 16) + b * 128;
           paged_wait(&rows_full[s], (j / kNA) & 1, ok);
+          const WtRows& rw = rows[s];
+          const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
           paged_wait(&s_full[b], (j >> 1) & 1, ok);
           if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
           tc_fence_after();
-          const WtRows& rw = rows[s];
           uint64_t add[2] = {0, 0};
           if (full && !EXTRA) {
             const uint64_t sc2 = pack2(scale2, scale2);

@@ -385,6 +385,31 @@ def test_rows_behind_the_length_leave_every_bit_of_key_weights(B, dtype, hd, nq,
         assert [torch.equal(a, b) for a, b in zip(r, results[0])] == [True] * 2
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("mask", [dict(), dict(softcap=20.0), dict(slopes=True)], ids=lambda m: "-".join(m) or "plain")
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 64, 4), ("bf16", 136, 4)])
+@pytest.mark.parametrize("n", [5, 200])
+def test_queries_without_an_lse_add_nothing_to_key_weights(B, dtype, hd, nq, n, mask, bad):
+    """Rows of padding, lse = -inf, whatever their q holds, beside rows that see every key of a tile."""
+    s = Setup(B, [(n, 500)], nq, 2, hd, 16, dtype, seed=14)
+    m = mask_of(mask, nq, 1)
+    cache = s.device()
+    _, lse = s.check_attention(cache, **m)
+    s.q[2:n:7] = bad
+    lse[2::7] = -math.inf
+    clean = s.q.clone()
+    clean[2:n:7] = 0
+    dev = {k: v.cuda() if torch.is_tensor(v) else v for k, v in m.items()}
+    got = []
+    for q in (s.q, clean):
+        w = torch.zeros(s.pos.shape, device="cuda")
+        cache.key_weight(q.cuda(), s.q_pos.cuda(), s.start.cuda(), lse, weight_out=w, weight=torch.zeros_like(w), **dev)
+        got.append(w)
+    assert torch.isfinite(got[0]).all() and torch.equal(got[0], got[1])
+    s.q = clean
+    s.check_weight(cache, lse, **m)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, dtype, seed=8)
