@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
     for (int i = 0; i < 2; ++i) {
       const int slot = k0 + warp * 16 + g + 8 * i;
       row[i] = slot < len ? paged_row(c, s, h, slot) : -1;
+      if (slot < len && row[i] < 0 && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

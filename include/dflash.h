@@ -653,7 +653,7 @@ typedef struct dflash_paged_cache {
 } dflash_paged_cache;
 
 /* Bits of dflash_paged_cache.status. */
-#define DFLASH_PAGED_BAD_PAGE 1 /* a page id outside [0, n_pages) */
+#define DFLASH_PAGED_BAD_PAGE 1 /* a page id outside [0, n_pages), of a row that the call looks up */
 #define DFLASH_PAGED_BAD_ROWS 2 /* a length beyond the table, or more new rows than length */
 #define DFLASH_PAGED_GAVE_UP 4  /* a bounded wait in a tensor-core kernel gave up */
 

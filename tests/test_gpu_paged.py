@@ -428,6 +428,39 @@ def test_bad_pages_and_lengths_are_bounded(B, dtype):
     s.check_attention(cache)
 
 
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("f32", 64), ("f32", 256)])
+@pytest.mark.parametrize("n", [4, 150])
+def test_every_call_reports_bad_pages(B, dtype, hd, n):
+    s = Setup(B, [(n, 400), (4, 60)], 8, 2, hd, 16, dtype, seed=8)
+    s.table[0, 2] = 10 ** 6
+    cache, args = s.device(), (s.q.cuda(), s.q_pos.cuda(), s.start.cuda())
+    out, lse = torch.zeros(s.rows, 8, hd, dtype=s.dt, device="cuda"), torch.zeros(s.rows, 8, device="cuda")
+    w, p, length = torch.zeros(s.pos.shape, device="cuda"), torch.zeros_like(cache.pos), torch.zeros_like(cache.length)
+    end = s.length.cuda()
+    for call in (lambda: cache.attention(*args, out, lse=lse), lambda: cache.key_weight(*args, lse, weight_out=w),
+                 lambda: cache.evict(50, 5, end, weight_out=w, pos_out=p, length_out=length),
+                 lambda: cache.evict(1000, 5, end, weight_out=w, pos_out=p, length_out=length)):
+        s.status.zero_()
+        call()
+        assert int(s.status) == B.PAGED_BAD_PAGE
+
+
+def test_an_eviction_of_rows_that_no_cta_holds_reports_bad_pages(B):
+    ps, pages = 1024, 1024
+    shape = (pages, 1, ps)
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None].contiguous()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pos = torch.arange(pages * ps, dtype=torch.int32, device="cuda").view(shape)
+    k = torch.zeros(*shape, 8, device="cuda")
+    c = B.PagedCache(k, k.clone(), pos, table, torch.tensor([pages * ps], dtype=torch.int32, device="cuda"), weight=torch.rand(shape, device="cuda"), status=status)
+    c.evict(pages * ps - 3000, 0, torch.tensor([pages * ps], dtype=torch.int32, device="cuda"))
+    assert int(status) == 0
+    c.length.fill_(pages * ps)
+    table[0, 700] = pages
+    c.evict(pages * ps - 3000, 0, torch.tensor([pages * ps], dtype=torch.int32, device="cuda"))
+    assert int(status) == B.PAGED_BAD_PAGE
+
+
 def test_row_ranges_beyond_the_tensor_are_cut(B):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, seed=8)
     cache = s.device()
