@@ -17,6 +17,10 @@ __device__ __forceinline__ int paged_length(const PagedView& c, int s) {
   const int n = c.length[s], cap = c.max_pages << c.lg_rows;
   return n < 0 ? 0 : (n > cap ? cap : n);
 }
+// Reports a length that was cut to `len`; one thread to a sequence.
+__device__ __forceinline__ void paged_report_length(const PagedView& c, int s, int len) {
+  if (c.status && c.length[s] != len) atomicOr(c.status, DFLASH_PAGED_BAD_ROWS);
+}
 // New rows [first, last) of sequence s, cut to [0, rows].
 __device__ __forceinline__ int2 paged_new_rows(const int* start, int s, int rows) {
   int a = start[s], b = start[s + 1];

@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
   const int2 ab = paged_new_rows(a.start, s, a.rows);
   const int len = paged_length(c, s), R = (ab.y - ab.x) * G;
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, s);
+  if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0) paged_report_length(c, s, len);
   const PagedScore ps = paged_score_of(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, e4 = lane & 3;
   for (int k0 = blockIdx.x * kBN; k0 < len; k0 += gridDim.x * kBN) {

@@ -375,6 +375,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   } else if (warp > wMma) {
     // ---- V's non-finite rows, in tiles that some query sees only in part
     const int half = warp - wMma - 1;
+    if (half == 0 && lane == 0 && h == 0 && z == 0 && t.tile == 0) paged_report_length(c, t.seq, len);
     const bool look = QT == 1 && direct;
     int rel = cur.next(), rel1 = cur.next(), page1 = -1;
     int4 pos4 = make_int4(0, 0, 0, 0);

@@ -123,6 +123,7 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   const PagedTile t = st;
   if (t.seq < 0) return;
   const int len = paged_length(c, t.seq);
+  if (threadIdx.x == 0 && h == 0 && z == 0 && t.tile == 0) paged_report_length(c, t.seq, len);
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
   PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
   const int r0 = t.tile * kBM, n_rows = min(kBM, t.count * G - r0);

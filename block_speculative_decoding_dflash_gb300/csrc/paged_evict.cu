@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_select_kernel(PagedEvictArg
   int* list = a.moves + ((size_t)s * c.nkv + h) * (1 + 2 * (size_t)a.max_moves);
   const int n = paged_length(c, s), b = a.budget;
   const long long guard = (long long)a.next_pos[s] - a.recent;
-  if (tid == 0 && h == 0 && blockIdx.x == 0 && c.status && c.length[s] != n) atomicOr(c.status, DFLASH_PAGED_BAD_ROWS);
+  if (tid == 0 && h == 0 && blockIdx.x == 0) paged_report_length(c, s, n);
   // a multiple of kThreads, so that a warp's share is whole words
   const int per = (n + ranks * kThreads - 1) / (ranks * kThreads) * kThreads;
   const int i0 = min(n, (int)cl.block_rank() * per), i1 = min(n, i0 + per), m = i1 - i0;

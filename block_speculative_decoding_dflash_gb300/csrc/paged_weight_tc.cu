@@ -290,6 +290,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
       }
     }
     if (!ok && c.status) atomicOr(c.status, DFLASH_PAGED_GAVE_UP);
+    if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0) paged_report_length(c, seq, len);
     tc_fence_before();
     __syncthreads();
     if (warp == wMma) {
@@ -484,6 +485,7 @@ paged_weight_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_cons
       paged_wait(&q_full[i], 1, landed);
     }
   }
+  if (threadIdx.x == 0 && h == 0 && blockIdx.x == 0) paged_report_length(c, seq, len);
   tc_fence_before();
   __syncthreads();
   if (warp == wMma) {

@@ -633,9 +633,9 @@ const char* ring_cache_last_error(const ring_cache* rc);
  * (append, key_weight's output, evict) need the sequences' pages to be
  * disjoint; attention does not. Positions lie in [0, 2^31).
  *
- * What only the device can see is bounded there: a length beyond the table is
- * cut to it, rows on a page id outside [0, n_pages) are neither read nor
- * written (and seen by no query), row ranges are cut to [0, rows]. */
+ * What only the device can see is bounded there: a length below 0 or beyond the
+ * table is cut to its bounds, rows on a page id outside [0, n_pages) are neither
+ * read nor written (and seen by no query), row ranges are cut to [0, rows]. */
 typedef struct dflash_paged_cache {
   void* k;                  /* [n_pages][kv_heads][page_rows][head_dim] */
   void* v;                  /* the same */
@@ -654,7 +654,8 @@ typedef struct dflash_paged_cache {
 
 /* Bits of dflash_paged_cache.status. */
 #define DFLASH_PAGED_BAD_PAGE 1 /* a page id outside [0, n_pages), of a row that the call looks up */
-#define DFLASH_PAGED_BAD_ROWS 2 /* a length beyond the table, or more new rows than length */
+#define DFLASH_PAGED_BAD_ROWS 2 /* a length below 0 or beyond the table, of a sequence that the call works
+                                   on; in an append also more new rows than length */
 #define DFLASH_PAGED_GAVE_UP 4  /* a bounded wait in a tensor-core kernel gave up */
 
 /* The new rows start[s] .. start[s + 1] - 1 of sequence s become the last rows
@@ -700,10 +701,10 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
  * exp(t) (natural log); a query that sees nothing gives out = 0 and lse =
  * -inf. What a query does not see, other sequences' queries among it, has no
  * influence on it, infinities and NaN included (the sizes of a batch have, on
- * how sums are split); infinities and NaN that it does see make what they reach infinite
- * or NaN. Softmax statistics and sums are fp32. out and lse
- * overlap no input. Rows outside [start[0], start[n_seq]) of out and lse are
- * left as they are. */
+ * how sums are split); infinities and NaN that it does see make what they reach
+ * infinite or NaN. Softmax statistics and sums are fp32. out and lse overlap no
+ * input. Rows outside [start[0], start[n_seq]) of out and lse are left as they
+ * are. */
 typedef struct dflash_paged_attention_args {
   const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */
   const int32_t* q_pos;     /* [rows] */

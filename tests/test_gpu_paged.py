@@ -461,6 +461,27 @@ def test_an_eviction_of_rows_that_no_cta_holds_reports_bad_pages(B):
     assert int(status) == B.PAGED_BAD_PAGE
 
 
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("bf16", 256), ("f32", 64)])
+@pytest.mark.parametrize("n", [4, 150])
+@pytest.mark.parametrize("length", [10 ** 6, -5])
+def test_every_call_reports_lengths_that_the_table_cannot_have(B, dtype, hd, n, length):
+    s = Setup(B, [(n, 320), (4, 60)], 8, 2, hd, 16, dtype, seed=8, spare=0)
+    cache, args = s.device(), (s.q.cuda(), s.q_pos.cuda(), s.start.cuda())
+    out, lse = torch.zeros(s.rows, 8, hd, dtype=s.dt, device="cuda"), torch.zeros(s.rows, 8, device="cuda")
+    w, p, left = torch.zeros(s.pos.shape, device="cuda"), torch.zeros_like(cache.pos), torch.zeros_like(cache.length)
+    kv = torch.zeros(s.rows, 2, hd, dtype=s.dt, device="cuda")
+    end = s.length.cuda()
+    cache.attention(*args, out, lse=lse)
+    assert int(s.status) == 0
+    cache.length[0] = length
+    for call in (lambda: cache.attention(*args, out, lse=lse), lambda: cache.key_weight(*args, lse, weight_out=w),
+                 lambda: cache.evict(50, 5, end, weight_out=w, pos_out=p, length_out=left),
+                 lambda: cache.append(s.q.cuda(), kv, kv, s.q_pos.cuda(), s.start.cuda(), out)):
+        s.status.zero_()
+        call()
+        assert int(s.status) == B.PAGED_BAD_ROWS
+
+
 def test_row_ranges_beyond_the_tensor_are_cut(B):
     s = Setup(B, [(4, 100), (4, 60)], 8, 2, 64, 16, seed=8)
     cache = s.device()
