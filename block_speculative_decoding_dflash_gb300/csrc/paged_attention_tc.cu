@@ -720,7 +720,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
               tmem_ld_wait();
               const float p = j & 1 ? bf_hi(ph) + bf_hi(pl) : bf_lo(ph) + bf_lo(pl);
               const long long row = paged_row(c, t.seq, h, slot);
-              if (row < 0 || !__any_sync(0xffffffffu, p != 0.f)) continue;
+              if (row < 0) continue;
+              // one of this row's keys, and seen by it (its weight may have left fp32)
+              const bool mine = w >= n0 && w < n1 && paged_sees(sees, c.pos[row]);
+              if (!__any_sync(0xffffffffu, mine)) continue;
               const bf16* vrow = static_cast<const bf16*>(c.v) + row * c.hd;
               for (int d = 0; d < HDP; d += 16) {
                 float o[16];
@@ -729,7 +732,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                   const float v = d + x < c.hd ? to_f(vrow[d + x]) : 0.f;
-                  if (p != 0.f) o[x] = fmaf(p, v, o[x]);
+                  if (mine) o[x] = fmaf(p, v, o[x]);
                 }
                 tmem_st16(o_at + d, o);
               }

@@ -292,6 +292,23 @@ def test_hidden_rows_may_hold_anything(B, dtype, hd, nq, n, bad):
     s.check_attention(cache)
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 128, 8), ("bf16", 136, 4)])
+@pytest.mark.parametrize("n", [6, 30, 200])
+def test_infinite_values_of_rows_with_no_weight_left_are_seen(B, dtype, hd, nq, n, bad):
+    """A row far away whose weight leaves fp32 (e^-150 and less) is seen all the same: what is infinite or NaN in its V
+    makes the outputs so, in a tile that is seen wholly and in one with a hidden row."""
+    s = Setup(B, [(n, 400)], nq, 2, hd, 16, dtype, seed=6)
+    at = lambda r: (int(s.table[0, r // 16]), slice(None), r % 16)  # noqa: E731
+    for hidden in (False, True):
+        s.v[at(40)][:, ::3] = bad
+        if hidden:
+            s.pos[at(41)] = 1 << 20                         # later than every query
+            s.v[at(41)] = math.nan
+        cache = s.device()
+        s.check_attention(cache, slopes=torch.full((nq,), 1.0))
+
+
 @pytest.mark.parametrize("mask", [dict(), dict(softcap=20.0), dict(softcap=20.0, slopes=True), dict(window=50)], ids=lambda m: "-".join(m) or "plain")
 @pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 128, 4), ("bf16", 200, 4)])
 @pytest.mark.parametrize("n", [3, 70, 200])
