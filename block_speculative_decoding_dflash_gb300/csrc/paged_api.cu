@@ -41,6 +41,14 @@ int need(const void* p, const char* name) {
   return DFLASH_OK;
 }
 int may(const void* p, const char* name) { return p ? need(p, name) : DFLASH_OK; }
+// An array that is read or written an element of four bytes at a time: a slice
+// of a larger one may start anywhere.
+int need4(const void* p, const char* name) {
+  if (!p) return refuse(DFLASH_EINVAL, "paged: %s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 3u) return refuse(DFLASH_EINVAL, "paged: %s is not 4-byte aligned", name);
+  return DFLASH_OK;
+}
+int may4(const void* p, const char* name) { return p ? need4(p, name) : DFLASH_OK; }
 
 #define PG(call)          \
   do {                    \
@@ -66,10 +74,9 @@ int check_cache(const dflash_paged_cache* c, PagedView* v) {
   PG(need(c->k, "cache.k"));
   PG(need(c->v, "cache.v"));
   PG(need(c->pos, "cache.pos"));
-  PG(need(c->table, "cache.table"));
-  PG(need(c->length, "cache.length"));
-  if (c->status && (reinterpret_cast<uintptr_t>(c->status) & 3u))
-    return refuse(DFLASH_EINVAL, "paged: cache.status is not 4-byte aligned");
+  PG(need4(c->table, "cache.table"));
+  PG(need4(c->length, "cache.length"));
+  PG(may4(c->status, "cache.status"));
   v->k = c->k; v->v = c->v; v->pos = c->pos; v->table = c->table; v->length = c->length; v->status = c->status;
   v->n_pages = c->n_pages;
   v->lg_rows = 0;
@@ -99,14 +106,14 @@ int check_attention(const dflash_paged_cache* c, const dflash_paged_attention_ar
   if (a->rows > 0) {
     PG(check_stride(a->q_stride, (int64_t)a->n_q_heads * c->head_dim, "q_stride"));
     PG(need(a->q, "q"));
-    PG(need(a->q_pos, "q_pos"));
+    PG(need4(a->q_pos, "q_pos"));
     if (!weights) PG(need(a->out, "out"));
-    if (weights) PG(need(a->lse, "lse"));
+    if (weights) PG(need4(a->lse, "lse"));
   }
-  PG(need(a->start, "start"));
-  PG(may(a->slopes, "slopes"));
-  PG(may(a->prefix, "prefix"));
-  PG(may(a->lse, "lse"));
+  PG(need4(a->start, "start"));
+  PG(may4(a->slopes, "slopes"));
+  PG(may4(a->prefix, "prefix"));
+  PG(may4(a->lse, "lse"));
   // (within these no product or quotient of the two leaves fp32)
   if (!(a->scale > 0.f && a->scale <= 1e18f)) return refuse(DFLASH_EINVAL, "paged attention: scale must be positive and at most 1e18");
   if (a->softcap != 0.f && !(a->softcap >= 1e-18f && a->softcap <= 1e18f))
@@ -158,7 +165,7 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
   for (int i = 0; i < a->rot_pairs; ++i)
     if (a->pair_axis_host[i] >= a->n_axes)
       return refuse(DFLASH_ERANGE, "paged append: pair_axis_host[%d] is not below n_axes", i);
-  PG(need(a->start, "start"));
+  PG(need4(a->start, "start"));
   PG(may(a->weight, "weight"));
   PG(may(a->q_norm, "q_norm"));
   PG(may(a->k_norm, "k_norm"));
@@ -169,8 +176,8 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
   PG(need(a->q, "q"));
   PG(need(a->k, "k"));
   PG(need(a->v, "v"));
-  PG(need(a->row_pos, "row_pos"));
-  if (a->rot_pairs > 0) PG(need(a->rope_pos, "rope_pos"));
+  PG(need4(a->row_pos, "row_pos"));
+  if (a->rot_pairs > 0) PG(need4(a->rope_pos, "rope_pos"));
   PG(need(a->q_out, "q_out"));
   if (a->q_out == a->q && a->q_stride != (int64_t)a->n_q_heads * hd)
     return refuse(DFLASH_EINVAL, "paged append: q_out may be q only when q is dense");
@@ -241,10 +248,10 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict
   PagedEvictArgs x;
   PG(check_evict(cache, a, &x));
   PG(need(a->weight, "weight"));
-  PG(need(a->next_pos, "next_pos"));
+  PG(need4(a->next_pos, "next_pos"));
   PG(need(a->weight_out, "weight_out"));
   PG(need(a->pos_out, "pos_out"));
-  PG(need(a->length_out, "length_out"));
+  PG(need4(a->length_out, "length_out"));
   PG(need(a->workspace, "workspace"));
   const int64_t bytes = evict_bytes(cache, a->budget);
   if (a->workspace_bytes < bytes)

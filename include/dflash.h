@@ -625,9 +625,12 @@ const char* ring_cache_last_error(const ring_cache* rc);
  * of sequence s is row r % page_rows of page table[s][r / page_rows]. A cached
  * row has a position for the masks and the distance bias, kept per kv head
  * because an eviction keeps other rows in each head; the order of a sequence's
- * rows says nothing. All arrays are the caller's, on the device, 16-byte
- * aligned; the calls below allocate nothing, keep nothing, never synchronize
- * and may be captured. `length` counts the rows of each sequence with the
+ * rows says nothing. All arrays are the caller's, on the device; K, V, pos,
+ * weights, q, k, v, gains, outputs of their types and workspaces are 16-byte
+ * aligned, the others (table, length, status, start, q_pos, row_pos, rope_pos,
+ * next_pos, length_out, slopes, prefix, lse) 4-byte aligned: a slice of a larger
+ * array will do. The calls below allocate nothing, keep nothing, never
+ * synchronize and may be captured. `length` counts the rows of each sequence with the
  * call's new ones included: an engine raises it (and fills the table) before
  * the append, and lowers it to trim rejected rows. Calls that write rows
  * (append, key_weight's output, evict) need the sequences' pages to be

@@ -540,6 +540,34 @@ def test_no_rows(B):
     cache.append(s.q.cuda(), empty, empty, s.q_pos.cuda(), s.start.cuda(), s.q.cuda())
 
 
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("f32", 64)])
+def test_index_arrays_may_start_at_any_element(B, dtype, hd):
+    """Slices of an engine's step buffers: everything that is read an element at a time."""
+    s = Setup(B, [(9, 300), (3, 50), (1, 7)], 8, 2, hd, 16, dtype, seed=15)
+    g = torch.Generator().manual_seed(1)
+    new = [torch.randn(13, h, hd, generator=g).to(s.dt).cuda() for h in (8, 2, 2)]
+    results = []
+    for off in (0, 1, 2, 3):
+        def put(t):
+            flat = torch.zeros(t.numel() + off, dtype=t.dtype, device="cuda")
+            flat[off:] = t.flatten().cuda()
+            return flat[off:].view(t.shape)
+        s.status = put(torch.zeros(1, dtype=torch.int32))
+        c = B.PagedCache(s.k.cuda(), s.v.cuda(), s.pos.cuda(), put(s.table), put(s.length), weight=s.weight.cuda(), status=s.status)
+        start, q_pos = put(s.start), put(s.q_pos)
+        q, out, lse = torch.zeros_like(new[0]), torch.zeros_like(new[0]), put(torch.zeros(13, 8))
+        c.append(*new, q_pos, start, q, rope_pos=put(torch.stack([s.q_pos, s.q_pos // 3])), pair_axis=bytes([0, 1] * (hd // 4)))
+        mask = dict(slopes=put(torch.linspace(0, 0.1, 8)), prefix=put(torch.tensor([3, 0, 1], dtype=torch.int32)), window=100)
+        c.attention(q, q_pos, start, out, lse=lse, **mask)
+        c.key_weight(q, q_pos, start, lse, **mask)
+        left = put(torch.zeros(3, dtype=torch.int32))
+        c.evict(40, 5, put(s.length), length_out=left)
+        assert int(s.status) == 0
+        results.append([t.clone() for t in (c.k, c.v, c.pos, c.weight, q, out, lse, left)])
+    for r in results[1:]:
+        assert all(torch.equal(torch.nan_to_num(x.float(), 55.0), torch.nan_to_num(y.float(), 55.0)) for x, y in zip(r, results[0]))
+
+
 @pytest.mark.parametrize("window", [0, 60])
 def test_the_same_call_gives_the_same_bits(B, window):
     s = Setup(B, [(40, 900), (1, 500)], 8, 2, 128, 16, seed=12)

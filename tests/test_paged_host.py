@@ -236,3 +236,42 @@ def test_c_calls_refuse_null(B):
     assert B.lib.dflash_paged_attention_workspace(None, None, ctypes.byref(n)) == B.EINVAL
     assert B.lib.dflash_paged_evict_workspace(None, None, None) == B.EINVAL
     assert B.last_error() != ""
+
+
+def test_misaligned_arrays_are_refused(B):
+    """Addresses within an element, and of arrays read 16 bytes at a time within those (nothing is launched: the checks come first)."""
+    k = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    rows = torch.zeros(4, 2, 16)
+    at = {n: k.data_ptr() if n in ("k", "v", "q", "out") else rows.data_ptr() for n in
+          ("k", "v", "pos", "table", "length", "status", "q", "q_pos", "start", "slopes", "prefix", "out", "lse", "workspace", "next_pos", "weight", "pos_out", "length_out")}
+
+    def cache(**a):
+        a = {**at, **a}
+        return B._PAGED_CACHE.pack(*(a[n] for n in ("k", "v", "pos", "table", "length", "status")), 4, 16, 2, 64, 1, 1, B.BF16)
+
+    def attention(**a):
+        a = {**at, **a}
+        args = B._PAGED_ATTENTION.pack(*(a[n] for n in ("q", "q_pos", "start", "slopes", "prefix", "out", "lse")), 256, 1, 4, 1, 0, 0, 0.1, 0.0, 0)
+        return B.lib.dflash_paged_attention_workspace(cache(), args + B._NO_WORKSPACE, ctypes.byref(ctypes.c_int64()))
+
+    def evict(**a):
+        a = {**at, **a}
+        args = B._PAGED_EVICT.pack(*(a[n] for n in ("weight", "next_pos", "weight", "pos_out", "length_out")), 4, 0)
+        return B.lib.dflash_paged_evict(cache(), args + B._PAGED_WORKSPACE.pack(at["workspace"], 0), None)
+
+    def workspace_of(**a):
+        return B.lib.dflash_paged_attention_workspace(cache(**a), B._PAGED_ATTENTION.pack(*(at[n] for n in ("q", "q_pos", "start", "slopes", "prefix", "out", "lse")),
+                                                                                         256, 1, 4, 1, 0, 0, 0.1, 0.0, 0) + B._NO_WORKSPACE, ctypes.byref(ctypes.c_int64()))
+
+    assert attention() == 0 and workspace_of() == 0
+    for call, names, wide in ((workspace_of, ("table", "length", "status"), ("k", "v", "pos")), (attention, ("q_pos", "start", "slopes", "prefix", "lse"), ("q", "out")),
+                              (evict, ("next_pos", "length_out"), ("weight", "pos_out"))):
+        for n in names:
+            for off in (1, 2):
+                assert call(**{n: at[n] + off}) == B.EINVAL and f"{n} is not 4-byte aligned" in B.last_error().replace("cache.", "")
+            if call is not evict:                        # (whose workspace is too small here: nothing runs)
+                assert call(**{n: at[n] + 4}) == 0
+            else:
+                assert call(**{n: at[n] + 4}) == B.EINVAL and "workspace" in B.last_error()
+        for n in wide:
+            assert call(**{n: at[n] + 8}) == B.EINVAL and "16-byte aligned" in B.last_error()
