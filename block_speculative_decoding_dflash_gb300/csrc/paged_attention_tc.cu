@@ -476,10 +476,10 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     }
     // The two-tile kernel's few rows have a loop of their own: their branch within
     // that of all others costs a prompt 3% (2048 rows over 32768 keys: 820 us, with
-    // it 843 us). With a cap or bias it costs nothing, and a second loop 4%.
+    // it 843 us; under a cap of 20: 1465 us, with it 1648 us).
 #pragma unroll
-    for (int alone = 0; alone < (QT == 2 && !EXTRA ? 2 : 1); ++alone) {
-      const bool two = QT == 2 && !EXTRA ? alone == 1 : two_parts;
+    for (int alone = 0; alone < (QT == 2 ? 2 : 1); ++alone) {
+      const bool two = QT == 2 ? alone == 1 : two_parts;
       if (two != two_parts) continue;
       for (int i = 0; i < N; ++i) {
         const int buf = QT == 2 ? q : (i & 1);
@@ -631,7 +631,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         };
         // what a stored pair leaves of them
         auto rest = [&](uint32_t hi, float p0, float p1) { return __uint_as_float(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi))); };
-        if (QT == 2 && (two || (EXTRA && late))) {
+        if (QT == 2 && two) {
 #pragma unroll 1
           for (int n = 0; n < 4; ++n) {
             float w[16], lo[16];
@@ -647,7 +647,22 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
               add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
             }
             tmem_st16(s_at + n * 16, w);
-            if (two) tmem_st16(s_at + low + n * 16, lo);
+            tmem_st16(s_at + low + n * 16, lo);
+          }
+        } else if (QT == 2 && EXTRA && late) {
+#pragma unroll 1
+          for (int n = 0; n < 4; ++n) {
+            float w[16];
+            tmem_ld32(s_at + n * 32, x[0]);
+            tmem_ld_wait32(x[0]);
+            cap_tanh32(x[0], cap, false, []() {});
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              float p0, p1;
+              w[j >> 1] = __uint_as_float(weigh(x[0] + j, p0, p1));
+              add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
+            }
+            tmem_st16(s_at + n * 16, w);
           }
         } else if (QT == 2) {
           tmem_ld32(s_at, x[0]);

@@ -382,6 +382,22 @@ def test_few_rows_beside_a_prompt_are_as_exact_as_alone(B, nq, hd, prompt):
     assert (np.abs(host(lse)[few] - want_lse) <= dt + 2.0 ** -20 + 4 * EPS * np.abs(want_lse)).all()
 
 
+@pytest.mark.parametrize("mask", [dict(softcap=2.0), dict(softcap=30.0, slopes=True), dict(window=7, softcap=4.0), dict(slopes=True)], ids=lambda m: "-".join(m))
+@pytest.mark.parametrize("nq,hd", [(8, 128), (6, 64)])
+def test_few_rows_beside_a_prompt_under_caps_and_biases(B, nq, hd, mask):
+    """The same with scores that are changed before they are weighed, in tiles that are seen wholly (a cap alone) and in part."""
+    s = Setup(B, [(300, 320), (1, 129), (1, 300), (2, 260), (3, 11)], nq, 2, hd, 16, seed=13, scale=0.3)
+    s.v = torch.where(torch.isnan(s.v), s.v, torch.where(s.v > 0, 1.0, -1.0).to(s.dt))
+    m = mask_of(mask, nq, 5)
+    cache = s.device()
+    out, _ = s.check_attention(cache, **m)
+    opts = {k: v.numpy().astype(np.float64) if torch.is_tensor(v) else v for k, v in m.items()}
+    want, _, mag = (x[300:] for x in P.attention(s.oracle(), host(s.q), s.q_pos.numpy(), s.start.numpy(), s.scale, **opts))
+    dt = s.score_error(m.get("softcap", 0.0), None if m.get("slopes") is None else m["slopes"].numpy())
+    off = np.abs(host(out)[300:] - want) / (unit("bf16") * np.abs(want) + (2 * (dt + 2.0 ** -20) + 300 * EPS + 2.0 ** -16) * mag)
+    assert off.max() <= 1.0, f"off by {off.max():.3g} of the tolerance"
+
+
 @pytest.mark.parametrize("dtype,hd,nq", [("bf16", 128, 8), ("bf16", 64, 6), ("f32", 128, 4), ("bf16", 200, 4)])
 @pytest.mark.parametrize("n", [200, 270])
 def test_rows_behind_the_length_leave_every_bit_of_key_weights(B, dtype, hd, nq, n):
