@@ -593,13 +593,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         const float sc = change || late ? 1.f : scale2;
         top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
         if (change) tmem_st_wait();
-        // (every row by its own maximum: other rows' only decide whether the warp
-        // comes here, where theirs are multiplied by 1)
-        const bool up = top > mx + kLazy;
-        if (__any_sync(0xffffffffu, up)) {
-          const float f = up ? ex2(mx - top) : 1.f;
+        // (rows of the next sequence, which a load brings along, have no say in it)
+        if (!valid) top = -INFINITY;
+        if (__any_sync(0xffffffffu, top > mx + kLazy)) {
+          const float mn = fmaxf(mx, top);
+          const float f = mn == -INFINITY ? 1.f : ex2(mx - mn);
           sum *= f;
-          if (up) mx = top;
+          mx = mn;
           if (i > 0) {
             // O holds the tiles before this one: their P V is done (with two
             // query tiles because S of this tile was issued after it)
