@@ -80,7 +80,9 @@ struct TcShape {
 };
 
 // EXTRA: a cap or a distance bias (their code would cost the others registers).
-template <int HDP, int QT, bool EXTRA>
+// MANY: with two query tiles, a batch of several sequences, some of few rows
+// perhaps (their code costs a call of 300 rows over 2000 keys 1 us of 26).
+template <int HDP, int QT, bool EXTRA, bool MANY>
 __global__ void __launch_bounds__(QT * 128 + 128, 1)
 paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mq32,
                      const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
@@ -190,7 +192,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
   const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
   const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
-  const bool two_parts = QT == 2 ? nt == 1 && n_tok <= 2 * t32 : rep > 1;   // of P, the second `low` columns on
+  const bool two_parts = QT == 2 ? MANY && nt == 1 && n_tok <= 2 * t32 : rep > 1;   // of P, the second `low` columns on
   constexpr int low = QT == 2 ? 128 : 64;
 
   // The page of a lane's four keys of a tile (-1: none) and their positions; a
@@ -310,7 +312,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
       paged_wait(&q_full, 0, ok);
       wait_k(0);
       qk(0, 0, 0, QT == 1 || nt == 1);
-      if (QT == 2 && two_parts) {
+      if (QT == 2 && MANY && two_parts) {
         for (int i = 0; i < N; ++i) {
           wait_v(i);
           paged_wait(&p_ready[0], i & 1, ok);
@@ -318,15 +320,16 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           tc_fence_after();
           const int s = (2 * i + 1) % NS;
           pv(0, 0, i, false);
-          if (leader) {
-            low_pv(0, v_desc + s * (C::kTileB >> 4));
-            tc_commit(&kv_empty[s]);
-          }
-          __syncwarp();
           if (i + 1 < N) {
             wait_k(i + 1);
             qk(0, 0, i + 1, true);
           }
+          if (leader) {                                  // beside the next tile's softmax
+            low_pv(0, v_desc + s * (C::kTileB >> 4));
+            tc_commit(&o_done);
+            tc_commit(&kv_empty[s]);
+          }
+          __syncwarp();
         }
       } else if (QT == 2) {
         if (nt == 2) qk(1, 1, 0, true);
@@ -478,8 +481,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     // that of all others costs a prompt 3% (2048 rows over 32768 keys: 820 us, with
     // it 843 us; under a cap of 20: 1465 us, with it 1648 us).
 #pragma unroll
-    for (int alone = 0; alone < (QT == 2 ? 2 : 1); ++alone) {
-      const bool two = QT == 2 ? alone == 1 : two_parts;
+    for (int few = 0; few < (QT == 2 && MANY ? 2 : 1); ++few) {
+      const bool two = QT == 2 ? few == 1 : two_parts;
       if (two != two_parts) continue;
       for (int i = 0; i < N; ++i) {
         const int buf = QT == 2 ? q : (i & 1);
@@ -593,6 +596,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         const float sc = change || late ? 1.f : scale2;
         top = EXTRA && late ? cap_tanh1(top, cap) : top * sc;
         if (change) tmem_st_wait();
+        if (QT == 2 && two && i > 0) {
+          // O and the second part of P are still in use by the last tile's product
+          paged_wait(&o_done, (i - 1) & 1, ok);
+          tc_fence_after();
+        }
         // (rows of the next sequence, which a load brings along, have no say in it)
         if (!valid) top = -INFINITY;
         if (__any_sync(0xffffffffu, top > mx + kLazy)) {
@@ -631,38 +639,23 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         };
         // what a stored pair leaves of them
         auto rest = [&](uint32_t hi, float p0, float p1) { return __uint_as_float(pack_bf16(p0 - bf_lo(hi), p1 - bf_hi(hi))); };
-        if (QT == 2 && two) {
+        if (QT == 2 && EXTRA && late) {
 #pragma unroll 1
           for (int n = 0; n < 4; ++n) {
             float w[16], lo[16];
-            tmem_ld32(s_at + n * 32, x[0]);
-            tmem_ld_wait32(x[0]);
-            if (EXTRA && late) cap_tanh32(x[0], cap, false, []() {});
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              float p0, p1;
-              const uint32_t hi = weigh(x[0] + j, p0, p1);
-              w[j >> 1] = __uint_as_float(hi);
-              lo[j >> 1] = rest(hi, p0, p1);
-              add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
-            }
-            tmem_st16(s_at + n * 16, w);
-            tmem_st16(s_at + low + n * 16, lo);
-          }
-        } else if (QT == 2 && EXTRA && late) {
-#pragma unroll 1
-          for (int n = 0; n < 4; ++n) {
-            float w[16];
             tmem_ld32(s_at + n * 32, x[0]);
             tmem_ld_wait32(x[0]);
             cap_tanh32(x[0], cap, false, []() {});
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               float p0, p1;
-              w[j >> 1] = __uint_as_float(weigh(x[0] + j, p0, p1));
+              const uint32_t hi = weigh(x[0] + j, p0, p1);
+              w[j >> 1] = __uint_as_float(hi);
+              if (two) lo[j >> 1] = rest(hi, p0, p1);
               add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
             }
             tmem_st16(s_at + n * 16, w);
+            if (two) tmem_st16(s_at + low + n * 16, lo);
           }
         } else if (QT == 2) {
           tmem_ld32(s_at, x[0]);
@@ -671,14 +664,17 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
             float* v = x[n & 1];
             tmem_ld_wait32(v);
             if (n < 3) tmem_ld32(s_at + (n + 1) * 32, x[(n + 1) & 1]);
-            float w[16];
+            float w[16], lo[16];
 #pragma unroll
             for (int j = 0; j < 32; j += 2) {
               float p0, p1;
-              w[j >> 1] = __uint_as_float(weigh(v + j, p0, p1));
+              const uint32_t hi = weigh(v + j, p0, p1);
+              w[j >> 1] = __uint_as_float(hi);
+              if (two) lo[j >> 1] = rest(hi, p0, p1);
               add[(j >> 1) & 1] = add2(add[(j >> 1) & 1], pack2(p0, p1));
             }
             tmem_st16(s_at + n * 16, w);                   // columns whose scores have been read
+            if (two) tmem_st16(s_at + low + n * 16, lo);
           }
         } else {
           // P's first part goes into columns 0 .. 63, its second into 64 .. 127; in
@@ -884,7 +880,8 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
     return cudaErrorInvalidValue;
   using C = TcShape<HDP, QT>;
   const bool extra = a.softcap > 0.f || a.slopes;
-  auto kernel = extra ? paged_attn_tc_kernel<HDP, QT, true> : paged_attn_tc_kernel<HDP, QT, false>;
+  auto kernel = extra ? paged_attn_tc_kernel<HDP, QT, true, false> : paged_attn_tc_kernel<HDP, QT, false, false>;
+  if (QT == 2 && a.c.n_seq > 1) kernel = extra ? paged_attn_tc_kernel<HDP, QT, true, QT == 2> : paged_attn_tc_kernel<HDP, QT, false, QT == 2>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};

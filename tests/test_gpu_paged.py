@@ -984,6 +984,60 @@ def test_a_loaded_gpu(B, n, lens, nq, nkv, hd, dtype):
     assert (per - n * (nq // nkv)).abs().max() <= n * (nq // nkv) * 2 * (s.score_error(0.0, None) + 2.0 ** -18)
 
 
+def capped64(s, cache, softcap=0.0):
+    """dense64 with scores under a cap: its cache's k scaled into t, capped, one sequence and kv head after the other."""
+    if not softcap:
+        return dense64(s, cache)
+    out, G, ps = torch.zeros(s.rows, s.nq, s.hd, dtype=torch.float64, device="cuda"), s.nq // s.nkv, cache.k.shape[2]
+    mag, lse = torch.zeros_like(out), torch.zeros(s.rows, s.nq, dtype=torch.float64, device="cuda")
+    for i in range(len(s.length)):
+        a, b, n = int(s.start[i]), int(s.start[i + 1]), int(s.length[i])
+        pages = cache.table[i, :-(-n // ps)].long()
+        for h in range(s.nkv if b > a else 0):
+            k, v, pos = (t[pages, h].flatten(0, 1)[:n] for t in (cache.k, cache.v, cache.pos))
+            heads = slice(h * G, (h + 1) * G)
+            t = softcap * torch.tanh(torch.einsum("ngd,ld->ngl", cache.q64[a:b, heads], k.double()) * s.scale / softcap)
+            t = t.masked_fill((pos[None] > s.q_pos[a:b].cuda()[:, None])[:, None], -math.inf)
+            p = t.softmax(-1)
+            lse[a:b, heads], out[a:b, heads], mag[a:b, heads] = t.logsumexp(-1), p @ v.double(), p @ v.double().abs()
+    return host(out), host(lse), host(mag)
+
+
+@pytest.mark.parametrize("mask", [dict(), dict(softcap=30.0)], ids=lambda m: "-".join(m) or "plain")
+@pytest.mark.parametrize("spare,max_len", [(0, 0), (400, 0), (400, 9000)])
+def test_prompt_chunks_with_decode_rows_in_long_tables(B, spare, max_len, mask):
+    """Chunks, verify blocks and single tokens of long sequences in one call, many times in a row, in tables that are far longer
+    than any of them."""
+    lens = [(700, 6000), (1, 9000), (16, 5000), (130, 130), (1, 1), (0, 700)] + [(1, 8500 - 200 * i) for i in range(30)]
+    nq, nkv, hd, ps = 16, 4, 128, 64
+    g = torch.Generator(device="cuda").manual_seed(3)
+    s = Setup.__new__(Setup)
+    s.B, s.dtype, s.hd, s.nq, s.nkv, s.scale, s.dt = B, "bf16", hd, nq, nkv, hd ** -0.5, torch.bfloat16
+    S, held = len(lens), -(-max(n for _, n in lens) // ps)
+    s.length = torch.tensor([n for _, n in lens], dtype=torch.int32)
+    s.start = torch.tensor([0] + [n for n, _ in lens], dtype=torch.int32).cumsum(0).to(torch.int32)
+    s.rows = int(s.start[-1])
+    s.q_pos = torch.cat([torch.arange(n - k, n) for k, n in lens]).to(torch.int32)
+    normal = lambda *shape: torch.randn(shape, generator=g, device="cuda").to(s.dt)  # noqa: E731
+    s.k, s.v, s.q = normal(S * held, nkv, ps, hd), normal(S * held, nkv, ps, hd), normal(s.rows, nq, hd)
+    pages = torch.randperm(S * held, generator=torch.Generator().manual_seed(1)).reshape(S, held).to(torch.int32)
+    s.table = torch.cat([pages, torch.full((S, spare), -1, dtype=torch.int32)], 1).contiguous()
+    s.pos = torch.zeros(S * held, nkv, ps, dtype=torch.int32)
+    s.pos[pages.long()] = torch.arange(held * ps, dtype=torch.int32).reshape(1, held, 1, ps).expand(S, held, nkv, ps)
+    s.weight = torch.zeros(S * held, nkv, ps)
+    cache = s.device()
+    cache.q64 = s.q.double()
+    outs = []
+    for _ in range(10):
+        out, lse = torch.full((s.rows, nq, hd), 77.0, dtype=s.dt, device="cuda"), torch.full((s.rows, nq), 77.0, device="cuda")
+        cache.attention(s.q, s.q_pos.cuda(), s.start.cuda(), out, lse=lse, max_len=max_len, **mask)
+        outs.append((out, lse))
+    torch.cuda.synchronize()
+    assert int(s.status) == 0 and all(torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1]) for o in outs)
+    want, want_lse, mag = capped64(s, cache, **mask)
+    s.compare(host(outs[0][0]), host(outs[0][1]), want, want_lse, mag, mask.get("softcap", 0.0), None)
+
+
 def test_offsets_beyond_32_bits(B):
     """A pool of more than 2^31 elements (5 GB): rows in its last pages."""
     pages, nkv, ps, hd = 1100, 8, 1024, 256
