@@ -87,16 +87,17 @@ __device__ __forceinline__ Raw8<float> round8(const float* v, float) {
 // 32 / (hd / 8) heads are worked on side by side. With r the head's 1 / rms,
 // a value becomes r (v A + w B): w the pair's other half, in the same lane
 // (adjacent pairs) or one shuffle away, A and B the gains times cos and sin,
-// which a lane holds for its dimensions. A lane whose dimensions are not rotated
-// takes w = +0 and B = -0, which leaves v A as it is to the sign of a zero,
-// whatever its neighbours hold. kU heads are requested before the
-// first is used, and the next ones as soon as one is in its registers. Bound by
-// the bytes of the rows, read once and written once, for thousands of rows; by
-// its chain of dependent loads for a few.
+// which a lane holds for its dimensions. kU heads are requested before the first
+// is used, and the next ones as soon as one is in its registers. PART: only a part
+// of the dimensions is rotated; the other lanes take w = +0 and B = -0, which
+// leaves v A as it is to the sign of a zero, whatever its neighbours hold (in
+// every lane's code this costs 4096 rows of heads of 96 dimensions 1 us of 33).
+// Bound by the bytes of the rows, read once and written once, for thousands of
+// rows; by its chain of dependent loads for a few.
 // Needs pairs to fill whole lanes: a multiple of 8 (NEOX) or 4. LPR: hd / 8
 // where it is 8 or 16 (head_dim 64 and 128), else 0.
 constexpr int kU = 2;
-template <typename T, int LPR, bool NEOX>
+template <typename T, int LPR, bool NEOX, bool PART>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_append_kernel(const __grid_constant__ PagedAppendArgs a, int per_warp, int splits) {
   pdl_enter();
   const PagedView& c = a.c;
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
   } else if (d0 < 2 * a.pairs) {
     pair = d0 >> 1;
   }
-  const uint32_t turns = pair >= 0 ? ~0u : 0u;            // keeps or clears the pairs' other halves
+  const uint32_t turns = !PART || pair >= 0 ? ~0u : 0u;   // keeps or clears the pairs' other halves
   Raw8<T> g_own, g_oth;                                   // the gains, requested before they are needed
   auto get_gain = [&](const void* g) {
     if (g && in) {
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 ? 6 : 5) paged_app
         b0 *= NEOX ? g_oth.at(j) : g_own.at(j + 1);
         b1 *= NEOX ? g_oth.at(j + 1) : g_own.at(j);
       }
-      if (pair < 0) b0 = b1 = -0.f;
+      if (PART && pair < 0) b0 = b1 = -0.f;
       A[j >> 1] = pack2(t0.x, t1.x);
       B[j >> 1] = pack2(b0, b1);
     }
@@ -326,8 +327,9 @@ __global__ void __launch_bounds__(kWarps * 32) paged_append_any_kernel(const __g
 
 template <typename T, int LPR>
 cudaError_t run_whole(const PagedAppendArgs& a, unsigned grid, int per_warp, int splits, cudaStream_t st) {
-  return a.neox ? launch_pdl(paged_append_kernel<T, LPR, true>, dim3(grid), dim3(kWarps * 32), 0, st, a, per_warp, splits)
-                : launch_pdl(paged_append_kernel<T, LPR, false>, dim3(grid), dim3(kWarps * 32), 0, st, a, per_warp, splits);
+  auto kernel = a.neox ? paged_append_kernel<T, LPR, true, false> : paged_append_kernel<T, LPR, false, false>;
+  if (2 * a.pairs < a.c.hd) kernel = a.neox ? paged_append_kernel<T, LPR, true, true> : paged_append_kernel<T, LPR, false, true>;
+  return launch_pdl(kernel, dim3(grid), dim3(kWarps * 32), 0, st, a, per_warp, splits);
 }
 
 template <typename T>
