@@ -40,11 +40,13 @@
 // look for such rows of V and zero them in shared memory, and the queries that
 // do see them add p v themselves.
 //
-// 2048 rows over 32768 keys: 0.81 ms, 1.32 PFLOP/s, bound by the softmax (one
-// exponential and about ten other operations a score) beside the products; 48
-// sequences that decode one token, up to 12345 keys: 264 us, 5.1 TB/s; a block of 4
-// in a window of 2048: 14 us, of which the first loads' chain (ranges, length,
-// page, rows) and the join are most.
+// 2048 rows over 32768 keys: 0.81 to 0.83 ms, 1.29 to 1.32 PFLOP/s; no pipe is full
+// (tensor 58%, issue 36%, special functions 30%): what is left are the waves (256
+// CTAs on 152 SMs) and each score's chain of dependent steps, a TMEM read, the
+// maximum, a second read, the exponential and a write, which two query tiles take in
+// turns. 48 sequences that decode one token, up to 12345 keys: 264 us, 5.1 TB/s; a
+// block of 4 in a window of 2048: 14 us, of which the first loads' chain (ranges,
+// length, page, rows) and the join are most.
 #include <cooperative_groups.h>
 #include <math.h>
 
@@ -192,7 +194,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
   const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
   const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
-  const bool two_parts = QT == 2 ? MANY && nt == 1 && n_tok <= 2 * t32 : rep > 1;   // of P, the second `low` columns on
+  // P in two parts, the second `low` columns on
+  const bool two_parts = QT == 2 ? MANY && nt == 1 && n_tok <= 2 * t32 : rep > 1;
   constexpr int low = QT == 2 ? 128 : 64;
 
   // The page of a lane's four keys of a tile (-1: none) and their positions; a

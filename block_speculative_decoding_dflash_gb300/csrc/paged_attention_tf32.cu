@@ -25,8 +25,8 @@
 // on the SM fills the rest. (With cp.async, 16 to a thread and tile, half of a
 // tile's time went into their instructions: 61 us.) Those blocks take 56 us, 2.3
 // TB/s, 64 such sequences 384 us, 2.8 TB/s: nothing waits for memory any more; the
-// time goes into taking values apart and into the products' latency (a warp
-// issues every fifth cycle; tensor pipe 31%, integer pipe 31%).
+// time goes into taking values apart and into the products' latency (no pipe is
+// full: issue 36%, tensor 31%, integer 31%; a warp waits for its own last step).
 #include <math.h>
 
 #include "paged_tc.cuh"

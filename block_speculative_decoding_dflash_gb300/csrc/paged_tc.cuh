@@ -170,9 +170,9 @@ __device__ __forceinline__ float cap_tanh(float x, float cap2) {
 // of it in fp32), with scale and cap2 in its coefficients: six packed
 // instructions to two values, where the exponential and the reciprocal would
 // bound capped attention (512 rows' key weights over 32768 keys, cap 20: 335 us
-// with it, 459 us without; 364 us since hidden scores have no say in the choice). Where some value of the warp is larger, all take the
-// exponential, whose error of a few 2^-24 of the cap is nothing beside scores of
-// half of it; under a cap so vast that it could be (cap2 > 1024) each value takes
+// with it, 459 us without; 365 us since hidden scores have no say in the choice).
+// Where some value of the warp is larger, all take the exponential, whose error of
+// a few 2^-24 of the cap is nothing beside scores of half of it; under a cap so vast that it could be (cap2 > 1024) each value takes
 // its own. (Each its own under every cap: 2048 rows over 32768 keys under a cap
 // of 2 took 3.40 ms instead of 1.98 ms.) limit: the largest |v| for the
 // polynomial, none where a power of the scale would leave fp32.

@@ -23,7 +23,8 @@ __device__ __forceinline__ void cut2(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
-// Of Q's and P's: hi rounded, so that lo has a bit less to hold. -0 is (-0, 0).
+// Of Q's and P's: hi rounded, so that lo has a bit less to hold. -0 is (-0, 0). (A
+// value within 2^-12 of the largest finite one becomes infinite; P is at most 1.)
 __device__ __forceinline__ void round2(float x, uint32_t& hi, uint32_t& lo) {
   hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));

@@ -6,9 +6,10 @@
 // for the whole pass and adds up its row of S^T in registers: no exchange
 // between threads, no atomics, and a fixed order. S has two buffers; the
 // exponentials of one run while the next is computed, and a second CTA on the SM
-// works while this one starts or ends. Bounded by the exponentials, one ex2 to a
-// score, against 2 head_dim flops on the tensor cores, for many query rows, and
-// by a CTA's start and end for few (16 rows over 6000 keys: 7.5 us).
+// works while this one starts or ends. Many query rows (512 over 32768 keys: 154 us,
+// 0.90 PFLOP/s) fill no pipe (issue 41%, special functions 38%, tensor 37%): what
+// bounds them is a tile's chain of four dependent TMEM reads and their exponentials.
+// Few are bound by a CTA's start and end (16 rows over 6000 keys: 7.5 us in a graph).
 // (Two key tiles to a CTA, which would halve the passes over the query rows, and
 // one CTA to an SM took 166 us instead of 154 us for 512 rows over 32768 keys.)
 #include <math.h>

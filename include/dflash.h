@@ -705,9 +705,10 @@ int dflash_paged_append(const dflash_paged_cache* cache, const dflash_paged_appe
  * -inf. What a query does not see, other sequences' queries among it, has no
  * influence on it, infinities and NaN included (the sizes of a batch have, on
  * how sums are split); infinities and NaN that it does see make what they reach
- * infinite or NaN. Softmax statistics and sums are fp32. out and lse overlap no
- * input. Rows outside [start[0], start[n_seq]) of out and lse are left as they
- * are. */
+ * infinite or NaN, but that a score of -inf may count as one that is not seen. (A
+ * q of fp32 within 2^-12 of the largest finite value counts as infinite.) Softmax
+ * statistics and sums are fp32. out and lse overlap no input. Rows outside
+ * [start[0], start[n_seq]) of out and lse are left as they are. */
 typedef struct dflash_paged_attention_args {
   const void* q;            /* [rows][n_q_heads][head_dim], rows q_stride elements apart */
   const int32_t* q_pos;     /* [rows] */
