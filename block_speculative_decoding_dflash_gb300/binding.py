@@ -600,6 +600,9 @@ _PAGED_ATTENTION = struct.Struct("=7Qq5i2fi")
 _PAGED_EVICT = struct.Struct("=5Q2i")
 _PAGED_WORKSPACE = struct.Struct("=Qq")
 _NO_WORKSPACE = _PAGED_WORKSPACE.pack(0, 0)
+_TREE_COMMIT = struct.Struct("=3Q2i")
+_SAMPLE = struct.Struct("=8Qq4i")
+_TREE_ACCEPT = struct.Struct("=9Q4i")
 
 _sig("dflash_paged_append", ctypes.c_int, _vp, _vp, _vp)
 _sig("dflash_paged_attention_workspace", ctypes.c_int, _vp, _vp, _vp)
@@ -607,6 +610,11 @@ _sig("dflash_paged_attention", ctypes.c_int, _vp, _vp, _vp)
 _sig("dflash_paged_key_weight", ctypes.c_int, _vp, _vp, _vp, ctypes.c_float, _vp, _vp)
 _sig("dflash_paged_evict_workspace", ctypes.c_int, _vp, _vp, _vp)
 _sig("dflash_paged_evict", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_tree_attention_workspace", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_paged_tree_attention", ctypes.c_int, _vp, _vp, _vp, _vp)
+_sig("dflash_paged_tree_commit", ctypes.c_int, _vp, _vp, _vp)
+_sig("dflash_sample", ctypes.c_int, _vp, _vp)
+_sig("dflash_tree_accept", ctypes.c_int, _vp, _vp)
 
 
 class PagedCache:
@@ -712,7 +720,7 @@ class PagedCache:
         handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
         self._check(call(self._c, *args, handle))
 
-    def _with_workspace(self, call, nbytes, args, workspace, stream):
+    def _with_workspace(self, call, nbytes, args, workspace, stream, *more):
         if workspace is not None:
             if workspace.dtype is not torch.uint8 or workspace.get_device() != self._index or not workspace.is_contiguous():
                 raise DFlashError(EINVAL, f"paged: workspace must be a dense uint8 tensor on {self.device}")
@@ -723,7 +731,7 @@ class PagedCache:
                 with torch.cuda.stream(stream):
                     workspace = self._no_bytes.new_empty(nbytes)
         ws = _NO_WORKSPACE if workspace is None else _PAGED_WORKSPACE.pack(workspace.data_ptr(), workspace.numel())
-        self._launch(call, stream, args + ws)
+        self._launch(call, stream, args + ws, *more)
 
     def append(self, q, k, v, row_pos, start, q_out, rope_pos=None, pair_axis=b"", theta=1e6, neox=True, q_norm=None,
                k_norm=None, eps=1e-6, stream=None):
@@ -780,6 +788,22 @@ class PagedCache:
                     raise
         self._with_workspace(lib.dflash_paged_attention, self._query(lib.dflash_paged_attention_workspace, args), args, workspace, stream)
 
+    def tree_attention(self, q, q_pos, start, tree_end, out, lse=None, scale=None, causal=True, window=0, softcap=0.0, slopes=None,
+                       prefix=None, max_len=0, workspace=None, stream=None):
+        """dflash_paged_tree_attention: attention() where each sequence's new rows are a tree in depth-first order; tree_end
+        [rows] (int32) is one past each row's subtree, counted from the sequence's first new row."""
+        args = self._attention_args(q, q_pos, start, self._need("out", out, self.dtype, q.shape), lse, scale, causal, window, softcap,
+                                    slopes, prefix, max_len)
+        end = self._need("tree_end", tree_end, torch.int32, (q.shape[0],))
+        if workspace is None:
+            try:
+                return self._launch(lib.dflash_paged_tree_attention, stream, args + _NO_WORKSPACE, end)
+            except DFlashError as e:
+                if e.code != EINVAL:
+                    raise
+        self._with_workspace(lib.dflash_paged_tree_attention, self._query(lib.dflash_paged_tree_attention_workspace, args), args, workspace,
+                             stream, end)
+
     def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
                    softcap=0.0, slopes=None, prefix=None, max_len=0, stream=None):
         """dflash_paged_key_weight: weight_out = decay * weight + the attention each cached row gets from q, whose lse and
@@ -809,3 +833,88 @@ class PagedCache:
         if held[0] != budget:
             self._evict_bytes = held = budget, self._query(lib.dflash_paged_evict_workspace, args)
         self._with_workspace(lib.dflash_paged_evict, held[1], args, workspace, stream)
+
+
+# ---- a verify round over trees of drafted tokens -------------------------------------
+
+
+def paged_tree_commit(caches, path, count, stream=None):
+    """dflash_paged_tree_commit: in every cache (PagedCache, a model's layers, of the same sizes) the rows path [n_seq, width] of each
+    sequence's tree, count [n_seq] of them, move to the front of the tree's rows, which end the sequence once `length` is
+    tree_accept's length_out. The caches' weights, where they have some, move along."""
+    caches = list(caches)
+    if not caches:
+        raise DFlashError(EINVAL, "paged tree commit: no caches")
+    first = caches[0]
+    if any(c._index != first._index for c in caches):
+        raise DFlashError(EINVAL, "paged tree commit: the caches are on several devices")
+    if path.dim() != 2:
+        raise DFlashError(EINVAL, "paged tree commit: path must be [n_seq, width]")
+    weights = struct.pack(f"={len(caches)}Q", *(0 if c.weight is None else c.weight.data_ptr() for c in caches))
+    held = ctypes.create_string_buffer(weights, len(weights))
+    args = first._pack(_TREE_COMMIT, first._need("path", path, torch.int32, (first.n_seq, path.shape[1])),
+                       first._need("count", count, torch.int32, (first.n_seq,)), ctypes.addressof(held), path.shape[1], len(caches))
+    first._launch(_commit, stream, b"".join(c._c for c in caches), args)
+
+
+def _commit(_, caches, args, handle):
+    return lib.dflash_paged_tree_commit(caches, args, handle)
+
+
+def _dense(call, device, name, t, dtype, shape):
+    """The address of t: a dense tensor of the given type and shape on the given GPU; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise DFlashError(EINVAL, f"{call}: {name} must be a dense {dtype} tensor of shape {tuple(shape)} on cuda:{device}, "
+                                  f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _call_on(call, device, stream, args):
+    """call(args, stream handle) with the device current."""
+    if device < 0:
+        raise DFlashError(EINVAL, "the tensors are not on a GPU")
+    if torch._C._cuda_getDevice() != device:
+        with torch.cuda.device(device):
+            return _call_on(call, device, stream, args)
+    rc = call(args, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream)
+    if rc:
+        raise DFlashError(rc, last_error(None))
+
+
+def sample(logits, uniform, token, prob=None, temperature=None, top_k=None, top_p=None, min_p=None, stream=None):
+    """dflash_sample: token [rows] (int32) drawn from logits [rows, vocab] (bf16 or fp32; rows may be apart) by uniform [rows] in
+    [0, 1), and prob [rows], its probability. temperature, top_k (int32), top_p, min_p: [rows] each, or None. On the current torch
+    stream or `stream`."""
+    if logits.dim() != 2 or logits.dtype not in (torch.bfloat16, torch.float32) or (logits.shape[1] > 1 and logits.shape[0] > 0 and logits.stride(1) != 1):
+        raise DFlashError(EINVAL, f"sample: logits must be [rows, vocab] in bf16 or fp32 with dense rows, got {logits.dtype} {tuple(logits.shape)} "
+                                  f"with strides {logits.stride()}")
+    device, (rows, vocab) = logits.get_device(), logits.shape
+
+    def at(name, t, dtype=torch.float32):
+        return _dense("sample", device, name, t, dtype, (rows,))
+
+    args = _SAMPLE.pack(logits.data_ptr(), at("uniform", uniform), at("temperature", temperature), at("top_k", top_k, torch.int32),
+                        at("top_p", top_p), at("min_p", min_p), at("token", token, torch.int32), at("prob", prob),
+                        logits.stride(0) if rows > 1 else vocab, rows, vocab, BF16 if logits.dtype is torch.bfloat16 else F32, 0)
+    _call_on(lib.dflash_sample, device, stream, args)
+
+
+def tree_accept(tree_end, start, draft, sampled, tokens, path, count, length=None, length_out=None, stream=None):
+    """dflash_tree_accept: the accepted path [n_seq, width] through each sequence's tree, the emitted tokens [n_seq, width] and their
+    number count [n_seq]; tree_end, draft, sampled [rows], start [n_seq + 1], length and length_out [n_seq], all int32. length_out
+    defaults to length."""
+    device, rows, n_seq = start.get_device(), tree_end.shape[0], start.shape[0] - 1
+    if path.dim() != 2:
+        raise DFlashError(EINVAL, "tree accept: path must be [n_seq, width]")
+    width = path.shape[1]
+
+    def at(name, t, shape):
+        return _dense("tree accept", device, name, t, torch.int32, shape)
+
+    args = _TREE_ACCEPT.pack(at("tree_end", tree_end, (rows,)), at("start", start, (n_seq + 1,)), at("draft", draft, (rows,)),
+                             at("sampled", sampled, (rows,)), at("tokens", tokens, (n_seq, width)), at("path", path, (n_seq, width)),
+                             at("count", count, (n_seq,)), at("length", length, (n_seq,)),
+                             at("length_out", length if length_out is None else length_out, (n_seq,)), rows, n_seq, width, 0)
+    _call_on(lib.dflash_tree_accept, device, stream, args)

@@ -404,6 +404,7 @@ struct PagedAttnArgs {
   const void* q;
   const int* q_pos; const int* start;
   const float* slopes; const int* prefix;
+  const int* tree;             // [rows] ends of the rows' subtrees, or NULL
   void* out;
   float* lse;
   float* part_o;               // [splits][rows * nq][hd], unnormalised
@@ -422,6 +423,7 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
 cudaError_t launch_paged_attention_tf32(int dtype, const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);
+cudaError_t launch_paged_tree_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_weight_tc(const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_key_weight(int dtype, const PagedAttnArgs& a, cudaStream_t st);
 
@@ -433,5 +435,33 @@ struct PagedEvictArgs {
   int budget, recent, max_moves;
 };
 cudaError_t launch_paged_evict(int dtype, const PagedEvictArgs& a, cudaStream_t st);
+
+// ---- trees of drafted tokens, sampling ---------------------------------------------
+struct TreeAcceptArgs {
+  const int* end; const int* start; const int* draft; const int* sampled;
+  int* tokens; int* path; int* count;
+  const int* length; int* length_out;  // or NULL
+  int rows, n_seq, width;
+};
+cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st);
+
+constexpr int kCommitCaches = 48;      // of one launch
+struct TreeCommitCache { void* k; void* v; int* pos; float* weight; const int* table; const int* length; int* status; };
+struct TreeCommitArgs {
+  TreeCommitCache cache[kCommitCaches];
+  const int* path; const int* count;
+  int width, n_caches, n_pages, lg_rows, nkv, n_seq, max_pages, vecs;   // vecs: 16-byte pieces of a row of K
+};
+cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t st);
+
+struct SampleArgs {
+  const void* logits;
+  const float* uniform;
+  const float* temperature; const int* top_k; const float* top_p; const float* min_p;   // [rows] each, or NULL
+  int* token; float* prob;
+  long long stride;
+  int rows, vocab;
+};
+cudaError_t launch_sample(int dtype, const SampleArgs& a, cudaStream_t st);
 
 }  // namespace dfl

@@ -124,6 +124,17 @@ __device__ __forceinline__ int paged_class(const PagedMask& m, int qmin, int qma
   return all && whole ? 2 : 1;
 }
 
+// Trees of drafted tokens: the new rows of a sequence, in depth-first order, are
+// its last `count` cached rows. New row j is seen by the new rows i with 0 <= i - j
+// < paged_tree_size(j): itself and its subtree, one unsigned comparison. `tree` starts
+// at the sequence's first new row. An older row (node < 0) has a size that every
+// difference is below.
+__device__ __forceinline__ int paged_tree_size(const int* tree, int count, int node) {
+  if (node < 0 || node >= count) return INT32_MAX;
+  const int end = min(tree[node], count) - node;
+  return end < 1 ? 1 : end;
+}
+
 // Classifies the key tiles [t0, t1) of `KEYS` rows of (s, h) against queries
 // at [qmin, qmax]: bit t - t0 of `some` / `all` in shared memory (zeroed here)
 // for classes >= 1 / 2. Called by every thread of the CTA, which synchronises

@@ -1,60 +1,16 @@
 // C ABI of the paged cache: argument checks and launches.
 #include <math.h>
-#include <stdarg.h>
-#include <stdio.h>
 
-#include "dflash.h"
-#include "kernels.h"
-
-namespace dfl {
-void set_global_error(const char* msg);
-}
+#include "refuse.h"
 
 using namespace dfl;
 
 namespace {
 
-int refuse(int code, const char* fmt, ...) {
-  char buf[256];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  try {
-    set_global_error(buf);
-  } catch (...) {
-  }
-  return code;
-}
-
-int launched(cudaError_t e, const char* what) {
-  if (e == cudaSuccess) return DFLASH_OK;
-  return refuse(DFLASH_ECUDA, "%s: %s (%s)", what, cudaGetErrorString(e), cudaGetErrorName(e));
-}
-
-bool misaligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
-
-// A device array that a call needs: not NULL and 16-byte aligned.
-int need(const void* p, const char* name) {
-  if (!p) return refuse(DFLASH_EINVAL, "paged: %s is NULL", name);
-  if (misaligned(p)) return refuse(DFLASH_EINVAL, "paged: %s is not 16-byte aligned", name);
-  return DFLASH_OK;
-}
+int need(const void* p, const char* name) { return need_aligned("paged", p, name, 16); }
 int may(const void* p, const char* name) { return p ? need(p, name) : DFLASH_OK; }
-// An array that is read or written an element of four bytes at a time: a slice
-// of a larger one may start anywhere.
-int need4(const void* p, const char* name) {
-  if (!p) return refuse(DFLASH_EINVAL, "paged: %s is NULL", name);
-  if (reinterpret_cast<uintptr_t>(p) & 3u) return refuse(DFLASH_EINVAL, "paged: %s is not 4-byte aligned", name);
-  return DFLASH_OK;
-}
+int need4(const void* p, const char* name) { return need_aligned("paged", p, name, 4); }
 int may4(const void* p, const char* name) { return p ? need4(p, name) : DFLASH_OK; }
-
-#define PG(call)          \
-  do {                    \
-    int rc_ = (call);     \
-    if (rc_) return rc_;  \
-  } while (0)
 
 int check_cache(const dflash_paged_cache* c, PagedView* v) {
   if (!c) return refuse(DFLASH_EINVAL, "paged: cache is NULL");
@@ -120,6 +76,7 @@ int check_attention(const dflash_paged_cache* c, const dflash_paged_attention_ar
     return refuse(DFLASH_EINVAL, "paged attention: softcap must be 0 or in [1e-18, 1e18]");
   if (a->max_len < 0) return refuse(DFLASH_EINVAL, "paged attention: max_len is negative");
   x->q = a->q; x->q_pos = a->q_pos; x->start = a->start; x->slopes = a->slopes; x->prefix = a->prefix;
+  x->tree = nullptr;
   x->out = a->out; x->lse = a->lse;
   x->part_o = nullptr; x->part_ml = nullptr;
   x->q_stride = a->q_stride; x->rows = a->rows; x->nq = a->n_q_heads; x->G = a->n_q_heads / c->kv_heads;
@@ -145,6 +102,21 @@ int check_evict(const dflash_paged_cache* c, const dflash_paged_evict_args* a, P
   if (a->budget < 1) return refuse(DFLASH_EINVAL, "paged evict: budget must be at least 1");
   if (a->recent < 0) return refuse(DFLASH_EINVAL, "paged evict: recent is negative");
   return DFLASH_OK;
+}
+
+int attend(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, PagedAttnArgs* x, void* stream) {
+  if (a->rows == 0) return DFLASH_OK;
+  const PagedPlan p = paged_attn_plan(cache->dtype, *x);
+  if (p.bytes > 0) {
+    PG(need(a->workspace, "workspace"));
+    if (a->workspace_bytes < p.bytes)
+      return refuse(DFLASH_EINVAL, "paged attention: workspace of %lld bytes, %lld needed", (long long)a->workspace_bytes, (long long)p.bytes);
+    x->part_o = static_cast<float*>(a->workspace);
+    x->part_ml = reinterpret_cast<float2*>(x->part_o + (int64_t)p.splits * a->rows * a->n_q_heads * cache->head_dim);
+  }
+  x->splits = p.splits;
+  x->cluster = p.cluster;
+  return launched(launch_paged_attention(cache->dtype, *x, p, static_cast<cudaStream_t>(stream)), "paged attention");
 }
 
 }  // namespace
@@ -210,18 +182,19 @@ int dflash_paged_attention_workspace(const dflash_paged_cache* cache, const dfla
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, void* stream) {
   PagedAttnArgs x;
   PG(check_attention(cache, a, false, &x));
-  if (a->rows == 0) return DFLASH_OK;
-  const PagedPlan p = paged_attn_plan(cache->dtype, x);
-  if (p.bytes > 0) {
-    PG(need(a->workspace, "workspace"));
-    if (a->workspace_bytes < p.bytes)
-      return refuse(DFLASH_EINVAL, "paged attention: workspace of %lld bytes, %lld needed", (long long)a->workspace_bytes, (long long)p.bytes);
-    x.part_o = static_cast<float*>(a->workspace);
-    x.part_ml = reinterpret_cast<float2*>(x.part_o + (int64_t)p.splits * a->rows * a->n_q_heads * cache->head_dim);
-  }
-  x.splits = p.splits;
-  x.cluster = p.cluster;
-  return launched(launch_paged_attention(cache->dtype, x, p, static_cast<cudaStream_t>(stream)), "paged attention");
+  return attend(cache, a, &x, stream);
+}
+
+int dflash_paged_tree_attention_workspace(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, int64_t* bytes_host) {
+  return dflash_paged_attention_workspace(cache, a, bytes_host);
+}
+
+int dflash_paged_tree_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, const int32_t* tree_end, void* stream) {
+  PagedAttnArgs x;
+  PG(check_attention(cache, a, false, &x));
+  if (a->rows > 0) PG(need4(tree_end, "tree_end"));
+  x.tree = tree_end;
+  return attend(cache, a, &x, stream);
 }
 
 int dflash_paged_key_weight(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, const float* weight_in,
@@ -260,6 +233,41 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict
   x.length_out = a->length_out; x.moves = static_cast<int*>(a->workspace);
   x.budget = a->budget; x.recent = a->recent; x.max_moves = evict_moves(cache, a->budget);
   return launched(launch_paged_evict(cache->dtype, x, static_cast<cudaStream_t>(stream)), "paged evict");
+}
+
+int dflash_paged_tree_commit(const dflash_paged_cache* caches, const dflash_paged_tree_commit_args* a, void* stream) {
+  if (!caches) return refuse(DFLASH_EINVAL, "paged tree commit: caches_host is NULL");
+  if (!a) return refuse(DFLASH_EINVAL, "paged tree commit: args is NULL");
+  if (a->n_caches < 1 || a->n_caches > 1024) return refuse(DFLASH_EINVAL, "paged tree commit: n_caches outside [1, 1024]");
+  if (a->width < 1 || a->width > (1 << 20)) return refuse(DFLASH_EINVAL, "paged tree commit: width outside [1, 2^20]");
+  const dflash_paged_cache* c0 = caches;
+  for (int i = 0; i < a->n_caches; ++i) {
+    const dflash_paged_cache* c = caches + i;
+    PagedView v;
+    PG(check_cache(c, &v));
+    if (c->n_pages != c0->n_pages || c->page_rows != c0->page_rows || c->kv_heads != c0->kv_heads || c->head_dim != c0->head_dim ||
+        c->n_seq != c0->n_seq || c->max_pages != c0->max_pages || c->dtype != c0->dtype)
+      return refuse(DFLASH_EINVAL, "paged tree commit: cache %d has other sizes or another type than the first", i);
+    if (a->weight_host) PG(may(a->weight_host[i], "weight"));
+  }
+  if ((int64_t)c0->n_seq * a->width >= (1ll << 31)) return refuse(DFLASH_ERANGE, "paged tree commit: n_seq * width reaches 2^31");
+  PG(need4(a->path, "path"));
+  PG(need4(a->count, "count"));
+  for (int first = 0; first < a->n_caches; first += kCommitCaches) {
+    TreeCommitArgs x;
+    x.n_caches = a->n_caches - first < kCommitCaches ? a->n_caches - first : kCommitCaches;
+    for (int i = 0; i < x.n_caches; ++i) {
+      PagedView v;
+      PG(check_cache(caches + first + i, &v));
+      x.cache[i] = TreeCommitCache{v.k, v.v, v.pos, a->weight_host ? a->weight_host[first + i] : nullptr, v.table, v.length, v.status};
+      x.lg_rows = v.lg_rows;
+    }
+    x.path = a->path; x.count = a->count; x.width = a->width;
+    x.n_pages = c0->n_pages; x.nkv = c0->kv_heads; x.n_seq = c0->n_seq; x.max_pages = c0->max_pages;
+    x.vecs = c0->head_dim * (c0->dtype == DFLASH_BF16 ? 2 : 4) / 16;
+    PG(launched(launch_tree_commit(x, static_cast<cudaStream_t>(stream)), "paged tree commit"));
+  }
+  return DFLASH_OK;
 }
 
 }  // extern "C"

@@ -283,7 +283,7 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
 
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
   cudaError_t e;
-  if (p.kind <= 2) e = launch_paged_attention_tc(a, p.kind, p.tiles, st);
+  if (p.kind <= 2) e = a.tree ? launch_paged_tree_attention_tc(a, p.kind, p.tiles, st) : launch_paged_attention_tc(a, p.kind, p.tiles, st);
   else e = launch_paged_attention_tf32(dtype, a, p.tiles, st);
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));

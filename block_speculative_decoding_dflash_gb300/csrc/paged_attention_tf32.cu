@@ -75,7 +75,8 @@ struct Tf32Shape {
   static constexpr size_t kSmem = kEnd + 1024;
 };
 
-template <typename T, int HDP>
+// TREE: of the sequence's new rows a query sees itself and those it descends from.
+template <typename T, int HDP, bool TREE>
 __global__ void __launch_bounds__(kWarps * 32, HDP * sizeof(T) > 512 ? 1 : 2)
 paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const __grid_constant__ PagedAttnArgs a) {
   using C = Tf32Shape<T, HDP>;
@@ -143,14 +144,17 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
     for (int e = threadIdx.x; e < kBM * HDP / 4; e += NT) *reinterpret_cast<float4*>(sq + e / (HDP / 4) * C::LDQ + e % (HDP / 4) * 4) = q_at(e / (HDP / 4), e % (HDP / 4) * 4);
   }
   paged_classify<kBN>(c, t.seq, h, len, m, s_qmin, s_qmax, sh.t0, sh.t1, some, all);
+  const int base = len - t.count;             // the first of the cached rows that are the tree
+  if (TREE && base < 0 && threadIdx.x == 0 && h == 0 && z == 0 && t.tile == 0 && c.status) atomicOr(c.status, DFLASH_PAGED_BAD_ROWS);
   // of the lane's two rows, g and g + 8
-  int pq[2];
+  int pq[2], row_of[2];
   PagedSees sees[2];
   float slope2[2], mx[2], sum[2], o[W][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int r = r0 + min(g + 8 * i, n_rows - 1);
     pq[i] = a.q_pos[t.first + r / G];
+    row_of[i] = r / G;
     sees[i] = paged_sees_of(m, pq[i]);
     slope2[i] = a.slopes ? a.slopes[h * G + r % G] * kLog2e : 0.f;
     mx[i] = -INFINITY;
@@ -204,7 +208,8 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   const uint8_t* v_at = sm + C::kV + warp * 8 * W / C::kCols * C::kSubB;
   const int v_byte = (warp * 8 * W + g * W) % C::kCols * (int)sizeof(T);
   for (; rel >= 0; buf ^= 1, phase ^= 1) {
-    const bool full = (all[rel >> 5] >> (rel & 31)) & 1u;
+    const bool tree = TREE && (sh.t0 + rel + 1) * kBN > base;
+    const bool full = ((all[rel >> 5] >> (rel & 31)) & 1u) && !tree;
     const int* rows = srow + buf * kBN;
     if (next >= 0) put_row(srow + (buf ^ 1) * kBN, next, page);
     const int after = cur.next();
@@ -215,6 +220,13 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       for (int x = 0; x < 2; ++x) {
         const int row = rows[warp * 8 + e4 + 4 * x];
         if (row >= 0) pk[x] = c.pos[row];
+      }
+    int node[2] = {-1, -1}, size[2] = {INT32_MAX, INT32_MAX};   // the same keys in the tree
+    if (tree)
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        node[x] = (sh.t0 + rel) * kBN + warp * 8 + e4 + 4 * x - base;
+        size[x] = paged_tree_size(a.tree + t.first, t.count, node[x]);
       }
     paged_wait(&k_full, phase, ok);
     // scores of rows g, g + 8 and keys 8 warp + e4, + 4
@@ -258,7 +270,7 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       float u = (s4[x] + odd[x] + (low[0][x] + low[1][x])) * scale2;
       if (a.softcap > 0.f) u = cap2 * tanhf(u);
       if (a.slopes) u -= slope2[i] * fabsf((float)(pq[i] - pk[x & 1]));
-      const bool v = full || paged_sees(sees[i], pk[x & 1]);
+      const bool v = full || (paged_sees(sees[i], pk[x & 1]) && (!tree || (unsigned)(row_of[i] - node[x & 1]) < (unsigned)size[x & 1]));
       s4[x] = v ? u : -INFINITY;
       seen |= (unsigned)v << x;
       top[i] = fmaxf(top[i], s4[x]);
@@ -429,18 +441,23 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   }
 }
 
-template <typename T, int HDP>
-cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+template <typename T, int HDP, bool TREE>
+cudaError_t run_as(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   // (fp32 rows are mapped as bf16 rows of twice the columns: the bytes are what counts)
   PagedView c = a.c;
   c.hd *= sizeof(T) / 2;
   CUtensorMap mk, mv;
   if (!paged_map_pages(&mk, c.k, c, kBN) || !paged_map_pages(&mv, c.v, c, kBN)) return cudaErrorInvalidValue;
-  auto kernel = paged_attn_tf32_kernel<T, HDP>;
+  auto kernel = paged_attn_tf32_kernel<T, HDP, TREE>;
   constexpr size_t smem = Tf32Shape<T, HDP>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), smem, st, mk, mv, a);
+}
+
+template <typename T, int HDP>
+cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
+  return a.tree ? run_as<T, HDP, true>(a, tiles, st) : run_as<T, HDP, false>(a, tiles, st);
 }
 
 }  // namespace

@@ -737,6 +737,24 @@ int dflash_paged_attention_workspace(const dflash_paged_cache* cache, const dfla
                                      int64_t* bytes_host);
 int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* args, void* stream);
 
+/* Attention of trees of drafted tokens: as dflash_paged_attention, but that the new
+ * rows of a sequence are a tree in depth-first order, and a row sees of them only
+ * itself and those it descends from. tree_end[r] (DEVICE [rows], 4-byte aligned) of
+ * the new row r = start[s] + j is one past the last row of j's subtree, counted like j
+ * from the sequence's first new row: row i descends from row j, or is it, iff j <= i <
+ * tree_end (an end of j or less counts as j + 1, one beyond the sequence's rows as
+ * their number). Which rows are a tree's is a matter of places: the sequence's n new
+ * rows are its last n cached rows, in their order, as dflash_paged_append leaves them.
+ * The mask over positions holds for all rows besides; a new row's position usually is
+ * the committed length plus its depth. With tree_end = n everywhere the tree is a
+ * chain, and the call is dflash_paged_attention with a causal mask.
+ * DFLASH_PAGED_BAD_ROWS also if a sequence has more new rows than length. Workspace
+ * and all else as dflash_paged_attention's. */
+int dflash_paged_tree_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* args,
+                                const int32_t* tree_end, void* stream);
+int dflash_paged_tree_attention_workspace(const dflash_paged_cache* cache, const dflash_paged_attention_args* args,
+                                          int64_t* bytes_host);
+
 /* What attention each cached row received: weight_out = decay * weight_in +
  * sum over the sequence's new rows and the heads of the kv head's group of
  * exp(t - lse), with t and the mask as in dflash_paged_attention and lse its
@@ -771,6 +789,86 @@ typedef struct dflash_paged_evict_args {
 int dflash_paged_evict_workspace(const dflash_paged_cache* cache, const dflash_paged_evict_args* args,
                                  int64_t* bytes_host);
 int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict_args* args, void* stream);
+
+/* ---- a verify round over trees of drafted tokens ------------------------------- */
+
+/* One token of each row of logits. With l the row's logits, T its temperature and M
+ * the largest l, a token weighs exp((l - M) / T). In descending order of l (equal ones:
+ * the lowest id first) a row keeps its first top_k tokens; of those as many as it takes
+ * for their weights to reach top_p of the sum of all top_k's; of those the ones that
+ * weigh at least min_p; the first one always. Of the kept tokens, in ascending order
+ * of their ids, the first is drawn at which the running sum of weights exceeds uniform
+ * times their sum. prob is the drawn token's share of that sum.
+ *
+ * A temperature below 2^-64 (0, negative, NaN) takes the largest logit, prob 1. A NaN
+ * logit counts as -inf, and -inf (or, of fp32 logits, what is further from M than fp32
+ * reaches) is never drawn; +inf counts as the type's largest number. A row with nothing
+ * to draw gives token -1, prob 0. A uniform number below 0 (or NaN) counts as 0, one of
+ * 1 or more draws the last kept token. Tokens that weigh less than 2^-44 are not drawn. Sums are
+ * 64-bit integers, the same in any order; a weight is right to 2^-35. */
+typedef struct dflash_sample_args {
+  const void* logits;       /* [rows][vocab], rows logit_stride elements apart; aligned to its elements */
+  const float* uniform;     /* [rows], in [0, 1) */
+  const float* temperature; /* [rows]; NULL: 1 */
+  const int32_t* top_k;     /* [rows], 0 or less: all; NULL: all */
+  const float* top_p;       /* [rows], 1 or more (or NaN): all; NULL: all */
+  const float* min_p;       /* [rows], 0 or less (or NaN): all, beyond 1 as 1; NULL: all */
+  int32_t* token;           /* [rows] */
+  float* prob;              /* [rows] or NULL */
+  int64_t logit_stride;     /* at least vocab */
+  int32_t rows;             /* 0..2^27 */
+  int32_t vocab;            /* 1..2^20 */
+  int32_t dtype;            /* DFLASH_F32 or DFLASH_BF16: logits */
+  int32_t reserved;         /* 0 */
+} dflash_sample_args;
+/* Enqueued on `stream`; no context, no workspace, no allocation. token and prob
+ * overlap no input; all arrays but the logits are 4-byte aligned. */
+int dflash_sample(const dflash_sample_args* args, void* stream);
+
+/* The walk through each sequence's tree (tree_end as in dflash_paged_tree_attention;
+ * row 0 is the last committed token): from row 0, emit the token sampled at the row
+ * and go on to the first child that was drafted as this token, until there is none or
+ * `width` rows are on the path. path[s] and tokens[s] get the rows on it, counted from
+ * the sequence's first new row (ascending), and the tokens emitted at them, -1 from
+ * count[s] on; the last emitted token is the next round's row 0. length_out[s] =
+ * length[s] - new rows + count[s], the length once only the path's rows are kept. A
+ * sequence without new rows has count 0. */
+typedef struct dflash_tree_accept_args {
+  const int32_t* tree_end;  /* [rows] */
+  const int32_t* start;     /* [n_seq + 1], ascending; cut to [0, rows] */
+  const int32_t* draft;     /* [rows] the token of each row (row 0's is not read) */
+  const int32_t* sampled;   /* [rows] the token sampled from each row's logits */
+  int32_t* tokens;          /* [n_seq][width] */
+  int32_t* path;            /* [n_seq][width] */
+  int32_t* count;           /* [n_seq] */
+  const int32_t* length;    /* [n_seq] or NULL */
+  int32_t* length_out;      /* [n_seq], may be length; NULL iff length is */
+  int32_t rows;             /* 0 or more */
+  int32_t n_seq;            /* 1..65535 */
+  int32_t width;            /* 1..2^20; n_seq * width < 2^31 */
+  int32_t reserved;         /* 0 */
+} dflash_tree_accept_args;
+/* Enqueued on `stream`; no context, no workspace, no allocation. All arrays are
+ * 4-byte aligned; the outputs overlap no input but length. */
+int dflash_tree_accept(const dflash_tree_accept_args* args, void* stream);
+
+/* Keeps of each sequence's tree the rows of its path: cached row b + path[s][i] moves to
+ * row b + i, i < count[s], with b = length[s] - count[s]; `length` is the one after the
+ * walk, and the tree's rows start at b. K, V, position and weight move, in every kv
+ * head, for n_caches caches (a model's layers; caches_host: HOST array) in one launch
+ * per 48 of them. The caches have the same sizes and type and share no pages; a
+ * sequence's path is ascending with path[i] >= i, otherwise DFLASH_PAGED_BAD_ROWS and
+ * the row that is out of order stays (as it does beyond the table; a sequence whose
+ * count or length cannot be stays as it is). Bit-exact copies; rows that are in their
+ * place are not touched, nor is what lies behind the kept rows. */
+typedef struct dflash_paged_tree_commit_args {
+  const int32_t* path;      /* [n_seq][width] */
+  const int32_t* count;     /* [n_seq] */
+  float* const* weight_host;/* HOST [n_caches]: each cache's weights (layout of pos) or NULL; NULL: none */
+  int32_t width;            /* 1..2^20; n_seq * width < 2^31 */
+  int32_t n_caches;         /* 1..1024 */
+} dflash_paged_tree_commit_args;
+int dflash_paged_tree_commit(const dflash_paged_cache* caches_host, const dflash_paged_tree_commit_args* args, void* stream);
 
 #ifdef __cplusplus
 }
