@@ -36,16 +36,18 @@ namespace cg = cooperative_groups;
 typedef unsigned long long u64;
 
 constexpr int kNT = 512, kWarps = kNT / 32;
-constexpr int kBins = kNT;
+constexpr int kBins = 512;
 constexpr int kMaxCtas = 8;
 constexpr int kSteps = 1024;               // of the exponential's table to a factor of 2
 constexpr int kUnit = 44;                  // weights are integers of 2^-44
+constexpr int kBinShift = 7;               // bins of a factor of 2^(1/8): 353 of them
 
-// 2^(-(i + 1) / 1024) as its first 24 bits and the rest. (A value of 1 would need a
-// bit more; a factor common to all weights makes no difference.)
+// 2^(-(i + 1) / 1024) as its first 24 bits and the rest, both times 2^42. (A value of
+// 1 would need a bit more; a factor common to all weights makes no difference.)
+constexpr double kScale = 4398046511104.0;
 struct PowTable {
-  float hi[kSteps], lo[kSteps];
-  constexpr PowTable() : hi(), lo() {
+  float2 v[kSteps];
+  constexpr PowTable() : v() {
     for (int i = 0; i < kSteps; ++i) {
       // Taylor's series at -(i + 1) / 1024 ln 2, in (-0.7, 0): below 2^-53 after 20 terms
       const double x = -(i + 1) / 1024.0 * 0.69314718055994530942;
@@ -54,50 +56,80 @@ struct PowTable {
         term *= x / k;
         sum += term;
       }
-      const long long whole = (long long)(sum * 16777216.0);
-      hi[i] = (float)((double)whole / 16777216.0);
-      lo[i] = (float)(sum - (double)whole / 16777216.0);
+      if (i == kSteps - 1) sum = 0.5;        // (its 24 bits start at one half)
+      const double whole = (double)(long long)(sum * 16777216.0) / 16777216.0;
+      v[i].x = (float)(whole * kScale);
+      v[i].y = (float)((sum - whole) * kScale);
     }
-    hi[kSteps - 1] = 0.5f;                 // (its 24 bits start at one half)
-    lo[kSteps - 1] = 0.f;
   }
 };
 __device__ constexpr PowTable kPow{};
 
-// The weight of a logit at distance M - l, for rows of one temperature.
+// The weight of a logit at distance M - l, for rows of one temperature. Written for the
+// pipes: a sum or a product takes half as long as an operation on bits or a comparison.
 struct Weigh {
   const float2* table;
-  float top, chi, clo, far;                // log2(e) / T in two parts; the distance beyond which a weight is zero
-  // The weight of a token within `far` as whole * 2^-shift units, before the shift drops bits.
+  float top, chi, clo, least;              // log2(e) / T in two parts; the smallest logit whose weight is not zero
+  __device__ __forceinline__ bool counts(float l) const { return l >= least; }
+  // The distance in steps of 2^-10 to a factor of 2, rounded, of a logit that counts.
+  __device__ __forceinline__ float steps(float p) const { return p + 12288.f; }   // 1.5 * 2^13: sums are multiples of 2^-10
+  static __device__ __forceinline__ int whole_steps(float t) { return __float_as_int(t) & 0x3fffff; }
+  __device__ __forceinline__ int bin(float l) const { return whole_steps(steps((top - l) * chi)) >> kBinShift; }
+  // The weight of a token that counts as whole * 2^-(steps / 2^10) units, before the
+  // shift drops bits; of others anything. No branches: a thread has several tokens' weights under way at once.
   // EXACT: M - l is an fp32 number (of bf16 logits, whose distance is one wherever it counts).
   template <bool EXACT>
-  __device__ __forceinline__ void parts(float l, u64& whole, int& shift) const {
+  __device__ __forceinline__ void parts(float l, u64& whole, int& i) const {
     const float d = top - l, p = d * chi;
     float e = fmaf(d, clo, fmaf(d, chi, -p));
     if (!EXACT) {
       const float b = d - top;
       e = fmaf((top - (d - b)) + (-l - b), chi, e);
     }
-    constexpr float kMagic = 12288.f;      // 1.5 * 2^13: sums are multiples of 2^-10
-    const float t = p + kMagic;
-    const int i = __float_as_int(t) & 0x3fffff;
-    const float r = (p - (t - kMagic)) + e;               // p = i / 1024 + r, |r| <= 2^-11
+    const float t = steps(p);
+    i = whole_steps(t);
+    const float r = (p - (t - 12288.f)) + e;              // p = i / 1024 + r, |r| <= 2^-11
     const float g = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);   // 2^-r - 1
     const float2 w = table[i & (kSteps - 1)];
-    const int c = __float2int_rn(fmaf(w.x, g, w.y) * 4398046511104.f);                   // the rest, in 2^-42
-    const int a = (__float_as_int(w.x) & 0x7fffff) | 0x800000;                           // the first 24 bits, in 2^-24
-    whole = (u64)(((long long)a << (kUnit - 24)) + ((long long)c << (kUnit - 42)));
-    shift = i >> 10;
+    const int c = __float2int_rn(fmaf(w.x, g, w.y));                                     // the rest, in 2^-42
+    // the first 24 bits are w.x's: its exponent is the same throughout
+    constexpr u64 kBias = ((u64)(127 + 41) << 23) - (1u << 23);
+    asm("{\n .reg .b64 t;\n mad.wide.u32 t, %1, %2, %3;\n mad.wide.s32 %0, %4, %5, t;\n}\n"
+        : "=l"(whole) : "r"(__float_as_int(w.x)), "r"(1 << (kUnit - 24)), "l"((u64)0 - (kBias << (kUnit - 24))), "r"(c), "r"(1 << (kUnit - 42)));
+  }
+  // (what the shift drops is made up for by a set last bit, on average)
+  template <bool EXACT>
+  __device__ __forceinline__ u64 of_counting(float l, int& i) const {
+    u64 whole;
+    parts<EXACT>(l, whole, i);
+    return (whole >> (i >> 10)) | 1ull;
   }
   template <bool EXACT>
   __device__ __forceinline__ u64 of(float l) const {
-    if (!(top - l <= far)) return 0ull;
-    u64 whole;
-    int shift;
-    parts<EXACT>(l, whole, shift);
-    return (whole >> shift) | 1ull;        // (what the shift drops is made up for by a set last bit, on average)
+    int i;
+    const u64 w = of_counting<EXACT>(l, i);
+    return counts(l) ? w : 0ull;
   }
 };
+
+// floor(f * x), or the next whole number up, of an fp32 number f in (0, 1): all bits of
+// the product, in integers. (Arithmetic in 64-bit floats has a few lanes to an SM.)
+__device__ __forceinline__ u64 share(float f, u64 x, bool up) {
+  const unsigned b = __float_as_uint(f), m = b >> 23 ? (b & 0x7fffffu) | 0x800000u : b;
+  const int s = 150 - max(1, (int)(b >> 23));             // f = m 2^-s, 24 <= s <= 149
+  const u64 lo = x * m, hi = __umul64hi(x, m);            // hi < 2^24
+  const u64 whole = s < 64 ? (hi << (64 - s)) | (lo >> s) : s < 128 ? hi >> (s - 64) : 0ull;
+  const bool rest = s < 64 ? (lo << (64 - s)) != 0 : (lo | (s < 128 ? hi & ((1ull << (s - 64)) - 1) : hi)) != 0;
+  return whole + (up && rest ? 1ull : 0ull);
+}
+// The place of a uniform number in a sum.
+__device__ __forceinline__ u64 drawn(float u, u64 total) { return u >= 1.f ? total - 1 : u > 0.f ? share(u, total, false) : 0ull; }
+
+// The next smaller number.
+__device__ __forceinline__ float least_below(float x) {
+  const int u = __float_as_int(x);
+  return x == 0.f ? __int_as_float((int)0x80000001u) : __int_as_float(u + (u < 0 ? 1 : -1));
+}
 
 // The order of floats as an unsigned number (-0 as 0).
 template <typename T>
@@ -138,6 +170,15 @@ struct Vec {
     }
     return u;
   }
+  static __device__ __forceinline__ float largest(const uint4& u) {
+    if constexpr (sizeof(T) == 2) {
+      __nv_bfloat162 m[4];
+      memcpy(m, &u, 16);
+      const __nv_bfloat162 x = __hmax2(__hmax2(m[0], m[1]), __hmax2(m[2], m[3]));
+      return fmaxf(__low2float(x), __high2float(x));
+    }
+    return fmaxf(fmaxf(at(u, 0), at(u, 1)), fmaxf(at(u, 2), at(u, 3)));
+  }
   static __device__ __forceinline__ float at(const uint4& u, int i) {
     const unsigned* w = reinterpret_cast<const unsigned*>(&u);
     if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
@@ -151,21 +192,37 @@ template <typename T>
 struct Row {
   const T* base;
   int lead, vocab;
-  __device__ __forceinline__ uint4 load(int j) const {
-    constexpr int N = Vec<T>::N;
-    const int v = j * N - lead;
-    if (v >= 0 && v + N <= vocab) return Vec<T>::clean(__ldcs(reinterpret_cast<const uint4*>(base + v)));
+  __device__ __forceinline__ bool whole(int j) const {
+    const int v = j * Vec<T>::N - lead;
+    return v >= 0 && v + Vec<T>::N <= vocab;
+  }
+  __device__ __forceinline__ uint4 raw(int j) const { return *reinterpret_cast<const uint4*>(base + (j * Vec<T>::N - lead)); }
+  __device__ __noinline__ uint4 ragged(int j) const {
     uint4 u;
     T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) e[i] = v + i >= 0 && v + i < vocab ? base[v + i] : from_f<T>(-INFINITY);
-    return Vec<T>::clean(u);
+    for (int i = 0; i < Vec<T>::N; ++i) {
+      const int v = j * Vec<T>::N - lead + i;
+      e[i] = v >= 0 && v < vocab ? base[v] : from_f<T>(-INFINITY);
+    }
+    return u;
   }
+  __device__ __forceinline__ uint4 load(int j) const { return Vec<T>::clean(whole(j) ? raw(j) : ragged(j)); }
 };
 
+// A list of tokens: one of a bin, or all that can still be drawn.
+constexpr int kEach = 4, kList = kEach * kNT;
+constexpr int kFew = 128;
 struct Shared {
   unsigned lo[2][kBins], hi[2][kBins];     // histograms, which take turns
-  float2 range;                            // of the CTA's logits
+  u64 list[kList];                         // tokens as a number that sorts them (see entry)
+  union {
+    struct { u64 all[kNT], few[kFew]; } sort;
+    float queue[kWarps][64];               // a warp's tokens above K on their way to a weight
+  };
+  float top;                               // of the CTA's logits
+  float chi, clo, far;                     // see Weigh; the distance beyond which a weight is zero
+  double cut;                              // how far from the largest logit min_p reaches
+  int listed;                              // may be more than kList: the list is cut
   u64 sum[kWarps];                         // of each warp's stretch: the weight above K,
   int equal[kWarps];                       // and how many are K
   unsigned kmin, kmax;
@@ -174,24 +231,66 @@ struct Shared {
   int found;
 };
 
+constexpr size_t kStaged = 180 * 1024;      // of a row, beside these and the table
+
 // Inclusive sums over the CTA's threads.
-__device__ __forceinline__ u64 scan_block(u64 x, u64* s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ u64 scan_warp(u64 x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const u64 y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
+  return x;
+}
+__device__ __forceinline__ u64 scan_block(u64 x, u64* s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = scan_warp(x);
   __syncthreads();
   if (lane == 31) s[warp] = x;
   __syncthreads();
-  u64 before = 0;
-  for (int i = 0; i < warp; ++i) before += s[i];
+  u64 before = lane < warp ? s[lane] : 0ull;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return x + before;
+}
+// Sorts one number of each of the first n threads, all different, ascending; the other threads' are ~0.
+__device__ __forceinline__ u64 sort_block(u64 x, int n, u64* s, u64* few) {
+  const int tid = threadIdx.x;
+  __syncthreads();
+  if (n <= kFew) {                          // each counts those before it
+    if (tid < n) s[tid] = x;
+    __syncthreads();
+    if (tid < n) {
+      int at = 0;
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) at += s[i] < x;
+      few[at] = x;
+    }
+    __syncthreads();
+    return tid < n ? few[tid] : ~0ull;
+  }
+  int all = 2 * kFew;
+  while (all < n) all <<= 1;
+  for (int size = 2; size <= all; size <<= 1)
+    for (int o = size >> 1; o; o >>= 1) {
+      u64 y;
+      if (o >= 32) {
+        __syncthreads();
+        s[tid] = x;
+        __syncthreads();
+        y = s[tid ^ o];
+      } else {
+        y = __shfl_xor_sync(0xffffffffu, x, o);
+      }
+      const bool up = (tid & size) == 0, first = (tid & o) == 0;
+      if ((y < x) == (up == first)) x = y;
+    }
+  return x;
 }
 
 template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   constexpr int N = Vec<T>::N;
   constexpr bool kExact = sizeof(T) == 2;
   extern __shared__ __align__(16) uint4 held[];
@@ -201,50 +300,58 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
   const int ctas = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long r = blockIdx.x / ctas;
-  for (int i = tid; i < kSteps; i += kNT) table[i] = make_float2(kPow.hi[i], kPow.lo[i]);
-  sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
+  for (int i = tid; i < kSteps; i += kNT) table[i] = kPow.v[i];
+  if (tid < kBins) sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
+  if (tid == 0) sh.listed = 0;
   pdl_enter();
 
-  // ---- the row's stretch of this warp, and the largest and smallest logit
+  // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
   Row<T> row;
   row.base = static_cast<const T*>(a.logits) + r * a.stride;
   row.lead = (int)((reinterpret_cast<uintptr_t>(row.base) & 15u) / sizeof(T));
   row.vocab = a.vocab;
+  // A lane loads and looks through every 32nd vector of its warp's stretch.
   const int vectors = (row.lead + a.vocab + N - 1) / N, per = (vectors + ctas - 1) / ctas, each = (per + kWarps - 1) / kWarps;
   const int c0 = min(vectors, rank * per), c1 = min(vectors, c0 + per);
   const int v0 = min(c1, c0 + warp * each), v1 = min(c1, v0 + each);
   auto vector = [&](int j) { return STAGED ? held[j - c0] : row.load(j); };
-  float hi = -INFINITY, lo = INFINITY;
-#pragma unroll 4
-  for (int j = v0 + lane; j < v1; j += 32) {
-    const uint4 u = row.load(j);
-    if (STAGED) held[j - c0] = u;
+  const float temp = a.temperature ? a.temperature[r] : 1.f;
+  const int top_k = a.top_k ? a.top_k[r] : 0;
+  const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u01 = a.uniform[r];
+  const bool greedy = !(temp >= 5.4210109e-20f);          // 2^-64
+  if (tid == kNT - 1) {
+    const double c = greedy ? 1.0 : 1.44269504088896340736 / (double)temp;
+    sh.chi = (float)c;
+    sh.clo = (float)(c - (double)sh.chi);
+    sh.far = fminf((float)(kUnit / c), FLT_MAX);
+    sh.cut = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : 0.0;
+  }
+  float hi = -INFINITY;
+  for (int j0 = v0 + lane; j0 < v1; j0 += 32 * 4) {   // (a row of 2^18 bf16 numbers: one pass)
+    uint4 u[4];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float l = Vec<T>::at(u, i);
-      hi = fmaxf(hi, l);
-      lo = fminf(lo, l == -INFINITY ? INFINITY : l);
+    for (int x = 0; x < 4; ++x)
+      if (j0 + x * 32 < v1 && row.whole(j0 + x * 32)) u[x] = row.raw(j0 + x * 32);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int j = j0 + x * 32;
+      if (j >= v1) continue;
+      if (!row.whole(j)) u[x] = row.ragged(j);
+      u[x] = Vec<T>::clean(u[x]);
+      if (STAGED) held[j - c0] = u[x];
+      hi = fmaxf(hi, Vec<T>::largest(u[x]));
     }
   }
+  const float own = hi;                    // of the vectors that this thread looks through
   hi = warp_max(hi);
-  lo = -warp_max(-lo);
-  if (lane == 0) sh.scan[warp] = ((u64)__float_as_uint(lo) << 32) | __float_as_uint(hi);
+  if (lane == 0) sh.scan[warp] = __float_as_uint(hi);
   __syncthreads();
-  if (tid == 0) {
-    for (int i = 0; i < kWarps; ++i) {
-      hi = fmaxf(hi, __uint_as_float((unsigned)sh.scan[i]));
-      lo = fminf(lo, __uint_as_float((unsigned)(sh.scan[i] >> 32)));
-    }
-    sh.range = make_float2(hi, lo);
+  if (warp == 0) {
+    hi = warp_max(lane < kWarps ? __uint_as_float((unsigned)sh.scan[lane]) : -INFINITY);
+    if (lane == 0) sh.top = hi;
   }
   cl.sync();
-  hi = -INFINITY;
-  lo = INFINITY;
-  for (int i = 0; i < ctas; ++i) {
-    const float2 x = *cl.map_shared_rank(&sh.range, i);
-    hi = fmaxf(hi, x.x);
-    lo = fminf(lo, x.y);
-  }
+  hi = warp_max(lane < ctas ? *cl.map_shared_rank(&sh.top, lane) : -INFINITY);
   if (hi == -INFINITY) {                   // nothing to choose from
     if (rank == 0 && tid == 0) {
       a.token[r] = -1;
@@ -253,60 +360,197 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
     cl.sync();
     return;
   }
-
-  // ---- the row's parameters
-  const float temp = a.temperature ? a.temperature[r] : 1.f;
-  const int top_k = a.top_k ? a.top_k[r] : 0;
-  const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f;
-  const bool greedy = !(temp >= 5.4210109e-20f);          // 2^-64
   Weigh weigh;
   weigh.table = table;
   weigh.top = hi;
-  {
-    const double c = greedy ? 1.0 : 1.44269504088896340736 / (double)temp;
-    weigh.chi = (float)c;
-    weigh.clo = (float)(c - (double)weigh.chi);
-    weigh.far = fminf((float)(kUnit / c), FLT_MAX);
+  weigh.chi = sh.chi;
+  weigh.clo = sh.clo;
+  // (of a vast temperature every logit whose distance is an fp32 number: FLT_MAX and half a step more)
+  weigh.least = fmaxf(hi - sh.far - (sh.far == FLT_MAX ? 0x1p102f : 0.f), -FLT_MAX);
+  auto put = [&](int token, float l, u64 total) {
+    a.token[r] = token;
+    if (!a.prob) return;
+    u64 whole;
+    int i;
+    weigh.parts<kExact>(l, whole, i);
+    a.prob[r] = (float)((double)whole * __longlong_as_double((long long)(1023 - (i >> 10)) << 52) / (double)total);
+  };
+
+  if (greedy) {                            // the first of the largest
+    int first = INT32_MAX;
+    if (own == hi)
+      for (int j = v0 + lane; j < v1 && first == INT32_MAX; j += 32) {
+        const uint4 u = vector(j);
+        for (int i = N - 1; i >= 0; --i)
+          if (Vec<T>::at(u, i) == hi) first = j * N - row.lead + i;
+      }
+    first = __reduce_min_sync(0xffffffffu, first);
+    if (lane == 0) sh.equal[warp] = first;
+    cl.sync();
+    if (rank == 0 && warp == 0) {
+      for (int i = lane; i < ctas * kWarps; i += 32) first = min(first, *cl.map_shared_rank(&sh.equal[i % kWarps], i / kWarps));
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) {
+        a.token[r] = first;
+        if (a.prob) a.prob[r] = 1.f;
+      }
+    }
+    cl.sync();
+    return;
   }
+
   int parity = 0;                          // the histogram in use
-  float K = greedy ? hi : -INFINITY;       // kept: what is above K, and the first t of those equal to K
-  u64 t = greedy ? 1 : 0;
-  bool all = !greedy;                      // no cut so far
+  // kept: what is above K, and the first t of those equal to K; at first what counts
+  float K = least_below(weigh.least);
+  u64 t = 0;
+  bool all = true;                         // no cut so far
 
   // The histogram of all CTAs: this thread's bin, and the sum up to and with it.
   auto merged = [&](bool weights, u64& bin, u64& upto) {
     cl.sync();
     bin = 0;
-    for (int i = 0; i < ctas; ++i) {
-      bin += *cl.map_shared_rank(&sh.lo[parity][tid], i);
-      if (weights) bin += (u64)*cl.map_shared_rank(&sh.hi[parity][tid], i) << 32;
-    }
+#pragma unroll
+    for (int i = 0; i < kMaxCtas; ++i)
+      if (i < ctas && tid < kBins) {
+        bin += *cl.map_shared_rank(&sh.lo[parity][tid], i);
+        if (weights) bin += (u64)*cl.map_shared_rank(&sh.hi[parity][tid], i) << 32;
+      }
     upto = scan_block(bin, sh.scan);
     if (tid == kNT - 1) sh.total = upto;
     parity ^= 1;
-    sh.lo[parity][tid] = sh.hi[parity][tid] = 0u;         // everyone has read it: they came to the last meeting since
+    if (tid < kBins) sh.lo[parity][tid] = sh.hi[parity][tid] = 0u;   // everyone has read it: they came to the last meeting since
     __syncthreads();
   };
   auto add = [&](bool weights, int bin, u64 w) {
     const unsigned old = atomicAdd(&sh.lo[parity][bin], (unsigned)w);
     if (weights) atomicAdd(&sh.hi[parity][bin], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
   };
+  // A token as a number: larger logits first, then lower ids.
+  auto entry = [&](float l, int token) { return (u64)~key_of<T>(l) << 32 | (unsigned)token; };
+  auto entry_logit = [&](u64 x) { return of_key<T>(sizeof(T) == 2 ? (unsigned)(~x >> 32) & 0xffffu : (unsigned)(~x >> 32)); };
+  auto list = [&](float l, int token) {
+    const int at = atomicAdd(&sh.listed, 1);
+    if (at < kList) sh.list[at] = entry(l, token);
+  };
+  // The lists of all CTAs, kEach entries to a thread (~0: none): their number, or -1 where some do not fit.
+  auto gathered = [&](u64 (&mine)[kEach]) {
+    cl.sync();
+    const int some = lane < ctas ? *cl.map_shared_rank(&sh.listed, lane) : 0;
+    int upto = some;
+#pragma unroll
+    for (int o = 1; o < kMaxCtas; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const int n = __shfl_sync(0xffffffffu, upto, kMaxCtas - 1);
+    const bool fit = __all_sync(0xffffffffu, some <= kList) && n <= kList;
+    int from[kEach] = {}, before[kEach] = {};
+#pragma unroll
+    for (int i = 0; i < kMaxCtas - 1; ++i) {
+      const int y = __shfl_sync(0xffffffffu, upto, i);
+#pragma unroll
+      for (int x = 0; x < kEach; ++x)
+        if (tid + x * kNT >= y) { from[x] = i + 1; before[x] = y; }
+    }
+#pragma unroll
+    for (int x = 0; x < kEach; ++x) {
+      mine[x] = ~0ull;
+      if (fit && tid + x * kNT < n) mine[x] = *cl.map_shared_rank(&sh.list[tid + x * kNT - before[x]], from[x]);
+    }
+    __syncthreads();                       // (what follows runs as whole warps)
+    return fit ? n : -1;
+  };
+
+  // ---- few tokens to choose from: top_k of them, by a list
+  if (top_k > 0 && top_k <= kNT / 2) {
+    // At least top_k threads have a token in the first bins that hold top_k of the
+    // threads' largest: whatever is further away is not among the first top_k.
+    if (weigh.counts(own)) atomicAdd(&sh.lo[parity][weigh.bin(own)], 1u);
+    u64 bin, upto;
+    merged(false, bin, upto);
+    const u64 want = (u64)top_k;
+    if (tid == kNT - 1 || upto >= want)
+      if (upto - bin < want) sh.found = tid;
+    __syncthreads();
+    const int last = sh.found;             // (of all bins, where fewer threads have a token)
+    if (weigh.counts(own) && weigh.bin(own) <= last)
+      for (int j = v0 + lane; j < v1; j += 32) {
+        const uint4 u = vector(j);
+        if (!(Vec<T>::largest(u) >= weigh.least)) continue;
+        for (int i = 0; i < N; ++i) {
+          const float l = Vec<T>::at(u, i);
+          if (weigh.counts(l) && weigh.bin(l) <= last) list(l, j * N - row.lead + i);
+        }
+      }
+    u64 xs[kEach];
+    const int n = gathered(xs);
+    if (n >= 0 && n <= kNT) {
+      if (rank == 0) {
+        u64 x = sort_block(xs[0], n, sh.sort.all, sh.sort.few);
+        // in descending order of logits: top_k, top_p, min_p
+        const float l = x == ~0ull ? -INFINITY : entry_logit(x);
+        u64 w = tid < n && tid < top_k ? weigh.of<kExact>(l) : 0ull;
+        const u64 before = scan_block(w, sh.scan) - w;
+        if (tid == kNT - 1) sh.total = before + w;
+        __syncthreads();
+        if (top_p < 1.f) {
+          if (before > 0 && (!(top_p > 0.f) || before >= share(top_p, sh.total, true))) w = 0;
+        }
+        if (min_p > 0.f && l < __double2float_ru((double)hi + sh.cut)) w = 0;
+        // the draw, in ascending order of ids
+        x = w ? x << 32 | x >> 32 : ~0ull;
+        const int kept = __syncthreads_count(w != 0);      // (the first ones)
+        x = sort_block(x, kept, sh.sort.all, sh.sort.few);
+        const float lt = entry_logit(x << 32 | x >> 32);
+        w = x == ~0ull ? 0ull : weigh.of<kExact>(lt);
+        const u64 upto_t = scan_block(w, sh.scan);
+        if (tid == kNT - 1) sh.total = upto_t;
+        __syncthreads();
+        const u64 total = sh.total, goal = drawn(u01, total);
+        if (w && goal < upto_t && goal >= upto_t - w) put((int)(x >> 32), lt, total);
+      }
+      cl.sync();
+      return;
+    }
+    cl.sync();                             // the lists are free again
+    if (tid == 0) sh.listed = 0;
+  }
+
   // Cuts what is kept so far (above K, t of those equal to K) where the running
   // count (or weight) reaches `part` (a share of all of it, for weights).
-  auto cut = [&](bool weights, double part) {
+  auto cut = [&](bool weights, float part) {
     const float K0 = K;
-    const u64 t0 = t, wK = !all && weights ? weigh.of<kExact>(K0) : 1ull;
+    const u64 t0 = t, wK = !all && weights ? weigh.of<kExact>(K0) : 1ull;  // (a K that is a logit)
     const u64 tail = all ? 0ull : t0 * wK;                // what those equal to K count
-    const float reach = fminf(weigh.far, hi - lo), scale = reach > 0.f ? (float)kBins / reach : 0.f;
-    auto bin_of = [&](float l) { return min(kBins - 1, (int)((hi - l) * scale)); };
-    auto in = [&](float l) { return l > K0 && hi - l <= weigh.far; };
-#pragma unroll 1
+    auto in = [&](float l) { return l > K0; };
     for (int j = v0 + lane; j < v1; j += 32) {
       const uint4 u = vector(j);
+#pragma unroll 1
+      for (int i0 = 0; i0 < N; i0 += 4) {
+        const uint2 half = N == 8 && i0 ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
+        const uint4 four = N == 8 ? make_uint4(half.x, half.y, 0, 0) : u;
+        u64 w[4];
+        int at[4];
+        unsigned old[4];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float l = Vec<T>::at(u, i);
-        if (in(l)) add(weights, bin_of(l), weights ? weigh.of<kExact>(l) : 1ull);
+        for (int i = 0; i < 4; ++i) {
+          const float l = Vec<T>::at(four, i);
+          w[i] = 1;
+          at[i] = 0;
+          if (weights) {
+            w[i] = weigh.of_counting<kExact>(l, at[i]);
+            at[i] >>= kBinShift;
+          } else {
+            at[i] = weigh.bin(l);
+          }
+          if (in(l)) old[i] = atomicAdd(&sh.lo[parity][at[i]], (unsigned)w[i]);
+        }
+        if (weights)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned up = (unsigned)(w[i] >> 32) + (old[i] + (unsigned)w[i] < old[i] ? 1u : 0u);
+            if (in(Vec<T>::at(four, i)) && up) atomicAdd(&sh.hi[parity][at[i]], up);
+          }
       }
     }
     u64 bin, upto;
@@ -314,10 +558,9 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
     const u64 total = sh.total + tail;
     u64 goal;                              // a token stays if what comes before it is below this
     if (weights) {
-      const double g = ceil(part * (double)total);
-      goal = g >= 18446744073709551615.0 ? ~0ull : g > 1.0 ? (u64)g : 1ull;
+      goal = part > 0.f ? max(share(part, total, true), 1ull) : 1ull;
     } else {
-      goal = (u64)part;
+      goal = (u64)top_k;
     }
     if (goal >= total) return;             // all of it
     if (goal > sh.total) {                 // reached among those equal to K
@@ -329,50 +572,73 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
       sh.found = tid;
       sh.found_before = upto - bin;
     }
-    if (tid == 0) { sh.kmin = 0xffffffffu; sh.kmax = 0u; }
+    if (tid == 0) {
+      sh.kmin = 0xffffffffu;
+      sh.kmax = 0u;
+      sh.listed = 0;
+    }
     __syncthreads();
     const int where = sh.found;
     u64 before = sh.found_before;
-    // the span of the bin in the order of floats
+    // the bin's tokens, and their span in the order of floats
     unsigned kmin = 0xffffffffu, kmax = 0u;
-#pragma unroll 1
-    for (int j = v0 + lane; j < v1; j += 32) {
-      const uint4 u = vector(j);
+    if (own > K0 && weigh.bin(own) <= where)
+      for (int j = v0 + lane; j < v1; j += 32) {
+        const uint4 u = vector(j);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float l = Vec<T>::at(u, i);
-        if (in(l) && bin_of(l) == where) {
-          const unsigned k = key_of<T>(l);
-          kmin = min(kmin, k);
-          kmax = max(kmax, k);
+        for (int i = 0; i < N; ++i) {
+          const float l = Vec<T>::at(u, i);
+          if (in(l) && weigh.bin(l) == where) {
+            const unsigned k = key_of<T>(l);
+            kmin = min(kmin, k);
+            kmax = max(kmax, k);
+            list(l, 0);
+          }
         }
       }
-    }
     kmin = __reduce_min_sync(0xffffffffu, kmin);
     kmax = __reduce_max_sync(0xffffffffu, kmax);
     if (lane == 0) {
       atomicMin(&sh.kmin, kmin);
       atomicMax(&sh.kmax, kmax);
     }
-    cl.sync();
+    u64 xs[kEach];
+    const int n = gathered(xs);
     for (int i = 0; i < ctas; ++i) {
       kmin = min(kmin, *cl.map_shared_rank(&sh.kmin, i));
       kmax = max(kmax, *cl.map_shared_rank(&sh.kmax, i));
     }
+    unsigned kx[kEach];
+    u64 wx[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+      const float l = xs[i] == ~0ull ? -INFINITY : entry_logit(xs[i]);
+      kx[i] = key_of<T>(l);
+      wx[i] = weights ? weigh.of<kExact>(l) : 1ull;
+    }
     while (kmin != kmax) {
       int shift = 0;
       while ((kmax - kmin) >> shift >= (unsigned)kBins) ++shift;
-#pragma unroll 1
-      for (int j = v0 + lane; j < v1; j += 32) {
-        const uint4 u = vector(j);
+      if (n >= 0) {                        // every CTA has them all
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float l = Vec<T>::at(u, i);
-          const unsigned k = key_of<T>(l);
-          if (k >= kmin && k <= kmax && in(l) && bin_of(l) == where) add(weights, (int)((kmax - k) >> shift), weights ? weigh.of<kExact>(l) : 1ull);
+        for (int i = 0; i < kEach; ++i)
+          if (xs[i] != ~0ull && kx[i] >= kmin && kx[i] <= kmax) add(weights, (int)((kmax - kx[i]) >> shift), wx[i]);
+        __syncthreads();
+        bin = tid < kBins ? sh.lo[parity][tid] | (u64)sh.hi[parity][tid] << 32 : 0ull;
+        upto = scan_block(bin, sh.scan);
+        if (tid < kBins) sh.lo[parity][tid] = sh.hi[parity][tid] = 0u;
+      } else {
+        for (int j = v0 + lane; j < v1; j += 32) {
+          const uint4 u = vector(j);
+#pragma unroll 1
+          for (int i = 0; i < N; ++i) {
+            const float l = Vec<T>::at(u, i);
+            const unsigned k = key_of<T>(l);
+            if (k >= kmin && k <= kmax && in(l) && weigh.bin(l) == where) add(weights, (int)((kmax - k) >> shift), weights ? weigh.of<kExact>(l) : 1ull);
+          }
         }
+        merged(weights, bin, upto);
       }
-      merged(weights, bin, upto);
       if (before + upto >= goal && before + upto - bin < goal) {
         sh.found = tid;
         sh.found_before = before + upto - bin;
@@ -386,15 +652,16 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
       __syncthreads();
     }
     K = of_key<T>(kmax);
-    t = weights ? (goal - before + weigh.of<kExact>(K) - 1) / weigh.of<kExact>(K) : goal - before;
+    const u64 w1 = weights ? weigh.of<kExact>(K) : 1ull;
+    t = (goal - before + w1 - 1) / w1;
     all = false;
+    cl.sync();                             // the lists and spans are free again
   };
-  if (!greedy && top_k > 0 && top_k < a.vocab) cut(false, (double)top_k);
-  if (!greedy && top_p < 1.f) cut(true, (double)fmaxf(top_p, 0.f));
-  if (!greedy && min_p > 0.f) {
+  if (top_k > 0 && top_k < a.vocab) cut(false, 0.f);
+  if (top_p < 1.f) cut(true, top_p);
+  if (min_p > 0.f) {
     // l >= M + T ln(min_p): the smallest fp32 that is
-    const double least = (double)hi + (double)temp * log((double)fminf(min_p, 1.f));
-    const float f = __double2float_ru(least);
+    const float f = __double2float_ru((double)hi + sh.cut);
     if (f > K) {
       K = f;
       t = ~0ull;
@@ -405,15 +672,55 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
   // ---- each warp's weight above K and number equal to K
   u64 sum = 0;
   int equal = 0;
+  if (all) {
+    for (int j = v0 + lane; j < v1; j += 32) {
+      const uint4 u = vector(j);
 #pragma unroll 1
-  for (int j = v0 + lane; j < v1; j += 32) {
-    const uint4 u = vector(j);
+      for (int i0 = 0; i0 < N; i0 += 4) {
+        const uint2 half = N == 8 && i0 ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
+        const uint4 four = N == 8 ? make_uint4(half.x, half.y, 0, 0) : u;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float l = Vec<T>::at(u, i);
-      if (l > K) sum += weigh.of<kExact>(l);
-      equal += l == K;
+        for (int i = 0; i < 4; ++i) {
+          const float l = Vec<T>::at(four, i);
+          int steps;
+          const u64 w = weigh.of_counting<kExact>(l, steps);
+          if (l > K) sum += w;
+        }
+      }
     }
+  } else {
+    // few of them: those that are kept come together before they are weighed
+    float* queue = sh.queue[warp];
+    int queued = 0;
+    auto weigh_queue = [&]() {
+      __syncwarp();
+      int steps;
+      const u64 w = weigh.of_counting<kExact>(queue[lane], steps);
+      if (lane < queued) sum += w;
+    };
+    for (int j0 = v0; j0 < v1; j0 += 32) {
+      const int j = j0 + lane;
+      const uint4 u = j < v1 ? vector(j) : make_uint4(0u, 0u, 0u, 0u);
+      const float most = j < v1 ? Vec<T>::largest(u) : -INFINITY;
+      if (!__any_sync(0xffffffffu, most >= K)) continue;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float l = Vec<T>::at(u, i);
+        const bool on = j < v1 && l > K;
+        equal += j < v1 && l == K;
+        const unsigned who = __ballot_sync(0xffffffffu, on);
+        if (on) queue[queued + __popc(who & ((1u << lane) - 1u))] = l;
+        queued += __popc(who);
+        if (queued >= 32) {
+          weigh_queue();
+          queued -= 32;
+          const float next = queue[32 + lane];
+          __syncwarp();
+          if (lane < queued) queue[lane] = next;
+        }
+      }
+    }
+    weigh_queue();
   }
   u64 all_sum = sum;
 #pragma unroll
@@ -439,11 +746,8 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
     sh.found = -1;
   }
   __syncthreads();
-  const u64 total = sh.total;
+  const u64 total = sh.total, goal = drawn(u01, total);
   __syncthreads();
-  // drawn: the first token at which the running sum exceeds u * total
-  const double u01 = (double)a.uniform[r], x = u01 > 0.0 ? u01 * (double)total : 0.0;
-  const u64 goal = x >= (double)total ? total - 1 : min((u64)x, total - 1);
   if (tid < ctas * kWarps && tid / kWarps == rank && goal < upto && goal >= upto - mine) {
     sh.found = tid % kWarps;               // the stretch that has it
     sh.found_before = upto - mine;
@@ -452,20 +756,20 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
   cl.sync();                               // no CTA leaves while another reads it
   if (warp != sh.found) return;
   u64 left = goal - sh.found_before;
-  int spare = (int)sh.total;
+  int spare = (int)min(sh.total, (u64)INT32_MAX);
   for (int j0 = v0; j0 < v1; j0 += 32) {
     const int j = j0 + lane;
-    uint4 u = make_uint4(0, 0, 0, 0);
-    u64 s = 0;
+    const uint4 u = j < v1 ? vector(j) : make_uint4(0u, 0u, 0u, 0u);
+    u64 w[N], s = 0;
     int n = 0;
-    if (j < v1) {
-      u = vector(j);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float l = Vec<T>::at(u, i);
-        if (l > K) s += weigh.of<kExact>(l);
-        n += l == K;
-      }
+    for (int i = 0; i < N; ++i) {
+      const float l = j < v1 ? Vec<T>::at(u, i) : -INFINITY;
+      int steps;
+      w[i] = weigh.of_counting<kExact>(l, steps);
+      if (!(l > K)) w[i] = 0ull;
+      s += w[i];
+      n += l == K;
     }
     int n_upto = n;
 #pragma unroll
@@ -473,36 +777,26 @@ __global__ void __launch_bounds__(kNT) sample_kernel(const SampleArgs a) {
       const int y = __shfl_up_sync(0xffffffffu, n_upto, o);
       if (lane >= o) n_upto += y;
     }
-    const int first = spare - (n_upto - n);               // equals that this lane may still keep
-    s += (u64)max(0, min(n, first)) * wK;
-    u64 s_upto = s;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const u64 y = __shfl_up_sync(0xffffffffu, s_upto, o);
-      if (lane >= o) s_upto += y;
-    }
+    int may = spare - (n_upto - n);                       // equals that this lane may still keep
+    s += (u64)max(0, min(n, may)) * wK;
+    const u64 s_upto = scan_warp(s);
     const unsigned hit = __ballot_sync(0xffffffffu, left < s_upto);
     if (hit) {
       if (lane == __ffs(hit) - 1) {
-        u64 run = s_upto - s;
-        int may = first;
+        u64 before = s_upto - s;
+        int at = -1;
+        float chosen = 0.f;
+#pragma unroll
         for (int i = 0; i < N; ++i) {
           const float l = Vec<T>::at(u, i);
-          u64 w = 0;
-          if (l > K) w = weigh.of<kExact>(l);
-          else if (l == K && may-- > 0) w = wK;
-          run += w;
-          if (left < run) {
-            a.token[r] = j * N - row.lead + i;
-            if (a.prob) {
-              u64 whole;
-              int shift;
-              weigh.parts<kExact>(l, whole, shift);
-              a.prob[r] = (float)((double)whole * __longlong_as_double((long long)(1023 - shift) << 52) / (double)total);
-            }
-            break;
+          if (l == K && may-- > 0) w[i] = wK;
+          before += w[i];
+          if (at < 0 && left < before) {
+            at = i;
+            chosen = l;
           }
         }
+        put(j * N - row.lead + at, chosen, total);
       }
       return;
     }
@@ -518,9 +812,9 @@ cudaError_t run(const SampleArgs& a, cudaStream_t st) {
   int ctas = 1;
   while (ctas < kMaxCtas && vectors > 1024ll * ctas) ctas *= 2;
   const size_t bytes = (size_t)((vectors + ctas - 1) / ctas) * 16;
-  const bool staged = bytes <= 200 * 1024;
+  const bool staged = bytes <= kStaged;
   auto kernel = staged ? sample_kernel<T, true> : sample_kernel<T, false>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStaged);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.rows * ctas));
