@@ -143,6 +143,22 @@ __device__ __forceinline__ float of_key(unsigned k) {
   return __int_as_float((int)(k & 0x80000000u ? k ^ 0x80000000u : ~k));
 }
 
+// bf16 logits by a bin for each number: the order of the numbers 2^-9 and more from
+// zero, zero, and the rest of either sign, which shares a bin (some ten thousand
+// numbers that hardly a logit is). A place counts from zero up and down.
+constexpr int kKeys = 4096;
+constexpr int kNear = 0x3b00;              // 2^-9
+__device__ __forceinline__ int place_of(int bits) {       // of the 16 bits, with their sign
+  const int mag = bits & 0x7fff, z = max(mag - kNear + 2, min(mag, 1));
+  return bits < 0 ? -z : z;
+}
+__device__ __forceinline__ int place_of(float l) { return place_of((int)__float_as_uint(l) >> 16); }
+__device__ __forceinline__ bool shared_place(int place) { return place == 1 || place == -1; }
+__device__ __forceinline__ float of_place(int place) {    // (0 for a shared one)
+  const int z = place < 0 ? -place : place;
+  return z < 2 ? 0.f : __int_as_float(((z - 2 + kNear) << 16) | (place < 0 ? (int)0x80000000u : 0));
+}
+
 template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
@@ -214,7 +230,17 @@ constexpr int kEach = 4, kList = kEach * kNT;
 constexpr int kFew = 128;
 struct Shared {
   unsigned lo[2][kBins], hi[2][kBins];     // histograms, which take turns
-  u64 list[kList];                         // tokens as a number that sorts them (see entry)
+  union {
+    u64 list[kList];                       // tokens as a number that sorts them (see entry)
+    unsigned keys[kKeys];                  // bf16: how many of the CTA's logits each bin has, from the largest down
+  };
+  unsigned near_lo[2], near_hi[2];         // the weight in the shared bins above and below zero
+  u64 slice, above;                        // of this CTA's share of the bins: their weight; at the cut, the weight above it
+  unsigned slice_count;
+  int pick;                                // the bin of the cut
+  u64 pick_t;
+  u64 part_sum;                            // of this CTA's part of the row: the weight above K,
+  int part_equal;                          // and how many are K
   union {
     struct { u64 all[kNT], few[kFew]; } sort;
     float queue[kWarps][64];               // a warp's tokens above K on their way to a weight
@@ -303,6 +329,11 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   for (int i = tid; i < kSteps; i += kNT) table[i] = kPow.v[i];
   if (tid < kBins) sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
   if (tid == 0) sh.listed = 0;
+  auto clear_keys = [&]() {
+    for (int i = tid; i < kKeys / 4; i += kNT) reinterpret_cast<uint4*>(sh.keys)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid < 2) sh.near_lo[tid] = sh.near_hi[tid] = 0u;
+  };
+  if (kExact) clear_keys();
   pdl_enter();
 
   // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
@@ -327,13 +358,14 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     sh.cut = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : 0.0;
   }
   float hi = -INFINITY;
-  for (int j0 = v0 + lane; j0 < v1; j0 += 32 * 4) {   // (a row of 2^18 bf16 numbers: one pass)
-    uint4 u[4];
+  constexpr int kAhead = 8;                // vectors requested together: all of a row of 2^18 bf16 numbers
+  for (int j0 = v0 + lane; j0 < v1; j0 += 32 * kAhead) {
+    uint4 u[kAhead];
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
+    for (int x = 0; x < kAhead; ++x)
       if (j0 + x * 32 < v1 && row.whole(j0 + x * 32)) u[x] = row.raw(j0 + x * 32);
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
+    for (int x = 0; x < kAhead; ++x) {
       const int j = j0 + x * 32;
       if (j >= v1) continue;
       if (!row.whole(j)) u[x] = row.ragged(j);
@@ -472,14 +504,14 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     if (tid == kNT - 1 || upto >= want)
       if (upto - bin < want) sh.found = tid;
     __syncthreads();
-    const int last = sh.found;             // (of all bins, where fewer threads have a token)
-    if (weigh.counts(own) && weigh.bin(own) <= last)
+    const int far = sh.found;              // (of all bins, where fewer threads have a token)
+    if (weigh.counts(own) && weigh.bin(own) <= far)
       for (int j = v0 + lane; j < v1; j += 32) {
         const uint4 u = vector(j);
         if (!(Vec<T>::largest(u) >= weigh.least)) continue;
         for (int i = 0; i < N; ++i) {
           const float l = Vec<T>::at(u, i);
-          if (weigh.counts(l) && weigh.bin(l) <= last) list(l, j * N - row.lead + i);
+          if (weigh.counts(l) && weigh.bin(l) <= far) list(l, j * N - row.lead + i);
         }
       }
     u64 xs[kEach];
@@ -514,7 +546,193 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     }
     cl.sync();                             // the lists are free again
     if (tid == 0) sh.listed = 0;
+    if (kExact) {
+      clear_keys();
+      __syncthreads();
+    }
   }
+
+  // Where the token is looked for at the end: the warps' stretches of the row, or of one CTA's part of it.
+  const uint4* source = held;
+  int first = v0, last = v1, origin = c0;
+  u64 total = 0, goal = 0;
+  bool placed = false;                     // total and goal are known
+
+  // ---- bf16: a bin for each number. The row's weights are those of some thousand
+  // numbers times their counts, a cut is found in one step, and what each CTA keeps
+  // follows from its own counts: weights of single tokens are taken of one CTA's
+  // part only, by all of them.
+  if constexpr (kExact) if (top_k > 0 || top_p < 1.f) {
+    // (down to the smallest bf16 number that counts)
+    const int low = __float_as_int(weigh.least), top = place_of(hi), bins = top - place_of((low + (low < 0 ? 0 : 0xffff)) >> 16) + 1;
+    if (bins <= kKeys) {
+      for (int j = v0 + lane; j < v1; j += 32) {
+        const uint4 u = vector(j);
+        const unsigned* words = reinterpret_cast<const unsigned*>(&u);
+        unsigned near = 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int bits = (int)(i & 1 ? words[i >> 1] : words[i >> 1] << 16) >> 16, place = place_of(bits);
+          const int b = top - place;
+          if (b < bins) atomicAdd(&sh.keys[b], 1u);
+          near |= (unsigned)(shared_place(place) && b < bins) << i;
+        }
+        for (; near; near &= near - 1) {
+          const float l = Vec<T>::at(u, __ffs(near) - 1);
+          const u64 w = weigh.of<true>(l);
+          const int side = l < 0.f;
+          const unsigned old = atomicAdd(&sh.near_lo[side], (unsigned)w);
+          atomicAdd(&sh.near_hi[side], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
+        }
+      }
+      bool shared_cut = false;             // within a shared bin: not from counts
+      {
+        const int share_of = kMaxCtas / ctas, mine = rank * (kKeys / ctas) + tid * share_of;   // this thread's bins
+        cl.sync();
+        // a bin of all CTAs
+        auto count_of = [&](int b) {
+          unsigned n = 0;
+#pragma unroll
+          for (int i = 0; i < kMaxCtas; ++i)
+            if (i < ctas) n += *cl.map_shared_rank(&sh.keys[b], i);
+          return n;
+        };
+        auto weight_of = [&](int b, unsigned n) {
+          const int place = top - b;
+          if (!shared_place(place)) return n ? n * weigh.of<true>(of_place(place)) : 0ull;
+          u64 w = 0;
+          for (int i = 0; n && i < ctas; ++i) {
+            w += *cl.map_shared_rank(&sh.near_lo[place < 0], i);
+            w += (u64)*cl.map_shared_rank(&sh.near_hi[place < 0], i) << 32;
+          }
+          return w;
+        };
+        unsigned n = 0;
+        u64 w = 0;
+        for (int i = 0; i < share_of; ++i) {
+          const unsigned x = count_of(mine + i);
+          n += x;
+          w += weight_of(mine + i, x);
+        }
+        const u64 n_upto = top_k > 0 ? scan_block(n, sh.scan) : 0ull, w_upto = scan_block(w, sh.scan);
+        if (tid == kNT - 1) {
+          sh.slice = w_upto;
+          sh.slice_count = (unsigned)n_upto;
+        }
+        cl.sync();
+        // what the CTAs before this one have, and all of them
+        u64 w_before = 0, w_all = 0;
+        unsigned n_before = 0, n_all = 0;
+        for (int i = 0; i < ctas; ++i) {
+          const u64 x = *cl.map_shared_rank(&sh.slice, i);
+          const unsigned y = *cl.map_shared_rank(&sh.slice_count, i);
+          if (i < rank) { w_before += x; n_before += y; }
+          w_all += x;
+          n_all += y;
+        }
+        // The bin where the running count (or weight) reaches `want`, found by the thread that has it.
+        auto pick = [&](bool weights, u64 want) {
+          const u64 upto = weights ? w_before + w_upto : n_before + n_upto, before = upto - (weights ? w : (u64)n);
+          if (tid == 0) sh.pick = -1;
+          __syncthreads();
+          if (before < want && want <= upto) {
+            u64 run = before, run_w = w_before + w_upto - w;
+            for (int i = 0; i < share_of; ++i) {
+              const unsigned x = count_of(mine + i);
+              const u64 wx = weight_of(mine + i, x), step = weights ? wx : (u64)x;
+              if (run + step >= want) {
+                const u64 one = x ? wx / x : 1ull;
+                sh.pick = mine + i;
+                sh.pick_t = weights ? (want - run + one - 1) / one : want - run;
+                sh.above = run_w;
+                break;
+              }
+              run += step;
+              run_w += wx;
+            }
+          }
+          cl.sync();
+          const int at = min(lane, ctas - 1), got = *cl.map_shared_rank(&sh.pick, at);
+          const u64 got_t = *cl.map_shared_rank(&sh.pick_t, at), got_above = *cl.map_shared_rank(&sh.above, at);
+          const int who = __ffs(__ballot_sync(0xffffffffu, got >= 0)) - 1, b = __shfl_sync(0xffffffffu, got, max(who, 0));
+          const int place = top - b;
+          if (who < 0 || shared_place(place)) {
+            shared_cut = true;
+          } else {
+            K = of_place(place);
+            t = __shfl_sync(0xffffffffu, got_t, who);
+            w_all = __shfl_sync(0xffffffffu, got_above, who);   // above K
+            all = false;
+          }
+        };
+        if (top_k > 0 && (unsigned)top_k < n_all) pick(false, (u64)top_k);
+        if (top_p < 1.f && !shared_cut) {
+          const u64 one = all ? 0ull : weigh.of<true>(K), want = top_p > 0.f ? max(share(top_p, w_all + t * one, true), 1ull) : 1ull;
+          if (want > w_all && !all) {
+            const u64 x = (want - w_all + one - 1) / one;   // reached among those equal to K
+            t = min(t, x);
+          } else if (want < w_all || !all) {
+            cl.sync();                     // the last pick has been read
+            pick(true, want);
+          }
+        }
+      }
+      if (min_p > 0.f && !shared_cut) {
+        const float f = __double2float_ru((double)hi + sh.cut);
+        if (f > K) {
+          K = f;
+          t = ~0ull;
+          all = false;
+        }
+      }
+      // (0 < |K| < 2^-9: a shared bin is kept in part)
+      if (!shared_cut && (K == 0.f || fabsf(K) >= 0x1p-9f)) {
+        // this CTA's weight above K, and how many are K
+        __syncthreads();
+        u64 sum = 0;
+        for (int b = tid; b < bins; b += kNT) {
+          const int place = top - b;
+          const unsigned n = sh.keys[b];
+          const float l = of_place(place);
+          if (shared_place(place)) {
+            if (place > 0 ? K <= 0.f : K < 0.f) sum += (u64)sh.near_lo[place < 0] | (u64)sh.near_hi[place < 0] << 32;
+          } else if (n && l > K) {
+            sum += n * weigh.of<true>(l);
+          }
+        }
+        const u64 upto = scan_block(sum, sh.scan);
+        if (tid == kNT - 1) {
+          const int b = top - place_of(K);
+          sh.part_sum = upto;
+          sh.part_equal = !all && b >= 0 && b < bins && of_place(top - b) == K ? (int)sh.keys[b] : 0;
+        }
+        cl.sync();
+        const u64 wK = all ? 0ull : weigh.of<true>(K), part = lane < ctas ? *cl.map_shared_rank(&sh.part_sum, lane) : 0ull,
+                  eq = lane < ctas ? (u64)*cl.map_shared_rank(&sh.part_equal, lane) : 0ull;
+        const u64 eq_before = scan_warp(eq) - eq, take = eq_before >= t ? 0ull : min(eq, t - eq_before), w = part + take * wK, w_upto = scan_warp(w);
+        total = __shfl_sync(0xffffffffu, w_upto, 31);
+        goal = drawn(u01, total);
+        const int who = __ffs(__ballot_sync(0xffffffffu, goal < w_upto)) - 1;
+        goal -= __shfl_sync(0xffffffffu, w_upto - w, who);
+        t = __shfl_sync(0xffffffffu, take, who);
+        placed = true;
+        // the CTA `who` has it: its part of the row, in stretches of all warps
+        origin = min(vectors, who * per);
+        const int end = min(vectors, origin + per), chunk = (per + ctas * kWarps - 1) / (ctas * kWarps);
+        first = min(end, origin + (rank * kWarps + warp) * chunk);
+        last = min(end, first + chunk);
+        if (STAGED) source = cl.map_shared_rank(held, who);
+      } else {
+        K = least_below(weigh.least);
+        t = 0;
+        all = true;
+        cl.sync();
+        if (tid == 0) sh.listed = 0;
+        __syncthreads();
+      }
+    }
+  }
+  auto there = [&](int j) { return STAGED ? source[j - origin] : row.load(j); };
 
   // Cuts what is kept so far (above K, t of those equal to K) where the running
   // count (or weight) reaches `part` (a share of all of it, for weights).
@@ -657,9 +875,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     all = false;
     cl.sync();                             // the lists and spans are free again
   };
-  if (top_k > 0 && top_k < a.vocab) cut(false, 0.f);
-  if (top_p < 1.f) cut(true, top_p);
-  if (min_p > 0.f) {
+  if (!placed && top_k > 0 && top_k < a.vocab) cut(false, 0.f);
+  if (!placed && top_p < 1.f) cut(true, top_p);
+  if (!placed && min_p > 0.f) {
     // l >= M + T ln(min_p): the smallest fp32 that is
     const float f = __double2float_ru((double)hi + sh.cut);
     if (f > K) {
@@ -672,9 +890,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   // ---- each warp's weight above K and number equal to K
   u64 sum = 0;
   int equal = 0;
-  if (all) {
-    for (int j = v0 + lane; j < v1; j += 32) {
-      const uint4 u = vector(j);
+  if (all || placed) {
+    for (int j = first + lane; j < last; j += 32) {
+      const uint4 u = there(j);
 #pragma unroll 1
       for (int i0 = 0; i0 < N; i0 += 4) {
         const uint2 half = N == 8 && i0 ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
@@ -685,6 +903,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           int steps;
           const u64 w = weigh.of_counting<kExact>(l, steps);
           if (l > K) sum += w;
+          if (!all) equal += l == K;
         }
       }
     }
@@ -698,16 +917,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       const u64 w = weigh.of_counting<kExact>(queue[lane], steps);
       if (lane < queued) sum += w;
     };
-    for (int j0 = v0; j0 < v1; j0 += 32) {
+    for (int j0 = first; j0 < last; j0 += 32) {
       const int j = j0 + lane;
-      const uint4 u = j < v1 ? vector(j) : make_uint4(0u, 0u, 0u, 0u);
-      const float most = j < v1 ? Vec<T>::largest(u) : -INFINITY;
+      const uint4 u = j < last ? there(j) : make_uint4(0u, 0u, 0u, 0u);
+      const float most = j < last ? Vec<T>::largest(u) : -INFINITY;
       if (!__any_sync(0xffffffffu, most >= K)) continue;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         const float l = Vec<T>::at(u, i);
-        const bool on = j < v1 && l > K;
-        equal += j < v1 && l == K;
+        const bool on = j < last && l > K;
+        equal += j < last && l == K;
         const unsigned who = __ballot_sync(0xffffffffu, on);
         if (on) queue[queued + __popc(who & ((1u << lane) - 1u))] = l;
         queued += __popc(who);
@@ -746,25 +965,28 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     sh.found = -1;
   }
   __syncthreads();
-  const u64 total = sh.total, goal = drawn(u01, total);
+  if (!placed) {
+    total = sh.total;
+    goal = drawn(u01, total);
+  }
   __syncthreads();
   if (tid < ctas * kWarps && tid / kWarps == rank && goal < upto && goal >= upto - mine) {
     sh.found = tid % kWarps;               // the stretch that has it
     sh.found_before = upto - mine;
     sh.total = take;                       // how many of the stretch's equals are kept
   }
-  cl.sync();                               // no CTA leaves while another reads it
-  if (warp != sh.found) return;
+  __syncthreads();
+  const bool chosen_here = warp == sh.found;
   u64 left = goal - sh.found_before;
   int spare = (int)min(sh.total, (u64)INT32_MAX);
-  for (int j0 = v0; j0 < v1; j0 += 32) {
+  for (int j0 = first; chosen_here && j0 < last; j0 += 32) {
     const int j = j0 + lane;
-    const uint4 u = j < v1 ? vector(j) : make_uint4(0u, 0u, 0u, 0u);
+    const uint4 u = j < last ? there(j) : make_uint4(0u, 0u, 0u, 0u);
     u64 w[N], s = 0;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float l = j < v1 ? Vec<T>::at(u, i) : -INFINITY;
+      const float l = j < last ? Vec<T>::at(u, i) : -INFINITY;
       int steps;
       w[i] = weigh.of_counting<kExact>(l, steps);
       if (!(l > K)) w[i] = 0ull;
@@ -798,11 +1020,12 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         }
         put(j * N - row.lead + at, chosen, total);
       }
-      return;
+      break;
     }
     left -= __shfl_sync(0xffffffffu, s_upto, 31);
     spare -= __shfl_sync(0xffffffffu, n_upto, 31);
   }
+  cl.sync();                               // no CTA leaves while another reads it
 }
 
 template <typename T>
