@@ -409,6 +409,8 @@ struct PagedAttnArgs {
   float* lse;
   float* part_o;               // [splits][rows * nq][hd], unnormalised
   float2* part_ml;             // [splits][rows * nq] (maximum in log2 units, sum)
+  int4* segment;               // [rows] first CTA, CTAs, token in the CTA, where a tree call is in segments
+  int target;                  // trees: segments of a head that run at once, 0: equal splits
   long long q_stride;
   int rows, nq, G, causal, window, splits, max_len;
   int cluster;                 // the splits are a cluster's CTAs, which join their partials themselves
@@ -418,8 +420,9 @@ struct PagedAttnArgs {
   float decay;
 };
 // How an attention call is split: chosen from sizes alone.
-struct PagedPlan { int kind, splits, cluster; long long tiles, bytes; };
+struct PagedPlan { int kind, splits, cluster, target; long long tiles, bytes; };
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
+PagedPlan paged_tree_plan(int dtype, const PagedAttnArgs& a);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
 cudaError_t launch_paged_attention_tf32(int dtype, const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);

@@ -77,6 +77,107 @@ __device__ __forceinline__ PagedTile paged_find_tile(const int* start, int n_seq
   return r;
 }
 
+// The same where sequences are cut into segments of keys, for batches of trees, so
+// that no sequence sets the time alone. `sms` CTAs of a head run at once; the segments
+// are as short as fills them once, or as many times as the batch has query tiles for,
+// or twice where that evens out sequences of different lengths. (A segment's start and
+// end take as long as about 8 key tiles, joining them 4.) Number `t` of the segments:
+// which sequence, which query tile, which of the tile's n ranges of keys. Up to 32
+// sequences come in the order of their segments' lengths, longest first, which fills
+// the SMs evenly.
+constexpr int kPagedLeastTiles = 4;
+struct PagedSegment { PagedTile t; int z, n; };
+__device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, const int* start, int rows, int per, int keys, int window,
+                                                           int sms, int t) {
+  const int lane = threadIdx.x & 31;
+  PagedSegment r{{-1, 0, 0, 0}, 0, 1};
+  // of sequence s: its new rows, its query tiles and the key tiles that they may see
+  int first = 0, count = 0, q_tiles = 0, k_tiles = 0;
+  auto look = [&](int s) {
+    first = count = q_tiles = k_tiles = 0;
+    if (s >= c.n_seq) return;
+    const int2 ab = paged_new_rows(start, s, rows);
+    first = ab.x;
+    count = ab.y - ab.x;
+    q_tiles = (count + per - 1) / per;
+    k_tiles = (paged_length(c, s) + keys - 1) / keys;
+    if (window > 0) k_tiles = min(k_tiles, (int)min(((long long)window + count) / keys + 2, 1ll << 20));
+  };
+  long long work = 0;
+  int tiles = 0;
+  for (int s0 = 0; s0 < c.n_seq; s0 += 32) {
+    look(s0 + lane);
+    work += (long long)q_tiles * k_tiles;
+    tiles += q_tiles;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) work += __shfl_xor_sync(0xffffffffu, work, o);
+  tiles = __reduce_add_sync(0xffffffffu, tiles);
+  int rounds = max(1, (tiles + sms - 1) / sms), length;
+  if (c.n_seq <= 32) {
+    const int longest = __reduce_max_sync(0xffffffffu, q_tiles ? k_tiles : 0);
+    // the shortest segments of which there are at most `most`
+    auto shortest = [&](int most) {
+      if (c.n_seq == 1 && tiles > 0) {
+        const int n = most / tiles;
+        return max(kPagedLeastTiles, (longest + n - 1) / n);
+      }
+      int lo = max(kPagedLeastTiles, (int)(work / most)), hi = max(lo, longest);
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (__reduce_add_sync(0xffffffffu, q_tiles * ((k_tiles + mid - 1) / mid)) <= most) hi = mid;
+        else lo = mid + 1;
+      }
+      return lo;
+    };
+    length = shortest(rounds * sms);
+    if (rounds == 1 && length + 8 + (length < longest ? 4 : 0) > (int)(work / sms) + (int)(work / sms) / 12 + 20) length = shortest(2 * sms);
+  } else {
+    // (the sum of the quotients rounded up is at most work / length + tiles)
+    const int spare = (rounds + 1) * sms - tiles;
+    length = max(kPagedLeastTiles, (int)((work + spare - 1) / spare));
+  }
+  for (int s0 = 0; s0 < c.n_seq; s0 += 32) {
+    if (c.n_seq > 32) look(s0 + lane);
+    int n = max(1, (k_tiles + length - 1) / length), mine = q_tiles * n, seq = s0 + lane;
+    if (c.n_seq <= 32 && c.n_seq > 1) {
+      const int each = q_tiles ? (k_tiles + n - 1) / n : -1;
+      int rank = 0, from = 0;
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const int other = __shfl_sync(0xffffffffu, each, i);
+        rank += other > each || (other == each && i < lane);
+      }
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) from = __shfl_sync(0xffffffffu, rank, i) == lane ? i : from;
+      n = __shfl_sync(0xffffffffu, n, from);
+      mine = __shfl_sync(0xffffffffu, mine, from);
+      first = __shfl_sync(0xffffffffu, first, from);
+      count = __shfl_sync(0xffffffffu, count, from);
+      seq = from;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, t < incl);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      t -= __shfl_sync(0xffffffffu, incl - mine, l);
+      r.n = __shfl_sync(0xffffffffu, n, l);
+      r.z = t % r.n;
+      r.t.seq = __shfl_sync(0xffffffffu, seq, l);
+      r.t.tile = t / r.n;
+      r.t.first = __shfl_sync(0xffffffffu, first, l);
+      r.t.count = __shfl_sync(0xffffffffu, count, l);
+      return r;
+    }
+    t -= __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return r;
+}
 // The mask of the header. What one query at pq sees is a range of positions
 // and the prefix: two unsigned comparisons, both false for kPagedNoPos.
 struct PagedMask { int causal, window, prefix; };

@@ -76,7 +76,7 @@ int check_attention(const dflash_paged_cache* c, const dflash_paged_attention_ar
     return refuse(DFLASH_EINVAL, "paged attention: softcap must be 0 or in [1e-18, 1e18]");
   if (a->max_len < 0) return refuse(DFLASH_EINVAL, "paged attention: max_len is negative");
   x->q = a->q; x->q_pos = a->q_pos; x->start = a->start; x->slopes = a->slopes; x->prefix = a->prefix;
-  x->tree = nullptr;
+  x->tree = nullptr; x->segment = nullptr; x->target = 0;
   x->out = a->out; x->lse = a->lse;
   x->part_o = nullptr; x->part_ml = nullptr;
   x->q_stride = a->q_stride; x->rows = a->rows; x->nq = a->n_q_heads; x->G = a->n_q_heads / c->kv_heads;
@@ -106,14 +106,18 @@ int check_evict(const dflash_paged_cache* c, const dflash_paged_evict_args* a, P
 
 int attend(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, PagedAttnArgs* x, void* stream) {
   if (a->rows == 0) return DFLASH_OK;
-  const PagedPlan p = paged_attn_plan(cache->dtype, *x);
+  const PagedPlan p = x->tree ? paged_tree_plan(cache->dtype, *x) : paged_attn_plan(cache->dtype, *x);
   if (p.bytes > 0) {
     PG(need(a->workspace, "workspace"));
     if (a->workspace_bytes < p.bytes)
       return refuse(DFLASH_EINVAL, "paged attention: workspace of %lld bytes, %lld needed", (long long)a->workspace_bytes, (long long)p.bytes);
     x->part_o = static_cast<float*>(a->workspace);
-    x->part_ml = reinterpret_cast<float2*>(x->part_o + (int64_t)p.splits * a->rows * a->n_q_heads * cache->head_dim);
+    // partials of every split of every row, or of every row of every segment
+    const int64_t parts = p.target ? p.tiles * cache->kv_heads * p.kind * 128 : (int64_t)p.splits * a->rows * a->n_q_heads;
+    x->part_ml = reinterpret_cast<float2*>(x->part_o + parts * cache->head_dim);
+    x->segment = reinterpret_cast<int4*>(x->part_ml + parts);
   }
+  x->target = p.target;
   x->splits = p.splits;
   x->cluster = p.cluster;
   return launched(launch_paged_attention(cache->dtype, *x, p, static_cast<cudaStream_t>(stream)), "paged attention");
@@ -186,7 +190,12 @@ int dflash_paged_attention(const dflash_paged_cache* cache, const dflash_paged_a
 }
 
 int dflash_paged_tree_attention_workspace(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, int64_t* bytes_host) {
-  return dflash_paged_attention_workspace(cache, a, bytes_host);
+  PagedAttnArgs x;
+  if (!bytes_host) return refuse(DFLASH_EINVAL, "paged attention: bytes_host is NULL");
+  *bytes_host = 0;
+  PG(check_attention(cache, a, false, &x));
+  if (a->rows > 0) *bytes_host = paged_tree_plan(cache->dtype, x).bytes;
+  return DFLASH_OK;
 }
 
 int dflash_paged_tree_attention(const dflash_paged_cache* cache, const dflash_paged_attention_args* a, const int32_t* tree_end, void* stream) {

@@ -13,6 +13,7 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kBN = 64;                    // keys of a key-weight tile
+constexpr int kSms = 152;
 
 // Score of a raw dot product in log2 units.
 struct PagedScore { float scale2, cap2; };
@@ -207,6 +208,61 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
   }
 }
 
+// The same of segments, a CTA to some heads of a token, whose segments lie where its
+// first one says. (A token of one segment has its output.)
+constexpr int kMergeWarps = 8;
+template <typename T>
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of) {
+  pdl_enter();
+  const int lane = threadIdx.x & 31, hd = a.c.hd, row = blockIdx.x;
+  const int4 s = a.segment[row];
+  if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
+  // (of a row that no CTA had, as descending starts may leave, anything)
+  if (s.y <= 1 || s.x < 0 || s.y > ctas - s.x || s.z < 0 || (s.z + 1) * a.G > rows_of) return;
+  for (int head = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); head < a.nq; head += gridDim.y * kMergeWarps) {
+    const size_t stride = (size_t)a.c.nkv * rows_of, p0 = ((size_t)s.x * a.c.nkv + head / a.G) * rows_of + s.z * a.G + head % a.G;
+    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+    constexpr int kU = 8;                    // segments requested together
+    for (int z0 = 0; z0 < s.y; z0 += kU) {
+      float2 ml[kU];
+      float4 x[kU];
+      float top = M;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const bool in = z0 + u < s.y;
+        ml[u] = in ? a.part_ml[p0 + (z0 + u) * stride] : make_float2(-INFINITY, 0.f);
+        x[u] = in && lane * 4 < hd ? *reinterpret_cast<const float4*>(a.part_o + (p0 + (z0 + u) * stride) * hd + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) top = fmaxf(top, ml[u].x);
+      const float base = top == -INFINITY ? 0.f : top, old = exp2f(M - base);
+      M = top;
+      L *= old;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) acc[d] *= old;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        if (ml[u].y == 0.f) continue;        // it saw nothing
+        const float f = exp2f(ml[u].x - base);
+        L += ml[u].y * f;
+        acc[0] = fmaf(f, x[u].x, acc[0]);
+        acc[1] = fmaf(f, x[u].y, acc[1]);
+        acc[2] = fmaf(f, x[u].z, acc[2]);
+        acc[3] = fmaf(f, x[u].w, acc[3]);
+      }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const long long at = (long long)row * a.nq + head;
+    if (lane * 4 < hd) {
+      __align__(8) T o[4];
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] = from_f<T>(acc[d] * inv);
+      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * hd + lane * 4) = *reinterpret_cast<const uint2*>(o);
+    }
+    if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  }
+}
+
 template <typename K>
 cudaError_t big_smem(K* kernel, size_t bytes) {
   return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
@@ -224,6 +280,8 @@ int expected_len(const PagedAttnArgs& a) {
   const int cap = a.c.max_pages << a.c.lg_rows;
   return a.max_len > 0 && a.max_len < cap ? a.max_len : cap;
 }
+// Rows of a segment's partials.
+long long paged_segment_rows(int kind) { return kind * 128; }
 // Tiles a batch of `units` query rows can have at most, `per` to a tile.
 long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
   return units / per + (a.c.n_seq < a.rows ? a.c.n_seq : a.rows);
@@ -234,7 +292,7 @@ long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
 // kind 1 and 2: tcgen05 (bf16, head_dim <= 128), that many tiles of 128 packed
 // query rows to a CTA; 16: mma.sync in tf32, that many rows.
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
-  PagedPlan p{0, 1, 0, 0, 0};
+  PagedPlan p{0, 1, 0, 0, 0, 0};
   const long long len = expected_len(a), units = (long long)a.rows * a.G;
   long long fill, least;
   if (dtype && a.c.hd <= 128) {
@@ -281,10 +339,34 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
   return p;
 }
 
+// For trees. Few query tiles over a few thousand keys as above. Otherwise the batch
+// goes in segments of keys that even out its sequences: the longest would set the
+// time.
+PagedPlan paged_tree_plan(int dtype, const PagedAttnArgs& a) {
+  PagedPlan p = paged_attn_plan(dtype, a);
+  const long long len = expected_len(a);
+  if (p.kind > 2 || p.cluster || len <= 1024 || a.c.n_seq > 1024) return p;
+  const int per = 128 / a.G * p.kind;
+  // (a sum of quotients rounded up, whatever the rows of each sequence are)
+  const long long most = a.c.n_seq < a.rows ? a.c.n_seq : a.rows;
+  const long long q_tiles = (a.rows + most * (per - 1)) / per;
+  p.target = a.c.nkv < kSms ? kSms / a.c.nkv : 1;
+  p.splits = 1;
+  // one round more than the query tiles need is the most that paged_find_segment makes
+  p.tiles = ((q_tiles + p.target - 1) / p.target + 1) * p.target;
+  p.bytes = p.tiles * a.c.nkv * paged_segment_rows(p.kind) * (a.c.hd + 2) * 4 + (long long)a.rows * 16;
+  return p;
+}
+
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st) {
   cudaError_t e;
   if (p.kind <= 2) e = a.tree ? launch_paged_tree_attention_tc(a, p.kind, p.tiles, st) : launch_paged_attention_tc(a, p.kind, p.tiles, st);
   else e = launch_paged_attention_tf32(dtype, a, p.tiles, st);
+  if (e == cudaSuccess && p.target) {
+    // (CTAs that find nothing to do take time too)
+    const int most = (a.nq + kMergeWarps - 1) / kMergeWarps, some = 1 + 1216 / a.rows;
+    return launch_pdl(paged_tree_merge_kernel<bf16>, dim3((unsigned)a.rows, some < most ? some : most), dim3(kMergeWarps * 32), 0, st, a, (int)p.tiles, (int)paged_segment_rows(p.kind));
+  }
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));
   return dtype ? launch_pdl(paged_attn_merge_kernel<bf16>, mg, dim3(128), 0, st, a)

@@ -107,7 +107,11 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 
   const PagedView& c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int h = blockIdx.y, z = blockIdx.z, G = a.G;
+  // Segments come in one row of CTAs, all heads of one after the other: those that a
+  // batch does not need are the last to start, when the others have their SMs.
+  const bool segments = TREE && a.target > 0;
+  const int h = segments ? blockIdx.x % c.nkv : blockIdx.y, bx = segments ? blockIdx.x / c.nkv : blockIdx.x, G = a.G;
+  int z = blockIdx.z, splits = a.splits;
   const int tpt = kPtKeys / G;                          // new rows of a tile
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* sm = smem_raw + (((raw + 1023) & ~1023u) - raw);
@@ -141,6 +145,18 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   }
   fence_proxy_async_shared();
   pdl_wait();
+  // every warp looks for the tile itself: no one waits for another's answer
+  PagedTile t;
+  if (segments) {                                        // z of the tile's `splits` segments is this CTA's
+
+    const PagedSegment g = paged_find_segment(c, a.start, a.rows, QT * tpt, kPtKeys, a.window, a.target, bx);
+    t = g.t;
+    z = g.z;
+    splits = g.n;
+  } else {
+    t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, bx);
+  }
+  if (segments && t.seq < 0) return;                     // one more than the batch needs
   // TMEM only once the kernel before has given its own back, and the next
   // kernel only once every CTA of this one has its share: neither can then
   // wait for columns that the other holds while it waits
@@ -148,8 +164,6 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tmem_alloc(&tmem_holder, 512);
     pdl_launch_dependents();
   }
-  // every warp looks for the tile itself: no one waits for another's answer
-  const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, 1, QT * tpt, blockIdx.x);
   int qmin = INT32_MAX, qmax = INT32_MIN, len = 0;
   PagedMask m{};
   if (t.seq >= 0) {
@@ -164,11 +178,61 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     qmin = __reduce_min_sync(0xffffffffu, qmin);
     qmax = __reduce_max_sync(0xffffffffu, qmax);
   }
-  PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, a.splits);
+  PagedShare sh = paged_range((len + kPtKeys - 1) / kPtKeys, a.window, z, splits);
   // One query tile without a window sees nearly every row there is: no
   // classification beforehand, the warps that need to know look at a tile's
   // positions, which they request a tile ahead.
-  const bool direct = paged_direct(sh) || (QT == 1 && !sh.by_share);
+  // (Not so for trees: with K and V streaming in, a load takes longer than a tile. 19
+  // sequences of 64 rows over 8192 keys: 225 us looked at on the way, 146 us classified.)
+  const bool direct = paged_direct(sh) || (QT == 1 && !TREE && !sh.by_share);
+  const int row0 = t.tile * QT * tpt;                    // the CTA's first new row, within the sequence
+  const int nt = (QT == 2 && row0 + tpt < t.count) ? 2 : 1;
+  // With one query tile of at most 64 (32) rows, its rows are there 2 (4) times,
+  // in quarters of 32 lanes, and a warp takes a half (a quarter) of the keys.
+  const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
+  const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
+  auto load_q = [&]() {
+    if (rep == 1) {
+      mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
+      for (int i = 0; i < nt; ++i)
+        for (int x = 0; x < C::kHalves; ++x)
+          tma_load_3d(sm + C::kQ + i * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, t.first + row0 + i * tpt, &q_full);
+    } else {
+      mbar_expect_tx(&q_full, 4 * C::kHalves * t32 * G * 128);
+      for (int i = 0; i < 4; ++i)
+        for (int x = 0; x < C::kHalves; ++x)
+          tma_load_3d(sm + C::kQ + x * C::kHalfB + i * 32 * 128, &mq32, x * 64, h * G, t.first + row0 + (i & (4 / rep - 1)) * t32, &q_full);
+    }
+  };
+  const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;   // of a tile's loads, a lane to each
+  auto row_of = [&](int rel) {
+    const int slot = (sh.t0 + rel) * kPtKeys + lane * box;
+    int y = (c.n_pages * c.nkv) << c.lg_rows;            // a row past the pool reads as zeros
+    if (lane < boxes && slot < len) {
+      const long long row = paged_row(c, t.seq, h, slot);
+      if (row >= 0) y = (int)row;
+      else if (c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+    }
+    return y;
+  };
+  auto load_kv = [&](int kv, int s, int y) {
+    if (lane == 0) mbar_expect_tx(&kv_full[s], C::kTileB);
+    __syncwarp();
+    if (lane < boxes)
+#pragma unroll
+      for (int x = 0; x < C::kHalves; ++x)
+        tma_load_2d(sm + C::kKV + s * C::kTileB + x * C::kHalfB + lane * box * 128, kv ? &mv : &mk, x * 64, y, &kv_full[s]);
+  };
+  // A segment's first tile is on its way while the tiles are classified; it is taken
+  // whether it is seen or not.
+  const bool early = segments && !direct && !sh.by_share && sh.t1 > sh.t0;
+  if (early && warp == wLoad) {
+    if (lane == 0) load_q();
+    const int y = row_of(0);
+    load_kv(0, 0, y);
+    load_kv(1, 1, y);
+    __syncwarp();
+  }
   if (direct) {
     for (int i = threadIdx.x; i <= sh.take >> 5; i += C::kThreads) {
       const int left = sh.take - i * 32;
@@ -177,6 +241,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     }
   } else {
     paged_classify<kPtKeys>(c, t.seq, h, len, m, qmin, qmax, sh.t0, sh.t1, some, all);
+    if (early && threadIdx.x == 0) atomicOr(&some[0], 1u);
   }
   tc_fence_before();
   __syncthreads();
@@ -187,17 +252,20 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     if (warp == wMma) tmem_dealloc(tmem, 512);
     return;
   }
-  paged_take(sh, some, z, a.splits);
+  paged_take(sh, some, z, splits);
   const int N = sh.take;                                 // tiles this CTA works on
-  const int row0 = t.tile * QT * tpt;                    // its first new row, within the sequence
-  const int nt = (QT == 2 && row0 + tpt < t.count) ? 2 : 1;
   PagedCursor cur(some, sh);
   bool ok = true;
-  // With one query tile of at most 64 (32) rows, its rows are there 2 (4) times,
-  // in quarters of 32 lanes, and a warp takes a half (a quarter) of the keys.
-  const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
-  const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
-  const bool joins = a.cluster || rep > 1;               // the output comes out of shared memory
+  const bool parts = segments && splits > 1 && rep == 1; // a segment's partials, which leave by way of shared memory
+  const bool joins = a.cluster || rep > 1 || parts;      // the output comes out of shared memory
+  // Where the partial of (token in this CTA's tiles, head of the group) goes. Of segments
+  // the merge hears where a token's are.
+  const size_t part0 = segments ? ((size_t)bx * c.nkv + h) * (QT * kPtKeys) : (size_t)z * a.rows * a.nq;
+  auto partial = [&](int token, int g) {
+    return segments ? part0 + token * G + g : part0 + (size_t)(t.first + row0 + token) * a.nq + h * G + g;
+  };
+  if (segments && h == 0 && z == 0)
+    for (int i = threadIdx.x; i < min(QT * tpt, t.count - row0); i += C::kThreads) a.segment[t.first + row0 + i] = make_int4(bx, splits, i, 0);
   // P in two parts, the second `low` columns on
   const bool two_parts = QT == 2 ? MANY && nt == 1 && n_tok <= 2 * t32 : rep > 1;
   constexpr int low = QT == 2 ? 128 : 64;
@@ -233,30 +301,15 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
 
   if (warp == wLoad) {
     // ---- loads: Q, then K and V of every tile, a box per page (or per 128 rows of one)
-    if (N > 0 && lane == 0) {
-      if (rep == 1) {
-        mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
-        for (int i = 0; i < nt; ++i)
-          for (int x = 0; x < C::kHalves; ++x)
-            tma_load_3d(sm + C::kQ + i * C::kTileB + x * C::kHalfB, &mq, x * 64, h * G, t.first + row0 + i * tpt, &q_full);
-      } else {
-        mbar_expect_tx(&q_full, 4 * C::kHalves * t32 * G * 128);
-        for (int i = 0; i < 4; ++i)
-          for (int x = 0; x < C::kHalves; ++x)
-            tma_load_3d(sm + C::kQ + x * C::kHalfB + i * 32 * 128, &mq32, x * 64, h * G, t.first + row0 + (i & (4 / rep - 1)) * t32, &q_full);
-      }
-    }
-    const int box = min(1 << c.lg_rows, kPtKeys), boxes = kPtKeys / box;
-    const int beyond = (c.n_pages * c.nkv) << c.lg_rows;   // a row past the pool reads as zeros
+    if (N > 0 && lane == 0 && !early) load_q();
     int issued = 0;
     for (int i = 0; i < N && ok; ++i) {
-      const int slot = (sh.t0 + cur.next()) * kPtKeys + lane * box;
-      int y = beyond;
-      if (lane < boxes && slot < len) {
-        const long long row = paged_row(c, t.seq, h, slot);
-        if (row >= 0) y = (int)row;
-        else if (c.status) atomicOr(c.status, DFLASH_PAGED_BAD_PAGE);
+      const int rel = cur.next();
+      if (i == 0 && early) {
+        issued = 2;
+        continue;
       }
+      const int y = row_of(rel);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv) {
         const int n = 2 * i + kv, s = n % NS;
@@ -265,13 +318,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           ok = false;                                    // the stage is not free: no further load
           break;
         }
-        if (lane == 0) mbar_expect_tx(&kv_full[s], C::kTileB);
-        __syncwarp();
         issued = n + 1;
-        if (lane < boxes)
-#pragma unroll
-          for (int x = 0; x < C::kHalves; ++x)
-            tma_load_2d(sm + C::kKV + s * C::kTileB + x * C::kHalfB + lane * box * 128, kv ? &mv : &mk, x * 64, y, &kv_full[s]);
+        load_kv(kv, s, y);
       }
     }
     // no copy may be in flight when the CTA ends, whatever became of the others
@@ -801,9 +849,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           tmem_ld_wait32(o);
         }
         if (!valid) continue;
-        if (joins || a.splits > 1) {
-          float* po = joins ? reinterpret_cast<float*>(sm) + (q * 128 + r) * kClusterLd + d
-                            : a.part_o + ((size_t)z * a.rows * a.nq + at) * c.hd + d;
+        if (joins || splits > 1) {
+          float* po = joins ? reinterpret_cast<float*>(sm) + (q * 128 + r) * kClusterLd + d : a.part_o + partial(q * tpt + tl, g) * c.hd + d;
 #pragma unroll
           for (int x = 0; x < 32; x += 4)
             if (d + x < c.hd && !none) *reinterpret_cast<float4*>(po + x) = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
@@ -821,20 +868,34 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
           }
         }
       }
+      if (TREE && parts) fence_proxy_async_shared();     // the row leaves as a bulk copy
       if (valid && !joins) {
-        if (a.splits > 1) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx, sum);
+        if (splits > 1) a.part_ml[partial(q * tpt + tl, g)] = make_float2(mx, sum);
         else if (a.lse) a.lse[at] = none ? -INFINITY : (mx + log2f(sum)) * kLn2;
       }
     }
   }
-  if (joins) {
+  if (parts) {
+    // Row by row as bulk copies: a thread's own stores would be 16 bytes at a time, each in
+    // a line of its own (a segment's end: 2 us, with them 8 us).
+    __syncthreads();
+    for (int R = threadIdx.x; R < nt * 128; R += C::kThreads) {
+      const int tl = (R & 127) / G;
+      if (tl >= tpt || row0 + (R >> 7) * tpt + tl >= t.count) continue;
+      const size_t part = partial((R >> 7) * tpt + tl, (R & 127) % G);
+      const float2 ml = s_ml[R];
+      a.part_ml[part] = ml;
+      if (ml.y != 0.f) bulk_store(a.part_o + part * c.hd, reinterpret_cast<const float*>(sm) + R * kClusterLd, c.hd * 4);
+    }
+    bulk_store_wait();
+  } else if (joins) {
     // The parts of a row, `rep` in each CTA and the CTAs of the cluster where
     // those are the splits, are joined out of shared memory 4 dimensions at a
     // time: o = sum_x o_x exp2(m_x - M) / sum_x l_x exp2(m_x - M).
     cg::cluster_group cl = cg::this_cluster();
     if (a.cluster) cl.sync();
     else __syncthreads();
-    const int ctas = a.cluster ? a.splits : 1, rows = nt * 128 / rep, quads = c.hd >> 2;
+    const int ctas = a.cluster ? splits : 1, rows = nt * 128 / rep, quads = c.hd >> 2;
     for (int e = (a.cluster ? z : 0) * C::kThreads + (int)threadIdx.x; e < rows * quads; e += ctas * C::kThreads) {
       const int R = e / quads, d = (e - R * quads) * 4, lr = rep > 1 ? R & 31 : R & 127;
       const int tl = lr / G + (rep > 1 ? (R >> 5) * t32 : 0), at_row = row0 + (rep > 1 ? 0 : (R >> 7) * tpt) + tl;
@@ -874,8 +935,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
         }
       }
       const size_t at = (size_t)(t.first + at_row) * a.nq + h * G + lr % G;
-      if (a.splits > 1 && !a.cluster) {
-        const size_t part = (size_t)z * a.rows * a.nq + at;
+      if (splits > 1 && !a.cluster) {
+        const size_t part = partial(at_row - row0, lr % G);
         *reinterpret_cast<float4*>(a.part_o + part * c.hd + d) = v;
         if (d == 0) a.part_ml[part] = make_float2(M, L);
         continue;
@@ -908,7 +969,7 @@ cudaError_t run(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)tiles, a.c.nkv, a.splits);
+  cfg.gridDim = a.target ? dim3((unsigned)(tiles * a.c.nkv)) : dim3((unsigned)tiles, a.c.nkv, a.splits);
   cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = st;
