@@ -409,7 +409,7 @@ struct PagedAttnArgs {
   float* lse;
   float* part_o;               // [splits][rows * nq][hd], unnormalised
   float2* part_ml;             // [splits][rows * nq] (maximum in log2 units, sum)
-  int4* segment;               // [rows] first CTA, CTAs, token in the CTA, where a tree call is in segments
+  int4* segment;               // [rows] trees: first segment of the sequence, segments of a tile, place in the sequence
   int target;                  // trees: segments of a head that run at once, 0: equal splits
   long long q_stride;
   int rows, nq, G, causal, window, splits, max_len;
@@ -423,6 +423,7 @@ struct PagedAttnArgs {
 struct PagedPlan { int kind, splits, cluster, target; long long tiles, bytes; };
 PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a);
 PagedPlan paged_tree_plan(int dtype, const PagedAttnArgs& a);
+long long paged_segment_rows(int kind);
 cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const PagedPlan& p, cudaStream_t st);
 cudaError_t launch_paged_attention_tf32(int dtype, const PagedAttnArgs& a, long long tiles, cudaStream_t st);
 cudaError_t launch_paged_attention_tc(const PagedAttnArgs& a, int q_tiles, long long tiles, cudaStream_t st);

@@ -87,8 +87,8 @@ __device__ __forceinline__ PagedTile paged_find_tile(const int* start, int n_seq
 // the SMs evenly.
 constexpr int kPagedLeastTiles = 4;
 struct PagedSegment { PagedTile t; int z, n; };
-__device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, const int* start, int rows, int per, int keys, int window,
-                                                           int sms, int t) {
+__device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, const int* start, int rows, int G, int per, int keys,
+                                                           int window, int sms, int t) {
   const int lane = threadIdx.x & 31;
   PagedSegment r{{-1, 0, 0, 0}, 0, 1};
   // of sequence s: its new rows, its query tiles and the key tiles that they may see
@@ -99,7 +99,7 @@ __device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, c
     const int2 ab = paged_new_rows(start, s, rows);
     first = ab.x;
     count = ab.y - ab.x;
-    q_tiles = (count + per - 1) / per;
+    q_tiles = (int)(((long long)count * G + per - 1) / per);
     k_tiles = (paged_length(c, s) + keys - 1) / keys;
     if (window > 0) k_tiles = min(k_tiles, (int)min(((long long)window + count) / keys + 2, 1ll << 20));
   };

@@ -113,7 +113,7 @@ int attend(const dflash_paged_cache* cache, const dflash_paged_attention_args* a
       return refuse(DFLASH_EINVAL, "paged attention: workspace of %lld bytes, %lld needed", (long long)a->workspace_bytes, (long long)p.bytes);
     x->part_o = static_cast<float*>(a->workspace);
     // partials of every split of every row, or of every row of every segment
-    const int64_t parts = p.target ? p.tiles * cache->kv_heads * p.kind * 128 : (int64_t)p.splits * a->rows * a->n_q_heads;
+    const int64_t parts = p.target ? p.tiles * cache->kv_heads * paged_segment_rows(p.kind) : (int64_t)p.splits * a->rows * a->n_q_heads;
     x->part_ml = reinterpret_cast<float2*>(x->part_o + parts * cache->head_dim);
     x->segment = reinterpret_cast<int4*>(x->part_ml + parts);
   }

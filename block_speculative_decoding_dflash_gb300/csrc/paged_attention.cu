@@ -208,56 +208,68 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
   }
 }
 
-// The same of segments, a CTA to some heads of a token, whose segments lie where its
-// first one says. (A token of one segment has its output.)
+// The same of segments, a CTA to some heads of a token. A segment has `rows_of` rows,
+// of `per` tokens, or (per 0) rows of heads one after the other, whichever tokens they
+// are. (A token of one segment has its output.)
 constexpr int kMergeWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of) {
+__global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of, int per) {
   pdl_enter();
   const int lane = threadIdx.x & 31, hd = a.c.hd, row = blockIdx.x;
   const int4 s = a.segment[row];
   if (row < a.start[0] || row >= a.start[a.c.n_seq]) return;
   // (of a row that no CTA had, as descending starts may leave, anything)
-  if (s.y <= 1 || s.x < 0 || s.y > ctas - s.x || s.z < 0 || (s.z + 1) * a.G > rows_of) return;
+  if (s.y <= 1 || s.y > ctas || s.x < 0 || s.x >= ctas || s.z < 0 || s.z >= a.rows) return;
   for (int head = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); head < a.nq; head += gridDim.y * kMergeWarps) {
-    const size_t stride = (size_t)a.c.nkv * rows_of, p0 = ((size_t)s.x * a.c.nkv + head / a.G) * rows_of + s.z * a.G + head % a.G;
-    float M = -INFINITY, L = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    constexpr int kU = 8;                    // segments requested together
-    for (int z0 = 0; z0 < s.y; z0 += kU) {
-      float2 ml[kU];
-      float4 x[kU];
-      float top = M;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const bool in = z0 + u < s.y;
-        ml[u] = in ? a.part_ml[p0 + (z0 + u) * stride] : make_float2(-INFINITY, 0.f);
-        x[u] = in && lane * 4 < hd ? *reinterpret_cast<const float4*>(a.part_o + (p0 + (z0 + u) * stride) * hd + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int u = 0; u < kU; ++u) top = fmaxf(top, ml[u].x);
-      const float base = top == -INFINITY ? 0.f : top, old = exp2f(M - base);
-      M = top;
-      L *= old;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc[d] *= old;
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (ml[u].y == 0.f) continue;        // it saw nothing
-        const float f = exp2f(ml[u].x - base);
-        L += ml[u].y * f;
-        acc[0] = fmaf(f, x[u].x, acc[0]);
-        acc[1] = fmaf(f, x[u].y, acc[1]);
-        acc[2] = fmaf(f, x[u].z, acc[2]);
-        acc[3] = fmaf(f, x[u].w, acc[3]);
-      }
-    }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int g = head % a.G, packed = s.z * a.G + g, tile = per ? s.z / per : packed / rows_of, place = per ? s.z % per * a.G + g : packed % rows_of;
+    const long long x = s.x + (long long)tile * s.y;       // the first of its segments
+    if (x + s.y > ctas) continue;
+    const size_t stride = (size_t)a.c.nkv * rows_of, p0 = ((size_t)x * a.c.nkv + head / a.G) * rows_of + place;
     const long long at = (long long)row * a.nq + head;
-    if (lane * 4 < hd) {
-      __align__(8) T o[4];
+    float M = -INFINITY, L = 0.f;
+    // 128 dimensions at a time, a lane to four
+    for (int d = lane * 4; d - lane * 4 < hd; d += 128) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      M = -INFINITY;
+      L = 0.f;
+      constexpr int kU = 8;                  // segments requested together
+      for (int z0 = 0; z0 < s.y; z0 += kU) {
+        float2 ml[kU];
+        float4 x[kU];
+        float top = M;
 #pragma unroll
-      for (int d = 0; d < 4; ++d) o[d] = from_f<T>(acc[d] * inv);
-      *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + at * hd + lane * 4) = *reinterpret_cast<const uint2*>(o);
+        for (int u = 0; u < kU; ++u) {
+          const bool in = z0 + u < s.y;
+          ml[u] = in ? a.part_ml[p0 + (z0 + u) * stride] : make_float2(-INFINITY, 0.f);
+          x[u] = in && d < hd ? *reinterpret_cast<const float4*>(a.part_o + (p0 + (z0 + u) * stride) * hd + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) top = fmaxf(top, ml[u].x);
+        const float base = top == -INFINITY ? 0.f : top, old = exp2f(M - base);
+        M = top;
+        L *= old;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] *= old;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (ml[u].y == 0.f) continue;      // it saw nothing
+          const float f = exp2f(ml[u].x - base);
+          L += ml[u].y * f;
+          acc[0] = fmaf(f, x[u].x, acc[0]);
+          acc[1] = fmaf(f, x[u].y, acc[1]);
+          acc[2] = fmaf(f, x[u].z, acc[2]);
+          acc[3] = fmaf(f, x[u].w, acc[3]);
+        }
+      }
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      if (d < hd) {
+        __align__(16) T o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = from_f<T>(acc[i] * inv);
+        T* out = static_cast<T*>(a.out) + at * hd + d;
+        if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(out) = *reinterpret_cast<const float4*>(o);
+        else *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(o);
+      }
     }
     if (lane == 0 && a.lse) a.lse[at] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
   }
@@ -280,8 +292,6 @@ int expected_len(const PagedAttnArgs& a) {
   const int cap = a.c.max_pages << a.c.lg_rows;
   return a.max_len > 0 && a.max_len < cap ? a.max_len : cap;
 }
-// Rows of a segment's partials.
-long long paged_segment_rows(int kind) { return kind * 128; }
 // Tiles a batch of `units` query rows can have at most, `per` to a tile.
 long long tile_bound(long long units, int per, const PagedAttnArgs& a) {
   return units / per + (a.c.n_seq < a.rows ? a.c.n_seq : a.rows);
@@ -339,18 +349,24 @@ PagedPlan paged_attn_plan(int dtype, const PagedAttnArgs& a) {
   return p;
 }
 
+// Rows of a segment's partials.
+long long paged_segment_rows(int kind) { return kind <= 2 ? kind * 128 : 16; }
+
 // For trees. Few query tiles over a few thousand keys as above. Otherwise the batch
 // goes in segments of keys that even out its sequences: the longest would set the
 // time.
 PagedPlan paged_tree_plan(int dtype, const PagedAttnArgs& a) {
   PagedPlan p = paged_attn_plan(dtype, a);
   const long long len = expected_len(a);
-  if (p.kind > 2 || p.cluster || len <= 1024 || a.c.n_seq > 1024) return p;
-  const int per = 128 / a.G * p.kind;
+  if (p.cluster || len <= 1024 || a.c.n_seq > 1024) return p;
+  const bool tc = p.kind <= 2;
+  const long long units = tc ? a.rows : (long long)a.rows * a.G, per = tc ? 128 / a.G * p.kind : p.kind;
   // (a sum of quotients rounded up, whatever the rows of each sequence are)
   const long long most = a.c.n_seq < a.rows ? a.c.n_seq : a.rows;
-  const long long q_tiles = (a.rows + most * (per - 1)) / per;
-  p.target = a.c.nkv < kSms ? kSms / a.c.nkv : 1;
+  const long long q_tiles = (units + most * (per - 1)) / per;
+  // CTAs that run at once (fp32 heads of more than 128 dimensions: one to an SM, as of the tcgen05 kernels)
+  const int at_once = tc || (!dtype && a.c.hd > 128) ? kSms : 2 * kSms;
+  p.target = a.c.nkv < at_once ? at_once / a.c.nkv : 1;
   p.splits = 1;
   // one round more than the query tiles need is the most that paged_find_segment makes
   p.tiles = ((q_tiles + p.target - 1) / p.target + 1) * p.target;
@@ -364,8 +380,11 @@ cudaError_t launch_paged_attention(int dtype, const PagedAttnArgs& a, const Page
   else e = launch_paged_attention_tf32(dtype, a, p.tiles, st);
   if (e == cudaSuccess && p.target) {
     // (CTAs that find nothing to do take time too)
-    const int most = (a.nq + kMergeWarps - 1) / kMergeWarps, some = 1 + 1216 / a.rows;
-    return launch_pdl(paged_tree_merge_kernel<bf16>, dim3((unsigned)a.rows, some < most ? some : most), dim3(kMergeWarps * 32), 0, st, a, (int)p.tiles, (int)paged_segment_rows(p.kind));
+    const int most = (a.nq + kMergeWarps - 1) / kMergeWarps, some = 1 + 1216 / a.rows, rows_of = (int)paged_segment_rows(p.kind);
+    const dim3 grid((unsigned)a.rows, some < most ? some : most);
+    const int per = p.kind <= 2 ? 128 / a.G * p.kind : 0;
+    return dtype ? launch_pdl(paged_tree_merge_kernel<bf16>, grid, dim3(kMergeWarps * 32), 0, st, a, (int)p.tiles, rows_of, per)
+                 : launch_pdl(paged_tree_merge_kernel<float>, grid, dim3(kMergeWarps * 32), 0, st, a, (int)p.tiles, rows_of, per);
   }
   if (e != cudaSuccess || p.splits <= 1 || p.cluster) return e;
   const dim3 mg((unsigned)(((long long)a.rows * a.nq + 3) / 4));

@@ -149,7 +149,7 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   PagedTile t;
   if (segments) {                                        // z of the tile's `splits` segments is this CTA's
 
-    const PagedSegment g = paged_find_segment(c, a.start, a.rows, QT * tpt, kPtKeys, a.window, a.target, bx);
+    const PagedSegment g = paged_find_segment(c, a.start, a.rows, 1, QT * tpt, kPtKeys, a.window, a.target, bx);
     t = g.t;
     z = g.z;
     splits = g.n;
@@ -259,13 +259,13 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   const bool parts = segments && splits > 1 && rep == 1; // a segment's partials, which leave by way of shared memory
   const bool joins = a.cluster || rep > 1 || parts;      // the output comes out of shared memory
   // Where the partial of (token in this CTA's tiles, head of the group) goes. Of segments
-  // the merge hears where a token's are.
+  // the merge hears where its sequence's start.
   const size_t part0 = segments ? ((size_t)bx * c.nkv + h) * (QT * kPtKeys) : (size_t)z * a.rows * a.nq;
   auto partial = [&](int token, int g) {
     return segments ? part0 + token * G + g : part0 + (size_t)(t.first + row0 + token) * a.nq + h * G + g;
   };
   if (segments && h == 0 && z == 0)
-    for (int i = threadIdx.x; i < min(QT * tpt, t.count - row0); i += C::kThreads) a.segment[t.first + row0 + i] = make_int4(bx, splits, i, 0);
+    for (int i = threadIdx.x; i < min(QT * tpt, t.count - row0); i += C::kThreads) a.segment[t.first + row0 + i] = make_int4(bx - t.tile * splits, splits, row0 + i, 0);
   // P in two parts, the second `low` columns on
   const bool two_parts = QT == 2 ? MANY && nt == 1 && n_tok <= 2 * t32 : rep > 1;
   constexpr int low = QT == 2 ? 128 : 64;

@@ -87,6 +87,7 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t k_full, v_full;
   __shared__ PagedTile st;
+  __shared__ int s_z, s_splits;
   __shared__ int s_qmin, s_qmax;
   __shared__ unsigned s_bad[kBN / 32];
   const uint32_t raw = smem_u32(smem_raw);
@@ -104,9 +105,14 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   }
   pdl_enter();
   const PagedView& c = a.c;
-  const int h = blockIdx.y, z = blockIdx.z, G = a.G, hd = c.hd;
+  const bool segments = TREE && a.target > 0;              // in one row of CTAs, see the tcgen05 kernel
+  const int h = segments ? blockIdx.x % c.nkv : blockIdx.y, bx = segments ? blockIdx.x / c.nkv : blockIdx.x, G = a.G, hd = c.hd;
   if (threadIdx.x < 32) {
-    const PagedTile t = paged_find_tile(a.start, c.n_seq, a.rows, G, kBM, blockIdx.x);
+    PagedSegment f{{}, (int)blockIdx.z, a.splits};
+    if (segments) f = paged_find_segment(c, a.start, a.rows, G, kBM, kBN, a.window, a.target, bx);
+    else f.t = paged_find_tile(a.start, c.n_seq, a.rows, G, kBM, bx);
+    const PagedTile t = f.t;
+    if (threadIdx.x == 0) { s_z = f.z; s_splits = f.n; }
     int lo = INT32_MAX, hi = INT32_MIN;
     if (t.seq >= 0) {
       const int r0 = t.tile * kBM, r1 = min(t.count * G, r0 + kBM);
@@ -123,11 +129,14 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   __syncthreads();
   const PagedTile t = st;
   if (t.seq < 0) return;
+  const int z = s_z, splits = s_splits;
   const int len = paged_length(c, t.seq);
   if (threadIdx.x == 0 && h == 0 && z == 0 && t.tile == 0) paged_report_length(c, t.seq, len);
   const PagedMask m = paged_mask(a.causal, a.window, a.prefix, t.seq);
-  PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, a.splits);
+  PagedShare sh = paged_range((len + kBN - 1) / kBN, a.window, z, splits);
   const int r0 = t.tile * kBM, n_rows = min(kBM, t.count * G - r0);
+  if (segments && h == 0 && z == 0)
+    for (int i = r0 / G + (int)threadIdx.x; i <= (r0 + n_rows - 1) / G; i += NT) a.segment[t.first + i] = make_int4(bx - t.tile * splits, splits, i, 0);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, e4 = lane & 3;
   // Q, zeros past hd and past the last row
   auto q_at = [&](int r, int d) {
@@ -167,7 +176,7 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
   // a score in log2 units: dot * scale2, or cap2 * tanh(dot * scale2)
   const float scale2 = a.softcap > 0.f ? a.scale / a.softcap : a.scale * kLog2e, cap2 = a.softcap * kLog2e;
   __syncthreads();
-  paged_take(sh, some, z, a.splits);
+  paged_take(sh, some, z, splits);
   PagedCursor cur(some, sh);
 
   // A row's place: its page is requested a tile before it is needed.
@@ -420,9 +429,10 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
     for (int w = 0; w < kWarps; ++w) total += smax[w * kBM + r];
     const size_t at = (size_t)(t.first + (r0 + r) / G) * a.nq + h * G + (r0 + r) % G;
     const bool none = total == 0.f;          // nothing seen (a NaN score makes the sum NaN)
-    const bool split = a.splits > 1;
+    const bool split = splits > 1;
+    const size_t part_at = segments ? ((size_t)bx * c.nkv + h) * kBM + r : (size_t)z * a.rows * a.nq + at;
     const float inv = none ? 0.f : (split ? 1.f : 1.f / total);
-    float* part = a.part_o + ((size_t)z * a.rows * a.nq + at) * hd;
+    float* part = a.part_o + part_at * hd;
     T* out = static_cast<T*>(a.out) + at * hd;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -436,7 +446,7 @@ paged_attn_tf32_kernel(const __grid_constant__ CUtensorMap mk, const __grid_cons
       }
     }
     if (warp || e4) continue;
-    if (split) a.part_ml[(size_t)z * a.rows * a.nq + at] = make_float2(mx[i], total);
+    if (split) a.part_ml[part_at] = make_float2(mx[i], total);
     else if (a.lse) a.lse[at] = none ? -INFINITY : (mx[i] + log2f(total)) * kLn2;
   }
 }
@@ -452,7 +462,7 @@ cudaError_t run_as(const PagedAttnArgs& a, long long tiles, cudaStream_t st) {
   constexpr size_t smem = Tf32Shape<T, HDP>::kSmem;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), smem, st, mk, mv, a);
+  return launch_pdl(kernel, a.target ? dim3((unsigned)(tiles * a.c.nkv)) : dim3((unsigned)tiles, a.c.nkv, a.splits), dim3(kWarps * 32), smem, st, mk, mv, a);
 }
 
 template <typename T, int HDP>
