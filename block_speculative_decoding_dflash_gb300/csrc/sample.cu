@@ -77,15 +77,10 @@ struct Weigh {
   __device__ __forceinline__ int bin(float l) const { return whole_steps(steps((top - l) * chi)) >> kBinShift; }
   // The weight of a token that counts as whole * 2^-(steps / 2^10) units, before the
   // shift drops bits; of others anything. No branches: a thread has several tokens' weights under way at once.
-  // EXACT: M - l is an fp32 number (of bf16 logits, whose distance is one wherever it counts).
-  template <bool EXACT>
   __device__ __forceinline__ void parts(float l, u64& whole, int& i) const {
     const float d = top - l, p = d * chi;
-    float e = fmaf(d, clo, fmaf(d, chi, -p));
-    if (!EXACT) {
-      const float b = d - top;
-      e = fmaf((top - (d - b)) + (-l - b), chi, e);
-    }
+    const float b = d - top;               // what d's rounding left: (M - (d - b)) + (-l - b)
+    const float e = fmaf((top - (d - b)) + (-l - b), chi, fmaf(d, clo, fmaf(d, chi, -p)));
     const float t = steps(p);
     i = whole_steps(t);
     const float r = (p - (t - 12288.f)) + e;              // p = i / 1024 + r, |r| <= 2^-11
@@ -98,16 +93,14 @@ struct Weigh {
         : "=l"(whole) : "r"(__float_as_int(w.x)), "r"(1 << (kUnit - 24)), "l"((u64)0 - (kBias << (kUnit - 24))), "r"(c), "r"(1 << (kUnit - 42)));
   }
   // (what the shift drops is made up for by a set last bit, on average)
-  template <bool EXACT>
   __device__ __forceinline__ u64 of_counting(float l, int& i) const {
     u64 whole;
-    parts<EXACT>(l, whole, i);
+    parts(l, whole, i);
     return (whole >> (i >> 10)) | 1ull;
   }
-  template <bool EXACT>
   __device__ __forceinline__ u64 of(float l) const {
     int i;
-    const u64 w = of_counting<EXACT>(l, i);
+    const u64 w = of_counting(l, i);
     return counts(l) ? w : 0ull;
   }
 };
@@ -318,7 +311,7 @@ __device__ __forceinline__ u64 sort_block(u64 x, int n, u64* s, u64* few) {
 template <typename T, bool STAGED>
 __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   constexpr int N = Vec<T>::N;
-  constexpr bool kExact = sizeof(T) == 2;
+  constexpr bool kBins16 = sizeof(T) == 2; // logits of 16 bits may have a bin for each number
   extern __shared__ __align__(16) uint4 held[];
   __shared__ Shared sh;
   __shared__ float2 table[kSteps];
@@ -333,7 +326,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     for (int i = tid; i < kKeys / 4; i += kNT) reinterpret_cast<uint4*>(sh.keys)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2) sh.near_lo[tid] = sh.near_hi[tid] = 0u;
   };
-  if (kExact) clear_keys();
+  if (kBins16) clear_keys();
   pdl_enter();
 
   // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
@@ -404,7 +397,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     if (!a.prob) return;
     u64 whole;
     int i;
-    weigh.parts<kExact>(l, whole, i);
+    weigh.parts(l, whole, i);
     a.prob[r] = (float)((double)whole * __longlong_as_double((long long)(1023 - (i >> 10)) << 52) / (double)total);
   };
 
@@ -508,7 +501,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     if (weigh.counts(own) && weigh.bin(own) <= far)
       for (int j = v0 + lane; j < v1; j += 32) {
         const uint4 u = vector(j);
-        if (!(Vec<T>::largest(u) >= weigh.least)) continue;
+        const float most = Vec<T>::largest(u);
+        if (!weigh.counts(most) || weigh.bin(most) > far) continue;
+#pragma unroll
         for (int i = 0; i < N; ++i) {
           const float l = Vec<T>::at(u, i);
           if (weigh.counts(l) && weigh.bin(l) <= far) list(l, j * N - row.lead + i);
@@ -521,7 +516,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         u64 x = sort_block(xs[0], n, sh.sort.all, sh.sort.few);
         // in descending order of logits: top_k, top_p, min_p
         const float l = x == ~0ull ? -INFINITY : entry_logit(x);
-        u64 w = tid < n && tid < top_k ? weigh.of<kExact>(l) : 0ull;
+        u64 w = tid < n && tid < top_k ? weigh.of(l) : 0ull;
         const u64 before = scan_block(w, sh.scan) - w;
         if (tid == kNT - 1) sh.total = before + w;
         __syncthreads();
@@ -534,7 +529,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         const int kept = __syncthreads_count(w != 0);      // (the first ones)
         x = sort_block(x, kept, sh.sort.all, sh.sort.few);
         const float lt = entry_logit(x << 32 | x >> 32);
-        w = x == ~0ull ? 0ull : weigh.of<kExact>(lt);
+        w = x == ~0ull ? 0ull : weigh.of(lt);
         const u64 upto_t = scan_block(w, sh.scan);
         if (tid == kNT - 1) sh.total = upto_t;
         __syncthreads();
@@ -546,7 +541,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     }
     cl.sync();                             // the lists are free again
     if (tid == 0) sh.listed = 0;
-    if (kExact) {
+    if (kBins16) {
       clear_keys();
       __syncthreads();
     }
@@ -562,7 +557,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   // numbers times their counts, a cut is found in one step, and what each CTA keeps
   // follows from its own counts: weights of single tokens are taken of one CTA's
   // part only, by all of them.
-  if constexpr (kExact) if (top_k > 0 || top_p < 1.f) {
+  if constexpr (kBins16) if (top_k > 0 || top_p < 1.f) {
     // (down to the smallest bf16 number that counts)
     const int low = __float_as_int(weigh.least), top = place_of(hi), bins = top - place_of((low + (low < 0 ? 0 : 0xffff)) >> 16) + 1;
     if (bins <= kKeys) {
@@ -579,7 +574,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         }
         for (; near; near &= near - 1) {
           const float l = Vec<T>::at(u, __ffs(near) - 1);
-          const u64 w = weigh.of<true>(l);
+          const u64 w = weigh.of(l);
           const int side = l < 0.f;
           const unsigned old = atomicAdd(&sh.near_lo[side], (unsigned)w);
           atomicAdd(&sh.near_hi[side], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
@@ -599,7 +594,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         };
         auto weight_of = [&](int b, unsigned n) {
           const int place = top - b;
-          if (!shared_place(place)) return n ? n * weigh.of<true>(of_place(place)) : 0ull;
+          if (!shared_place(place)) return n ? n * weigh.of(of_place(place)) : 0ull;
           u64 w = 0;
           for (int i = 0; n && i < ctas; ++i) {
             w += *cl.map_shared_rank(&sh.near_lo[place < 0], i);
@@ -667,7 +662,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         };
         if (top_k > 0 && (unsigned)top_k < n_all) pick(false, (u64)top_k);
         if (top_p < 1.f && !shared_cut) {
-          const u64 one = all ? 0ull : weigh.of<true>(K), want = top_p > 0.f ? max(share(top_p, w_all + t * one, true), 1ull) : 1ull;
+          const u64 one = all ? 0ull : weigh.of(K), want = top_p > 0.f ? max(share(top_p, w_all + t * one, true), 1ull) : 1ull;
           if (want > w_all && !all) {
             const u64 x = (want - w_all + one - 1) / one;   // reached among those equal to K
             t = min(t, x);
@@ -697,7 +692,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           if (shared_place(place)) {
             if (place > 0 ? K <= 0.f : K < 0.f) sum += (u64)sh.near_lo[place < 0] | (u64)sh.near_hi[place < 0] << 32;
           } else if (n && l > K) {
-            sum += n * weigh.of<true>(l);
+            sum += n * weigh.of(l);
           }
         }
         const u64 upto = scan_block(sum, sh.scan);
@@ -707,7 +702,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           sh.part_equal = !all && b >= 0 && b < bins && of_place(top - b) == K ? (int)sh.keys[b] : 0;
         }
         cl.sync();
-        const u64 wK = all ? 0ull : weigh.of<true>(K), part = lane < ctas ? *cl.map_shared_rank(&sh.part_sum, lane) : 0ull,
+        const u64 wK = all ? 0ull : weigh.of(K), part = lane < ctas ? *cl.map_shared_rank(&sh.part_sum, lane) : 0ull,
                   eq = lane < ctas ? (u64)*cl.map_shared_rank(&sh.part_equal, lane) : 0ull;
         const u64 eq_before = scan_warp(eq) - eq, take = eq_before >= t ? 0ull : min(eq, t - eq_before), w = part + take * wK, w_upto = scan_warp(w);
         total = __shfl_sync(0xffffffffu, w_upto, 31);
@@ -738,7 +733,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   // count (or weight) reaches `part` (a share of all of it, for weights).
   auto cut = [&](bool weights, float part) {
     const float K0 = K;
-    const u64 t0 = t, wK = !all && weights ? weigh.of<kExact>(K0) : 1ull;  // (a K that is a logit)
+    const u64 t0 = t, wK = !all && weights ? weigh.of(K0) : 1ull;  // (a K that is a logit)
     const u64 tail = all ? 0ull : t0 * wK;                // what those equal to K count
     auto in = [&](float l) { return l > K0; };
     for (int j = v0 + lane; j < v1; j += 32) {
@@ -756,7 +751,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           w[i] = 1;
           at[i] = 0;
           if (weights) {
-            w[i] = weigh.of_counting<kExact>(l, at[i]);
+            w[i] = weigh.of_counting(l, at[i]);
             at[i] >>= kBinShift;
           } else {
             at[i] = weigh.bin(l);
@@ -832,7 +827,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     for (int i = 0; i < kEach; ++i) {
       const float l = xs[i] == ~0ull ? -INFINITY : entry_logit(xs[i]);
       kx[i] = key_of<T>(l);
-      wx[i] = weights ? weigh.of<kExact>(l) : 1ull;
+      wx[i] = weights ? weigh.of(l) : 1ull;
     }
     while (kmin != kmax) {
       int shift = 0;
@@ -852,7 +847,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           for (int i = 0; i < N; ++i) {
             const float l = Vec<T>::at(u, i);
             const unsigned k = key_of<T>(l);
-            if (k >= kmin && k <= kmax && in(l) && weigh.bin(l) == where) add(weights, (int)((kmax - k) >> shift), weights ? weigh.of<kExact>(l) : 1ull);
+            if (k >= kmin && k <= kmax && in(l) && weigh.bin(l) == where) add(weights, (int)((kmax - k) >> shift), weights ? weigh.of(l) : 1ull);
           }
         }
         merged(weights, bin, upto);
@@ -870,7 +865,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       __syncthreads();
     }
     K = of_key<T>(kmax);
-    const u64 w1 = weights ? weigh.of<kExact>(K) : 1ull;
+    const u64 w1 = weights ? weigh.of(K) : 1ull;
     t = (goal - before + w1 - 1) / w1;
     all = false;
     cl.sync();                             // the lists and spans are free again
@@ -893,18 +888,13 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   if (all || placed) {
     for (int j = first + lane; j < last; j += 32) {
       const uint4 u = there(j);
-#pragma unroll 1
-      for (int i0 = 0; i0 < N; i0 += 4) {
-        const uint2 half = N == 8 && i0 ? make_uint2(u.z, u.w) : make_uint2(u.x, u.y);
-        const uint4 four = N == 8 ? make_uint4(half.x, half.y, 0, 0) : u;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float l = Vec<T>::at(four, i);
-          int steps;
-          const u64 w = weigh.of_counting<kExact>(l, steps);
-          if (l > K) sum += w;
-          if (!all) equal += l == K;
-        }
+      for (int i = 0; i < N; ++i) {
+        const float l = Vec<T>::at(u, i);
+        int steps;
+        const u64 w = weigh.of_counting(l, steps);
+        if (l > K) sum += w;
+        if (!all) equal += l == K;
       }
     }
   } else {
@@ -914,7 +904,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     auto weigh_queue = [&]() {
       __syncwarp();
       int steps;
-      const u64 w = weigh.of_counting<kExact>(queue[lane], steps);
+      const u64 w = weigh.of_counting(queue[lane], steps);
       if (lane < queued) sum += w;
     };
     for (int j0 = first; j0 < last; j0 += 32) {
@@ -950,7 +940,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     sh.equal[warp] = all_equal;
   }
   cl.sync();
-  const u64 wK = all ? 0ull : weigh.of<kExact>(K);
+  const u64 wK = all ? 0ull : weigh.of(K);
   u64 mine = 0, eq = 0;
   if (tid < ctas * kWarps) {
     mine = *cl.map_shared_rank(&sh.sum[tid % kWarps], tid / kWarps);
@@ -988,7 +978,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     for (int i = 0; i < N; ++i) {
       const float l = j < last ? Vec<T>::at(u, i) : -INFINITY;
       int steps;
-      w[i] = weigh.of_counting<kExact>(l, steps);
+      w[i] = weigh.of_counting(l, steps);
       if (!(l > K)) w[i] = 0ull;
       s += w[i];
       n += l == K;
