@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
 // are. (A token of one segment has its output.)
 constexpr int kMergeWarps = 8;
 template <typename T>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of, int per) {
+__global__ void __launch_bounds__(kMergeWarps * 32, 4) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of, int per) {
   pdl_enter();
   const int lane = threadIdx.x & 31, hd = a.c.hd, row = blockIdx.x;
   const int4 s = a.segment[row];
@@ -232,7 +232,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(Page
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       M = -INFINITY;
       L = 0.f;
-      constexpr int kU = 8;                  // segments requested together
+      constexpr int kU = 6;                  // segments requested together
+      const float2* at_ml = a.part_ml + p0;
+      const float* at_o = a.part_o + p0 * hd + d;
+      const size_t step_o = stride * hd;
       for (int z0 = 0; z0 < s.y; z0 += kU) {
         float2 ml[kU];
         float4 x[kU];
@@ -240,8 +243,10 @@ __global__ void __launch_bounds__(kMergeWarps * 32) paged_tree_merge_kernel(Page
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
           const bool in = z0 + u < s.y;
-          ml[u] = in ? a.part_ml[p0 + (z0 + u) * stride] : make_float2(-INFINITY, 0.f);
-          x[u] = in && d < hd ? *reinterpret_cast<const float4*>(a.part_o + (p0 + (z0 + u) * stride) * hd + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+          ml[u] = in ? *at_ml : make_float2(-INFINITY, 0.f);
+          x[u] = in && d < hd ? *reinterpret_cast<const float4*>(at_o) : make_float4(0.f, 0.f, 0.f, 0.f);
+          at_ml += stride;
+          at_o += step_o;
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) top = fmaxf(top, ml[u].x);
