@@ -258,6 +258,9 @@ int dflash_paged_tree_commit(const dflash_paged_cache* caches, const dflash_page
         c->n_seq != c0->n_seq || c->max_pages != c0->max_pages || c->dtype != c0->dtype)
       return refuse(DFLASH_EINVAL, "paged tree commit: cache %d has other sizes or another type than the first", i);
     if (a->weight_host) PG(may(a->weight_host[i], "weight"));
+    for (int j = 0; j < i; ++j)            // (a row that moves twice would be lost)
+      if (c->k == caches[j].k || c->v == caches[j].v || c->pos == caches[j].pos)
+        return refuse(DFLASH_EINVAL, "paged tree commit: caches %d and %d share an array", j, i);
   }
   if ((int64_t)c0->n_seq * a->width >= (1ll << 31)) return refuse(DFLASH_ERANGE, "paged tree commit: n_seq * width reaches 2^31");
   PG(need4(a->path, "path"));

@@ -215,6 +215,36 @@ def test_trees_after_long_texts_many_times(B, nq, nkv, hd, dtype, window, n):
     assert torch.equal(outs[0][0], first[0]) and int(s.status) == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,spare", [([(3, 1100 + 9 * i) for i in range(36)], 1), ([(1 + i % 3, 30 + i % 9) for i in range(270)], 70),
+                                        ([(1 + 5 * (i % 3), 150 * i + 60) for i in range(24)], 0)])
+def test_trees_of_many_sequences(B, lens, spare, dtype):
+    """More sequences than are put in order, more than are cut into segments, and all lengths in one call."""
+    s = Trees(B, lens, 2, 1, 64, 16, dtype, seed=1, spare=spare, lead=1, tail=2)
+    s.check(s.device())
+    assert int(s.status) == 0
+
+
+def test_more_query_tiles_than_segments_are_made_for(B):
+    s = Trees(B, [(1500, 1600)], 128, 8, 64, 16, seed=1, shape="chain")
+    cache = s.device()
+    out, lse = s.call(cache)
+    want, want_lse = torch.full_like(out, 77.0), torch.full_like(lse, 77.0)
+    cache.attention(s.q.cuda(), s.q_pos.cuda(), s.start.cuda(), want, lse=want_lse)
+    assert torch.allclose(out.float(), want.float(), rtol=2.0 ** -7, atol=2.0 ** -9) and torch.allclose(lse, want_lse, rtol=1e-6, atol=1e-5)
+
+
+@pytest.mark.parametrize("starts", [[0, 9, 4, 12], [12, 5, 9, 0], [-3, 40, 50, 60], [5, 5, 5, 5]])
+def test_row_ranges_that_cannot_be(B, starts):
+    """Descending and overlong ranges are cut; rows in none of them are not written."""
+    s = Trees(B, [(4, 2000), (4, 300), (4, 1500)], 4, 2, 64, 16, seed=4)
+    s.start = torch.tensor(starts, dtype=torch.int32)
+    out, lse = s.call(s.device())
+    held = {r for a, b in zip(starts, starts[1:]) for r in range(max(a, 0), min(b, 12))}
+    free = [r for r in range(12) if r not in held]
+    assert (out[free] == 77).all() and (lse[free] == 77).all()
+
+
 # ---- sampling ----------------------------------------------------------------------------
 
 

@@ -192,7 +192,7 @@ def test_tree_attention_refuses_a_small_workspace(B):
     refused(B, c.tree_attention, "workspace", **attention_args(q=torch.zeros(5, 4, 64), out=torch.zeros(5, 4, 64), workspace=torch.zeros(4, dtype=torch.uint8)))
 
 
-@pytest.mark.parametrize("what", ["none", "sizes", "type", "width", "path", "count", "many"])
+@pytest.mark.parametrize("what", ["none", "sizes", "type", "width", "path", "count", "many", "twice"])
 def test_commit_refuses(B, what):
     make = lambda **o: B.PagedCache.allocate(**{**dict(n_pages=4, page_rows=16, kv_heads=2, head_dim=64, n_seq=3, max_pages=2), **o}, device="cpu")  # noqa: E731
     a = dict(caches=[make(), make()], path=ints(3, 4), count=ints(3))
@@ -208,8 +208,10 @@ def test_commit_refuses(B, what):
         a["path"] = ints(2, 4)
     elif what == "count":
         a["count"] = torch.zeros(3, dtype=torch.int64)
-    else:
+    elif what == "many":
         a["caches"] = a["caches"][:1] * 1025
+    else:
+        a["caches"][1] = a["caches"][0]                  # a row that moves twice would be lost
     refused(B, B.paged_tree_commit, **a)
 
 
