@@ -24,6 +24,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <utility>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "launch.cuh"
@@ -228,22 +230,24 @@ struct Shared {
     unsigned keys[kKeys];                  // bf16: how many of the CTA's logits each bin has, from the largest down
   };
   unsigned near_lo[2], near_hi[2];         // the weight in the shared bins above and below zero
-  u64 slice, above;                        // of this CTA's share of the bins: their weight; at the cut, the weight above it
-  unsigned slice_count;
-  int pick;                                // the bin of the cut
-  u64 pick_t;
-  u64 part_sum;                            // of this CTA's part of the row: the weight above K,
-  int part_equal;                          // and how many are K
+  // What every CTA says to every other, in the order of the CTAs:
+  float tops[kMaxCtas];                    // the largest logit,
+  int firsts[kMaxCtas];                    // and the first token that has it (of rows that take it)
+  u64 slices[kMaxCtas];                    // its share of the bins: their weight
+  unsigned slice_counts[kMaxCtas];
+  u64 part_sums[kMaxCtas];                 // its part of the row: the weight above K,
+  int part_equals[kMaxCtas];               // and how many are K
+  u64 sums[kMaxCtas * kWarps];             // the same of each warp's stretch
+  int equals[kMaxCtas * kWarps];
+  int pick;                                // and the one that has it: the bin of the cut (-1: none said so), what of it stays,
+  u64 pick_t, above;                       // and the weight above it
   union {
     struct { u64 all[kNT], few[kFew]; } sort;
     float queue[kWarps][64];               // a warp's tokens above K on their way to a weight
   };
-  float top;                               // of the CTA's logits
   float chi, clo, far;                     // see Weigh; the distance beyond which a weight is zero
   double cut;                              // how far from the largest logit min_p reaches
   int listed;                              // may be more than kList: the list is cut
-  u64 sum[kWarps];                         // of each warp's stretch: the weight above K,
-  int equal[kWarps];                       // and how many are K
   unsigned kmin, kmax;
   u64 scan[kWarps];
   u64 found_before, total;
@@ -321,12 +325,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   const long long r = blockIdx.x / ctas;
   for (int i = tid; i < kSteps; i += kNT) table[i] = kPow.v[i];
   if (tid < kBins) sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
-  if (tid == 0) sh.listed = 0;
+  if (tid == 0) {
+    sh.listed = 0;
+    sh.pick = -1;
+  }
   auto clear_keys = [&]() {
     for (int i = tid; i < kKeys / 4; i += kNT) reinterpret_cast<uint4*>(sh.keys)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2) sh.near_lo[tid] = sh.near_hi[tid] = 0u;
   };
   if (kBins16) clear_keys();
+  auto started = cl.barrier_arrive();      // (no CTA writes into another before that has done this)
   pdl_enter();
 
   // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
@@ -371,18 +379,50 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   hi = warp_max(hi);
   if (lane == 0) sh.scan[warp] = __float_as_uint(hi);
   __syncthreads();
-  if (warp == 0) {
-    hi = warp_max(lane < kWarps ? __uint_as_float((unsigned)sh.scan[lane]) : -INFINITY);
-    if (lane == 0) sh.top = hi;
+  hi = warp_max(lane < kWarps ? __uint_as_float((unsigned)sh.scan[lane]) : -INFINITY);   // the CTA's
+  cl.barrier_wait(std::move(started));
+
+  if (greedy) {                            // the first of the largest: the first CTA hears of all, which need not wait
+    int first = INT32_MAX;
+    if (own == hi && hi > -INFINITY)
+      for (int j = v0 + lane; j < v1 && first == INT32_MAX; j += 32) {
+        const uint4 u = vector(j);
+        for (int i = N - 1; i >= 0; --i)
+          if (Vec<T>::at(u, i) == hi) first = j * N - row.lead + i;
+      }
+    first = __reduce_min_sync(0xffffffffu, first);
+    __syncthreads();
+    if (lane == 0) sh.scan[warp] = (u64)first;
+    __syncthreads();
+    if (warp == 0) {
+      first = __reduce_min_sync(0xffffffffu, lane < kWarps ? (int)sh.scan[lane] : INT32_MAX);
+      if (lane == 0) {
+        *cl.map_shared_rank(&sh.tops[rank], 0) = hi;
+        *cl.map_shared_rank(&sh.firsts[rank], 0) = first;
+      }
+    }
+    auto told = cl.barrier_arrive();
+    if (rank) return;
+    cl.barrier_wait(std::move(told));
+    if (warp == 0) {
+      const float top = lane < ctas ? sh.tops[lane] : -INFINITY, most = warp_max(top);
+      first = __reduce_min_sync(0xffffffffu, lane < ctas && top == most ? sh.firsts[lane] : INT32_MAX);
+      if (lane == 0) {
+        a.token[r] = most > -INFINITY ? first : -1;
+        if (a.prob) a.prob[r] = most > -INFINITY ? 1.f : 0.f;
+      }
+    }
+    return;
   }
+
+  if (warp == 0 && lane < ctas) *cl.map_shared_rank(&sh.tops[rank], lane) = hi;
   cl.sync();
-  hi = warp_max(lane < ctas ? *cl.map_shared_rank(&sh.top, lane) : -INFINITY);
+  hi = warp_max(lane < ctas ? sh.tops[lane] : -INFINITY);
   if (hi == -INFINITY) {                   // nothing to choose from
     if (rank == 0 && tid == 0) {
       a.token[r] = -1;
       if (a.prob) a.prob[r] = 0.f;
     }
-    cl.sync();
     return;
   }
   Weigh weigh;
@@ -400,29 +440,6 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     weigh.parts(l, whole, i);
     a.prob[r] = (float)((double)whole * __longlong_as_double((long long)(1023 - (i >> 10)) << 52) / (double)total);
   };
-
-  if (greedy) {                            // the first of the largest
-    int first = INT32_MAX;
-    if (own == hi)
-      for (int j = v0 + lane; j < v1 && first == INT32_MAX; j += 32) {
-        const uint4 u = vector(j);
-        for (int i = N - 1; i >= 0; --i)
-          if (Vec<T>::at(u, i) == hi) first = j * N - row.lead + i;
-      }
-    first = __reduce_min_sync(0xffffffffu, first);
-    if (lane == 0) sh.equal[warp] = first;
-    cl.sync();
-    if (rank == 0 && warp == 0) {
-      for (int i = lane; i < ctas * kWarps; i += 32) first = min(first, *cl.map_shared_rank(&sh.equal[i % kWarps], i / kWarps));
-      first = __reduce_min_sync(0xffffffffu, first);
-      if (lane == 0) {
-        a.token[r] = first;
-        if (a.prob) a.prob[r] = 1.f;
-      }
-    }
-    cl.sync();
-    return;
-  }
 
   int parity = 0;                          // the histogram in use
   // kept: what is above K, and the first t of those equal to K; at first what counts
@@ -498,22 +515,31 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       if (upto - bin < want) sh.found = tid;
     __syncthreads();
     const int far = sh.found;              // (of all bins, where fewer threads have a token)
+    bool room = true;
     if (weigh.counts(own) && weigh.bin(own) <= far)
-      for (int j = v0 + lane; j < v1; j += 32) {
+      for (int j = v0 + lane; j < v1 && room; j += 32) {
         const uint4 u = vector(j);
         const float most = Vec<T>::largest(u);
         if (!weigh.counts(most) || weigh.bin(most) > far) continue;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float l = Vec<T>::at(u, i);
-          if (weigh.counts(l) && weigh.bin(l) <= far) list(l, j * N - row.lead + i);
+          if (room && weigh.counts(l) && weigh.bin(l) <= far) {
+            // into the first CTA's list
+            const int at = atomicAdd(cl.map_shared_rank(&sh.listed, 0), 1);
+            room = at < kNT;               // (else that list is of no use)
+            if (room) *cl.map_shared_rank(&sh.list[at], 0) = entry(l, j * N - row.lead + i);
+          }
         }
       }
-    u64 xs[kEach];
-    const int n = gathered(xs);
-    if (n >= 0 && n <= kNT) {
-      if (rank == 0) {
-        u64 x = sort_block(xs[0], n, sh.sort.all, sh.sort.few);
+    cl.sync();
+    const int n = __shfl_sync(0xffffffffu, lane == 0 ? *cl.map_shared_rank(&sh.listed, 0) : 0, 0);
+    if (n <= kNT) {
+      // the first CTA does the rest; the others are done once they have heard that it can
+      auto heard = cl.barrier_arrive();
+      if (rank) return;
+      {
+        u64 x = sort_block(tid < n ? sh.list[tid] : ~0ull, n, sh.sort.all, sh.sort.few);
         // in descending order of logits: top_k, top_p, min_p
         const float l = x == ~0ull ? -INFINITY : entry_logit(x);
         u64 w = tid < n && tid < top_k ? weigh.of(l) : 0ull;
@@ -536,7 +562,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         const u64 total = sh.total, goal = drawn(u01, total);
         if (w && goal < upto_t && goal >= upto_t - w) put((int)(x >> 32), lt, total);
       }
-      cl.sync();
+      cl.barrier_wait(std::move(heard));
       return;
     }
     cl.sync();                             // the lists are free again
@@ -610,17 +636,18 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           w += weight_of(mine + i, x);
         }
         const u64 n_upto = top_k > 0 ? scan_block(n, sh.scan) : 0ull, w_upto = scan_block(w, sh.scan);
-        if (tid == kNT - 1) {
-          sh.slice = w_upto;
-          sh.slice_count = (unsigned)n_upto;
-        }
+        if (tid == kNT - 1)
+          for (int i = 0; i < ctas; ++i) {
+            *cl.map_shared_rank(&sh.slices[rank], i) = w_upto;
+            *cl.map_shared_rank(&sh.slice_counts[rank], i) = (unsigned)n_upto;
+          }
         cl.sync();
         // what the CTAs before this one have, and all of them
         u64 w_before = 0, w_all = 0;
         unsigned n_before = 0, n_all = 0;
         for (int i = 0; i < ctas; ++i) {
-          const u64 x = *cl.map_shared_rank(&sh.slice, i);
-          const unsigned y = *cl.map_shared_rank(&sh.slice_count, i);
+          const u64 x = sh.slices[i];
+          const unsigned y = sh.slice_counts[i];
           if (i < rank) { w_before += x; n_before += y; }
           w_all += x;
           n_all += y;
@@ -628,8 +655,6 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         // The bin where the running count (or weight) reaches `want`, found by the thread that has it.
         auto pick = [&](bool weights, u64 want) {
           const u64 upto = weights ? w_before + w_upto : n_before + n_upto, before = upto - (weights ? w : (u64)n);
-          if (tid == 0) sh.pick = -1;
-          __syncthreads();
           if (before < want && want <= upto) {
             u64 run = before, run_w = w_before + w_upto - w;
             for (int i = 0; i < share_of; ++i) {
@@ -637,9 +662,11 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
               const u64 wx = weight_of(mine + i, x), step = weights ? wx : (u64)x;
               if (run + step >= want) {
                 const u64 one = x ? wx / x : 1ull;
-                sh.pick = mine + i;
-                sh.pick_t = weights ? (want - run + one - 1) / one : want - run;
-                sh.above = run_w;
+                for (int c = 0; c < ctas; ++c) {
+                  *cl.map_shared_rank(&sh.pick, c) = mine + i;
+                  *cl.map_shared_rank(&sh.pick_t, c) = weights ? (want - run + one - 1) / one : want - run;
+                  *cl.map_shared_rank(&sh.above, c) = run_w;
+                }
                 break;
               }
               run += step;
@@ -647,16 +674,13 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
             }
           }
           cl.sync();
-          const int at = min(lane, ctas - 1), got = *cl.map_shared_rank(&sh.pick, at);
-          const u64 got_t = *cl.map_shared_rank(&sh.pick_t, at), got_above = *cl.map_shared_rank(&sh.above, at);
-          const int who = __ffs(__ballot_sync(0xffffffffu, got >= 0)) - 1, b = __shfl_sync(0xffffffffu, got, max(who, 0));
-          const int place = top - b;
-          if (who < 0 || shared_place(place)) {
+          const int b = sh.pick, place = top - b;
+          if (b < 0 || shared_place(place)) {
             shared_cut = true;
           } else {
             K = of_place(place);
-            t = __shfl_sync(0xffffffffu, got_t, who);
-            w_all = __shfl_sync(0xffffffffu, got_above, who);   // above K
+            t = sh.pick_t;
+            w_all = sh.above;              // above K
             all = false;
           }
         };
@@ -667,7 +691,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
             const u64 x = (want - w_all + one - 1) / one;   // reached among those equal to K
             t = min(t, x);
           } else if (want < w_all || !all) {
-            cl.sync();                     // the last pick has been read
+            __syncthreads();               // (the last pick has been read)
+            if (tid == 0) sh.pick = -1;
+            cl.sync();
             pick(true, want);
           }
         }
@@ -698,12 +724,15 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         const u64 upto = scan_block(sum, sh.scan);
         if (tid == kNT - 1) {
           const int b = top - place_of(K);
-          sh.part_sum = upto;
-          sh.part_equal = !all && b >= 0 && b < bins && of_place(top - b) == K ? (int)sh.keys[b] : 0;
+          const int eq = !all && b >= 0 && b < bins && of_place(top - b) == K ? (int)sh.keys[b] : 0;
+          for (int i = 0; i < ctas; ++i) {
+            *cl.map_shared_rank(&sh.part_sums[rank], i) = upto;
+            *cl.map_shared_rank(&sh.part_equals[rank], i) = eq;
+          }
         }
         cl.sync();
-        const u64 wK = all ? 0ull : weigh.of(K), part = lane < ctas ? *cl.map_shared_rank(&sh.part_sum, lane) : 0ull,
-                  eq = lane < ctas ? (u64)*cl.map_shared_rank(&sh.part_equal, lane) : 0ull;
+        const u64 wK = all ? 0ull : weigh.of(K), part = lane < ctas ? sh.part_sums[lane] : 0ull,
+                  eq = lane < ctas ? (u64)sh.part_equals[lane] : 0ull;
         const u64 eq_before = scan_warp(eq) - eq, take = eq_before >= t ? 0ull : min(eq, t - eq_before), w = part + take * wK, w_upto = scan_warp(w);
         total = __shfl_sync(0xffffffffu, w_upto, 31);
         goal = drawn(u01, total);
@@ -935,16 +964,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) all_sum += __shfl_xor_sync(0xffffffffu, all_sum, o);
   const int all_equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) {
-    sh.sum[warp] = all_sum;
-    sh.equal[warp] = all_equal;
+  if (lane < ctas) {
+    *cl.map_shared_rank(&sh.sums[rank * kWarps + warp], lane) = all_sum;
+    *cl.map_shared_rank(&sh.equals[rank * kWarps + warp], lane) = all_equal;
   }
   cl.sync();
   const u64 wK = all ? 0ull : weigh.of(K);
   u64 mine = 0, eq = 0;
   if (tid < ctas * kWarps) {
-    mine = *cl.map_shared_rank(&sh.sum[tid % kWarps], tid / kWarps);
-    eq = (u64)*cl.map_shared_rank(&sh.equal[tid % kWarps], tid / kWarps);
+    mine = sh.sums[tid];
+    eq = (u64)sh.equals[tid];
   }
   const u64 eq_before = scan_block(eq, sh.scan) - eq;
   const u64 take = eq_before >= t ? 0 : min(eq, t - eq_before);
@@ -1015,7 +1044,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     left -= __shfl_sync(0xffffffffu, s_upto, 31);
     spare -= __shfl_sync(0xffffffffu, n_upto, 31);
   }
-  cl.sync();                               // no CTA leaves while another reads it
+  if (placed) cl.sync();                   // no CTA leaves while another reads it
 }
 
 template <typename T>
