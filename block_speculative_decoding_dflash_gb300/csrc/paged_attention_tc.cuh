@@ -40,13 +40,15 @@
 // look for such rows of V and zero them in shared memory, and the queries that
 // do see them add p v themselves.
 //
-// 2048 rows over 32768 keys: 0.81 to 0.83 ms, 1.29 to 1.32 PFLOP/s; no pipe is full
+// 2048 rows over 32768 keys: 0.77 ms, 1.40 PFLOP/s; no pipe is full
 // (tensor 58%, issue 36%, special functions 30%): what is left are the waves (256
 // CTAs on 152 SMs) and each score's chain of dependent steps, a TMEM read, the
 // maximum, a second read, the exponential and a write, which two query tiles take in
 // turns. 48 sequences that decode one token, up to 12345 keys: 264 us, 5.1 TB/s; a
 // block of 4 in a window of 2048: 14 us, of which the first loads' chain (ranges,
-// length, page, rows) and the join are most.
+// length, page, rows) and the join are most. 24 trees of up to 64 rows and 12345
+// keys: 186 us, 3.5 TB/s, two rounds of segments of 1.7 us a key tile and 8 us for
+// both ends; a tree of 64 rows over 32768 keys 48 us, 11 of them the merge.
 #pragma once
 
 #include <cooperative_groups.h>

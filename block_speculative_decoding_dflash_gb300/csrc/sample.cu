@@ -4,10 +4,19 @@
 // With M the row's largest logit a token's weight is w = 2^-((M - l) log2(e) / T).
 // What the filters keep is a prefix of the tokens in descending order (ties: the
 // lowest index first), so all of them together come down to one logit K and a
-// number t: tokens above K are kept, of those equal to K the first t. Nothing is
-// sorted: a histogram over M - l finds the bin in which the count (top-k) or the
-// weight (top-p) is reached, histograms over the order of floats within that bin
-// find K.
+// number t: tokens above K are kept, of those equal to K the first t. The row is not
+// sorted. There are three ways to K:
+// * top_k of up to 256: a histogram of the threads' largest logits gives a distance
+//   that holds top_k of them; the few tokens within it go to a list in the
+//   cluster's first CTA, which sorts it, filters and draws (1 row of 202048: 11 us,
+//   by histograms 32 us).
+// * bf16 under top_p or a large top_k: a count of each bf16 number that is near enough to
+//   M to weigh anything. A few thousand weights, times their counts, are the row's, a
+//   running sum over them has K, and the CTA that has the draw is known from the counts
+//   as well (16 rows of 202048 and top_p: 30 us, by histograms 47 us).
+// * otherwise a histogram over M - l finds the bin in which the count (top_k) or the
+//   weight (top_p) is reached, a list or histograms over the order of floats within
+//   that bin find K (48 fp32 rows of 65537, some of them with top_p: 32 us).
 //
 // Sums of weights decide which token is drawn, so they are exact: a weight is an
 // integer, in units of 2^-44 of (nearly) the largest, a function of l, M and T alone;
@@ -18,8 +27,15 @@
 //
 // A cluster of CTAs holds a row in its shared memory, each warp an unbroken stretch
 // of the vocabulary; the logits are read from memory once. The CTAs exchange
-// maxima, histograms and the warps' sums; each works out the outcome for itself, and
-// the one that has the token writes it.
+// maxima, histograms and sums; each works out the outcome for itself, and the one
+// that has the token writes it.
+//
+// 256 rows of 202048 in bf16 with mixed filters: 145 us, 0.7 TB/s. Neither HBM (9%) nor
+// issue (44%) bounds it: an atomic on shared memory takes 18 clocks for a warp's 32
+// logits, a weight some 20 instructions, and every meeting of a cluster 1 us, most of it
+// waiting. Two CTAs of 64 registers and half of the SM's shared memory
+// each work in the other's waits (one CTA of 1024 threads: 16 rows wait for a second
+// round; three, with spills: 10 to 17% slower).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>

@@ -296,7 +296,7 @@ int dflash_sync_round(dflash_ctx* ctx, int32_t* tokens_host, int32_t* n_host);
  * a + 1 and, when p_draft is not NULL, p_draft [block] = p_i(d_{i+1}) (0 for
  * the last row). uniforms [block] fp32 in [0, 1) are caller-drawn (device).
  * Keeps n, a and the bonus on the device for dflash_commit like the greedy
- * verify. Top-k / top-p filtering is not applied. ERANGE unless 2 <= block
+ * verify. Top-k / top-p filtering is not applied (dflash_sample has it). ERANGE unless 2 <= block
  * <= max_block; EINVAL for a NULL pointer, temperature <= 0 or softcap < 0. */
 int dflash_verify_sampled(dflash_ctx* ctx, const void* target_logits, int32_t block,
                           const int32_t* draft_ids, const float* uniforms, float temperature,
