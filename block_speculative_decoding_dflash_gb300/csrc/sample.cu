@@ -174,20 +174,26 @@ template <typename T>
 struct Vec {
   static constexpr int N = 16 / sizeof(T);
   // NaN counts as -inf, +inf as the type's largest number.
-  static __device__ __forceinline__ uint4 clean(uint4 u) {
-    unsigned* w = reinterpret_cast<unsigned*>(&u);
+  static __device__ __forceinline__ bool odd(const uint4& u) {   // holds one of them, or -inf
     if constexpr (sizeof(T) == 2) {
       const unsigned any = ((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
                            ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u);
-      if (any & 0x80008000u)
+      return any & 0x80008000u;
+    }
+    return (((u.x & 0x7f800000u) + 0x00800000u) | ((u.y & 0x7f800000u) + 0x00800000u) |
+            ((u.z & 0x7f800000u) + 0x00800000u) | ((u.w & 0x7f800000u) + 0x00800000u)) >> 31;
+  }
+  static __device__ __forceinline__ uint4 clean(uint4 u) {
+    unsigned* w = reinterpret_cast<unsigned*>(&u);
+    if constexpr (sizeof(T) == 2) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int s = 0; s < 32; s += 16) {
-            const unsigned x = (w[i] >> s) & 0xffffu;
-            const unsigned y = x == 0x7f80u ? 0x7f7fu : (x & 0x7fffu) > 0x7f80u ? 0xff80u : x;
-            w[i] ^= (x ^ y) << s;
-          }
+        for (int s = 0; s < 32; s += 16) {
+          const unsigned x = (w[i] >> s) & 0xffffu;
+          const unsigned y = x == 0x7f80u ? 0x7f7fu : (x & 0x7fffu) > 0x7f80u ? 0xff80u : x;
+          w[i] ^= (x ^ y) << s;
+        }
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -211,6 +217,12 @@ struct Vec {
     if constexpr (sizeof(T) == 2) return __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
     return __uint_as_float(w[i]);
   }
+  // The same of an i that is not known when this is compiled.
+  static __device__ __forceinline__ float some(const uint4& u, int i) {
+    const int k = sizeof(T) == 2 ? i >> 1 : i;
+    const unsigned w = k & 2 ? (k & 1 ? u.w : u.z) : (k & 1 ? u.y : u.x);
+    return __uint_as_float(sizeof(T) == 4 ? w : i & 1 ? w & 0xffff0000u : w << 16);
+  }
 };
 
 // A row as vectors of 16 bytes: vector j holds the elements j * N - lead + 0 .. N - 1,
@@ -223,7 +235,8 @@ struct Row {
     const int v = j * Vec<T>::N - lead;
     return v >= 0 && v + Vec<T>::N <= vocab;
   }
-  __device__ __forceinline__ uint4 raw(int j) const { return *reinterpret_cast<const uint4*>(base + (j * Vec<T>::N - lead)); }
+  __device__ __forceinline__ const uint4* at(int j) const { return reinterpret_cast<const uint4*>(base + (j * Vec<T>::N - lead)); }
+  __device__ __forceinline__ uint4 raw(int j) const { return *at(j); }
   __device__ __noinline__ uint4 ragged(int j) const {
     uint4 u;
     T* e = reinterpret_cast<T*>(&u);
@@ -233,17 +246,27 @@ struct Row {
     }
     return u;
   }
-  __device__ __forceinline__ uint4 load(int j) const { return Vec<T>::clean(whole(j) ? raw(j) : ragged(j)); }
+  __device__ __forceinline__ uint4 load(int j) const {
+    const uint4 u = whole(j) ? raw(j) : ragged(j);
+    return Vec<T>::odd(u) ? Vec<T>::clean(u) : u;
+  }
 };
+
+// 16 bytes on their way to shared memory; all of a thread's are there.
+__device__ __forceinline__ void copy_async(uint4* to, const uint4* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((unsigned)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // A list of tokens: one of a bin, or all that can still be drawn.
 constexpr int kEach = 4, kList = kEach * kNT;
-constexpr int kFew = 128;
+constexpr int kFew = kNT / 2;
 struct Shared {
   unsigned lo[2][kBins], hi[2][kBins];     // histograms, which take turns
   union {
     u64 list[kList];                       // tokens as a number that sorts them (see entry)
-    unsigned keys[kKeys];                  // bf16: how many of the CTA's logits each bin has, from the largest down
+    unsigned keys[kKeys + 32];             // bf16: how many of the CTA's logits each bin has, from the largest down, and a
+                                           // place for each lane's others
   };
   unsigned near_lo[2], near_hi[2];         // the weight in the shared bins above and below zero
   // What every CTA says to every other, in the order of the CTAs:
@@ -255,8 +278,8 @@ struct Shared {
   int part_equals[kMaxCtas];               // and how many are K
   u64 sums[kMaxCtas * kWarps];             // the same of each warp's stretch
   int equals[kMaxCtas * kWarps];
-  int pick;                                // and the one that has it: the bin of the cut (-1: none said so), what of it stays,
-  u64 pick_t, above;                       // and the weight above it
+  int pick[2];                             // and the one that has it: the bin of the cut by top_k and by top_p (-1: none said
+  u64 pick_t[2], above[2];                 // so), what of it stays, and the weight above it
   union {
     struct { u64 all[kNT], few[kFew]; } sort;
     float queue[kWarps][64];               // a warp's tokens above K on their way to a weight
@@ -297,15 +320,16 @@ __device__ __forceinline__ u64 scan_block(u64 x, u64* s) {
 __device__ __forceinline__ u64 sort_block(u64 x, int n, u64* s, u64* few) {
   const int tid = threadIdx.x;
   __syncthreads();
-  if (n <= kFew) {                          // each counts those before it
+  if (n <= kFew) {                         // counts those before each, by several threads to one
+    const int lg = n <= kFew / 4 ? 3 : n <= kFew / 2 ? 2 : 1, e = tid >> lg, step = 1 << lg;
     if (tid < n) s[tid] = x;
     __syncthreads();
-    if (tid < n) {
-      int at = 0;
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) at += s[i] < x;
-      few[at] = x;
-    }
+    x = e < n ? s[e] : 0ull;
+    int at = 0;
+#pragma unroll 4
+    for (int i = tid & (step - 1); i < n; i += step) at += s[i] < x;
+    for (int o = 1; o < step; o <<= 1) at += __shfl_xor_sync(0xffffffffu, at, o);
+    if (e < n && (tid & (step - 1)) == 0) few[at] = x;
     __syncthreads();
     return tid < n ? few[tid] : ~0ull;
   }
@@ -340,10 +364,10 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long r = blockIdx.x / ctas;
   for (int i = tid; i < kSteps; i += kNT) table[i] = kPow.v[i];
-  if (tid < kBins) sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
+  sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
   if (tid == 0) {
     sh.listed = 0;
-    sh.pick = -1;
+    sh.pick[0] = sh.pick[1] = -1;
   }
   auto clear_keys = [&]() {
     for (int i = tid; i < kKeys / 4; i += kNT) reinterpret_cast<uint4*>(sh.keys)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -351,6 +375,11 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   };
   if (kBins16) clear_keys();
   auto started = cl.barrier_arrive();      // (no CTA writes into another before that has done this)
+  // (as whole warps: one that has come apart stays so behind a barrier of threads, and takes twice as long)
+  auto meet = [&]() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+  };
   pdl_enter();
 
   // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
@@ -375,21 +404,23 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     sh.cut = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : 0.0;
   }
   float hi = -INFINITY;
-  constexpr int kAhead = 8;                // vectors requested together: all of a row of 2^18 bf16 numbers
-  for (int j0 = v0 + lane; j0 < v1; j0 += 32 * kAhead) {
-    uint4 u[kAhead];
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x)
-      if (j0 + x * 32 < v1 && row.whole(j0 + x * 32)) u[x] = row.raw(j0 + x * 32);
-#pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int j = j0 + x * 32;
-      if (j >= v1) continue;
-      if (!row.whole(j)) u[x] = row.ragged(j);
-      u[x] = Vec<T>::clean(u[x]);
-      if (STAGED) held[j - c0] = u[x];
-      hi = fmaxf(hi, Vec<T>::largest(u[x]));
+  // (A loop over what is there already, as short as can be: unrolled with the loads in
+  // registers the code comes in more slowly than the row.)
+  if (STAGED) {
+    for (int j = v0 + lane; j < v1; j += 32) {
+      if (row.whole(j)) copy_async(&held[j - c0], row.at(j));
+      else held[j - c0] = row.ragged(j);
     }
+    copies_done();
+  }
+#pragma unroll 1
+  for (int j = v0 + lane; j < v1; j += 32) {
+    uint4 u = STAGED ? held[j - c0] : row.whole(j) ? row.raw(j) : row.ragged(j);
+    if (Vec<T>::odd(u)) {
+      u = Vec<T>::clean(u);
+      if (STAGED) held[j - c0] = u;
+    }
+    hi = fmaxf(hi, Vec<T>::largest(u));
   }
   const float own = hi;                    // of the vectors that this thread looks through
   hi = warp_max(hi);
@@ -432,7 +463,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   }
 
   if (warp == 0 && lane < ctas) *cl.map_shared_rank(&sh.tops[rank], lane) = hi;
-  cl.sync();
+  meet();
   hi = warp_max(lane < ctas ? sh.tops[lane] : -INFINITY);
   if (hi == -INFINITY) {                   // nothing to choose from
     if (rank == 0 && tid == 0) {
@@ -465,18 +496,22 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
 
   // The histogram of all CTAs: this thread's bin, and the sum up to and with it.
   auto merged = [&](bool weights, u64& bin, u64& upto) {
-    cl.sync();
+    meet();
     bin = 0;
+    static_assert(kBins == kNT, "a thread to each bin");
+    unsigned lo[kMaxCtas], hi[kMaxCtas] = {};               // (all of them requested together)
 #pragma unroll
-    for (int i = 0; i < kMaxCtas; ++i)
-      if (i < ctas && tid < kBins) {
-        bin += *cl.map_shared_rank(&sh.lo[parity][tid], i);
-        if (weights) bin += (u64)*cl.map_shared_rank(&sh.hi[parity][tid], i) << 32;
-      }
+    for (int i = 0; i < kMaxCtas; ++i) {
+      const int c = min(i, ctas - 1);
+      lo[i] = *cl.map_shared_rank(&sh.lo[parity][tid], c);
+      if (weights) hi[i] = *cl.map_shared_rank(&sh.hi[parity][tid], c);
+    }
+#pragma unroll
+    for (int i = 0; i < kMaxCtas; ++i) bin += i < ctas ? (u64)hi[i] << 32 | lo[i] : 0ull;
     upto = scan_block(bin, sh.scan);
     if (tid == kNT - 1) sh.total = upto;
     parity ^= 1;
-    if (tid < kBins) sh.lo[parity][tid] = sh.hi[parity][tid] = 0u;   // everyone has read it: they came to the last meeting since
+    sh.lo[parity][tid] = sh.hi[parity][tid] = 0u;   // everyone has read it: they came to the last meeting since
     __syncthreads();
   };
   auto add = [&](bool weights, int bin, u64 w) {
@@ -492,7 +527,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   };
   // The lists of all CTAs, kEach entries to a thread (~0: none): their number, or -1 where some do not fit.
   auto gathered = [&](u64 (&mine)[kEach]) {
-    cl.sync();
+    meet();
     const int some = lane < ctas ? *cl.map_shared_rank(&sh.listed, lane) : 0;
     int upto = some;
 #pragma unroll
@@ -519,6 +554,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     return fit ? n : -1;
   };
 
+  // How many tokens of weight `one` reach a sum.
+  auto reached = [](u64 sum, u64 one) { return (sum + one - 1) / one; };
+
   // ---- few tokens to choose from: top_k of them, by a list
   if (top_k > 0 && top_k <= kNT / 2) {
     // At least top_k threads have a token in the first bins that hold top_k of the
@@ -537,18 +575,20 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         const uint4 u = vector(j);
         const float most = Vec<T>::largest(u);
         if (!weigh.counts(most) || weigh.bin(most) > far) continue;
+        unsigned near = 0;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float l = Vec<T>::at(u, i);
-          if (room && weigh.counts(l) && weigh.bin(l) <= far) {
-            // into the first CTA's list
-            const int at = atomicAdd(cl.map_shared_rank(&sh.listed, 0), 1);
-            room = at < kNT;               // (else that list is of no use)
-            if (room) *cl.map_shared_rank(&sh.list[at], 0) = entry(l, j * N - row.lead + i);
-          }
+          near |= (unsigned)(weigh.counts(l) && weigh.bin(l) <= far) << i;
+        }
+        for (; near && room; near &= near - 1) {
+          // into the first CTA's list
+          const int i = __ffs(near) - 1, at = atomicAdd(cl.map_shared_rank(&sh.listed, 0), 1);
+          room = at < kNT;                 // (else that list is of no use)
+          if (room) *cl.map_shared_rank(&sh.list[at], 0) = entry(Vec<T>::some(u, i), j * N - row.lead + i);
         }
       }
-    cl.sync();
+    meet();
     const int n = __shfl_sync(0xffffffffu, lane == 0 ? *cl.map_shared_rank(&sh.listed, 0) : 0, 0);
     if (n <= kNT) {
       // the first CTA does the rest; the others are done once they have heard that it can
@@ -581,7 +621,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       cl.barrier_wait(std::move(heard));
       return;
     }
-    cl.sync();                             // the lists are free again
+    meet();                             // the lists are free again
     if (tid == 0) sh.listed = 0;
     if (kBins16) {
       clear_keys();
@@ -611,12 +651,12 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         for (int i = 0; i < N; ++i) {
           const int bits = (int)(i & 1 ? words[i >> 1] : words[i >> 1] << 16) >> 16, place = place_of(bits);
           const int b = top - place;
-          if (b < bins) atomicAdd(&sh.keys[b], 1u);
-          near |= (unsigned)(shared_place(place) && b < bins) << i;
+          atomicAdd(&sh.keys[b < bins ? b : kKeys + lane], 1u);   // (with a branch to each logit a third slower)
+          near |= (unsigned)shared_place(place) << i;
         }
         for (; near; near &= near - 1) {
-          const float l = Vec<T>::at(u, __ffs(near) - 1);
-          const u64 w = weigh.of(l);
+          const float l = Vec<T>::some(u, __ffs(near) - 1);
+          const u64 w = top - place_of(l) < bins ? weigh.of(l) : 0ull;
           const int side = l < 0.f;
           const unsigned old = atomicAdd(&sh.near_lo[side], (unsigned)w);
           atomicAdd(&sh.near_hi[side], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
@@ -625,24 +665,27 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       bool shared_cut = false;             // within a shared bin: not from counts
       {
         const int share_of = kMaxCtas / ctas, mine = rank * (kKeys / ctas) + tid * share_of;   // this thread's bins
-        cl.sync();
+        meet();
         // a bin of all CTAs
         auto count_of = [&](int b) {
-          unsigned n = 0;
+          unsigned n = 0, of[kMaxCtas];
 #pragma unroll
-          for (int i = 0; i < kMaxCtas; ++i)
-            if (i < ctas) n += *cl.map_shared_rank(&sh.keys[b], i);
+          for (int i = 0; i < kMaxCtas; ++i) of[i] = *cl.map_shared_rank(&sh.keys[b], min(i, ctas - 1));
+#pragma unroll
+          for (int i = 0; i < kMaxCtas; ++i) n += i < ctas ? of[i] : 0u;
           return n;
         };
+        // the shared bins' weights: of one CTA by each lane, all of a side by every lane of it
+        u64 near = 0;
+        if ((lane >> 1) < ctas)
+          near = *cl.map_shared_rank(&sh.near_lo[lane & 1], lane >> 1) | (u64)*cl.map_shared_rank(&sh.near_hi[lane & 1], lane >> 1) << 32;
+        __syncwarp();
+#pragma unroll
+        for (int o = 2; o < 2 * kMaxCtas; o <<= 1) near += __shfl_xor_sync(0xffffffffu, near, o);
+        const u64 above_zero = __shfl_sync(0xffffffffu, near, 0), below_zero = __shfl_sync(0xffffffffu, near, 1);
         auto weight_of = [&](int b, unsigned n) {
           const int place = top - b;
-          if (!shared_place(place)) return n ? n * weigh.of(of_place(place)) : 0ull;
-          u64 w = 0;
-          for (int i = 0; n && i < ctas; ++i) {
-            w += *cl.map_shared_rank(&sh.near_lo[place < 0], i);
-            w += (u64)*cl.map_shared_rank(&sh.near_hi[place < 0], i) << 32;
-          }
-          return w;
+          return shared_place(place) ? place > 0 ? above_zero : below_zero : n ? n * weigh.of(of_place(place)) : 0ull;
         };
         unsigned n = 0;
         u64 w = 0;
@@ -657,7 +700,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
             *cl.map_shared_rank(&sh.slices[rank], i) = w_upto;
             *cl.map_shared_rank(&sh.slice_counts[rank], i) = (unsigned)n_upto;
           }
-        cl.sync();
+        meet();
         // what the CTAs before this one have, and all of them
         u64 w_before = 0, w_all = 0;
         unsigned n_before = 0, n_all = 0;
@@ -674,14 +717,15 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           if (before < want && want <= upto) {
             u64 run = before, run_w = w_before + w_upto - w;
             for (int i = 0; i < share_of; ++i) {
-              const unsigned x = count_of(mine + i);
-              const u64 wx = weight_of(mine + i, x), step = weights ? wx : (u64)x;
+              const unsigned x = share_of > 1 ? count_of(mine + i) : n;
+              const u64 wx = share_of > 1 ? weight_of(mine + i, x) : w, step = weights ? wx : (u64)x;
               if (run + step >= want) {
-                const u64 one = x ? wx / x : 1ull;
+                const int place = top - (mine + i);
+                const u64 stay = !weights ? want - run : shared_place(place) ? 0ull : reached(want - run, weigh.of(of_place(place)));
                 for (int c = 0; c < ctas; ++c) {
-                  *cl.map_shared_rank(&sh.pick, c) = mine + i;
-                  *cl.map_shared_rank(&sh.pick_t, c) = weights ? (want - run + one - 1) / one : want - run;
-                  *cl.map_shared_rank(&sh.above, c) = run_w;
+                  *cl.map_shared_rank(&sh.pick[weights], c) = mine + i;
+                  *cl.map_shared_rank(&sh.pick_t[weights], c) = stay;
+                  *cl.map_shared_rank(&sh.above[weights], c) = run_w;
                 }
                 break;
               }
@@ -689,14 +733,14 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
               run_w += wx;
             }
           }
-          cl.sync();
-          const int b = sh.pick, place = top - b;
+          meet();
+          const int b = sh.pick[weights], place = top - b;
           if (b < 0 || shared_place(place)) {
             shared_cut = true;
           } else {
             K = of_place(place);
-            t = sh.pick_t;
-            w_all = sh.above;              // above K
+            t = sh.pick_t[weights];
+            w_all = sh.above[weights];              // above K
             all = false;
           }
         };
@@ -704,12 +748,8 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         if (top_p < 1.f && !shared_cut) {
           const u64 one = all ? 0ull : weigh.of(K), want = top_p > 0.f ? max(share(top_p, w_all + t * one, true), 1ull) : 1ull;
           if (want > w_all && !all) {
-            const u64 x = (want - w_all + one - 1) / one;   // reached among those equal to K
-            t = min(t, x);
+            t = min(t, reached(want - w_all, one));         // among those equal to K
           } else if (want < w_all || !all) {
-            __syncthreads();               // (the last pick has been read)
-            if (tid == 0) sh.pick = -1;
-            cl.sync();
             pick(true, want);
           }
         }
@@ -746,7 +786,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
             *cl.map_shared_rank(&sh.part_equals[rank], i) = eq;
           }
         }
-        cl.sync();
+        meet();
         const u64 wK = all ? 0ull : weigh.of(K), part = lane < ctas ? sh.part_sums[lane] : 0ull,
                   eq = lane < ctas ? (u64)sh.part_equals[lane] : 0ull;
         const u64 eq_before = scan_warp(eq) - eq, take = eq_before >= t ? 0ull : min(eq, t - eq_before), w = part + take * wK, w_upto = scan_warp(w);
@@ -766,7 +806,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         K = least_below(weigh.least);
         t = 0;
         all = true;
-        cl.sync();
+        meet();
         if (tid == 0) sh.listed = 0;
         __syncthreads();
       }
@@ -822,8 +862,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     }
     if (goal >= total) return;             // all of it
     if (goal > sh.total) {                 // reached among those equal to K
-      const u64 n = (goal - sh.total + wK - 1) / wK;
-      if (n < t0) t = n;
+      t = min(t0, reached(goal - sh.total, wK));
       return;
     }
     if (upto >= goal && upto - bin < goal) {
@@ -911,9 +950,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     }
     K = of_key<T>(kmax);
     const u64 w1 = weights ? weigh.of(K) : 1ull;
-    t = (goal - before + w1 - 1) / w1;
+    t = reached(goal - before, w1);
     all = false;
-    cl.sync();                             // the lists and spans are free again
+    meet();                             // the lists and spans are free again
   };
   if (!placed && top_k > 0 && top_k < a.vocab) cut(false, 0.f);
   if (!placed && top_p < 1.f) cut(true, top_p);
@@ -984,7 +1023,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     *cl.map_shared_rank(&sh.sums[rank * kWarps + warp], lane) = all_sum;
     *cl.map_shared_rank(&sh.equals[rank * kWarps + warp], lane) = all_equal;
   }
-  cl.sync();
+  meet();
   const u64 wK = all ? 0ull : weigh.of(K);
   u64 mine = 0, eq = 0;
   if (tid < ctas * kWarps) {
@@ -1060,7 +1099,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     left -= __shfl_sync(0xffffffffu, s_upto, 31);
     spare -= __shfl_sync(0xffffffffu, n_upto, 31);
   }
-  if (placed) cl.sync();                   // no CTA leaves while another reads it
+  if (placed) meet();                   // no CTA leaves while another reads it
 }
 
 template <typename T>
