@@ -289,6 +289,7 @@ struct Shared {
   int listed;                              // may be more than kList: the list is cut
   unsigned kmin, kmax;
   u64 scan[kWarps];
+  unsigned scan_n[kWarps];
   u64 found_before, total;
   int found;
 };
@@ -311,10 +312,29 @@ __device__ __forceinline__ u64 scan_block(u64 x, u64* s) {
   __syncthreads();
   if (lane == 31) s[warp] = x;
   __syncthreads();
-  u64 before = lane < warp ? s[lane] : 0ull;
+  u64 before = (lane & (kWarps - 1)) < warp ? s[lane & (kWarps - 1)] : 0ull;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  for (int o = kWarps / 2; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
   return x + before;
+}
+// The same of a sum and a count.
+__device__ __forceinline__ void scan_block(u64& x, unsigned& n, u64* s, unsigned* sn) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 y = __shfl_up_sync(0xffffffffu, x, o);
+    const unsigned m = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) { x += y; n += m; }
+  }
+  __syncthreads();
+  if (lane == 31) { s[warp] = x; sn[warp] = n; }
+  __syncthreads();
+  u64 before = (lane & (kWarps - 1)) < warp ? s[lane & (kWarps - 1)] : 0ull;
+  unsigned m = lane < warp ? sn[lane] : 0u;
+#pragma unroll
+  for (int o = kWarps / 2; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  x += before;
+  n += __reduce_add_sync(0xffffffffu, m);
 }
 // Sorts one number of each of the first n threads, all different, ascending; the other threads' are ~0.
 __device__ __forceinline__ u64 sort_block(u64 x, int n, u64* s, u64* few) {
@@ -767,7 +787,8 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         // this CTA's weight above K, and how many are K
         __syncthreads();
         u64 sum = 0;
-        for (int b = tid; b < bins; b += kNT) {
+        const int upto_K = all ? bins : min(bins, top - place_of(K) + 1);
+        for (int b = tid; b < upto_K; b += kNT) {
           const int place = top - b;
           const unsigned n = sh.keys[b];
           const float l = of_place(place);
@@ -1025,15 +1046,18 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   }
   meet();
   const u64 wK = all ? 0ull : weigh.of(K);
-  u64 mine = 0, eq = 0;
+  u64 mine = 0;
+  unsigned eq = 0;
   if (tid < ctas * kWarps) {
     mine = sh.sums[tid];
-    eq = (u64)sh.equals[tid];
+    eq = (unsigned)sh.equals[tid];
   }
-  const u64 eq_before = scan_block(eq, sh.scan) - eq;
-  const u64 take = eq_before >= t ? 0 : min(eq, t - eq_before);
+  u64 upto = mine;
+  unsigned eq_upto = eq;
+  scan_block(upto, eq_upto, sh.scan, sh.scan_n);
+  const u64 take = min((u64)eq_upto, t) - min((u64)(eq_upto - eq), t);   // of those equal to K, in order, the first t
   mine += take * wK;
-  const u64 upto = scan_block(mine, sh.scan);
+  upto += min((u64)eq_upto, t) * wK;
   if (tid == kNT - 1) {
     sh.total = upto;
     sh.found = -1;
