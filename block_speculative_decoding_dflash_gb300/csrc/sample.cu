@@ -383,6 +383,11 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   const int ctas = (int)cl.num_blocks(), rank = (int)cl.block_rank();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long r = blockIdx.x / ctas;
+  // (as whole warps: one that has come apart stays so behind a barrier of threads, and takes twice as long)
+  auto meet = [&]() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+  };
   for (int i = tid; i < kSteps; i += kNT) table[i] = kPow.v[i];
   sh.lo[0][tid] = sh.hi[0][tid] = sh.lo[1][tid] = sh.hi[1][tid] = 0u;
   if (tid == 0) {
@@ -395,11 +400,6 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   };
   if (kBins16) clear_keys();
   auto started = cl.barrier_arrive();      // (no CTA writes into another before that has done this)
-  // (as whole warps: one that has come apart stays so behind a barrier of threads, and takes twice as long)
-  auto meet = [&]() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-  };
   pdl_enter();
 
   // ---- the row's stretch of this warp, and the largest logit of the row and of each thread
@@ -416,13 +416,6 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   const int top_k = a.top_k ? a.top_k[r] : 0;
   const float top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f, u01 = a.uniform[r];
   const bool greedy = !(temp >= 5.4210109e-20f);          // 2^-64
-  if (tid == kNT - 1) {
-    const double c = greedy ? 1.0 : 1.44269504088896340736 / (double)temp;
-    sh.chi = (float)c;
-    sh.clo = (float)(c - (double)sh.chi);
-    sh.far = fminf((float)(kUnit / c), FLT_MAX);
-    sh.cut = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : 0.0;
-  }
   float hi = -INFINITY;
   // (A loop over what is there already, as short as can be: unrolled with the loads in
   // registers the code comes in more slowly than the row.)
@@ -431,8 +424,16 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       if (row.whole(j)) copy_async(&held[j - c0], row.at(j));
       else held[j - c0] = row.ragged(j);
     }
-    copies_done();
   }
+  // (64-bit floats, while the row is on its way)
+  if (tid == kNT - 1) {
+    const double c = greedy ? 1.0 : 1.44269504088896340736 / (double)temp;
+    sh.chi = (float)c;
+    sh.clo = (float)(c - (double)sh.chi);
+    sh.far = fminf((float)(kUnit / c), FLT_MAX);
+    sh.cut = min_p > 0.f ? (double)temp * log((double)fminf(min_p, 1.f)) : 0.0;
+  }
+  if (STAGED) copies_done();
 #pragma unroll 1
   for (int j = v0 + lane; j < v1; j += 32) {
     uint4 u = STAGED ? held[j - c0] : row.whole(j) ? row.raw(j) : row.ragged(j);
