@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(128, HDP > 128 ? 2 : 4) paged_weight_tf32_kern
 // The same of segments, a CTA to some heads of a token. A segment has `rows_of` rows,
 // of `per` tokens, or (per 0) rows of heads one after the other, whichever tokens they
 // are. (A token of one segment has its output.) Bound by the partials' way from L2 and
-// HBM: 10 us for 64 rows of 19 segments, 16 heads; six segments are requested together.
+// HBM: 10 us for 64 rows of 19 segments, 32 heads.
 constexpr int kMergeWarps = 8;
 template <typename T>
 __global__ void __launch_bounds__(kMergeWarps * 32, 4) paged_tree_merge_kernel(PagedAttnArgs a, int ctas, int rows_of, int per) {
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32, 4) paged_tree_merge_kernel(P
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       M = -INFINITY;
       L = 0.f;
-      constexpr int kU = 6;                  // segments requested together
+      constexpr int kU = 4;                  // segments requested together (more cost registers: 182 us to 186 us for 24 trees)
       const float2* at_ml = a.part_ml + p0;
       const float* at_o = a.part_o + p0 * hd + d;
       const size_t step_o = stride * hd;

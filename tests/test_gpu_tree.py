@@ -335,6 +335,25 @@ def test_sample_ties_go_to_the_lowest_id(B, dtype, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("vocab", [300, 4100, 40000])
+def test_sample_of_logits_near_zero(B, dtype, vocab):
+    """Logits of both signs down to 2^-20, all of a row, beside larger ones, or with the largest at 2^-9."""
+    rows = 24
+    g = torch.Generator().manual_seed(vocab + 1)
+    x = torch.exp2(torch.rand(rows, vocab, generator=g) * 12 - 20) * (torch.randint(0, 2, (rows, vocab), generator=g) * 2 - 1)
+    x[8:16, ::3] = torch.randn(8, vocab, generator=g)[:, ::3] * 2
+    x[16:] = x[16:].clamp(max=2.0 ** -9)
+    x[16:, vocab // 2] = 2.0 ** -9
+    x[::4, 1::5] = 0.0
+    x = x.to(torch.bfloat16 if dtype == "bf16" else torch.float32).cuda()
+    r = np.random.default_rng(vocab)
+    u, p = r.random(rows, dtype=np.float32), r.random(rows, dtype=np.float32)
+    check_draws(B, x, u, near_allowed=1, top_p=p)
+    check_draws(B, x, u, near_allowed=1, top_k=r.integers(257, vocab + 3, rows), temperature=0.05 + r.random(rows, dtype=np.float32))
+    check_draws(B, x, u, near_allowed=1, top_p=p, top_k=r.integers(1, vocab + 3, rows), min_p=r.random(rows, dtype=np.float32) * np.float32(0.5))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("vocab", [17, 4100])
 def test_sample_rows_with_infinities_and_nan(B, dtype, vocab):
     big = float(torch.finfo(torch.bfloat16 if dtype == "bf16" else torch.float32).max)
