@@ -923,10 +923,15 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     }
     u64 xs[kEach];
     const int n = gathered(xs);
-    for (int i = 0; i < ctas; ++i) {
-      kmin = min(kmin, *cl.map_shared_rank(&sh.kmin, i));
-      kmax = max(kmax, *cl.map_shared_rank(&sh.kmax, i));
+    kmin = 0xffffffffu;
+    kmax = 0u;
+    if (lane < ctas) {
+      kmin = *cl.map_shared_rank(&sh.kmin, lane);
+      kmax = *cl.map_shared_rank(&sh.kmax, lane);
     }
+    __syncwarp();
+    kmin = __reduce_min_sync(0xffffffffu, kmin);
+    kmax = __reduce_max_sync(0xffffffffu, kmax);
     unsigned kx[kEach];
     u64 wx[kEach];
 #pragma unroll
