@@ -361,7 +361,7 @@ long long paged_segment_rows(int kind) { return kind <= 2 ? kind * 128 : 16; }
 // For trees. Few query tiles over a few thousand keys as above, and as many of them as
 // are several rounds of CTAs too. Otherwise the batch goes in segments of keys that
 // even out its sequences: the longest would set the time (24 trees of up to 64 rows and
-// 12345 keys: 214 us in equal splits, 186 us in segments).
+// 12345 keys: 214 us in equal splits, 182 us in segments).
 PagedPlan paged_tree_plan(int dtype, const PagedAttnArgs& a) {
   PagedPlan p = paged_attn_plan(dtype, a);
   const long long len = expected_len(a);

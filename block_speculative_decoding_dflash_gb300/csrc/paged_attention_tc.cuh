@@ -47,8 +47,8 @@
 // turns. 48 sequences that decode one token, up to 12345 keys: 264 us, 5.1 TB/s; a
 // block of 4 in a window of 2048: 14 us, of which the first loads' chain (ranges,
 // length, page, rows) and the join are most. 24 trees of up to 64 rows and 12345
-// keys: 186 us, 3.5 TB/s, two rounds of segments of 1.7 us a key tile and 8 us for
-// both ends; a tree of 64 rows over 32768 keys 48 us, 11 of them the merge.
+// keys: 182 us, 3.6 TB/s, two rounds of segments of 1.7 us a key tile and 16 us for
+// both ends; a tree of 64 rows over 32768 keys 48 us, 10 of them the merge.
 #pragma once
 
 #include <cooperative_groups.h>

@@ -8,12 +8,12 @@
 // sorted. There are three ways to K:
 // * top_k of up to 256: a histogram of the threads' largest logits gives a distance
 //   that holds top_k of them; the few tokens within it go to a list in the
-//   cluster's first CTA, which sorts it, filters and draws (1 row of 202048: 11 us,
+//   cluster's first CTA, which sorts it, filters and draws (1 row of 202048: 10 us,
 //   by histograms 32 us).
 // * bf16 under top_p or a large top_k: a count of each bf16 number that is near enough to
 //   M to weigh anything. A few thousand weights, times their counts, are the row's, a
 //   running sum over them has K, and the CTA that has the draw is known from the counts
-//   as well (16 rows of 202048 and top_p: 30 us, by histograms 47 us).
+//   as well (16 rows of 202048 and top_p: 26 us, by histograms 47 us).
 // * otherwise a histogram over M - l finds the bin in which the count (top_k) or the
 //   weight (top_p) is reached, a list or histograms over the order of floats within
 //   that bin find K (48 fp32 rows of 65537, some of them with top_p: 32 us).
@@ -30,12 +30,13 @@
 // maxima, histograms and sums; each works out the outcome for itself, and the one
 // that has the token writes it.
 //
-// 256 rows of 202048 in bf16 with mixed filters: 145 us, 0.7 TB/s. Neither HBM (9%) nor
-// issue (44%) bounds it: an atomic on shared memory takes 18 clocks for a warp's 32
-// logits, a weight some 20 instructions, and every meeting of a cluster 1 us, most of it
-// waiting. Two CTAs of 64 registers and half of the SM's shared memory
-// each work in the other's waits (one CTA of 1024 threads: 16 rows wait for a second
-// round; three, with spills: 10 to 17% slower).
+// 256 rows of 202048 in bf16 with mixed filters: 130 us, 0.8 TB/s. Without filters a
+// weight's 35 instructions bound it; elsewhere a chain of short steps does, for which the
+// instructions themselves often come too late, and every meeting of a cluster takes
+// 0.9 us. Two CTAs of 64 registers and half of the SM's shared memory each work in the
+// other's waits (one CTA of 1024 threads: 16 rows wait for a second round; three, with
+// spills: 10 to 17% slower). More CTAs to a row do not find room at once, fewer do no
+// more at a time (16 rows by 16: 41 us, by 8: 26 us; 256 rows by 4: 132 us).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
