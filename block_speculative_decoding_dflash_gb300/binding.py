@@ -8,6 +8,7 @@ been built -- there is no fallback implementation.
 
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import struct
@@ -845,16 +846,17 @@ def paged_tree_commit(caches, path, count, stream=None):
     caches = list(caches)
     if not caches:
         raise DFlashError(EINVAL, "paged tree commit: no caches")
-    first = caches[0]
-    if any(c._index != first._index for c in caches):
-        raise DFlashError(EINVAL, "paged tree commit: the caches are on several devices")
+    first, index = caches[0], caches[0]._index
+    for c in caches:
+        if c._index != index:
+            raise DFlashError(EINVAL, "paged tree commit: the caches are on several devices")
     if path.dim() != 2:
         raise DFlashError(EINVAL, "paged tree commit: path must be [n_seq, width]")
-    weights = struct.pack(f"={len(caches)}Q", *(0 if c.weight is None else c.weight.data_ptr() for c in caches))
-    held = ctypes.create_string_buffer(weights, len(weights))
-    args = first._pack(_TREE_COMMIT, first._need("path", path, torch.int32, (first.n_seq, path.shape[1])),
-                       first._need("count", count, torch.int32, (first.n_seq,)), ctypes.addressof(held), path.shape[1], len(caches))
-    first._launch(_commit, stream, b"".join(c._c for c in caches), args)
+    weights = array.array("Q", [0 if c.weight is None else c.weight.data_ptr() for c in caches])
+    width, seqs = path.shape[1], (first.n_seq,)
+    args = first._pack(_TREE_COMMIT, first._need("path", path, torch.int32, (first.n_seq, width)), first._need("count", count, torch.int32, seqs),
+                       weights.buffer_info()[0], width, len(caches))
+    first._launch(_commit, stream, b"".join([c._c for c in caches]), args)
 
 
 def _commit(_, caches, args, handle):

@@ -11,7 +11,7 @@ namespace {
 // One warp walks one tree. The children of a row follow it, each behind the subtree
 // of the one before; the warp keeps the tree's rows in shared memory, where a step
 // of the walk takes some tens of cycles and not a memory latency. Bound by the launch
-// and three dependent loads (256 trees of up to 64 rows: 7 us cold, 8 us a call).
+// and three dependent loads (256 trees of up to 64 rows: 4.2 us in a graph).
 constexpr int kAcceptWarps = 4, kAcceptHeld = 256;
 
 __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const TreeAcceptArgs a) {
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 // head, or one head's position or weight, and moves it row by row. Row i of the path
 // goes to a place at or before its own, and later rows come from places behind it,
 // so a thread that goes in order overwrites nothing that it still needs. Bound by its
-// chain of loads, count, path, page, row (48 sequences and 24 layers: 12 us cold, 0.8
+// chain of loads, count, path, page, row (48 sequences and 24 layers: 8.8 us in a graph, 1.1
 // TB/s), which is why eight rows are requested together.
 constexpr int kCommitThreads = 256, kCommitRows = 64;
 
