@@ -52,9 +52,9 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
 // head, or one head's position or weight, and moves it row by row. Row i of the path
 // goes to a place at or before its own, and later rows come from places behind it,
 // so a thread that goes in order overwrites nothing that it still needs. Bound by its
-// chain of loads, count, path, page, row (48 sequences and 24 layers: 8.8 us in a graph, 1.1
+// chain of loads, count, path, page, row (48 sequences and 24 layers: 7.3 us in a graph, 1.4
 // TB/s), which is why eight rows are requested together.
-constexpr int kCommitThreads = 256, kCommitRows = 64;
+constexpr int kCommitThreads = 512, kCommitRows = 64;         // at most; a CTA has kCommitRows threads at least
 
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __grid_constant__ TreeCommitArgs a) {
   __shared__ long long from[kCommitRows], to[kCommitRows];   // rows of head 0, -1: not to be moved
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const __gri
   if (bad_rows) count = 0;
   const int* path = a.path + (long long)s * a.width;
   const int per_head = 2 * a.vecs + (c.weight ? 2 : 1), columns = a.nkv * per_head;
-  const int e = blockIdx.x * kCommitThreads + tid, head = e / per_head, x = e % per_head;
+  const int e = blockIdx.x * blockDim.x + tid, head = e / per_head, x = e % per_head;
   for (int i0 = 0; i0 < count; i0 += kCommitRows) {
     __syncthreads();
     const int n = min(kCommitRows, count - i0);
@@ -125,8 +125,10 @@ cudaError_t launch_tree_accept(const TreeAcceptArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_tree_commit(const TreeCommitArgs& a, cudaStream_t st) {
-  const int columns = a.nkv * (2 * a.vecs + 2);
-  return launch_pdl(tree_commit_kernel, dim3((columns + kCommitThreads - 1) / kCommitThreads, a.n_seq, a.n_caches), dim3(kCommitThreads), 0, st, a);
+  // as few CTAs as there can be, and of as few warps (48 sequences of 272 columns in 24 layers by CTAs of 256: 8.8 us)
+  const int columns = a.nkv * (2 * a.vecs + 2), ctas = (columns + kCommitThreads - 1) / kCommitThreads;
+  const int threads = ((columns + ctas - 1) / ctas + 31) & ~31;
+  return launch_pdl(tree_commit_kernel, dim3(ctas, a.n_seq, a.n_caches), dim3(threads < kCommitRows ? kCommitRows : threads), 0, st, a);
 }
 
 }  // namespace dfl
