@@ -13,7 +13,7 @@
 // * bf16 under top_p or a large top_k: a count of each bf16 number that is near enough to
 //   M to weigh anything. A few thousand weights, times their counts, are the row's, a
 //   running sum over them has K, and the CTA that has the draw is known from the counts
-//   as well (16 rows of 202048 and top_p: 26 us, by histograms 47 us).
+//   as well (16 rows of 202048 and top_p: 25 us, by histograms 47 us).
 // * otherwise a histogram over M - l finds the bin in which the count (top_k) or the
 //   weight (top_p) is reached, a list or histograms over the order of floats within
 //   that bin find K (48 fp32 rows of 65537, some of them with top_p: 32 us).
@@ -30,7 +30,7 @@
 // maxima, histograms and sums; each works out the outcome for itself, and the one
 // that has the token writes it.
 //
-// 256 rows of 202048 in bf16 with mixed filters: 130 us, 0.8 TB/s. Without filters a
+// 256 rows of 202048 in bf16 with mixed filters: 127 us, 0.8 TB/s. Without filters a
 // weight's 35 instructions bound it; elsewhere a chain of short steps does, for which the
 // instructions themselves often come too late, and every meeting of a cluster takes
 // 0.9 us. Two CTAs of 64 registers and half of the SM's shared memory each work in the
@@ -261,7 +261,7 @@ __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;
 
 // A list of tokens: one of a bin, or all that can still be drawn.
 constexpr int kEach = 4, kList = kEach * kNT;
-constexpr int kFew = kNT / 2;
+constexpr int kFew = kNT / 2, kNears = 1024;
 struct Shared {
   unsigned lo[2][kBins], hi[2][kBins];     // histograms, which take turns
   union {
@@ -284,9 +284,11 @@ struct Shared {
   union {
     struct { u64 all[kNT], few[kFew]; } sort;
     float queue[kWarps][64];               // a warp's tokens above K on their way to a weight
+    float nears[kNears];                   // logits of the shared bins on theirs
   };
   float chi, clo, far;                     // see Weigh; the distance beyond which a weight is zero
   double cut;                              // how far from the largest logit min_p reaches
+  int near_listed;                         // may be more than kNears
   int listed;                              // may be more than kList: the list is cut
   unsigned kmin, kmax;
   u64 scan[kWarps];
@@ -398,6 +400,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   auto clear_keys = [&]() {
     for (int i = tid; i < kKeys / 4; i += kNT) reinterpret_cast<uint4*>(sh.keys)[i] = make_uint4(0u, 0u, 0u, 0u);
     if (tid < 2) sh.near_lo[tid] = sh.near_hi[tid] = 0u;
+    if (tid == 0) sh.near_listed = 0;
   };
   if (kBins16) clear_keys();
   auto started = cl.barrier_arrive();      // (no CTA writes into another before that has done this)
@@ -665,6 +668,12 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
     // (down to the smallest bf16 number that counts)
     const int low = __float_as_int(weigh.least), top = place_of(hi), bins = top - place_of((low + (low < 0 ? 0 : 0xffff)) >> 16) + 1;
     if (bins <= kKeys) {
+      auto add_near = [&](float l) {
+        const u64 w = weigh.of(l);
+        const int side = l < 0.f;
+        const unsigned old = atomicAdd(&sh.near_lo[side], (unsigned)w);
+        atomicAdd(&sh.near_hi[side], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
+      };
       for (int j = v0 + lane; j < v1; j += 32) {
         const uint4 u = vector(j);
         const unsigned* words = reinterpret_cast<const unsigned*>(&u);
@@ -676,14 +685,18 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           atomicAdd(&sh.keys[b < bins ? b : kKeys + lane], 1u);   // (with a branch to each logit a third slower)
           near |= (unsigned)shared_place(place) << i;
         }
+        // Few are in a shared bin. Their weights wait until the end, where all warps take them together
+        // (at once each would hold its warp up, and all others with it: 256 rows 130 us, so 127 us).
         for (; near; near &= near - 1) {
           const float l = Vec<T>::some(u, __ffs(near) - 1);
-          const u64 w = top - place_of(l) < bins ? weigh.of(l) : 0ull;
-          const int side = l < 0.f;
-          const unsigned old = atomicAdd(&sh.near_lo[side], (unsigned)w);
-          atomicAdd(&sh.near_hi[side], (unsigned)(w >> 32) + (old + (unsigned)w < old ? 1u : 0u));
+          if (top - place_of(l) >= bins) continue;
+          const int at = atomicAdd(&sh.near_listed, 1);
+          if (at < kNears) sh.nears[at] = l;
+          else add_near(l);
         }
       }
+      __syncthreads();
+      for (int i = tid; i < min(sh.near_listed, kNears); i += kNT) add_near(sh.nears[i]);
       bool shared_cut = false;             // within a shared bin: not from counts
       {
         const int share_of = kMaxCtas / ctas, mine = rank * (kKeys / ctas) + tid * share_of;   // this thread's bins
