@@ -16,7 +16,7 @@
 //   as well (16 rows of 202048 and top_p: 25 us, by histograms 47 us).
 // * otherwise a histogram over M - l finds the bin in which the count (top_k) or the
 //   weight (top_p) is reached, a list or histograms over the order of floats within
-//   that bin find K (48 fp32 rows of 65537, some of them with top_p: 32 us).
+//   that bin find K (48 fp32 rows of 65537 and top_p: 33 us).
 //
 // Sums of weights decide which token is drawn, so they are exact: a weight is an
 // integer, in units of 2^-44 of (nearly) the largest, a function of l, M and T alone;
@@ -30,13 +30,13 @@
 // maxima, histograms and sums; each works out the outcome for itself, and the one
 // that has the token writes it.
 //
-// 256 rows of 202048 in bf16 with mixed filters: 127 us, 0.8 TB/s. Without filters a
+// 256 rows of 202048 in bf16 with mixed filters: 130 us, 0.8 TB/s. Without filters a
 // weight's 35 instructions bound it; elsewhere a chain of short steps does, for which the
 // instructions themselves often come too late, and every meeting of a cluster takes
 // 0.9 us. Two CTAs of 64 registers and half of the SM's shared memory each work in the
 // other's waits (one CTA of 1024 threads: 16 rows wait for a second round; three, with
-// spills: 10 to 17% slower). More CTAs to a row do not find room at once, fewer do no
-// more at a time (16 rows by 16: 41 us, by 8: 26 us; 256 rows by 4: 132 us).
+// spills: 10 to 17% slower). More CTAs to a row do not find room at once (16 rows by 16:
+// 41 us, by 8: 26 us).
 #include <cooperative_groups.h>
 #include <float.h>
 #include <math.h>
@@ -297,7 +297,8 @@ struct Shared {
   int found;
 };
 
-constexpr size_t kStaged = 180 * 1024;      // of a row, beside these and the table
+// of a row, beside these and the table, by one CTA on an SM and by each of two
+constexpr size_t kStaged = 180 * 1024, kStagedTwo = 70 * 1024;
 
 // Inclusive sums over the CTA's threads.
 __device__ __forceinline__ u64 scan_warp(u64 x) {
@@ -699,7 +700,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       for (int i = tid; i < min(sh.near_listed, kNears); i += kNT) add_near(sh.nears[i]);
       bool shared_cut = false;             // within a shared bin: not from counts
       {
-        const int share_of = kMaxCtas / ctas, mine = rank * (kKeys / ctas) + tid * share_of;   // this thread's bins
+        // this thread's bins
+        const int some = (kKeys + ctas - 1) / ctas, share_of = (some + kNT - 1) / kNT, mine = rank * some + tid * share_of;
+        const int n_mine = max(0, min(min(share_of, some - tid * share_of), kKeys - mine));
         meet();
         // a bin of all CTAs
         auto count_of = [&](int b) {
@@ -724,7 +727,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
         };
         unsigned n = 0;
         u64 w = 0;
-        for (int i = 0; i < share_of; ++i) {
+        for (int i = 0; i < n_mine; ++i) {
           const unsigned x = count_of(mine + i);
           n += x;
           w += weight_of(mine + i, x);
@@ -751,7 +754,7 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
           const u64 upto = weights ? w_before + w_upto : n_before + n_upto, before = upto - (weights ? w : (u64)n);
           if (before < want && want <= upto) {
             u64 run = before, run_w = w_before + w_upto - w;
-            for (int i = 0; i < share_of; ++i) {
+            for (int i = 0; i < n_mine; ++i) {
               const unsigned x = share_of > 1 ? count_of(mine + i) : n;
               const u64 wx = share_of > 1 ? weight_of(mine + i, x) : w, step = weights ? wx : (u64)x;
               if (run + step >= want) {
@@ -1151,9 +1154,26 @@ cudaError_t run(const SampleArgs& a, cudaStream_t st) {
   // 16-byte vectors of a row, wherever it starts
   const long long vectors = ((long long)a.vocab * sizeof(T) + 15) / 16 + 1;
   int ctas = 1;
-  while (ctas < kMaxCtas && vectors > 1024ll * ctas) ctas *= 2;
-  const size_t bytes = (size_t)((vectors + ctas - 1) / ctas) * 16;
-  const bool staged = bytes <= kStaged;
+  while (ctas < kMaxCtas && vectors > 512ll * ctas) ctas *= 2;
+  auto part = [&]() { return (size_t)((vectors + ctas - 1) / ctas) * 16; };
+  // Of more rows than run at once, fewer CTAs to a row: what a row takes besides looking
+  // at its logits is the same for all of them. (48 fp32 rows of 65537 under top_p by 8:
+  // 47 us, by 5: 33 us, by 4: 37 us; 64 rows: 52, 52 and 37 us; 256 bf16 rows of 32000 by
+  // 4: 90 us, by 1: 48 us.) But only where its part still fits beside another CTA's, up
+  // to a hundred rows or so (48 bf16 rows of 202048 with mixed filters by 8: 36 us, by 4,
+  // which read their logits again in each pass: 49 us; 256 rows under top_p: 182 us and
+  // 164 us). A cluster is of CTAs of one GPC, so what runs at once goes by its size.
+  static const struct { int most, fewer; } kFit[kMaxCtas + 1] = {{}, {}, {160, 1}, {}, {76, 2}, {52, 4}, {}, {}, {36, 5}};
+  while (ctas > 1 && a.rows > kFit[ctas].most) {
+    const int before = ctas;
+    ctas = kFit[ctas].fewer;
+    if (part() > kStagedTwo && (ctas < 4 || a.rows <= 100)) {
+      ctas = before;
+      break;
+    }
+  }
+  const size_t bytes = part();
+  const bool staged = bytes <= (a.rows * ctas <= 152 ? kStaged : kStagedTwo);
   auto kernel = staged ? sample_kernel<T, true> : sample_kernel<T, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kStaged);
   if (e != cudaSuccess) return e;

@@ -434,6 +434,17 @@ def test_sample_many_rows(B):
     B.sample(x[:0], torch.zeros(0, device="cuda"), token)
 
 
+@pytest.mark.parametrize("rows, vocab, dtype", [(41, 30000, "f32"), (101, 150001, "bf16"), (120, 20000, "bf16"), (120, 65537, "f32"), (330, 9000, "bf16")])
+def test_sample_by_fewer_ctas_to_a_row(B, rows, vocab, dtype):
+    """So many rows that each has fewer CTAs, whose part of it is in shared memory or not; every third row has a large top_k."""
+    r = np.random.default_rng(rows)
+    x = logits_like(rows, vocab, dtype, rows)
+    k = np.where(np.arange(rows) % 3 == 0, r.integers(300, vocab, rows), np.where(r.random(rows) < 0.5, 0, r.integers(1, 300, rows)))
+    par = dict(temperature=np.where(r.random(rows) < 0.1, 0.0, r.random(rows) + 0.4), top_k=k, top_p=np.where(r.random(rows) < 0.3, 1.0, r.random(rows)),
+               min_p=np.where(r.random(rows) < 0.5, 0.0, r.random(rows) * 0.2))
+    check_draws(B, x, r.random(rows, dtype=np.float32), near_allowed=1, **par)
+
+
 def test_sample_without_prob_and_rows_untouched(B):
     x = logits_like(4, 300, "f32", 13)
     token = torch.full((6,), -7, dtype=torch.int32, device="cuda")
