@@ -657,6 +657,7 @@ class PagedCache:
                                     BF16 if k.dtype == torch.bfloat16 else F32)
         self._axis = b"", None                                    # the last pair_axis and its buffer
         self._evict_bytes = 0, 0                                  # the last budget and its workspace
+        self._tree_bytes = None, 0                                # the last tree attention's sizes and its workspace
         self._no_bytes = torch.empty(0, dtype=torch.uint8, device=self.device)
         # the C side checks sizes and alignment with every call; once here so a
         # bad cache is refused when it is made
@@ -796,14 +797,17 @@ class PagedCache:
         args = self._attention_args(q, q_pos, start, self._need("out", out, self.dtype, q.shape), lse, scale, causal, window, softcap,
                                     slopes, prefix, max_len)
         end = self._need("tree_end", tree_end, torch.int32, (q.shape[0],))
-        if workspace is None:
+        sizes = *q.shape[:2], max_len
+        held = self._tree_bytes                                   # the workspace goes by these sizes and the cache's
+        if workspace is None and held[0] != sizes:
             try:
                 return self._launch(lib.dflash_paged_tree_attention, stream, args + _NO_WORKSPACE, end)
             except DFlashError as e:
                 if e.code != EINVAL:
                     raise
-        self._with_workspace(lib.dflash_paged_tree_attention, self._query(lib.dflash_paged_tree_attention_workspace, args), args, workspace,
-                             stream, end)
+        if held[0] != sizes:
+            self._tree_bytes = held = sizes, self._query(lib.dflash_paged_tree_attention_workspace, args)
+        self._with_workspace(lib.dflash_paged_tree_attention, held[1], args, workspace, stream, end)
 
     def key_weight(self, q, q_pos, start, lse, weight_out=None, weight=None, decay=1.0, scale=None, causal=True, window=0,
                    softcap=0.0, slopes=None, prefix=None, max_len=0, stream=None):
