@@ -138,19 +138,24 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
   }
-  // query rows that no load fills: zeros, so that nothing depends on what was there
-  for (int e = threadIdx.x; e < QT * C::kHalves * kPtKeys; e += C::kThreads) {
-    const int r = e & (kPtKeys - 1);
-    if (r < tpt * G && (QT == 2 || (r & 31) < 32 / G * G || G > 32)) continue;
+  // Query rows that no load fills are zeros, so that nothing depends on what was there:
+  // those past a tile's tokens, and past a quarter's of a tile that is there 2 or 4 times.
+  auto clear_q = [&](bool tile, bool quarters) {
+    for (int e = threadIdx.x; e < QT * C::kHalves * kPtKeys; e += C::kThreads) {
+      const int r = e & (kPtKeys - 1);
+      if (!(tile && r >= tpt * G) && !(quarters && G <= 32 && (r & 31) >= 32 / G * G)) continue;
 #pragma unroll
-    for (int d = 0; d < 8; ++d) *reinterpret_cast<uint4*>(sm + C::kQ + (e >> 7) * C::kHalfB + r * 128 + d * 16) = make_uint4(0, 0, 0, 0);
-  }
-  fence_proxy_async_shared();
+      for (int d = 0; d < 8; ++d) *reinterpret_cast<uint4*>(sm + C::kQ + (e >> 7) * C::kHalfB + r * 128 + d * 16) = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_shared();
+  };
+  // (a quarter's last rows are a whole tile's tokens where the group does not divide 32:
+  // the load of Q overwrites these zeros, behind a barrier of the CTA)
+  if (!segments) clear_q(true, QT == 1);
   pdl_wait();
   // every warp looks for the tile itself: no one waits for another's answer
   PagedTile t;
   if (segments) {                                        // z of the tile's `splits` segments is this CTA's
-
     const PagedSegment g = paged_find_segment(c, a.start, a.rows, 1, QT * tpt, kPtKeys, a.window, a.target, bx);
     t = g.t;
     z = g.z;
@@ -193,6 +198,8 @@ paged_attn_tc_kernel(const __grid_constant__ CUtensorMap mq, const __grid_consta
   // in quarters of 32 lanes, and a warp takes a half (a quarter) of the keys.
   const int t32 = 32 / G, n_tok = min(tpt, t.count - row0);
   const int rep = QT == 2 || n_tok > 2 * t32 ? 1 : (n_tok > t32 ? 2 : 4);
+  // (a segment's Q may be loaded before the CTA's next barrier: only rows that this load leaves out)
+  if (segments) clear_q(rep == 1, rep > 1);
   auto load_q = [&]() {
     if (rep == 1) {
       mbar_expect_tx(&q_full, nt * C::kHalves * tpt * G * 128);
