@@ -86,24 +86,27 @@ __device__ constexpr PowTable kPow{};
 
 // The weight of a logit at distance M - l, for rows of one temperature. Written for the
 // pipes: a sum or a product takes half as long as an operation on bits or a comparison.
+// Every rounding is written out: a product that the compiler joins to a sum in one place
+// and not in another would give a token two bins, or two weights.
 struct Weigh {
   const float2* table;
   float top, chi, clo, least;              // log2(e) / T in two parts; the smallest logit whose weight is not zero
   __device__ __forceinline__ bool counts(float l) const { return l >= least; }
   // The distance in steps of 2^-10 to a factor of 2, rounded, of a logit that counts.
-  __device__ __forceinline__ float steps(float p) const { return p + 12288.f; }   // 1.5 * 2^13: sums are multiples of 2^-10
+  __device__ __forceinline__ float distance(float d) const { return __fmul_rn(d, chi); }
+  __device__ __forceinline__ float steps(float p) const { return __fadd_rn(p, 12288.f); }   // 1.5 * 2^13: sums are multiples of 2^-10
   static __device__ __forceinline__ int whole_steps(float t) { return __float_as_int(t) & 0x3fffff; }
-  __device__ __forceinline__ int bin(float l) const { return whole_steps(steps((top - l) * chi)) >> kBinShift; }
+  __device__ __forceinline__ int bin(float l) const { return whole_steps(steps(distance(top - l))) >> kBinShift; }
   // The weight of a token that counts as whole * 2^-(steps / 2^10) units, before the
   // shift drops bits; of others anything. No branches: a thread has several tokens' weights under way at once.
   __device__ __forceinline__ void parts(float l, u64& whole, int& i) const {
-    const float d = top - l, p = d * chi;
+    const float d = top - l, p = distance(d);
     const float b = d - top;               // what d's rounding left: (M - (d - b)) + (-l - b)
     const float e = fmaf((top - (d - b)) + (-l - b), chi, fmaf(d, clo, fmaf(d, chi, -p)));
     const float t = steps(p);
     i = whole_steps(t);
     const float r = (p - (t - 12288.f)) + e;              // p = i / 1024 + r, |r| <= 2^-11
-    const float g = r * fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f);   // 2^-r - 1
+    const float g = __fmul_rn(r, fmaf(r, fmaf(r, -0.0555041087f, 0.240226507f), -0.693147181f));   // 2^-r - 1
     const float2 w = table[i & (kSteps - 1)];
     const int c = __float2int_rn(fmaf(w.x, g, w.y));                                     // the rest, in 2^-42
     // the first 24 bits are w.x's: its exponent is the same throughout
@@ -957,7 +960,8 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
       kx[i] = key_of<T>(l);
       wx[i] = weights ? weigh.of(l) : 1ull;
     }
-    while (kmin != kmax) {
+    // (nine bits of a float at a time: four times end it, whatever the sums are)
+    for (int pass = 0; pass < 4 && kmin != kmax; ++pass) {
       int shift = 0;
       while ((kmax - kmin) >> shift >= (unsigned)kBins) ++shift;
       if (n >= 0) {                        // every CTA has them all
