@@ -91,7 +91,8 @@ __device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, c
                                                            int window, int sms, int t) {
   const int lane = threadIdx.x & 31;
   PagedSegment r{{-1, 0, 0, 0}, 0, 1};
-  // of sequence s: its new rows, its query tiles and the key tiles that they may see
+  // of sequence s: its new rows, its query tiles and the key tiles that they may see (one
+  // at least: rows of an empty sequence have a segment too, which writes that they saw nothing)
   int first = 0, count = 0, q_tiles = 0, k_tiles = 0;
   auto look = [&](int s) {
     first = count = q_tiles = k_tiles = 0;
@@ -100,7 +101,7 @@ __device__ __forceinline__ PagedSegment paged_find_segment(const PagedView& c, c
     first = ab.x;
     count = ab.y - ab.x;
     q_tiles = (int)(((long long)count * G + per - 1) / per);
-    k_tiles = (paged_length(c, s) + keys - 1) / keys;
+    k_tiles = max(1, (paged_length(c, s) + keys - 1) / keys);
     if (window > 0) k_tiles = min(k_tiles, (int)min(((long long)window + count) / keys + 2, 1ll << 20));
   };
   long long work = 0;

@@ -54,3 +54,18 @@ def test_groups_that_do_not_divide_a_tile(B, lens, nq, nkv, hd):
     for _ in range(20):
         out, lse = s.call(cache)
         assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+
+
+EMPTY = [(9, 23, 3600, "bf16", 32, 8, 128), (3, 29, 3600, "bf16", 24, 8, 64), (9, 23, 1500, "f32", 16, 16, 64), (12, 60, 1500, "bf16", 16, 8, 128)]
+
+
+@pytest.mark.parametrize("long,empty,length,dtype,nq,nkv,hd", EMPTY)
+def test_new_rows_of_empty_sequences(B, long, empty, length, dtype, nq, nkv, hd):
+    """Rows of sequences whose length is 0 see nothing and are reported, however many there are beside long texts."""
+    lens = [(1, length if i < long else 1) for i in range(long + empty)]
+    lens = lens[long:long + empty // 2] + lens[:long] + lens[long + empty // 2:]
+    s = Trees(B, lens, nq, nkv, hd, 64, dtype, seed=long)
+    s.length[[i for i, (_, n) in enumerate(lens) if n == 1]] = 0
+    cache = s.device()
+    s.check(cache)
+    assert in_segments(s, cache, 128 if dtype == "bf16" else 16) and int(s.status) == B.PAGED_BAD_ROWS
