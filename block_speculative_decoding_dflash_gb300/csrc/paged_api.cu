@@ -1,11 +1,15 @@
 // C ABI of the paged cache: argument checks and launches.
 #include <math.h>
 
+#include <algorithm>
+
 #include "refuse.h"
 
 using namespace dfl;
 
 namespace {
+
+constexpr int kCommitMost = 1024;          // caches of one commit
 
 int need(const void* p, const char* name) { return need_aligned("paged", p, name, 16); }
 int may(const void* p, const char* name) { return p ? need(p, name) : DFLASH_OK; }
@@ -121,6 +125,39 @@ int attend(const dflash_paged_cache* cache, const dflash_paged_attention_args* a
   x->splits = p.splits;
   x->cluster = p.cluster;
   return launched(launch_paged_attention(cache->dtype, *x, p, static_cast<cudaStream_t>(stream)), "paged attention");
+}
+
+// All caches are moved at once, so a row that is in two arrays, or in one that is given
+// twice, would be lost. (The arrays of a kind usually come in the order of their addresses:
+// the four kinds are merged. 24 caches: a call of 10.6 us, with all arrays sorted 11.4 us.)
+int check_apart(const dflash_paged_cache* caches, const dflash_paged_tree_commit_args* a) {
+  struct Array { uintptr_t begin; int cache; };
+  constexpr auto before = [](const Array& x, const Array& y) { return x.begin < y.begin; };
+  Array all[4][kCommitMost];
+  int n[4] = {}, at[4] = {}, last = -1;
+  auto add = [&](int kind, const void* p, int cache) {
+    if (p) all[kind][n[kind]++] = Array{reinterpret_cast<uintptr_t>(p), cache};
+  };
+  for (int i = 0; i < a->n_caches; ++i) {
+    add(0, caches[i].k, i);
+    add(1, caches[i].v, i);
+    add(2, caches[i].pos, i);
+    add(3, a->weight_host ? a->weight_host[i] : nullptr, i);
+  }
+  for (int kind = 0; kind < 4; ++kind)
+    if (!std::is_sorted(all[kind], all[kind] + n[kind], before)) std::sort(all[kind], all[kind] + n[kind], before);
+  const size_t rows = (size_t)caches->n_pages * caches->kv_heads * caches->page_rows;
+  const size_t row = (size_t)caches->head_dim * (caches->dtype == DFLASH_BF16 ? 2 : 4);
+  for (uintptr_t end = 0;;) {
+    int next = -1;
+    for (int kind = 0; kind < 4; ++kind)
+      if (at[kind] < n[kind] && (next < 0 || all[kind][at[kind]].begin < all[next][at[next]].begin)) next = kind;
+    if (next < 0) return DFLASH_OK;
+    const Array& x = all[next][at[next]++];
+    if (x.begin < end) return refuse(DFLASH_EINVAL, "paged tree commit: arrays of caches %d and %d overlap", last, x.cache);
+    end = x.begin + rows * (next < 2 ? row : 4);
+    last = x.cache;
+  }
 }
 
 }  // namespace
@@ -247,7 +284,7 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict
 int dflash_paged_tree_commit(const dflash_paged_cache* caches, const dflash_paged_tree_commit_args* a, void* stream) {
   if (!caches) return refuse(DFLASH_EINVAL, "paged tree commit: caches_host is NULL");
   if (!a) return refuse(DFLASH_EINVAL, "paged tree commit: args is NULL");
-  if (a->n_caches < 1 || a->n_caches > 1024) return refuse(DFLASH_EINVAL, "paged tree commit: n_caches outside [1, 1024]");
+  if (a->n_caches < 1 || a->n_caches > kCommitMost) return refuse(DFLASH_EINVAL, "paged tree commit: n_caches outside [1, %d]", kCommitMost);
   if (a->width < 1 || a->width > (1 << 20)) return refuse(DFLASH_EINVAL, "paged tree commit: width outside [1, 2^20]");
   const dflash_paged_cache* c0 = caches;
   for (int i = 0; i < a->n_caches; ++i) {
@@ -258,10 +295,8 @@ int dflash_paged_tree_commit(const dflash_paged_cache* caches, const dflash_page
         c->n_seq != c0->n_seq || c->max_pages != c0->max_pages || c->dtype != c0->dtype)
       return refuse(DFLASH_EINVAL, "paged tree commit: cache %d has other sizes or another type than the first", i);
     if (a->weight_host) PG(may(a->weight_host[i], "weight"));
-    for (int j = 0; j < i; ++j)            // (a row that moves twice would be lost)
-      if (c->k == caches[j].k || c->v == caches[j].v || c->pos == caches[j].pos)
-        return refuse(DFLASH_EINVAL, "paged tree commit: caches %d and %d share an array", j, i);
   }
+  PG(check_apart(caches, a));
   if ((int64_t)c0->n_seq * a->width >= (1ll << 31)) return refuse(DFLASH_ERANGE, "paged tree commit: n_seq * width reaches 2^31");
   PG(need4(a->path, "path"));
   PG(need4(a->count, "count"));

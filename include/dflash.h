@@ -856,8 +856,8 @@ int dflash_tree_accept(const dflash_tree_accept_args* args, void* stream);
  * row b + i, i < count[s], with b = length[s] - count[s]; `length` is the one after the
  * walk, and the tree's rows start at b. K, V, position and weight move, in every kv
  * head, for n_caches caches (a model's layers; caches_host: HOST array) in one launch
- * per 48 of them. The caches have the same sizes and type and share no pages (EINVAL
- * where two have the same k, v or pos); a
+ * per 48 of them. The caches have the same sizes and type, and of all their k, v, pos
+ * and weights no two overlap (EINVAL: a row that moved twice would be lost); a
  * sequence's path is ascending with path[i] >= i, otherwise DFLASH_PAGED_BAD_ROWS and
  * the row that is out of order stays (as it does beyond the table; a sequence whose
  * count or length cannot be stays as it is). Bit-exact copies; rows that are in their

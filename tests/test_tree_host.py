@@ -215,6 +215,26 @@ def test_commit_refuses(B, what):
     refused(B, B.paged_tree_commit, **a)
 
 
+@pytest.mark.parametrize("what", ["k", "v", "pos", "weight", "k as v", "k as its own v", "part", "pos as weight"])
+def test_commit_refuses_arrays_that_overlap(B, what):
+    """All caches are moved at once: a row that is in two arrays would move twice."""
+    shape, pages = (4, 2, 16), 4
+    t = [{"k": torch.zeros(*shape, 64), "v": torch.zeros(*shape, 64), "pos": ints(*shape), "weight": torch.zeros(shape)} for _ in range(60)]
+    if what in t[0]:
+        t[57][what] = t[3][what]                         # (of another launch, too)
+    elif what == "k as v":
+        t[1]["v"] = t[0]["k"]
+    elif what == "k as its own v":
+        t[2]["v"] = t[2]["k"]
+    elif what == "part":
+        pool = torch.zeros(2 * pages - 1, *shape[1:], 64)
+        t[0]["k"], t[1]["k"] = pool[:pages], pool[pages - 1:]
+    else:
+        t[5]["pos"] = t[7]["weight"].view(torch.int32)
+    caches = [B.PagedCache(x["k"], x["v"], x["pos"], ints(3, 2), ints(3), weight=x["weight"]) for x in t]
+    refused(B, B.paged_tree_commit, "overlap", caches=caches, path=ints(3, 4), count=ints(3))
+
+
 def test_structs_are_the_header_s(B, tmp_path):
     """The packed layouts against the C compiler's."""
     import shutil
