@@ -910,7 +910,7 @@ def sample(logits, uniform, token, prob=None, temperature=None, top_k=None, top_
 def tree_accept(tree_end, start, draft, sampled, tokens, path, count, length=None, length_out=None, stream=None):
     """dflash_tree_accept: the accepted path [n_seq, width] through each sequence's tree, the emitted tokens [n_seq, width] and their
     number count [n_seq]; tree_end, draft, sampled [rows], start [n_seq + 1], length and length_out [n_seq], all int32. length_out
-    defaults to length."""
+    defaults to length. A row whose sampled token is negative (sample's -1) is not on a path, nor what follows it."""
     device, rows, n_seq = start.get_device(), tree_end.shape[0], start.shape[0] - 1
     if path.dim() != 2:
         raise DFlashError(EINVAL, "tree accept: path must be [n_seq, width]")

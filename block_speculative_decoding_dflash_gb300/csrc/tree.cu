@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kAcceptWarps * 32) tree_accept_kernel(const Tr
   int count = 0;
   for (int cur = n > 0 ? 0 : -1; cur >= 0 && count < a.width; ++count) {
     const int said = at(2, cur);
+    if (said < 0) break;                     // the row had nothing to draw: the walk ends before it
     if (lane == 0) {
       a.tokens[(long long)s * a.width + count] = said;
       a.path[(long long)s * a.width + count] = cur;

@@ -803,7 +803,7 @@ int dflash_paged_evict(const dflash_paged_cache* cache, const dflash_paged_evict
  * A temperature below 2^-64 (0, negative, NaN) takes the largest logit, prob 1. A NaN
  * logit counts as -inf, and -inf (or, of fp32 logits, what is further from M than fp32
  * reaches) is never drawn; +inf counts as the type's largest number. A row with nothing
- * to draw gives token -1, prob 0. A uniform number below 0 (or NaN) counts as 0, one of
+ * to draw gives token -1, prob 0 (dflash_tree_accept takes no such token). A uniform number below 0 (or NaN) counts as 0, one of
  * 1 or more draws the last kept token. Tokens that weigh less than 2^-44 are not drawn. Sums are
  * 64-bit integers, the same in any order; a weight is right to 2^-35. */
 typedef struct dflash_sample_args {
@@ -832,7 +832,11 @@ int dflash_sample(const dflash_sample_args* args, void* stream);
  * the sequence's first new row (ascending), and the tokens emitted at them, -1 from
  * count[s] on; the last emitted token is the next round's row 0. length_out[s] =
  * length[s] - new rows + count[s], the length once only the path's rows are kept. A
- * sequence without new rows has count 0. */
+ * sequence without new rows has count 0.
+ * A row whose sampled token is negative, as dflash_sample gives a row with nothing to
+ * draw, ends the walk and is not on the path: the token emitted before it, its own, is the
+ * next round's row 0 and draws again. Where row 0 has none the count is 0, and row 0
+ * stays what it was. */
 typedef struct dflash_tree_accept_args {
   const int32_t* tree_end;  /* [rows] */
   const int32_t* start;     /* [n_seq + 1], ascending; cut to [0, rows] */

@@ -99,10 +99,10 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, largest=np
 
 
 def accept(end, draft, sampled, width):
-    """(path, emitted tokens) of one tree."""
+    """(path, emitted tokens) of one tree; a negative token is none, and its row is not walked."""
     up, path = parents(end), []
     cur = 0 if len(end) else -1
-    while cur >= 0 and len(path) < width:
+    while cur >= 0 and sampled[cur] >= 0 and len(path) < width:
         path.append(cur)
         cur = next((i for i in range(len(end)) if up[i] == cur and draft[i] == sampled[cur]), -1)
     return path, [int(sampled[i]) for i in path]

@@ -42,6 +42,12 @@ def test_oracle_walk_by_hand():
     assert T.accept(END, draft, [5] * 9, 9) == ([0], [5]) and T.accept([], [], [], 4) == ([], [])
 
 
+def test_oracle_walk_ends_before_a_row_with_nothing_to_draw():
+    draft = [0, 11, 12, 13, 14, 15, 16, 15, -1]
+    assert T.accept(END, draft, [14, 0, 0, 0, 15, -1, 99, 0, 0], 9) == ([0, 4], [14, 15])
+    assert T.accept(END, draft, [-1] * 9, 9) == ([], []) and T.accept(END, draft, [-1, 0, 0, 0, 0, 0, 0, 0, 7], 9) == ([], [])
+
+
 def test_oracle_attention_of_a_path_is_the_chain_s():
     """A node's row is what causal attention gives it when only its path has been appended."""
     r = np.random.default_rng(2)
