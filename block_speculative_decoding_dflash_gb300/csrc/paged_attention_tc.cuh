@@ -29,8 +29,9 @@
 // in the half of S's columns that the first leaves free, or, of a sequence that
 // a batch with prompts gives to the two-tile kernel, in the S of the tile that
 // it does not have: what a batch holds beside a decode row does not change how
-// exact the row is. For many rows, where the products are the bound, it is
-// rounded: half a step, 2^-8 relative at most and independent from key to key,
+// exact the row is. For many rows, a prompt's, where the products are the bound, and a
+// tree's that fill more than 64 of the tile's, where they share the time with the softmax,
+// it is rounded: half a step, 2^-8 relative at most and independent from key to key,
 // adds as much error to an output as the output's own rounding to bf16 does
 // (measured against fp64: 0.0023 of the norm instead of 0.0017). The sum of p is
 // taken before, in fp32.

@@ -25,15 +25,15 @@
 // total, and a row's token is another than exact arithmetic's with a probability of
 // 2^-22 or so even where all of 2^18 tokens weigh the same.
 //
-// A cluster of CTAs holds a row in its shared memory, each warp an unbroken stretch
-// of the vocabulary; the logits are read from memory once. The CTAs exchange
-// maxima, histograms and sums; each works out the outcome for itself, and the one
-// that has the token writes it.
+// A cluster of CTAs has a row, each warp an unbroken stretch of the vocabulary. They
+// hold it in their shared memory where it fits; long rows of large batches do not, and
+// are read again, from L2, in each pass. The CTAs exchange maxima, histograms and
+// sums; each works out the outcome for itself, and the one that has the token writes it.
 //
-// 256 rows of 202048 in bf16 with mixed filters: 130 us, 0.8 TB/s. Without filters a
-// weight's 35 instructions bound it; elsewhere a chain of short steps does, for which the
-// instructions themselves often come too late, and every meeting of a cluster takes
-// 0.9 us. Two CTAs of 64 registers and half of the SM's shared memory each work in the
+// 256 rows of 202048 in bf16 with mixed filters (four CTAs to a row, which hold none of
+// it): 131 us, 0.8 TB/s, issue 42%. Without filters a weight's 35 instructions bound it;
+// elsewhere a chain of short steps does, for which the instructions themselves often come
+// too late, and every meeting of a cluster takes 0.9 us. Two CTAs of 64 registers and half of the SM's shared memory each work in the
 // other's waits (one CTA of 1024 threads: 16 rows wait for a second round; three, with
 // spills: 10 to 17% slower). More CTAs to a row do not find room at once (16 rows by 16:
 // 41 us, by 8: 26 us).
@@ -667,7 +667,9 @@ __global__ void __launch_bounds__(kNT, 2) sample_kernel(const SampleArgs a) {
   // ---- bf16: a bin for each number. The row's weights are those of some thousand
   // numbers times their counts, a cut is found in one step, and what each CTA keeps
   // follows from its own counts: weights of single tokens are taken of one CTA's
-  // part only, by all of them.
+  // part only, by all of them. Not without top_k and top_p, where nothing is looked for
+  // but the draw, which costs one weight a token at most (256 rows of 202048 without filters
+  // 155 us, by counting 162, under min_p 95 and 161; 16 rows 22 and 26, 14 and 26).
   if constexpr (kBins16) if (top_k > 0 || top_p < 1.f) {
     // (down to the smallest bf16 number that counts)
     const int low = __float_as_int(weigh.least), top = place_of(hi), bins = top - place_of((low + (low < 0 ? 0 : 0xffff)) >> 16) + 1;
@@ -1161,12 +1163,20 @@ cudaError_t run(const SampleArgs& a, cudaStream_t st) {
   while (ctas < kMaxCtas && vectors > 512ll * ctas) ctas *= 2;
   auto part = [&]() { return (size_t)((vectors + ctas - 1) / ctas) * 16; };
   // Of more rows than run at once, fewer CTAs to a row: what a row takes besides looking
-  // at its logits is the same for all of them. (48 fp32 rows of 65537 under top_p by 8:
-  // 47 us, by 5: 33 us, by 4: 37 us; 64 rows: 52, 52 and 37 us; 256 bf16 rows of 32000 by
-  // 4: 90 us, by 1: 48 us.) But only where its part still fits beside another CTA's, up
-  // to a hundred rows or so (48 bf16 rows of 202048 with mixed filters by 8: 36 us, by 4,
-  // which read their logits again in each pass: 49 us; 256 rows under top_p: 182 us and
-  // 164 us). A cluster is of CTAs of one GPC, so what runs at once goes by its size.
+  // at its logits is the same for all of them. A cluster is of CTAs of one GPC, so what
+  // runs at once goes by its size; the steps, 36 rows by 8, 52 by 5, 76 by 4 and 160 by 2,
+  // are a few rows above that. Under top_p, by 1, 2, 4, 5 and 8 CTAs:
+  //   40 fp32 rows of 65537: 93, 40, 36, 33 and 44 us; 64 rows: 94, 40, 37, 52 and 52;
+  //   100 rows: 94, 69, 58, 62 and 76; 200 rows: 120, 111, 101, 115 and 145
+  //   100 bf16 rows of 32000: 32, 33, 40, 48 and 57 us; 200 rows: 48, 52, 70, 89 and 107
+  // At a step itself the next fewer are ahead (36 fp32 rows of 65537 by 8: 37 us, by
+  // 5: 32; 76 rows by 4: 55 us, by 2: 40), and up to 45 rows by 6, which are none of the
+  // choices, take 30 us.
+  // But up to a hundred rows only where its part still fits beside another CTA's, and then
+  // four at least: what is not held is read again in each pass (bf16 rows of 202048 by 8,
+  // which hold them, and by 4: 48 rows under top_p 44 us both, without filters 40 and 43;
+  // 100 rows 76 and 70, 66 and 72; 256 rows 178 and 164, 157 and 154, by 2 171 and 151, by 1
+  // 226 and 162. By 5, which hold none either, 48 rows take 37 and 34.)
   static const struct { int most, fewer; } kFit[kMaxCtas + 1] = {{}, {}, {160, 1}, {}, {76, 2}, {52, 4}, {}, {}, {36, 5}};
   while (ctas > 1 && a.rows > kFit[ctas].most) {
     const int before = ctas;
